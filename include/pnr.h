@@ -410,6 +410,137 @@ typedef struct pnr_profile {
 int pnr_profile_enable(int on);
 int pnr_last_profile(pnr_profile* out);
 
+/*
+ * ---- Sequence mixing next to the recurrent cells ------------------------------------------
+ *
+ * Linear attention with a decay for each head: the linear recurrence whose state is a
+ * matrix, evaluated exactly (no Newton iteration), for each batch row and state head:
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T          S [D_k, D_v], S_0 = state_in or zeros
+ *   o_t = scale * S_t^T q_t
+ * H query heads share H_kv state heads in consecutive groups of H / H_kv: query head h reads
+ * the state of head h / (H / H_kv); keys, values, decays and states belong to the state head.
+ *
+ * Layout (device pointers, owned by the caller; elements of `dtype` unless stated):
+ *   q          [B, T, H, D_k]         k [B, T, H_kv, D_k]         v [B, T, H_kv, D_v]
+ *              with element strides {batch, token, head} of their own in the descriptor (all
+ *              >= 0; the last axis contiguous), so slices of one projection need no copy
+ *   log_decay  fp32: [H_kv] (PNR_DECAY_HEAD) or [B, T, H_kv] (PNR_DECAY_TOKEN).  A decay
+ *              exp(g) <= 1 is meant, g <= 0; g below -104, -inf included, forgets the state
+ *              completely (exp(g) is 0 in fp32); g > 0 is taken as it is
+ *   state_in, state_out   fp32 [B, H_kv, D_k, D_v]
+ *   o          [B, T, H, D_v] contiguous
+ *   lens       int32 [B] or NULL: row b has min(max(lens[b], 0), T) tokens.  What lies behind
+ *              a row's end is not read (it may hold anything), its outputs and gradients are
+ *              zeros, and the state is the one after the row's last token (an empty row hands
+ *              state_in on)
+ * Supported: dtype PNR_F32 and PNR_BF16, 1 <= D_k, D_v <= 128 (others PNR_E_UNSUPPORTED).
+ * Products are accumulated, and states, decays and sums held, in fp32.
+ *
+ * None of these calls waits for the device or allocates: the work is enqueued on
+ * desc->stream, so they may be recorded into a HIP graph.  Return PNR_OK or a negative
+ * pnr_status.
+ */
+enum pnr_decay_kind { PNR_DECAY_HEAD = 0, PNR_DECAY_TOKEN = 1 };
+
+typedef struct pnr_linattn {
+  int32_t B, T;          /* batch >= 1, tokens >= 0                                    */
+  int32_t H, H_kv;       /* query heads, state heads; H_kv divides H                   */
+  int32_t D_k, D_v;      /* head sizes of keys and queries, of values and outputs      */
+  int32_t dtype;         /* pnr_dtype of q, k, v, o and their gradients                */
+  int32_t decay;         /* pnr_decay_kind                                             */
+  double scale;
+  int64_t q_stride[3], k_stride[3], v_stride[3];   /* elements: batch, token, head      */
+  const int32_t* lens;   /* [B] or NULL                                                */
+  void* stream;          /* hipStream_t, NULL = default stream                         */
+  void* workspace;       /* device scratch, 256-byte aligned                           */
+  size_t workspace_bytes;
+} pnr_linattn;
+
+/*
+ * All tokens of a sequence at once (a prompt, or the forward pass of a layer), in chunks
+ * along time.  state_in may be NULL (zeros), state_out NULL (not wanted); they may be the
+ * same buffer.  Workspace: pnr_linattn_workspace_bytes() bytes (0: none needed, or an invalid
+ * request, which pnr_linattn_forward then names; pure host arithmetic).  With T = 0 only
+ * state_out is written.
+ */
+size_t pnr_linattn_workspace_bytes(const pnr_linattn* desc);
+int pnr_linattn_forward(const pnr_linattn* desc, const void* q, const void* k, const void* v,
+                        const float* log_decay, const float* state_in, void* o, float* state_out);
+
+/*
+ * One token for each of B running requests (T is not read; the token strides and lens are
+ * not either): q [B, H, D_k], k [B, H_kv, D_k], v [B, H_kv, D_v], log_decay [H_kv] or
+ * [B, H_kv], o [B, H, D_v] contiguous.  state_in and state_out are pools
+ * [n_slots, H_kv, D_k, D_v]; request b's state is read from and written to slot slots[b]
+ * (int32 [B]), or slot b when slots is NULL (n_slots >= B then).  A slot outside
+ * [0, n_slots) marks an idle row: its o is zeros and no state is touched.  No two rows may
+ * name the same slot.  state_in and state_out may be the same buffer (updated in place);
+ * otherwise slots that no row names keep what they held in state_out.  No workspace.
+ */
+int pnr_linattn_step(const pnr_linattn* desc, const void* q, const void* k, const void* v,
+                     const float* log_decay, const float* state_in, const int32_t* slots, int n_slots,
+                     void* o, float* state_out);
+
+/*
+ * Gradients of a loss through pnr_linattn_forward, given grad_o = dL/do (contiguous, as o)
+ * and grad_state_out = dL/dstate_out (NULL: zeros):
+ *   grad_q, grad_k, grad_v   dtype, contiguous [B, T, heads, D]; keys' and values' gradients
+ *                            are summed over the query heads that share them
+ *   grad_log_decay           fp32, as log_decay ([H_kv]: summed over rows and tokens, in an
+ *                            order that does not change from call to call)
+ *   grad_state_in            fp32 [B, H_kv, D_k, D_v]
+ * Every gradient output may be NULL (not wanted); all are overwritten.  The states are
+ * recomputed from the inputs.  Workspace: pnr_linattn_workspace_bytes_backward() bytes
+ * (0: invalid request).
+ */
+size_t pnr_linattn_workspace_bytes_backward(const pnr_linattn* desc);
+int pnr_linattn_backward(const pnr_linattn* desc, const void* q, const void* k, const void* v,
+                         const float* log_decay, const float* state_in, const void* grad_o,
+                         const float* grad_state_out, void* grad_q, void* grad_k, void* grad_v,
+                         float* grad_log_decay, float* grad_state_in);
+
+/*
+ * Group norm with an activation, channels last.  x [N, L, C] contiguous; C is split into
+ * `groups` runs of C / groups channels, and each (row n, group) is normalised over its L
+ * positions and its channels (biased variance):
+ *   z = (x - mean) / sqrt(var + eps) * weight + bias
+ *   y = act(z), or with a gate  y = z * act(gate)
+ * L = 1 normalises every token by heads (the norm after linear attention, N = B T); L > 1
+ * a whole map or sequence.  weight, bias fp32 [C], or both NULL; gate as x or NULL; lens int32
+ * [N] or NULL: only the first min(max(lens[n], 0), L) positions of row n belong to it: the
+ * others are not read, and y and the gradients are zeros there (a row with none has mean 0
+ * and rstd 1 / sqrt(eps)).  mean, rstd: fp32 [N, groups] outputs, kept for the backward pass
+ * (NULL: not wanted).  dtype PNR_F32 or PNR_BF16 (x, gate, y and their gradients).  The calls
+ * wait for nothing and allocate nothing.  Workspace sizes: 0 means none needed, or an
+ * invalid request, which the call then names.
+ */
+enum pnr_act { PNR_ACT_NONE = 0, PNR_ACT_SILU = 1, PNR_ACT_GELU = 2 /* tanh form */ };
+
+typedef struct pnr_norm {
+  int32_t N, L, C, groups;   /* N, C >= 1, L >= 0, groups divides C                    */
+  int32_t dtype, act;        /* pnr_dtype, pnr_act                                     */
+  double eps;                /* > 0                                                    */
+  const int32_t* lens;       /* [N] or NULL                                            */
+  void* stream;
+  void* workspace;           /* device scratch, 256-byte aligned                       */
+  size_t workspace_bytes;
+} pnr_norm;
+
+size_t pnr_groupnorm_workspace_bytes(const pnr_norm* desc);
+int pnr_groupnorm(const pnr_norm* desc, const void* x, const float* weight, const float* bias,
+                  const void* gate, void* y, float* mean, float* rstd);
+
+/*
+ * Gradients through pnr_groupnorm, given grad_y and the forward call's mean and rstd:
+ * grad_x, grad_gate (dtype, as x), grad_weight, grad_bias (fp32 [C], summed over N and L in
+ * an order that does not change from call to call).  Each may be NULL; grad_gate needs a
+ * gate, grad_weight a weight.  eps is not read.  All are overwritten.
+ */
+size_t pnr_groupnorm_workspace_bytes_backward(const pnr_norm* desc);
+int pnr_groupnorm_backward(const pnr_norm* desc, const void* x, const float* weight, const float* bias,
+                           const void* gate, const void* grad_y, const float* mean, const float* rstd,
+                           void* grad_x, float* grad_weight, float* grad_bias, void* grad_gate);
+
 #ifdef __cplusplus
 }
 #endif

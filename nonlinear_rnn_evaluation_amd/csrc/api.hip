@@ -81,6 +81,20 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
+}  // namespace
+
+// the same record, for entry points that live in other files
+namespace pnr {
+int record_error(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last.err, sizeof g_last.err, fmt, ap);
+  va_end(ap);
+  return code;
+}
+}  // namespace pnr
+
+namespace {
 size_t align_up(size_t v, size_t a = 256) { return (v + a - 1) / a * a; }
 size_t dsize(int dt) { return dt == PNR_F64 ? 8 : (dt == PNR_F32 ? 4 : 2); }
 

@@ -23,6 +23,8 @@ JAC_FULL, JAC_DIAG, JAC_ZERO = 0, 1, 2
 F64, F32, BF16 = 0, 1, 2
 OK, NOT_CONVERGED, NONFINITE = 0, 1, 2
 E_INVALID, E_UNSUPPORTED, E_WORKSPACE, E_HIP = -1, -2, -3, -4
+DECAY_HEAD, DECAY_TOKEN = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
 STATIC_SCRATCH_BYTES = 64 << 20   # PNR_STATIC_SCRATCH_BYTES of include/pnr.h
 
 _DT = {torch.float64: F64, torch.float32: F32, torch.bfloat16: BF16}
@@ -44,6 +46,21 @@ class PnrParams(ctypes.Structure):
 class PnrProfile(ctypes.Structure):
     _fields_ = [("total_ms", ctypes.c_double), ("proj_ms", ctypes.c_double), ("newton_ms", ctypes.c_double),
                 ("out_ms", ctypes.c_double), ("passes", ctypes.c_int32), ("resid_only", ctypes.c_int32)]
+
+
+class PnrLinattn(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("D_k", ctypes.c_int32), ("D_v", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("decay", ctypes.c_int32), ("scale", ctypes.c_double), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("lens", ctypes.c_void_p),
+                ("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PnrNorm(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("L", ctypes.c_int32), ("C", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("lens", ctypes.c_void_p), ("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 _lib = None
@@ -115,6 +132,19 @@ def load() -> ctypes.CDLL:
     lib.pnr_profile_enable.restype = ctypes.c_int
     lib.pnr_last_profile.argtypes = [P(PnrProfile)]
     lib.pnr_last_profile.restype = ctypes.c_int
+    vp = ctypes.c_void_p
+    for name, args, res in (
+            ("pnr_linattn_workspace_bytes", [P(PnrLinattn)], ctypes.c_size_t),
+            ("pnr_linattn_forward", [P(PnrLinattn)] + [vp] * 7, ctypes.c_int),
+            ("pnr_linattn_step", [P(PnrLinattn)] + [vp] * 6 + [ctypes.c_int, vp, vp], ctypes.c_int),
+            ("pnr_linattn_workspace_bytes_backward", [P(PnrLinattn)], ctypes.c_size_t),
+            ("pnr_linattn_backward", [P(PnrLinattn)] + [vp] * 12, ctypes.c_int),
+            ("pnr_groupnorm_workspace_bytes", [P(PnrNorm)], ctypes.c_size_t),
+            ("pnr_groupnorm", [P(PnrNorm)] + [vp] * 7, ctypes.c_int),
+            ("pnr_groupnorm_workspace_bytes_backward", [P(PnrNorm)], ctypes.c_size_t),
+            ("pnr_groupnorm_backward", [P(PnrNorm)] + [vp] * 11, ctypes.c_int)):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, res
     _lib = lib
     return lib
 
@@ -289,6 +319,51 @@ def pnr_last_profile() -> Optional[dict]:
     return {name: getattr(p, name) for name, _ in PnrProfile._fields_}
 
 
+def pnr_linattn_workspace_bytes(desc: PnrLinattn) -> int:
+    return load().pnr_linattn_workspace_bytes(ctypes.byref(desc))
+
+
+def pnr_linattn_forward(desc: PnrLinattn, q: int, k: int, v: int, log_decay: int, state_in: Optional[int],
+                        o: Optional[int], state_out: Optional[int]) -> int:
+    return load().pnr_linattn_forward(ctypes.byref(desc), q, k, v, log_decay, state_in, o, state_out)
+
+
+def pnr_linattn_step(desc: PnrLinattn, q: int, k: int, v: int, log_decay: int, state_in: int,
+                     slots: Optional[int], n_slots: int, o: int, state_out: int) -> int:
+    return load().pnr_linattn_step(ctypes.byref(desc), q, k, v, log_decay, state_in, slots, n_slots, o, state_out)
+
+
+def pnr_linattn_workspace_bytes_backward(desc: PnrLinattn) -> int:
+    return load().pnr_linattn_workspace_bytes_backward(ctypes.byref(desc))
+
+
+def pnr_linattn_backward(desc: PnrLinattn, q: int, k: int, v: int, log_decay: int, state_in: Optional[int],
+                         grad_o: int, grad_state_out: Optional[int], grad_q: Optional[int], grad_k: Optional[int],
+                         grad_v: Optional[int], grad_log_decay: Optional[int], grad_state_in: Optional[int]) -> int:
+    return load().pnr_linattn_backward(ctypes.byref(desc), q, k, v, log_decay, state_in, grad_o, grad_state_out,
+                                       grad_q, grad_k, grad_v, grad_log_decay, grad_state_in)
+
+
+def pnr_groupnorm_workspace_bytes(desc: PnrNorm) -> int:
+    return load().pnr_groupnorm_workspace_bytes(ctypes.byref(desc))
+
+
+def pnr_groupnorm(desc: PnrNorm, x: int, weight: Optional[int], bias: Optional[int], gate: Optional[int], y: int,
+                  mean: Optional[int], rstd: Optional[int]) -> int:
+    return load().pnr_groupnorm(ctypes.byref(desc), x, weight, bias, gate, y, mean, rstd)
+
+
+def pnr_groupnorm_workspace_bytes_backward(desc: PnrNorm) -> int:
+    return load().pnr_groupnorm_workspace_bytes_backward(ctypes.byref(desc))
+
+
+def pnr_groupnorm_backward(desc: PnrNorm, x: int, weight: Optional[int], bias: Optional[int], gate: Optional[int],
+                           grad_y: int, mean: int, rstd: int, grad_x: Optional[int], grad_weight: Optional[int],
+                           grad_bias: Optional[int], grad_gate: Optional[int]) -> int:
+    return load().pnr_groupnorm_backward(ctypes.byref(desc), x, weight, bias, gate, grad_y, mean, rstd, grad_x,
+                                         grad_weight, grad_bias, grad_gate)
+
+
 # ---- torch-level conveniences (allocation + marshalling) ---------------------------------
 class PnrError(RuntimeError):
     pass
@@ -441,3 +516,198 @@ def scan(kind: int, A: torch.Tensor, b: torch.Tensor, tile_len: int = 0) -> torc
     if rc < 0:
         raise PnrError(f"pnr_scan returned {rc}: {pnr_last_error()}")
     return d
+
+
+# ---- sequence mixing: linear attention with per-head decay, group norm with an activation ------
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
+    """A strided [..., D] operand: the last axis contiguous, the others as they are."""
+    _check(t, name, dtype, shape)
+    if not t.is_cuda:
+        raise ValueError("libpnr takes device tensors")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return t
+
+
+def _same_device(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _workspace(need: int, workspace: Optional[torch.Tensor], device: torch.device, desc) -> Optional[torch.Tensor]:
+    """Points the descriptor at `workspace`, or at a new one where that is missing or too small."""
+    if need:
+        if workspace is None or workspace.numel() * workspace.element_size() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        _same_device(device, workspace=workspace)
+        desc.workspace = _ptr(workspace)
+        desc.workspace_bytes = workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _raise(what: str, rc: int) -> None:
+    if rc < 0:
+        raise PnrError(f"{what} returned {rc}: {pnr_last_error()}")
+
+
+def _linattn(q, k, v, log_decay, scale, lens, step: bool) -> tuple:
+    """The descriptor of a linear-attention call and the four inputs' pointers."""
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"linear attention takes float32 or bfloat16 (got {q.dtype})")
+    if q.dim() != (3 if step else 4) or k.dim() != q.dim() or v.dim() != q.dim():
+        raise ValueError("q, k, v must be " + ("[B, heads, D]" if step else "[B, T, heads, D]"))
+    lead = tuple(q.shape[:-2])
+    H, Dk = q.shape[-2:]
+    Hkv, Dv = v.shape[-2:]
+    _rows(q, "q", q.dtype, (*lead, H, Dk))
+    _rows(k, "k", q.dtype, (*lead, Hkv, Dk))
+    _rows(v, "v", q.dtype, (*lead, Hkv, Dv))
+    token = log_decay.dim() != 1
+    g = _arg(log_decay, "log_decay", torch.float32, (*lead, Hkv) if token else (Hkv,))
+    _same_device(q.device, k=k, v=v, log_decay=log_decay, lens=lens)
+    strides = [(t.stride(0), 0 if step else t.stride(1), t.stride(-2)) for t in (q, k, v)]
+    desc = PnrLinattn(lead[0], 1 if step else lead[1], H, Hkv, Dk, Dv, _DT[q.dtype], DECAY_TOKEN if token else DECAY_HEAD,
+                      Dk ** -0.5 if scale is None else scale, *[(ctypes.c_int64 * 3)(*x) for x in strides],
+                      _arg(lens, "lens", torch.int32, lead[:1]), _stream())
+    return desc, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g)
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
+                     scale: Optional[float] = None, state: Optional[torch.Tensor] = None,
+                     lens: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None,
+                     state_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_linattn_forward: S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t over whole
+    sequences.  q [B,T,H,D_k], k [B,T,H_kv,D_k], v [B,T,H_kv,D_v] (float32 or bfloat16, strided as
+    they come, last axis contiguous), log_decay float32 [H_kv] or [B,T,H_kv], state (the state
+    before the first token, zeros if None) float32 [B,H_kv,D_k,D_v], lens int32 [B] (tokens of
+    each row, T if None); scale None is D_k ** -0.5.  Returns dict(o=[B,T,H,D_v], state=the state
+    after each row's last token, workspace)."""
+    desc, ptrs = _linattn(q, k, v, log_decay, scale, lens, False)
+    B, T, H, Dk = q.shape
+    Hkv, Dv = v.shape[-2:]
+    if o is None:
+        o = torch.empty(B, T, H, Dv, dtype=q.dtype, device=q.device)
+    if state_out is None:
+        state_out = torch.empty(B, Hkv, Dk, Dv, dtype=torch.float32, device=q.device)
+    _same_device(q.device, state=state, o=o, state_out=state_out)
+    shape = (B, Hkv, Dk, Dv)
+    workspace = _workspace(pnr_linattn_workspace_bytes(desc), workspace, q.device, desc)
+    rc = pnr_linattn_forward(desc, *ptrs, _arg(state, "state", torch.float32, shape),
+                             _arg(o, "o", q.dtype, (B, T, H, Dv)), _arg(state_out, "state_out", torch.float32, shape))
+    _raise("pnr_linattn_forward", rc)
+    return {"o": o, "state": state_out, "workspace": workspace}
+
+
+def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                          state: torch.Tensor, *, scale: Optional[float] = None, slots: Optional[torch.Tensor] = None,
+                          state_out: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_linattn_step: one token for each of B requests.  q [B,H,D_k], k [B,H_kv,D_k],
+    v [B,H_kv,D_v], log_decay float32 [H_kv] or [B,H_kv]; state float32 [n_slots,H_kv,D_k,D_v], the
+    pool of running requests' states, of which request b has slot slots[b] (int32 [B]; slot b if
+    None; a slot outside the pool marks an idle row).  The pool is updated in place unless
+    state_out gives another one of its shape.  Returns dict(o=[B,H,D_v], state=the updated pool)."""
+    desc, ptrs = _linattn(q, k, v, log_decay, scale, None, True)
+    B, H, Dk = q.shape
+    Hkv, Dv = v.shape[-2:]
+    if state_out is None:
+        state_out = state
+    if o is None:
+        o = torch.empty(B, H, Dv, dtype=q.dtype, device=q.device)
+    _same_device(q.device, state=state, slots=slots, o=o, state_out=state_out)
+    shape = (state.shape[0], Hkv, Dk, Dv)
+    rc = pnr_linattn_step(desc, *ptrs, _arg(state, "state", torch.float32, shape),
+                          _arg(slots, "slots", torch.int32, (B,)), shape[0], _arg(o, "o", q.dtype, (B, H, Dv)),
+                          _arg(state_out, "state_out", torch.float32, shape))
+    _raise("pnr_linattn_step", rc)
+    return {"o": o, "state": state_out}
+
+
+def linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                              grad_o: torch.Tensor, *, scale: Optional[float] = None,
+                              state: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                              grad_state: Optional[torch.Tensor] = None,
+                              want=("q", "k", "v", "log_decay", "state"),
+                              workspace: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_linattn_backward: gradients through linear_attention of these arguments, given
+    grad_o = dL/do [B,T,H,D_v] and grad_state = dL/d(returned state) (zeros if None).  Returns
+    {name: gradient} for the names in `want` (q, k, v in their dtype; log_decay and state in
+    float32; "state" only where a state is given) and "workspace"."""
+    desc, ptrs = _linattn(q, k, v, log_decay, scale, lens, False)
+    B, T, H, Dk = q.shape
+    Hkv, Dv = v.shape[-2:]
+    shape = (B, Hkv, Dk, Dv)
+    _same_device(q.device, grad_o=grad_o, state=state, grad_state=grad_state)
+    like = dict(q=(q.shape, q.dtype), k=(k.shape, q.dtype), v=(v.shape, q.dtype),
+                log_decay=(log_decay.shape, torch.float32), state=(shape, torch.float32))
+    unknown = set(want) - set(like)
+    if unknown:
+        raise ValueError(f"no gradient named {sorted(unknown)}")
+    out = {n: torch.empty(like[n][0], dtype=like[n][1], device=q.device) for n in want
+           if n != "state" or state is not None}
+    need = pnr_linattn_workspace_bytes_backward(desc)
+    workspace = _workspace(need, workspace, q.device, desc)
+    rc = pnr_linattn_backward(desc, *ptrs, _arg(state, "state", torch.float32, shape),
+                              _arg(grad_o, "grad_o", q.dtype, (B, T, H, Dv)),
+                              _arg(grad_state, "grad_state", torch.float32, shape),
+                              *[_ptr(out.get(n)) for n in ("q", "k", "v", "log_decay", "state")])
+    _raise("pnr_linattn_backward", rc)
+    out["workspace"] = workspace
+    return out
+
+
+def _norm(x, groups, weight, bias, gate, act, eps, lens) -> tuple:
+    """The descriptor of a group-norm call and the pointers of x, weight, bias and gate."""
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"group norm takes float32 or bfloat16 (got {x.dtype})")
+    if x.dim() != 3:
+        raise ValueError(f"x must be [N, L, C] (got {tuple(x.shape)})")
+    N, L, C = x.shape
+    _same_device(x.device, weight=weight, bias=bias, gate=gate, lens=lens)
+    ptrs = (_ptr(x), _arg(weight, "weight", torch.float32, (C,)), _arg(bias, "bias", torch.float32, (C,)),
+            _arg(gate, "gate", x.dtype, (N, L, C)))
+    return PnrNorm(N, L, C, groups, _DT[x.dtype], act, eps, _arg(lens, "lens", torch.int32, (N,)), _stream()), ptrs
+
+
+def group_norm(x: torch.Tensor, groups: int, *, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, act: int = ACT_NONE,
+               eps: float = 1e-5, lens: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_groupnorm on x [N, L, C], channels last: every run of C / groups channels is normalised
+    over itself and the L positions, scaled by weight and bias (float32 [C], both or neither), then
+    y = act(z), or z act(gate) with a gate like x.  lens int32 [N]: the positions of each row.
+    L = 1 is the norm of N tokens by heads.  Returns dict(y, mean, rstd [N, groups], workspace)."""
+    desc, ptrs = _norm(x, groups, weight, bias, gate, act, eps, lens)
+    if y is None:
+        y = torch.empty_like(x)
+    _same_device(x.device, y=y)
+    mean, rstd = torch.empty(2, x.shape[0], max(groups, 1), dtype=torch.float32, device=x.device).unbind(0)
+    workspace = _workspace(pnr_groupnorm_workspace_bytes(desc), workspace, x.device, desc)
+    rc = pnr_groupnorm(desc, *ptrs, _arg(y, "y", x.dtype, tuple(x.shape)), mean.data_ptr(), rstd.data_ptr())
+    _raise("pnr_groupnorm", rc)
+    return {"y": y, "mean": mean, "rstd": rstd, "workspace": workspace}
+
+
+def group_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean: torch.Tensor, rstd: torch.Tensor, *,
+                        weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                        gate: Optional[torch.Tensor] = None, act: int = ACT_NONE,
+                        lens: Optional[torch.Tensor] = None, want=("x", "weight", "bias", "gate"),
+                        workspace: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_groupnorm_backward: gradients through group_norm of these arguments, given grad_y and the
+    mean and rstd that it returned.  Returns {name: gradient} for the names in `want` whose
+    argument is given (x and gate in x's dtype, weight and bias float32) and "workspace"."""
+    desc, ptrs = _norm(x, groups, weight, bias, gate, act, 1e-5, lens)
+    args = dict(x=x, weight=weight, bias=bias, gate=gate)
+    unknown = set(want) - set(args)
+    if unknown:
+        raise ValueError(f"no gradient named {sorted(unknown)}")
+    _same_device(x.device, grad_y=grad_y, mean=mean, rstd=rstd)
+    out = {n: torch.empty_like(args[n]) for n in want if args[n] is not None}
+    workspace = _workspace(pnr_groupnorm_workspace_bytes_backward(desc), workspace, x.device, desc)
+    stats = (x.shape[0], groups)
+    rc = pnr_groupnorm_backward(desc, *ptrs, _arg(grad_y, "grad_y", x.dtype, tuple(x.shape)),
+                                _arg(mean, "mean", torch.float32, stats), _arg(rstd, "rstd", torch.float32, stats),
+                                *[_ptr(out.get(n)) for n in ("x", "weight", "bias", "gate")])
+    _raise("pnr_groupnorm_backward", rc)
+    out["workspace"] = workspace
+    return out

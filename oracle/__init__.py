@@ -38,6 +38,9 @@ What it computes (sources are the five pages on this method):
 * ``newton_dense(..., jac_rank=r)`` -- the dense GRU with a low-rank approximation of its
   Jacobian (ParaRNN overview, "Newton's Iteration": low-rank approximations among the
   approximate-Newton strategies; ``oracle.lowrank``).
+* ``linear_attention`` / ``linear_attention_grad`` -- the linear recurrence with a matrix state
+  and a decay for each head, token by token, and its gradients from the adjoint's recurrence.
+* ``group_norm`` / ``group_norm_grad`` -- group norm with an activation, channels last.
 * ``newton_chunked`` -- the sequence evaluated chunk by chunk, each chunk from the
   previous chunk's last state (ParaRNN overview, "Experimental Results": chunking to
   bound the memory of long sequences).
@@ -57,6 +60,8 @@ from .damped import lm_step_dense, lm_step_kalman, damped_step
 from .chunked import newton_chunked
 from .lowrank import lowrank_matrix, truncated
 from .backward import bptt, cell_vjp
+from .linattn import linear_attention, linear_attention_grad
+from .groupnorm import group_norm, group_norm_grad
 
 __all__ = [
     "CELL_GRU", "CELL_GRU_DIAG", "CELL_LSTM_DIAG", "JAC_FULL", "JAC_DIAG", "JAC_ZERO",
@@ -67,4 +72,5 @@ __all__ = [
     "scan_loop", "scan_doubling", "compose",
     "lm_step_dense", "lm_step_kalman", "damped_step",
     "newton_chunked", "bptt", "cell_vjp", "lowrank_matrix", "truncated",
+    "linear_attention", "linear_attention_grad", "group_norm", "group_norm_grad",
 ]
