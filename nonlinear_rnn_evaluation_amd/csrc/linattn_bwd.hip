@@ -1,0 +1,198 @@
+// Gradients of the linear attention.
+//
+// With D_t = dL/dS_t:  D_t = scale q_t do_t^T + exp(g_{t+1}) D_{t+1}, and
+//   dq_t = scale S_t do_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t,  dS_0 = exp(g_1) D_1:
+// dq, dk and dv are the forward recurrence in other roles (linattn_tile.h).
+//
+// dg_t = <D_t, exp(g_t) S_{t-1}> is the sum of all products that cross from tokens before t to
+// tokens from t on.  Inside a chunk of C tokens with the state S at its start and E what later
+// chunks send back, it is
+//   sum_{i >= t > j} W_ij + sum_{i >= t} b_i + sum_{j < t} c_j + exp(G_C) <S, E>,
+//   W_ij = scale exp(G_i - G_j) (do_i . v_j)(q_i . k_j),  b_i = the part of q_i . dq_i that comes
+//   from S,  c_j = the part of k_j . dk_j that comes from E.
+// No term is subtracted from a larger one except within a chunk, in fp32: the global form
+// dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t would carry every token's rounding to the first.
+// The last term follows from <S, E> at the segment's end X by X <- X + sum b - sum c per chunk.
+#include <type_traits>
+
+#include "linattn_tile.h"
+
+namespace pnr {
+namespace linattn {
+namespace {
+
+struct DecayArgs {
+  LinAttn a;
+  const float *u, *b, *c;    // [B][Hkv][T]; u = sum_j W_tj - sum_i W_it
+  const float* x_end;        // [B][Hkv][nseg], or nullptr: zeros
+  int seg_chunks, nseg;
+  float* gg;                 // [B][T][Hkv] (per token), or
+  double* seg_sum;           // [B][Hkv][nseg]
+};
+
+__device__ __forceinline__ float wave_suffix_sum(float v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const float y = __shfl_down(v, d);
+    if (lane + d < 64) v += y;
+  }
+  return v;
+}
+
+// A wave a segment, its chunks from the last to the first.
+__global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs p) {
+  const LinAttn& a = p.a;
+  const int lane = threadIdx.x & 63;
+  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (w >= (int64_t)a.B * a.Hkv * p.nseg) return;
+  const int seg = w % p.nseg, h = w / p.nseg % a.Hkv, b = w / p.nseg / a.Hkv;
+  const int n = row_len(a.lens, b, a.T);
+  const size_t base = ((size_t)b * a.Hkv + h) * a.T;
+  const int c_lo = seg * p.seg_chunks, c_hi = min(c_lo + p.seg_chunks, (a.T + kChunk - 1) / kChunk);
+  float x = p.x_end ? p.x_end[w] : 0.0f;
+  double sum = 0.0;
+  for (int ch = c_hi - 1; ch >= c_lo; --ch) {
+    const int t = ch * kChunk + lane;
+    const bool in = t < a.T;
+    const float u = in ? p.u[base + t] : 0.0f, bb = in ? p.b[base + t] : 0.0f, cc = in ? p.c[base + t] : 0.0f;
+    const float ub = wave_suffix_sum(u + bb, lane), cs = wave_suffix_sum(cc, lane);
+    const float b_all = __shfl(wave_suffix_sum(bb, lane), 0), c_all = __shfl(cs, 0);
+    const float g = a.g[a.decay_token ? ((size_t)b * a.T + (in ? t : 0)) * a.Hkv + h : (size_t)h];
+    x -= c_all;                                   // exp(G_C) <S, E>
+    // a decay that forgets everything passes no gradient
+    const float d = t < n && !(g <= kLogDecayMin) ? ub + (c_all - cs) + x : 0.0f;
+    if (p.gg && in) p.gg[((size_t)b * a.T + t) * a.Hkv + h] = d;
+    sum += d;
+    x += b_all;
+  }
+  if (p.seg_sum) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) p.seg_sum[w] = sum;
+  }
+}
+
+__global__ void __launch_bounds__(64) decay_head_kernel(const double* seg_sum, int B, int Hkv, int nseg, float* gg) {
+  const int h = blockIdx.x;
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < (int64_t)B * nseg; i += 64) s += seg_sum[((i / nseg) * Hkv + h) * nseg + i % nseg];
+#pragma unroll
+  for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+  if (threadIdx.x == 0) gg[h] = (float)s;
+}
+
+struct BackwardLayout {
+  Plan plan;
+  size_t s = 0, e = 0, last = 0, decay = 0, u = 0, b = 0, c = 0, x_end = 0, seg_sum = 0, total = 0;
+};
+BackwardLayout backward_layout(const LinAttn& a) {
+  BackwardLayout l;
+  l.plan = make_plan(a);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t rows = (size_t)a.B * a.Hkv, segs = rows * l.plan.nseg, tokens = rows * a.T * 4;
+  if (l.plan.nseg > 1) l.s = take(l.plan.states), l.e = take(l.plan.states), l.decay = take(segs * 4);
+  l.last = take(rows * a.Dk * a.Dv * 4);
+  l.u = take(tokens), l.b = take(tokens), l.c = take(tokens);
+  l.x_end = take(segs * 4);
+  l.seg_sum = take(segs * 8);
+  l.total = off;
+  return l;
+}
+
+}  // namespace
+}  // namespace linattn
+
+using namespace linattn;
+
+size_t linattn_workspace_backward(const LinAttn& a) { return backward_layout(a).total; }
+
+hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, const LinAttnGrads& d, char* ws,
+                                   hipStream_t st) {
+  const BackwardLayout l = backward_layout(a);
+  const int G = a.H / a.Hkv, nseg = l.plan.nseg;
+  const int64_t rows = (int64_t)a.B * a.Hkv;
+  float *S = (float*)(ws + l.s), *E = (float*)(ws + l.e), *last = (float*)(ws + l.last);
+  float *u = (float*)(ws + l.u), *b = (float*)(ws + l.b), *c = (float*)(ws + l.c);
+  hipError_t e = hipSuccess;
+
+  RoleArgs base{};
+  base.a = a;
+  base.vec = rows_vec(a.q, a.Dk, a.bf16) && rows_vec(a.k, a.Dk, a.bf16) && rows_vec(a.v, a.Dv, a.bf16) &&
+             rows_vec(d.go, a.Dv, a.bf16);
+  base.seg_chunks = l.plan.seg_chunks, base.nseg = nseg;
+  base.p_scale = a.scale;
+  // forward in time: keys k, values v; backward: keys q, values do, times the scale
+  RoleArgs fwd = base, rev = base;
+  fwd.nkv = 1, fwd.nq = G, fwd.inter_scale = a.scale, fwd.upd_scale = 1.0f;
+  rev.nkv = G, rev.nq = 1, rev.inter_scale = 1.0f, rev.upd_scale = a.scale;
+  fwd.s_in = state_in, rev.s_in = d.gstate_out;
+  // states are needed at the segments' starts (forward in time) and ends (backward)
+  const bool need_s = d.gq || d.gg, need_e = d.gk || d.gv || d.gg || d.gstate_in;
+  if (nseg > 1) {
+    ScanArgs sc[2];
+    int count = 0;
+    float* decay = (float*)(ws + l.decay);
+    if (need_s) {
+      RoleArgs p = fwd;
+      p.y = a.k, p.z = a.v, p.dk = a.Dk, p.dv = a.Dv;
+      p.s_out = S, p.seg_decay = decay;
+      if ((e = run_role<false, kSum>(p, st)) != hipSuccess) return e;
+      sc[count++] = {S, decay, state_in, last, nseg, a.Dk * a.Dv, 0};
+      fwd.s_in = S;
+    }
+    if (need_e) {
+      RoleArgs p = rev;
+      p.y = a.q, p.z = d.go, p.dk = a.Dk, p.dv = a.Dv;
+      p.s_out = E, p.seg_decay = decay;
+      if ((e = run_role<true, kSum>(p, st)) != hipSuccess) return e;
+      sc[count++] = {E, decay, d.gstate_out, d.gstate_in, nseg, a.Dk * a.Dv, 1};
+      rev.s_in = E;
+    }
+    if (count && (e = launch_scan(sc, count, rows, st)) != hipSuccess) return e;
+  }
+
+  if (d.gq || d.gg) {
+    RoleArgs p = fwd;
+    p.x = d.go, p.y = a.v, p.z = a.k, p.e = a.q;
+    p.dk = a.Dv, p.dv = a.Dk, p.transposed = 1;
+    p.o = d.gq, p.vec_out = a.Dk % 4 == 0 && (uintptr_t)d.gq % 16 == 0;
+    p.u = u, p.b = b;
+    if (nseg == 1) p.s_out = last;
+    if ((e = run_role<false, kDotQ>(p, st)) != hipSuccess) return e;
+  }
+  const bool want_e = d.gstate_in && nseg == 1;
+  if (d.gk || d.gg || want_e) {
+    RoleArgs p = rev;
+    p.x = a.v, p.y = d.go, p.z = a.q, p.e = a.k;
+    p.dk = a.Dv, p.dv = a.Dk, p.transposed = 1;
+    p.o = d.gk, p.vec_out = a.Dk % 4 == 0 && (uintptr_t)d.gk % 16 == 0;
+    p.c = c;
+    if (d.gg && (d.gstate_out || nseg > 1)) p.x_end = (float*)(ws + l.x_end), p.s_entry = S, p.s_last = last;
+    if (nseg == 1) p.s_out = d.gstate_in;
+    if ((e = run_role<true, kDotK>(p, st)) != hipSuccess) return e;
+  }
+  if (d.gv) {
+    RoleArgs p = rev;
+    p.x = a.k, p.y = a.q, p.z = d.go;
+    p.dk = a.Dk, p.dv = a.Dv;
+    p.o = d.gv, p.vec_out = a.Dv % 4 == 0 && (uintptr_t)d.gv % 16 == 0;
+    if ((e = run_role<true, kOut>(p, st)) != hipSuccess) return e;
+  }
+  if (d.gg) {
+    DecayArgs p{a, u, b, c, nullptr, l.plan.seg_chunks, nseg, nullptr, nullptr};
+    if (a.decay_token) p.gg = d.gg; else p.seg_sum = (double*)(ws + l.seg_sum);
+    if (d.gstate_out || nseg > 1) p.x_end = (float*)(ws + l.x_end);
+    const int64_t waves = rows * nseg;
+    decay_grad_kernel<<<(unsigned)((waves + 3) / 4), 256, 0, st>>>(p);
+    if (!a.decay_token) decay_head_kernel<<<a.Hkv, 64, 0, st>>>(p.seg_sum, a.B, a.Hkv, nseg, d.gg);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace pnr

@@ -1,0 +1,711 @@
+// The chunk kernel of the linear attention: device code shared by linattn_fwd.hip and
+// linattn_bwd.hip.
+//
+// One recurrence in several roles.  With queries x, keys y, values z, tokens of a chunk
+// 1..C, G_i = g_1 + ... + g_i and S the state at the chunk's start,
+//   out_i = exp(G_i) S^T x_i + sum_{j <= i} exp(G_i - G_j) (x_i . y_j) z_j
+//   S    <- exp(G_C) S + sum_j exp(G_C - G_j) y_j z_j^T
+// and against time, S being what later chunks send back,
+//   out_i = exp(G_C - G_i) S^T x_i + sum_{j >= i} exp(G_j - G_i) (x_i . y_j) z_j
+//   S    <- exp(G_C) S + sum_j exp(G_j) y_j z_j^T.
+//         x    y    z    direction   state
+//   o     q    k    v    forward     S
+//   dq    do   v    k    forward     S transposed
+//   dk    v    do   q    backward    dL/dS transposed
+//   dv    k    q    do   backward    dL/dS
+#pragma once
+
+#include "seq_ops.h"
+
+namespace pnr {
+namespace linattn {
+
+constexpr int kChunk = 64;
+constexpr int kThreads = 256;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+enum Kind {
+  kSum = 0,     // only the state's sum over the segment, from zero
+  kOut = 1,     // outputs
+  kDotQ = 2,    // dq, and from it u and b of the decay's gradient
+  kDotK = 3,    // dk, and from it c of the decay's gradient
+};
+
+struct RoleArgs {
+  LinAttn a;
+  Rows x, y, z, e;       // queries, keys, values; the rows that the outputs' dot products are taken with
+  int nq, nkv;           // heads of x, e and the outputs, and of y and z, per state head; one of them is 1
+  int dk, dv;            // columns of x and y, and of z, e and the outputs
+  int transposed;        // states are stored [dv][dk]
+  int vec;               // rows of x, y, z, e may be read in 16-byte pieces
+  int vec_out;           // outputs may be written four at a time
+  float p_scale, inter_scale, upd_scale;   // on scores, on S^T x, on y z^T
+  const float* s_in;     // [B][Hkv][nseg] states at the segments' entry, or nullptr: zeros
+  float* s_out;          // [B][Hkv][nseg] states at the segments' exit, or nullptr
+  float* seg_decay;      // kSum: [B][Hkv][nseg] the segment's whole decay, or nullptr
+  void* o;
+  float *u, *b, *c;      // [B][Hkv][T] (kDotQ: u and b, kDotK: c)
+  float* x_end;          // kDotK: [B][Hkv][nseg] <state after the segment's last token, s_in>, or nullptr
+  const float* s_entry;  // ... that state, for all but the last segment: the next one's entry, [B][Hkv][nseg]
+  const float* s_last;   // ... and after the last, [B][Hkv]
+  int seg_chunks, nseg;
+};
+
+// ---- fragments ---------------------------------------------------------------------------
+// An MFMA operand covers 16 rows (or columns) x 32 of the summed index: lane l holds row
+// l & 15 and eight summed indexes, those of its group g = l >> 4.  Which eight is free as long
+// as both operands agree: "natural" is 8 g + e; "split" is 4 g + e (e < 4) and 16 + 4 g + e - 4, the
+// order in which two stacked accumulator tiles hold their rows, so that a state in
+// accumulators is an operand without leaving its registers.
+template <bool kBf16>
+struct Mma;
+
+template <>
+struct Mma<true> {
+  using Elt = uint16_t;
+  using Frag = bf16x8;
+  static constexpr int kPiece = 8;     // elements of a 16-byte piece
+  static constexpr int kPad = 8;       // elements of padding a row: rows start 4 banks apart
+  static __device__ __forceinline__ f32x4 mul(Frag a, Frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ Frag rows(const Elt* p) { return *(const Frag*)p; }
+  static __device__ __forceinline__ Frag rows_split(const Elt* p) {
+    struct { uint2 a, b; } w{*(const uint2*)p, *(const uint2*)(p + 16)};
+    return __builtin_bit_cast(Frag, w);
+  }
+  // eight rows (natural order) of one column: two transposing reads of 4 rows x 16 columns, for
+  // which lane i of a group points at row i / 4, columns 4 (i % 4) .. + 3
+  static __device__ __forceinline__ Frag cols(const Elt* tile, int pitch, int row0, int col0, int lane) {
+    const Elt* p = tile + (row0 + (lane >> 4) * 8 + ((lane >> 2) & 3)) * pitch + col0 + (lane & 3) * 4;
+    using L = __attribute__((address_space(3))) s16x4;
+    struct { s16x4 a, b; } w{__builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)p),
+                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + 4 * pitch))};
+    return __builtin_bit_cast(Frag, w);
+  }
+  static __device__ __forceinline__ bool finite(Frag f) {
+    struct W { uint32_t w[4]; } w = __builtin_bit_cast(W, f);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m |= (w.w[i] & 0x7f807f80u) + 0x00800080u;
+    return (m & 0x80008000u) == 0;
+  }
+};
+
+template <>
+struct Mma<false> {
+  using Elt = float;
+  struct Frag { float v[8]; };
+  static constexpr int kPiece = 4;
+  static constexpr int kPad = 4;
+  static __device__ __forceinline__ f32x4 mul(const Frag& a, const Frag& b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+    return c;
+  }
+  static __device__ __forceinline__ Frag two(const float* p, const float* q) {
+    Frag f;
+    const float4 a = *(const float4*)p, b = *(const float4*)q;
+    f.v[0] = a.x, f.v[1] = a.y, f.v[2] = a.z, f.v[3] = a.w;
+    f.v[4] = b.x, f.v[5] = b.y, f.v[6] = b.z, f.v[7] = b.w;
+    return f;
+  }
+  static __device__ __forceinline__ Frag rows(const Elt* p) { return two(p, p + 4); }
+  static __device__ __forceinline__ Frag rows_split(const Elt* p) { return two(p, p + 16); }
+  static __device__ __forceinline__ Frag cols(const Elt* tile, int pitch, int row0, int col0, int lane) {
+    Frag f;
+    const Elt* p = tile + (row0 + (lane >> 4) * 8) * pitch + col0 + (lane & 15);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = p[e * pitch];
+    return f;
+  }
+  static __device__ __forceinline__ bool finite(const Frag& f) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m |= (__float_as_uint(f.v[e]) & 0x7f800000u) + 0x00800000u;
+    return (m & 0x80000000u) == 0;
+  }
+};
+
+// Eight fp32 values as an operand: in fp32 as they are; in bf16 as the sum of kParts bf16 values,
+// each the rounding of what the ones before it leave.  One part is good to 2^-9 of each value, and
+// goes where the result is rounded to bf16 anyway; three are good to 2^-27, and go where a
+// result in fp32 depends on them (two, 2^-18, showed in such results: 2e-6 of a state).
+template <bool kBf16, int kParts>
+struct Split;
+template <int kParts>
+struct Split<true, kParts> {
+  bf16x8 part[kParts];
+  __device__ __forceinline__ explicit Split(float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        part[k][e] = (__bf16)v[e];
+        if (k + 1 < kParts) v[e] -= (float)part[k][e];
+      }
+  }
+  // the smallest part first
+  __device__ __forceinline__ f32x4 mul_a(const bf16x8& b, f32x4 c) const {
+#pragma unroll
+    for (int k = kParts; k--;) c = Mma<true>::mul(part[k], b, c);
+    return c;
+  }
+  __device__ __forceinline__ f32x4 mul_b(const bf16x8& a, f32x4 c) const {
+#pragma unroll
+    for (int k = kParts; k--;) c = Mma<true>::mul(a, part[k], c);
+    return c;
+  }
+};
+template <int kParts>
+struct Split<false, kParts> {
+  Mma<false>::Frag f;
+  __device__ __forceinline__ explicit Split(float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = v[e];
+  }
+  __device__ __forceinline__ f32x4 mul_a(const Mma<false>::Frag& b, f32x4 c) const { return Mma<false>::mul(f, b, c); }
+  __device__ __forceinline__ f32x4 mul_b(const Mma<false>::Frag& a, f32x4 c) const { return Mma<false>::mul(a, f, c); }
+};
+
+// ---- tiles ---------------------------------------------------------------------------------
+// 64 rows x kCols of one operand on its way from memory to LDS: 16-byte pieces in registers.
+template <bool kBf16, int kCols>
+struct Stage {
+  using M = Mma<kBf16>;
+  using Elt = typename M::Elt;
+  static constexpr int kPerRow = kCols / M::kPiece;
+  static constexpr int kN = kChunk * kPerRow / kThreads;
+  static constexpr int kPitch = kCols + M::kPad;
+  uint4 v[kN];
+
+  // Rows t0 .. t0 + 63 of batch row b and head h; rows at or past n and columns past `cols` are
+  // zeros.  `vec`: every piece is one aligned load, and 64 rows span less than 2^31 bytes, so an
+  // address is a uniform base and a 32-bit offset.
+  __device__ __forceinline__ void load(const Rows& r, int b, int64_t h, int t0, int n, int cols, bool vec) {
+    constexpr int kStep = kThreads / kPerRow;            // rows between a thread's pieces
+    const Elt* base = (const Elt*)r.p + b * r.sb + h * r.sh + t0 * r.st;
+    const int row = threadIdx.x / kPerRow, c = (threadIdx.x % kPerRow) * M::kPiece;
+    const bool in = c < cols;
+    if (vec) {
+      const uint32_t off = (uint32_t)(row * (int)r.st + c) * (uint32_t)sizeof(Elt);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (in && t0 + row + i * kStep < n) v[i] = *(const uint4*)((const char*)(base + i * kStep * r.st) + off);
+      }
+    } else {
+      for (int i = 0; i < kN; ++i) {
+        Elt e[M::kPiece];
+        const bool live = in && t0 + row + i * kStep < n;
+#pragma unroll
+        for (int k = 0; k < M::kPiece; ++k)
+          e[k] = live && c + k < cols ? base[(int64_t)(row + i * kStep) * r.st + c + k] : Elt(0);
+        uint4 w;
+        __builtin_memcpy(&w, e, 16);
+#pragma unroll
+        for (int q = 0; q < kN; ++q)
+          if (q == i) v[q] = w;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(Elt* tile) const {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int p = threadIdx.x + i * kThreads;
+      *(uint4*)(tile + (p / kPerRow) * kPitch + (p % kPerRow) * M::kPiece) = v[i];
+    }
+  }
+};
+
+__device__ __forceinline__ float row16_sum(float v) {      // over the 16 lanes of a group
+  v += __shfl_xor(v, 1);
+  v += __shfl_xor(v, 2);
+  v += __shfl_xor(v, 4);
+  return v + __shfl_xor(v, 8);
+}
+__device__ __forceinline__ float group_sum(float v) {      // over the four groups
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// LDS of one block.
+template <bool kBf16, int DK, int DV, Kind kind>
+struct Shared {
+  using Elt = typename Mma<kBf16>::Elt;
+  static constexpr bool kSumOnly = kind == kSum;
+  alignas(16) Elt x[kSumOnly ? 1 : kChunk * Stage<kBf16, DK>::kPitch];
+  alignas(16) Elt y[kChunk * Stage<kBf16, DK>::kPitch];
+  alignas(16) Elt z[kChunk * Stage<kBf16, DV>::kPitch];
+  alignas(16) Elt e[kind == kDotQ || kind == kDotK ? kChunk * Stage<kBf16, DV>::kPitch : 1];
+  alignas(16) Elt p[kSumOnly ? 1 : kChunk * Stage<kBf16, kChunk>::kPitch];   // scores [i][j]
+  alignas(16) float ghi[kChunk], glo[kChunk];   // G in units of log2, as a sum of two floats
+  float inter[kChunk], upd[kChunk];             // the weights of S^T x and of y z^T
+  float total;                                  // exp(G_C)
+  float dot[kind == kDotQ || kind == kDotK ? 4 : 1][kChunk];
+  float row[kind == kDotQ ? kChunk : 1], col[kind == kDotQ ? 10 : 1][16];
+};
+
+// A block walks the chunks of one segment of one state head, with the state in accumulators:
+// wave w holds the columns w DV / 4 .. of S, all DK rows.  A chunk:
+//   scores    each wave 16 query rows: P^T = Y X^T, weighted, to LDS           (P is rounded to the
+//             element type: one rounding of each score before a sum over up to 64 of them)
+//   inter     O^T = S^T X^T, weighted; S enters as bf16 (one rounding), or as three bf16 parts
+//             where a dot product in fp32 is taken from it
+//   intra     O^T += Z^T P^T
+//   update    S = exp(G_C) S + Y^T (w Z), w Z as three bf16 parts
+template <bool kBf16, int DK, int DV, bool kReverse, Kind kind>
+__global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs p) {
+  using M = Mma<kBf16>;
+  using Elt = typename M::Elt;
+  using Frag = typename M::Frag;
+  constexpr int NT = DV / 64;               // column tiles of 16 of a wave
+  constexpr int KT = DK / 16;               // row tiles of S
+  constexpr int NW = NT * 16;
+  constexpr int PK = Stage<kBf16, DK>::kPitch, PV = Stage<kBf16, DV>::kPitch, PP = Stage<kBf16, kChunk>::kPitch;
+  constexpr bool kDots = kind == kDotQ || kind == kDotK;
+  constexpr int kParts = kDots ? 3 : 1;
+  using Sh = Shared<kBf16, DK, DV, kind>;
+  extern __shared__ __align__(16) char smem[];
+  Sh& sh = *(Sh*)smem;
+
+  const LinAttn& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l15 = lane & 15, g4 = (lane >> 4) * 4;
+  const int seg = blockIdx.x % p.nseg;
+  const int h = blockIdx.x / p.nseg % a.Hkv, b = blockIdx.x / p.nseg / a.Hkv;
+  const int n = row_len(a.lens, b, a.T);
+  const int c_lo = seg * p.seg_chunks, c_all = (a.T + kChunk - 1) / kChunk;
+  const int c_hi = min(c_lo + p.seg_chunks, c_all);
+  const int live = min(c_hi, (n + kChunk - 1) / kChunk);       // chunks c_lo .. live - 1 hold tokens
+  const int nsub = p.nq > p.nkv ? p.nq : p.nkv;
+  const size_t sbase = (size_t)blockIdx.x * p.dk * p.dv;
+  const int col0 = wave * NW;                                  // the wave's first column
+
+  f32x4 S[KT][NT];
+  auto s_at = [&](int kt, int nt, int r) {     // element (row, column) of accumulator register r
+    const int i = kt * 16 + g4 + r, j = col0 + nt * 16 + l15;
+    return sbase + (p.transposed ? (size_t)j * p.dk + i : (size_t)i * p.dv + j);
+  };
+  auto s_in_range = [&](int kt, int nt, int r) { return kt * 16 + g4 + r < p.dk && col0 + nt * 16 + l15 < p.dv; };
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        S[kt][nt][r] = (kind != kSum && p.s_in && s_in_range(kt, nt, r)) ? p.s_in[s_at(kt, nt, r)] : 0.0f;
+
+  if constexpr (kind == kDotK) {
+    if (p.x_end) {
+      const size_t size = (size_t)p.dk * p.dv;
+      const float* after = seg + 1 < p.nseg ? p.s_entry + size : p.s_last - sbase + blockIdx.x / p.nseg * size;
+      float s = 0.0f;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (s_in_range(kt, nt, r)) s += S[kt][nt][r] * after[s_at(kt, nt, r)];
+      s = row16_sum(group_sum(s));
+      if (lane == 0) sh.dot[0][wave] = s;
+      __syncthreads();
+      if (tid == 0) p.x_end[blockIdx.x] = sh.dot[0][0] + sh.dot[0][1] + sh.dot[0][2] + sh.dot[0][3];
+    }
+  }
+
+  Stage<kBf16, DK> sx, sy;
+  Stage<kBf16, DV> sz, se;
+  float g_next = 0.0f;
+  const bool vec = p.vec;
+  auto fetch = [&](int c, int sub) {
+    const int t0 = c * kChunk;
+    if constexpr (kind != kSum)
+      if (p.nq > 1 || sub == 0) {
+        sx.load(p.x, b, (int64_t)h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dk, vec);
+        if constexpr (kDots) se.load(p.e, b, (int64_t)h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dv, vec);
+      }
+    if (p.nkv > 1 || sub == 0) {
+      const int64_t hh = (int64_t)h * p.nkv + (p.nkv > 1 ? sub : 0);
+      sy.load(p.y, b, hh, t0, n, p.dk, vec);
+      sz.load(p.z, b, hh, t0, n, p.dv, vec);
+    }
+    if (sub == 0 && wave == 0) {
+      const int t = t0 + lane;
+      g_next = t < n ? clamp_log_decay(a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h]) : 0.0f;
+    }
+  };
+
+  double seg_log = 0.0;                       // wave 0: log2 of the segment's decay
+  const int count = live > c_lo ? (live - c_lo) * nsub : 0;
+  if (count > 0) fetch(kReverse ? live - 1 : c_lo, 0);
+  float u_acc = 0.0f, b_acc = 0.0f;           // threads 0..63 (kDots): sums over the query heads
+  f32x4 O[4][NT];
+
+  for (int it = 0; it < count; ++it) {
+    const int c = kReverse ? live - 1 - it / nsub : c_lo + it / nsub, sub = it % nsub, t0 = c * kChunk;
+    const bool new_x = p.nq > 1 || sub == 0, new_yz = p.nkv > 1 || sub == 0;
+    __syncthreads();
+    if constexpr (kind != kSum)
+      if (new_x) {
+        sx.store(sh.x);
+        if constexpr (kDots) se.store(sh.e);
+      }
+    if (new_yz) {
+      sy.store(sh.y);
+      sz.store(sh.z);
+    }
+    if (sub == 0 && wave == 0) {
+      // G: an inclusive scan over the chunk in 64 bits, because differences of sums of log
+      // decays (each down to -104) are what counts
+      double x = (double)g_next * 1.4426950408889634;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const double y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+      }
+      const double end = __shfl(x, 63);
+      const float hi = (float)x;
+      sh.ghi[lane] = hi;
+      sh.glo[lane] = (float)(x - (double)hi);
+      const float from_start = __builtin_amdgcn_exp2f((float)x), to_end = __builtin_amdgcn_exp2f((float)(end - x));
+      sh.inter[lane] = (kReverse ? to_end : from_start) * p.inter_scale;
+      sh.upd[lane] = (kReverse ? from_start : to_end) * p.upd_scale;
+      if (lane == 0) sh.total = __builtin_amdgcn_exp2f((float)end);
+      seg_log += end;
+    }
+    auto fetch_next = [&] {
+      if (it + 1 < count) fetch(kReverse ? live - 1 - (it + 1) / nsub : c_lo + (it + 1) / nsub, (it + 1) % nsub);
+    };
+    if constexpr (kind == kSum) fetch_next();
+    __syncthreads();
+
+    if constexpr (kind != kSum) {
+      // ---- scores of the wave's 16 queries: lane column i, four rows j a register block
+      const int i = wave * 16 + l15;
+      f32x4 P[4], A[4];
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) P[jt] = A[jt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < DK / 32; ++k) {
+        const Frag xf = M::rows(sh.x + i * PK + k * 32 + g4 * 2);
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt)
+          if (kReverse ? jt >= wave : jt <= wave)
+            P[jt] = M::mul(M::rows(sh.y + (jt * 16 + l15) * PK + k * 32 + g4 * 2), xf, P[jt]);
+      }
+      if constexpr (kind == kDotQ) {
+#pragma unroll
+        for (int k = 0; k < DV / 32; ++k) {
+          const Frag ef = M::rows(sh.e + i * PV + k * 32 + g4 * 2);
+#pragma unroll
+          for (int jt = 0; jt < 4; ++jt)
+            if (jt <= wave) A[jt] = M::mul(M::rows(sh.z + (jt * 16 + l15) * PV + k * 32 + g4 * 2), ef, A[jt]);
+        }
+      }
+      const float gi = sh.ghi[i], gi_lo = sh.glo[i];
+      float row = 0.0f;
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        Elt pe[4];
+        if (kReverse ? jt >= wave : jt <= wave) {
+          const float4 gh = *(const float4*)&sh.ghi[jt * 16 + g4], gl = *(const float4*)&sh.glo[jt * 16 + g4];
+          const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = jt * 16 + g4 + r;
+            const float d = (gi - ghv[r]) + (gi_lo - glv[r]);
+            const float w = __builtin_amdgcn_exp2f(kReverse ? -d : d) * p.p_scale;
+            const bool in = kReverse ? j >= i : j <= i;
+            const float s = in ? P[jt][r] * w : 0.0f;
+            if constexpr (kind == kDotQ) {
+              const float t = j < i ? s * A[jt][r] : 0.0f;
+              row += t;
+              const float cs = row16_sum(t);
+              if (l15 == 0) sh.col[wave * (wave + 1) / 2 + jt][g4 + r] = cs;
+            }
+            if constexpr (kBf16) pe[r] = f32_to_bf16(s); else pe[r] = s;
+          }
+        } else {
+          pe[0] = pe[1] = pe[2] = pe[3] = Elt(0);
+        }
+        __builtin_memcpy(__builtin_assume_aligned(sh.p + i * PP + jt * 16 + g4, 4 * sizeof(Elt)), pe, 4 * sizeof(Elt));
+      }
+      if constexpr (kind == kDotQ) {
+        row = group_sum(row);
+        if (lane < 16) sh.row[i] = row;
+      }
+      // the next tiles are on their way during what follows (asked for any earlier, they would
+      // share the registers with the scores)
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_next();
+      __builtin_amdgcn_sched_barrier(0);
+      // ---- what the state gives: O^T = S^T X^T
+      if (new_x) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) O[m][nt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < DK / 32; ++k) {
+          Frag xf[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) xf[m] = M::rows_split(sh.x + (m * 16 + l15) * PK + k * 32 + g4);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float v[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = S[2 * k][nt][r], v[4 + r] = S[2 * k + 1][nt][r];
+            const Split<kBf16, kParts> sf(v);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) O[m][nt] = sf.mul_a(xf[m], O[m][nt]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float w = sh.inter[m * 16 + l15];
+          float d = 0.0f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            O[m][nt] *= w;
+            if constexpr (kDots) {
+              const Elt* er = sh.e + (m * 16 + l15) * PV + col0 + nt * 16 + g4;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) d += O[m][nt][r] * Elem<kBf16>::load(er + r);
+            }
+          }
+          if constexpr (kDots) {
+            d = group_sum(d);
+            if (lane < 16) sh.dot[wave][m * 16 + l15] = d;
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- the wave's columns of Z, all 64 rows
+    Frag zf[2][NT];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) zf[k][nt] = M::cols(sh.z, PV, k * 32, col0 + nt * 16, lane);
+
+    if constexpr (kind != kSum) {
+      bool fine = true;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) fine = fine && M::finite(zf[k][nt]);
+      if (__all(fine)) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (kReverse ? (k == 1 || m < 2) : (k == 0 || m >= 2)) {
+              const Frag pf = M::rows(sh.p + (m * 16 + l15) * PP + k * 32 + g4 * 2);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) O[m][nt] = M::mul(zf[k][nt], pf, O[m][nt]);
+            }
+      } else {
+        // an infinity or a NaN among the values reaches only the outputs that may see its token:
+        // a zero score times it would not be zero, so masked products are left out one by one
+        for (int m = 0; m < 4; ++m) {
+          const int i = m * 16 + l15;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float s = 0.0f;
+              for (int j = kReverse ? i : 0; j < (kReverse ? kChunk : i + 1); ++j)
+                s += Elem<kBf16>::load(sh.p + i * PP + j) * Elem<kBf16>::load(sh.z + j * PV + col0 + nt * 16 + g4 + r);
+#pragma unroll
+              for (int mm = 0; mm < 4; ++mm)
+                if (mm == m) O[mm][nt][r] += s;
+            }
+        }
+      }
+      if constexpr (kDots) {
+        if (tid < kChunk) {
+          if (new_x) b_acc += sh.dot[0][tid] + sh.dot[1][tid] + sh.dot[2][tid] + sh.dot[3][tid];
+          if constexpr (kind == kDotQ) {
+            const int jt = tid >> 4;
+            float s = 0.0f;
+            for (int w = jt; w < 4; ++w) s += sh.col[w * (w + 1) / 2 + jt][tid & 15];
+            u_acc += sh.row[tid] - s;
+          }
+          if (sub == nsub - 1) {
+            const int t = t0 + tid;
+            if (t < a.T) {
+              const size_t at = ((size_t)b * a.Hkv + h) * a.T + t;
+              if constexpr (kind == kDotQ) {
+                p.u[at] = u_acc;
+                p.b[at] = b_acc;
+              } else {
+                p.c[at] = b_acc;
+              }
+            }
+            u_acc = b_acc = 0.0f;
+          }
+        }
+      }
+      if ((p.nq > 1 || sub == nsub - 1) && p.o) {
+        Elt* out = (Elt*)p.o;
+        const int64_t oh = (int64_t)h * p.nq + (p.nq > 1 ? sub : 0);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int t = t0 + m * 16 + l15;
+          if (t >= a.T) continue;
+          Elt* row = out + (((size_t)b * a.T + t) * a.Hkv * p.nq + oh) * p.dv;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int j = col0 + nt * 16 + g4;
+            Elt v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float f = t < n ? O[m][nt][r] : 0.0f;
+              if constexpr (kBf16) v[r] = f32_to_bf16(f); else v[r] = f;
+            }
+            if (p.vec_out) {
+              if (j < p.dv) __builtin_memcpy(__builtin_assume_aligned(row + j, 4 * sizeof(Elt)), v, 4 * sizeof(Elt));
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (j + r < p.dv) row[j + r] = v[r];
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the state's update, once for each pair of keys and values
+    if (p.nkv > 1 || sub == nsub - 1) {
+      if (p.nkv == 1 || sub == 0) {
+        const float total = sh.total;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) S[kt][nt] *= total;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float* wp = sh.upd + k * 32 + g4 * 2;
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = wp[e];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if constexpr (kBf16) v[e] = w[e] * (float)zf[k][nt][e]; else v[e] = w[e] * zf[k][nt].v[e];
+          }
+          const Split<kBf16, 3> wz(v);
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            const Frag yf = M::cols(sh.y, PK, k * 32, kt * 16, lane);
+            S[kt][nt] = wz.mul_b(yf, S[kt][nt]);
+          }
+        }
+      }
+    }
+  }
+
+  // ---- chunks without tokens: zeros
+  if constexpr (kind != kSum) {
+    for (int c = max(live, c_lo); c < c_hi; ++c) {
+      const int t0 = c * kChunk, rows = min(kChunk, a.T - t0);
+      if (p.o)
+        for (int q = tid; q < rows * p.nq * p.dv; q += kThreads) {
+          const int t = t0 + q / (p.nq * p.dv), j = q % (p.nq * p.dv);
+          ((Elt*)p.o)[(((size_t)b * a.T + t) * a.Hkv + h) * p.nq * p.dv + j] = Elt(0);
+        }
+      if constexpr (kDots)
+        for (int t = tid; t < rows; t += kThreads) {
+          const size_t at = ((size_t)b * a.Hkv + h) * a.T + t0 + t;
+          if constexpr (kind == kDotQ)
+            p.u[at] = p.b[at] = 0.0f;
+          else
+            p.c[at] = 0.0f;
+        }
+    }
+  }
+  if (p.s_out)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (s_in_range(kt, nt, r)) p.s_out[s_at(kt, nt, r)] = S[kt][nt][r];
+  if (kind == kSum && p.seg_decay && tid == 0) p.seg_decay[blockIdx.x] = __builtin_amdgcn_exp2f((float)seg_log);
+}
+
+template <bool kBf16, int DK, int DV, bool kReverse, Kind kind>
+hipError_t launch_chunk(const RoleArgs& p, hipStream_t st) {
+  constexpr size_t lds = sizeof(Shared<kBf16, DK, DV, kind>);
+  static_assert(lds <= 160 * 1024, "LDS of a block");
+  const auto fn = chunk_kernel<kBf16, DK, DV, kReverse, kind>;
+  if constexpr (lds > 64 * 1024) {
+    static const hipError_t raised = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (raised != hipSuccess) return raised;
+  }
+  fn<<<(unsigned)p.a.B * p.a.Hkv * p.nseg, kThreads, lds, st>>>(p);
+  return hipGetLastError();
+}
+
+// The narrowest tiles that hold the head sizes: 64 or 128 columns.
+template <bool kReverse, Kind kind>
+hipError_t run_role(const RoleArgs& p, hipStream_t st) {
+  const bool k128 = p.dk > 64, v128 = p.dv > 64;
+  auto go = [&](auto bf) {
+    constexpr bool kB = decltype(bf)::value;
+    if (k128) return v128 ? launch_chunk<kB, 128, 128, kReverse, kind>(p, st) : launch_chunk<kB, 128, 64, kReverse, kind>(p, st);
+    return v128 ? launch_chunk<kB, 64, 128, kReverse, kind>(p, st) : launch_chunk<kB, 64, 64, kReverse, kind>(p, st);
+  };
+  return p.a.bf16 ? go(std::true_type{}) : go(std::false_type{});
+}
+
+inline bool rows_vec(const Rows& r, int cols, int bf16) {
+  const int e = bf16 ? 8 : 4;
+  return cols % e == 0 && r.sb % e == 0 && r.st % e == 0 && r.sh % e == 0 && (uintptr_t)r.p % 16 == 0 &&
+         r.st < (1 << 22);
+}
+
+// ---- segments ------------------------------------------------------------------------------
+struct Plan {
+  int seg_chunks, nseg;
+  size_t states;       // bytes of the segments' states
+};
+
+// Few rows and a long axis: the axis is cut into segments that run side by side, at the price of
+// one more pass over the keys and values for the segments' own sums.
+inline Plan make_plan(const LinAttn& a) {
+  const int chunks = (a.T + kChunk - 1) / kChunk;
+  const int64_t rows = (int64_t)a.B * a.Hkv;
+  Plan p{chunks > 0 ? chunks : 1, 1, 0};
+  const int64_t want = 512 / rows;
+  if (want >= 2 && chunks >= 8) {
+    const int seg = (int)((chunks + want - 1) / want);
+    p.seg_chunks = seg < 4 ? 4 : seg;
+    p.nseg = (chunks + p.seg_chunks - 1) / p.seg_chunks;
+  }
+  p.states = ((size_t)rows * p.nseg * a.Dk * a.Dv * 4 + 255) / 256 * 256;
+  return p;
+}
+
+// In place over the segments' own sums: entry states, and the last exit state.  `reverse` runs from
+// the last segment to the first.
+struct ScanArgs {
+  float* seg;              // [rows][nseg][size]
+  const float* decay;      // [rows][nseg]
+  const float* s_in;       // [rows][size] or nullptr
+  float* s_out;            // [rows][size] or nullptr
+  int nseg, size, reverse;
+};
+hipError_t launch_scan(const ScanArgs* p, int count, int64_t rows, hipStream_t st);
+
+}  // namespace linattn
+}  // namespace pnr
