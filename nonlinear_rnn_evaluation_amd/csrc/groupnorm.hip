@@ -2,186 +2,851 @@
 //   n = (x - mean) rstd,  z = n w + b,  y = act(z)  or  z act(gate)
 //   dz = dy act'(z)  or  dy act(gate);   dgate = dy z act'(gate)
 //   u = dz w,  dx = rstd (u - mean(u) - n mean(u n)),  dw = sum dz n,  db = sum dz
+//
+// Two layouts of the work, both bound by memory:
+//   tokens (L = 1, groups of up to some thousand channels): a group is one contiguous run that
+//     1..64 lanes hold in registers, so x, the gate and dy are read once and the sums are wave
+//     shuffles.  A thread keeps its channels over all its tokens: weight and bias are
+//     loaded once, and dw and db are sums in registers until the block's end.
+//   maps (L > 1, or wider groups): the rows of a map are cut into slabs of whole lines, a block
+//     a slab and a range of channels: a pass for the sums, a pass for the outputs, which
+//     finds x in the last-level cache where the tensor fits it.
+// Variances come from deviations (two passes over registers, or running means that are joined by
+// their counts), never from a difference of sums of squares.  All of it is fp32 up to
+// the one rounding of each output.
+#include <initializer_list>
+#include <type_traits>
+
 #include "seq_ops.h"
 
 namespace pnr {
 namespace {
 
+// ---- activations -----------------------------------------------------------------------------
 __device__ __forceinline__ float sigmoid(float u) { return __builtin_amdgcn_rcpf(1.0f + __expf(-u)); }
 
 // gelu(u) = u sigmoid(2 a), a = sqrt(2/pi) (u + 0.044715 u^3): 0.5 (1 + tanh a) = sigmoid(2 a)
 __device__ __forceinline__ float gelu_arg(float u) { return 1.5957691216057308f * u * fmaf(0.044715f * u, u, 1.0f); }
 
-__device__ __forceinline__ float act_value(int act, float u) {
-  if (act == PNR_ACT_SILU) return u * sigmoid(u);
-  if (act == PNR_ACT_GELU) return u * sigmoid(gelu_arg(u));
-  return u;
+template <int V>
+__device__ __forceinline__ void act_values(int act, float (&u)[V]) {
+  if (act == PNR_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[i] *= sigmoid(u[i]);
+  } else if (act == PNR_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[i] *= sigmoid(gelu_arg(u[i]));
+  }
 }
 
-// act(u) and act'(u)
-__device__ __forceinline__ float act_grad(int act, float u, float& value) {
-  if (act == PNR_ACT_NONE) {
-    value = u;
-    return 1.0f;
-  }
-  const float s = sigmoid(act == PNR_ACT_SILU ? u : gelu_arg(u));
-  value = u * s;
-  const float da = act == PNR_ACT_SILU ? 1.0f : 1.5957691216057308f * fmaf(0.134145f * u, u, 1.0f);
-  return fmaf(value * da, 1.0f - s, s);
-}
-
-__device__ float block_sum(float v) {
-  __shared__ float w[4];
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return w[0] + w[1] + w[2] + w[3];
-}
-
-template <bool kBf16>
-__global__ void __launch_bounds__(256) norm_kernel(Norm a, void* y_, float* mean, float* rstd) {
-  using E = Elem<kBf16>;
-  using T = typename E::type;
-  for (unsigned ng = blockIdx.x; ng < (unsigned)a.N * a.groups; ng += gridDim.x) {
-  const int W = a.C / a.groups, g = ng % a.groups;
-  const int n = ng / a.groups;
-  const int len = row_len(a.lens, n, a.L);
-  const size_t base = (size_t)n * a.L * a.C + (size_t)g * W;
-  const T* x = (const T*)a.x + base;
-  const T* gate = a.gate ? (const T*)a.gate + base : nullptr;
-  T* y = (T*)y_ + base;
-  const long cnt = (long)len * W;
-  auto at = [&](long i) { return (size_t)(i / W) * a.C + i % W; };
-  float s = 0.0f;
-  for (long i = threadIdx.x; i < cnt; i += 256) s += E::load(x + at(i));
-  const float m = cnt ? block_sum(s) / cnt : 0.0f;
-  s = 0.0f;
-  for (long i = threadIdx.x; i < cnt; i += 256) {
-    const float d = E::load(x + at(i)) - m;
-    s += d * d;
-  }
-  const float r = 1.0f / sqrtf((cnt ? block_sum(s) / cnt : 0.0f) + a.eps);
-  if (threadIdx.x == 0) {
-    if (mean) mean[ng] = m;
-    if (rstd) rstd[ng] = r;
-  }
-  for (long i = threadIdx.x; i < (long)a.L * W; i += 256) {
-    float v = 0.0f;
-    if (i < cnt) {
-      const int c = g * W + (int)(i % W);
-      v = (E::load(x + at(i)) - m) * r;
-      if (a.weight) v = fmaf(v, a.weight[c], a.bias[c]);
-      v = gate ? v * act_value(a.act, E::load(gate + at(i))) : act_value(a.act, v);
+// u -> act(u), d = act'(u)
+template <int V>
+__device__ __forceinline__ void act_grads(int act, float (&u)[V], float (&d)[V]) {
+  if (act == PNR_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = sigmoid(u[i]);
+      u[i] *= s;
+      d[i] = fmaf(u[i], 1.0f - s, s);
     }
-    E::store(y + at(i), v);
-  }
-  }
-}
-
-// dz and n of one element; with a gate also dgate
-template <bool kBf16>
-__device__ __forceinline__ void element_grad(const Norm& a, const void* gy, size_t at, int c, float m, float r,
-                                             float& n, float& dz, float& dgate) {
-  using E = Elem<kBf16>;
-  using T = typename E::type;
-  n = (E::load((const T*)a.x + at) - m) * r;
-  const float z = a.weight ? fmaf(n, a.weight[c], a.bias[c]) : n;
-  const float dy = E::load((const T*)gy + at);
-  float val;
-  if (a.gate) {
-    const float d = act_grad(a.act, E::load((const T*)a.gate + at), val);
-    dz = dy * val;
-    dgate = dy * z * d;
+  } else if (act == PNR_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = sigmoid(gelu_arg(u[i])), da = 1.5957691216057308f * fmaf(0.134145f * u[i], u[i], 1.0f);
+      u[i] *= s;
+      d[i] = fmaf(u[i] * da, 1.0f - s, s);
+    }
   } else {
-    dz = dy * act_grad(a.act, z, val);
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = 1.0f;
   }
 }
 
-template <bool kBf16>
-__global__ void __launch_bounds__(256) norm_grad_kernel(Norm a, const void* gy, const float* mean, const float* rstd,
-                                                        void* gx_, void* gg_) {
+// ---- pieces: V neighbouring channels, one 16-byte access (V = 8 bf16, 4 fp32) or one element -------
+template <bool kBf16, bool kVec>
+struct Piece {
   using E = Elem<kBf16>;
   using T = typename E::type;
-  for (unsigned ng = blockIdx.x; ng < (unsigned)a.N * a.groups; ng += gridDim.x) {
-  const int W = a.C / a.groups, g = ng % a.groups;
-  const int n = ng / a.groups;
-  const int len = row_len(a.lens, n, a.L);
-  const size_t base = (size_t)n * a.L * a.C + (size_t)g * W;
-  const long cnt = (long)len * W;
-  const float m = mean[ng], r = rstd[ng];
-  float s1 = 0.0f, s2 = 0.0f;
-  for (long i = threadIdx.x; i < cnt; i += 256) {
-    float h, dz, dg;
-    const int c = g * W + (int)(i % W);
-    element_grad<kBf16>(a, gy, base + (size_t)(i / W) * a.C + i % W, c, m, r, h, dz, dg);
-    const float u = a.weight ? dz * a.weight[c] : dz;
-    s1 += u;
-    s2 += u * h;
-  }
-  const float m1 = cnt ? block_sum(s1) / cnt : 0.0f, m2 = cnt ? block_sum(s2) / cnt : 0.0f;
-  for (long i = threadIdx.x; i < (long)a.L * W; i += 256) {
-    const size_t at = base + (size_t)(i / W) * a.C + i % W;
-    float dx = 0.0f, dg = 0.0f;
-    if (i < cnt) {
-      float h, dz;
-      const int c = g * W + (int)(i % W);
-      element_grad<kBf16>(a, gy, at, c, m, r, h, dz, dg);
-      const float u = a.weight ? dz * a.weight[c] : dz;
-      dx = r * (u - m1 - h * m2);
+  static constexpr int V = kVec ? (kBf16 ? 8 : 4) : 1;
+  static __device__ __forceinline__ void load(const void* p, size_t at, float (&f)[V]) {
+    const T* s = (const T*)p + at;
+    if constexpr (!kVec) {
+      f[0] = E::load(s);
+    } else {
+      const uint4 w = *(const uint4*)s;
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kBf16) {
+          f[2 * i] = __uint_as_float(u[i] << 16);
+          f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        } else {
+          f[i] = __uint_as_float(u[i]);
+        }
+      }
     }
-    if (gx_) E::store((T*)gx_ + at, dx);
-    if (gg_) E::store((T*)gg_ + at, dg);
   }
+  static __device__ __forceinline__ void store(void* p, size_t at, const float (&f)[V]) {
+    T* d = (T*)p + at;
+    if constexpr (!kVec) {
+      E::store(d, f[0]);
+    } else {
+      T v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (kBf16) v[i] = f32_to_bf16(f[i]); else v[i] = f[i];
+      }
+      uint4 w;
+      __builtin_memcpy(&w, v, 16);
+      *(uint4*)d = w;
+    }
+  }
+};
+
+template <int V>
+__device__ __forceinline__ void load_params(const float* p, int c, float missing, float (&f)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = p ? p[c + i] : missing;
+}
+
+// dy -> dz, and with a gate dgate -> gate; z -> unspecified
+template <int V>
+__device__ __forceinline__ void back_through_act(int act, bool gated, float (&dy)[V], float (&z)[V], float (&gate)[V]) {
+  float d[V];
+  if (gated) {
+    act_grads(act, gate, d);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float a = gate[i];
+      gate[i] = dy[i] * z[i] * d[i];
+      dy[i] *= a;
+    }
+  } else {
+    act_grads(act, z, d);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dy[i] *= d[i];
   }
 }
 
-// dw and db: a block a channel, over all rows and positions
-template <bool kBf16>
-__global__ void __launch_bounds__(256) norm_param_kernel(Norm a, const void* gy, const float* mean, const float* rstd,
-                                                         float* gw, float* gb) {
-  const int c = blockIdx.x, g = c / (a.C / a.groups);
-  float s1 = 0.0f, s2 = 0.0f;
-  for (size_t i = threadIdx.x; i < (size_t)a.N * a.L; i += 256) {
-    const int n = (int)(i / a.L);
-    if ((int)(i % a.L) >= row_len(a.lens, n, a.L)) continue;
-    float h, dz, dg;
-    element_grad<kBf16>(a, gy, i * a.C + c, c, mean[(size_t)n * a.groups + g], rstd[(size_t)n * a.groups + g], h, dz, dg);
-    s1 += dz * h;
-    s2 += dz;
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  for (int d = 1; d < lanes; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// ---- tokens ------------------------------------------------------------------------------------
+struct TokenPlan {
+  int lanes;       // lanes a group
+  int ppl;         // pieces a lane: 1, 2, 4 or 8; 0: the group is too wide
+  int gb, nb;      // groups, and tokens, a block holds at a time
+};
+TokenPlan token_plan(int W, int groups, int V) {
+  TokenPlan t{};
+  const int pieces = (W + V - 1) / V;
+  if (W % V || pieces > 512) return t;
+  t.lanes = 1;
+  while (t.lanes < pieces && t.lanes < 64) t.lanes *= 2;
+  t.ppl = 1;
+  while (t.ppl * t.lanes < pieces) t.ppl *= 2;
+  t.gb = groups < 256 / t.lanes ? groups : 256 / t.lanes;
+  t.nb = 256 / (t.lanes * t.gb);
+  return t;
+}
+
+struct TokenArgs {
+  Norm a;
+  TokenPlan t;
+  void* y;                    // forward
+  float *mean, *rstd;
+  const void* gy;             // backward
+  const float *mean_in, *rstd_in;
+  void *gx, *ggate;
+  float* part;                // [gridDim.x][2][C]: sums of dz n and of dz, or nullptr
+};
+
+// x is read once; C = 2048 in 16 groups, bf16 with a gate: see the table of cases
+template <bool kBf16, bool kVec, int PPL>
+__global__ void __launch_bounds__(256) token_kernel(TokenArgs p) {
+  using P = Piece<kBf16, kVec>;
+  constexpr int V = P::V;
+  const Norm& a = p.a;
+  const int W = a.C / a.groups, lanes = p.t.lanes;
+  const int sub = threadIdx.x % lanes, slot = threadIdx.x / lanes;
+  const int g = blockIdx.y * p.t.gb + slot % p.t.gb, ns = slot / p.t.gb;
+  const bool mine = ns < p.t.nb && g < a.groups;
+  const float inv = 1.0f / W;
+  float w[PPL][V], b[PPL][V];
+#pragma unroll
+  for (int k = 0; k < PPL; ++k) {
+    const int c = (sub + k * lanes) * V;
+    const bool in = mine && c < W;
+    load_params<V>(in ? a.weight : nullptr, g * W + c, 1.0f, w[k]);
+    load_params<V>(in ? a.bias : nullptr, g * W + c, 0.0f, b[k]);
   }
-  s1 = block_sum(s1), s2 = block_sum(s2);
-  if (threadIdx.x == 0) {
-    if (gw) gw[c] = s1;
-    if (gb) gb[c] = s2;
+  for (int64_t n0 = (int64_t)blockIdx.x * p.t.nb; n0 < a.N; n0 += (int64_t)gridDim.x * p.t.nb) {
+    const int64_t n = n0 + ns;
+    const bool there = mine && n < a.N, live = there && (!a.lens || a.lens[n] > 0);
+    const size_t base = (size_t)n * a.C + (size_t)g * W;
+    float x[PPL][V], gate[PPL][V];
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PPL; ++k) {
+      const int c = (sub + k * lanes) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[k][i] = gate[k][i] = 0.0f;
+      if (live && c < W) {
+        P::load(a.x, base + c, x[k]);
+        if (a.gate) P::load(a.gate, base + c, gate[k]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += x[k][i];
+    }
+    const float mean = lanes_sum(s, lanes) * inv;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PPL; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        x[k][i] -= mean;
+        s += (sub + k * lanes) * V < W ? x[k][i] * x[k][i] : 0.0f;
+      }
+    const float rstd = 1.0f / sqrtf(fmaf(lanes_sum(s, lanes), inv, a.eps));
+    if (there && sub == 0) {
+      if (p.mean) p.mean[n * a.groups + g] = mean;
+      if (p.rstd) p.rstd[n * a.groups + g] = rstd;
+    }
+#pragma unroll
+    for (int k = 0; k < PPL; ++k) {
+      const int c = (sub + k * lanes) * V;
+      if (!there || c >= W) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[k][i] = fmaf(x[k][i] * rstd, w[k][i], b[k][i]);
+      if (a.gate) {
+        act_values(a.act, gate[k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[k][i] *= gate[k][i];
+      } else {
+        act_values(a.act, x[k]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[k][i] = live ? x[k][i] : 0.0f;
+      P::store(p.y, base + c, x[k]);
+    }
   }
 }
 
-}  // namespace
+template <bool kBf16, bool kVec, int PPL>
+__global__ void __launch_bounds__(256) token_grad_kernel(TokenArgs p) {
+  using P = Piece<kBf16, kVec>;
+  constexpr int V = P::V;
+  const Norm& a = p.a;
+  const int W = a.C / a.groups, lanes = p.t.lanes;
+  const int sub = threadIdx.x % lanes, slot = threadIdx.x / lanes;
+  const int g = blockIdx.y * p.t.gb + slot % p.t.gb, ns = slot / p.t.gb;
+  const bool mine = ns < p.t.nb && g < a.groups;
+  const float inv = 1.0f / W;
+  float w[PPL][V], b[PPL][V], dw[PPL][V], db[PPL][V];
+#pragma unroll
+  for (int k = 0; k < PPL; ++k) {
+    const int c = (sub + k * lanes) * V;
+    const bool in = mine && c < W;
+    load_params<V>(in ? a.weight : nullptr, g * W + c, 1.0f, w[k]);
+    load_params<V>(in ? a.bias : nullptr, g * W + c, 0.0f, b[k]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
+  }
+  for (int64_t n0 = (int64_t)blockIdx.x * p.t.nb; n0 < a.N; n0 += (int64_t)gridDim.x * p.t.nb) {
+    const int64_t n = n0 + ns;
+    const bool there = mine && n < a.N, live = there && (!a.lens || a.lens[n] > 0);
+    const size_t base = (size_t)n * a.C + (size_t)g * W;
+    const float mean = live ? p.mean_in[n * a.groups + g] : 0.0f, rstd = live ? p.rstd_in[n * a.groups + g] : 0.0f;
+    float h[PPL][V], gy[PPL][V], gate[PPL][V];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PPL; ++k) {
+      const int c = (sub + k * lanes) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[k][i] = mean, gy[k][i] = gate[k][i] = 0.0f;
+      if (live && c < W) {
+        P::load(a.x, base + c, h[k]);
+        P::load(p.gy, base + c, gy[k]);
+        if (a.gate) P::load(a.gate, base + c, gate[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < PPL; ++k) {
+      float z[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[k][i] = (h[k][i] - mean) * rstd;
+        z[i] = fmaf(h[k][i], w[k][i], b[k][i]);
+      }
+      back_through_act(a.act, a.gate != nullptr, gy[k], z, gate[k]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dw[k][i] = fmaf(gy[k][i], h[k][i], dw[k][i]);
+        db[k][i] += gy[k][i];
+        gy[k][i] *= w[k][i];
+        s1 += gy[k][i];
+        s2 = fmaf(gy[k][i], h[k][i], s2);
+      }
+    }
+    s1 = lanes_sum(s1, lanes) * inv;
+    s2 = lanes_sum(s2, lanes) * inv;
+#pragma unroll
+    for (int k = 0; k < PPL; ++k) {
+      const int c = (sub + k * lanes) * V;
+      if (!there || c >= W) continue;
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[k][i] = rstd * (gy[k][i] - s1 - h[k][i] * s2);
+      if (p.gx) P::store(p.gx, base + c, h[k]);
+      if (p.ggate) P::store(p.ggate, base + c, gate[k]);
+    }
+  }
+  if (!p.part) return;
+  // the block's tokens of a channel meet in LDS, in the order of their slots
+  __shared__ float red[256 * V];
+  float* out = p.part + (size_t)blockIdx.x * 2 * a.C;
+  const int width = p.t.gb * lanes;            // threads that hold one token
+#pragma unroll
+  for (int k = 0; k < PPL; ++k)
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < V; ++i) red[threadIdx.x * V + i] = which ? db[k][i] : dw[k][i];
+      __syncthreads();
+      const int c = (sub + k * lanes) * V;
+      if (mine && ns == 0 && c < W)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float s = 0.0f;
+          for (int m = 0; m < p.t.nb; ++m) s += red[(threadIdx.x + m * width) * V + i];
+          out[(size_t)which * a.C + g * W + c + i] = s;
+        }
+    }
+}
 
-size_t groupnorm_workspace(const Norm&) { return 0; }
+// dw, db: sums of [rows][2][C] over the rows; 32 channels a block, 8 runs of rows joined in order
+__global__ void __launch_bounds__(256) param_sum_kernel(const float* part, int64_t rows, int C, float* gw, float* gb) {
+  __shared__ float red[8][32];
+  const int i = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+  float s = 0.0f;
+  if (i < 2 * C)
+    for (int64_t r = run; r < rows; r += 8) s += part[r * 2 * C + i];
+  red[run][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (run == 0 && i < 2 * C) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
+    float* out = i < C ? gw : gb;
+    if (out) out[i < C ? i : i - C] = s;
+  }
+}
 
-hipError_t launch_groupnorm(const Norm& a, void* y, float* mean, float* rstd, char*, hipStream_t st) {
-  const unsigned grid = (unsigned)a.N * a.groups < 65536u ? (unsigned)a.N * a.groups : 65536u;
-  if (a.bf16)
-    norm_kernel<true><<<grid, 256, 0, st>>>(a, y, mean, rstd);
-  else
-    norm_kernel<false><<<grid, 256, 0, st>>>(a, y, mean, rstd);
+// ---- maps --------------------------------------------------------------------------------------
+struct MapPlan {
+  int tile;        // channels a block: whole groups, or (single) one wide group
+  int single;
+  int ct, rt;      // threads along channels and along rows
+  int ctiles, nsplit, rows;   // blocks along channels and rows, rows a block
+};
+MapPlan map_plan(const Norm& a, int V) {
+  MapPlan m{};
+  const int W = a.C / a.groups;
+  int lcm = W;
+  while (lcm % V) lcm += W;                    // at most V steps
+  m.single = lcm > 256 * V;
+  if (m.single) {
+    m.tile = W;
+    m.ct = 256, m.rt = 1;
+  } else {
+    m.tile = 256 * V / lcm * lcm;
+    if (m.tile > a.C) m.tile = a.C;
+    m.ct = m.tile / V, m.rt = 256 / m.ct;
+  }
+  m.ctiles = (a.C + m.tile - 1) / m.tile;
+  // about four blocks a CU, of eight rows a thread at least
+  int64_t split = 1024 / ((int64_t)a.N * m.ctiles);
+  const int64_t most = a.L / (8 * m.rt);
+  if (split > most) split = most;
+  if (split > 64) split = 64;
+  if (split < 1) split = 1;
+  m.rows = (int)((a.L + split - 1) / split);
+  m.nsplit = m.rows > 0 ? (a.L + m.rows - 1) / m.rows : 1;
+  return m;
+}
+// a map's pieces must not straddle groups where a block holds a single wide one
+bool map_vec(const Norm& a, int V) {
+  const int W = a.C / a.groups;
+  if (a.C % V) return false;
+  int lcm = W;
+  while (lcm % V) lcm += W;
+  return lcm <= 256 * V || W % V == 0;
+}
+
+struct MapArgs {
+  Norm a;
+  MapPlan m;
+  float2* stats;              // [N][nsplit][groups]: mean and sum of squared deviations of a slab
+  void* y;
+  float *mean, *rstd;
+  const void* gy;
+  const float *mean_in, *rstd_in;
+  float* part;                // [N][nsplit][2][C]: sums of dz n and of dz over a slab
+  float* chan;                // [N][2][C]: over a row
+  float2* means;              // [N][groups]: mean(u n), mean(u)
+  void *gx, *ggate;
+};
+
+struct MapBlock {
+  int n, split, c0, cols, r0, r1, len;
+};
+__device__ __forceinline__ MapBlock map_block(const Norm& a, const MapPlan& m) {
+  MapBlock k;
+  const unsigned id = blockIdx.x;
+  k.split = id % m.nsplit;
+  k.c0 = id / m.nsplit % m.ctiles * m.tile;
+  k.n = id / m.nsplit / m.ctiles;
+  k.cols = min(m.tile, a.C - k.c0);
+  k.len = row_len(a.lens, k.n, a.L);
+  k.r0 = k.split * m.rows;
+  k.r1 = min(k.r0 + m.rows, a.L);
+  return k;
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = lanes_sum(v, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return red[0] + red[1] + red[2] + red[3];
+}
+
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(256) map_stats_kernel(MapArgs p) {
+  using P = Piece<kBf16, kVec>;
+  constexpr int V = P::V;
+  const Norm& a = p.a;
+  const MapPlan& m = p.m;
+  const MapBlock k = map_block(a, m);
+  const int W = a.C / a.groups, r1 = min(k.r1, k.len);
+  const int ct = threadIdx.x % m.ct, rt = threadIdx.x / m.ct;
+  const void* x = a.x;
+  const size_t base = (size_t)k.n * a.L * a.C + k.c0;
+  __shared__ float2 part[256 * V];
+  __shared__ float red[4];
+  float2* out = p.stats + ((size_t)k.n * m.nsplit + k.split) * a.groups + k.c0 / W;
+  // running mean and squared deviations of the thread's rows, channel by channel
+  float mean[V], dev[V], all_mean = 0.0f, all_dev = 0.0f, all_count = 0.0f;
+  for (int c = ct * V; c < k.cols; c += m.ct * V) {
+    float count = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mean[i] = dev[i] = 0.0f;
+    if (rt < m.rt)
+      for (int r = k.r0 + rt; r < r1; r += 4 * m.rt) {
+        float f[4][V];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r + q * m.rt < r1) P::load(x, base + (size_t)(r + q * m.rt) * a.C + c, f[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (r + q * m.rt < r1) {
+            count += 1.0f;
+            const float inv = __builtin_amdgcn_rcpf(count);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float d = f[q][i] - mean[i];
+              mean[i] = fmaf(d, inv, mean[i]);
+              dev[i] = fmaf(d, f[q][i] - mean[i], dev[i]);
+            }
+          }
+      }
+    if (m.single && count > 0.0f) {
+      // one group: join the channels as they come
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float total = all_count + count, d = mean[i] - all_mean, f = count / total;
+        all_dev += dev[i] + d * d * all_count * f;
+        all_mean = fmaf(d, f, all_mean);
+        all_count = total;
+      }
+    }
+  }
+  if (m.single) {
+    const float n = (float)(r1 > k.r0 ? r1 - k.r0 : 0) * W;
+    const float gm = block_sum(all_mean * all_count, red) / fmaxf(n, 1.0f);
+    const float d = all_mean - gm;
+    const float gd = block_sum(all_dev + d * d * all_count, red);
+    if (threadIdx.x == 0) *out = make_float2(gm, gd);
+    return;
+  }
+  if (rt < m.rt && ct * V < k.cols)
+#pragma unroll
+    for (int i = 0; i < V; ++i) part[rt * m.tile + ct * V + i] = make_float2(mean[i], dev[i]);
+  __syncthreads();
+  // groups: `lanes` lanes each over rt x W pairs, weighted by their counts of rows
+  int lanes = 64;
+  while (lanes > 1 && lanes / 2 >= m.rt * W) lanes /= 2;
+  const int rows = r1 > k.r0 ? r1 - k.r0 : 0, sub = threadIdx.x % lanes, ng = k.cols / W;
+  for (int g0 = 0; g0 < ng; g0 += 256 / lanes) {
+    const int g = g0 + threadIdx.x / lanes;
+    float s = 0.0f;
+    if (g < ng)
+      for (int q = sub; q < m.rt * W; q += lanes) {
+        const int r = q / W;
+        const float c = (float)((rows - r + m.rt - 1) / m.rt);
+        if (rows > r) s += c * part[r * m.tile + g * W + q % W].x;
+      }
+    const float gm = lanes_sum(s, lanes) / fmaxf((float)rows * W, 1.0f);
+    s = 0.0f;
+    if (g < ng)
+      for (int q = sub; q < m.rt * W; q += lanes) {
+        const int r = q / W;
+        const float c = (float)((rows - r + m.rt - 1) / m.rt);
+        const float2 e = part[r * m.tile + g * W + q % W];
+        if (rows > r) s += e.y + c * (e.x - gm) * (e.x - gm);
+      }
+    const float gd = lanes_sum(s, lanes);
+    if (g < ng && sub == 0) out[g] = make_float2(gm, gd);
+  }
+}
+
+template <bool kBf16, bool kVec>
+__global__ void __launch_bounds__(256) map_norm_kernel(MapArgs p) {
+  using P = Piece<kBf16, kVec>;
+  constexpr int V = P::V;
+  const Norm& a = p.a;
+  const MapPlan& m = p.m;
+  const MapBlock k = map_block(a, m);
+  const int W = a.C / a.groups, g0 = k.c0 / W, ng = k.cols / W;
+  __shared__ float2 group[256 * V];            // mean and rstd
+  for (int g = threadIdx.x; g < ng; g += 256) {
+    // the slabs' means and deviations, joined by their counts
+    const float2* s = p.stats + (size_t)k.n * m.nsplit * a.groups + g0 + g;
+    float count = 0.0f, mean = 0.0f, dev = 0.0f;
+    for (int q = 0; q < m.nsplit; ++q) {
+      const int rows = min((q + 1) * m.rows, k.len) - q * m.rows;
+      if (rows <= 0) break;
+      const float c = (float)rows * W, total = count + c, f = c / total;
+      const float2 e = s[(size_t)q * a.groups];
+      const float d = e.x - mean;
+      dev += e.y + d * d * count * f;
+      mean = fmaf(d, f, mean);
+      count = total;
+    }
+    const float rstd = 1.0f / sqrtf(dev / fmaxf(count, 1.0f) + a.eps);
+    group[g] = make_float2(mean, rstd);
+    if (k.split == 0) {
+      if (p.mean) p.mean[(size_t)k.n * a.groups + g0 + g] = mean;
+      if (p.rstd) p.rstd[(size_t)k.n * a.groups + g0 + g] = rstd;
+    }
+  }
+  __syncthreads();
+  const int ct = threadIdx.x % m.ct, rt = threadIdx.x / m.ct;
+  if (rt >= m.rt) return;
+  const size_t base = (size_t)k.n * a.L * a.C + k.c0;
+  for (int c = ct * V; c < k.cols; c += m.ct * V) {
+    float w[V], b[V], mean[V];
+    load_params<V>(a.weight, k.c0 + c, 1.0f, w);
+    load_params<V>(a.bias, k.c0 + c, 0.0f, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 e = group[(c + i) / W];
+      mean[i] = e.x;
+      w[i] *= e.y;
+    }
+    for (int r = k.r0 + rt; r < k.r1; r += 4 * m.rt) {
+      float f[4][V], gate[4][V];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (r + q * m.rt < k.r1) {
+          const size_t at = base + (size_t)(r + q * m.rt) * a.C + c;
+          if (r + q * m.rt < k.len) {
+            P::load(a.x, at, f[q]);
+            if (a.gate) P::load(a.gate, at, gate[q]);
+          }
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (r + q * m.rt >= k.r1) continue;
+        if (r + q * m.rt < k.len) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[q][i] = fmaf(f[q][i] - mean[i], w[i], b[i]);
+          if (a.gate) {
+            act_values(a.act, gate[q]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[q][i] *= gate[q][i];
+          } else {
+            act_values(a.act, f[q]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[q][i] = 0.0f;
+        }
+        P::store(p.y, base + (size_t)(r + q * m.rt) * a.C + c, f[q]);
+      }
+    }
+  }
+}
+
+// Per channel, over a slab: sums of dz n and of dz (kSums); or the gradients of x and the gate.
+template <bool kBf16, bool kVec, bool kSums>
+__global__ void __launch_bounds__(256) map_grad_kernel(MapArgs p) {
+  using P = Piece<kBf16, kVec>;
+  constexpr int V = P::V;
+  constexpr int U = 2;                         // rows in flight
+  const Norm& a = p.a;
+  const MapPlan& m = p.m;
+  const MapBlock k = map_block(a, m);
+  const int W = a.C / a.groups, r1 = kSums ? min(k.r1, k.len) : k.r1;
+  const int ct = threadIdx.x % m.ct, rt = threadIdx.x / m.ct;
+  const size_t base = (size_t)k.n * a.L * a.C + k.c0;
+  __shared__ float red[kSums ? 256 * V : 1];
+  for (int c0 = 0; c0 < k.cols; c0 += m.ct * V) {
+    const int c = c0 + ct * V;
+    const bool mine = rt < m.rt && c < k.cols;
+    float w[V], b[V], mean[V], rstd[V], m1[V], m2[V], dw[V], db[V];
+    load_params<V>(mine ? a.weight : nullptr, k.c0 + c, 1.0f, w);
+    load_params<V>(mine ? a.bias : nullptr, k.c0 + c, 0.0f, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const size_t g = (size_t)k.n * a.groups + (mine ? (k.c0 + c + i) / W : 0);
+      mean[i] = p.mean_in[g];
+      rstd[i] = p.rstd_in[g];
+      dw[i] = db[i] = 0.0f;
+      if constexpr (!kSums) {
+        const float2 e = p.means[g];
+        m2[i] = e.x, m1[i] = e.y;
+      }
+    }
+    if (mine)
+      for (int r = k.r0 + rt; r < r1; r += U * m.rt) {
+        float x[U][V], gy[U][V], gate[U][V];
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+          if (r + q * m.rt < r1 && r + q * m.rt < k.len) {
+            const size_t at = base + (size_t)(r + q * m.rt) * a.C + c;
+            P::load(a.x, at, x[q]);
+            P::load(p.gy, at, gy[q]);
+            if (a.gate) P::load(a.gate, at, gate[q]);
+          }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          if (r + q * m.rt >= r1) continue;
+          const size_t at = base + (size_t)(r + q * m.rt) * a.C + c;
+          if (r + q * m.rt < k.len) {
+            float z[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              x[q][i] = (x[q][i] - mean[i]) * rstd[i];
+              z[i] = fmaf(x[q][i], w[i], b[i]);
+            }
+            back_through_act(a.act, a.gate != nullptr, gy[q], z, gate[q]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              if constexpr (kSums) {
+                dw[i] = fmaf(gy[q][i], x[q][i], dw[i]);
+                db[i] += gy[q][i];
+              } else {
+                x[q][i] = rstd[i] * (gy[q][i] * w[i] - m1[i] - x[q][i] * m2[i]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[q][i] = gate[q][i] = 0.0f;
+          }
+          if constexpr (!kSums) {
+            if (p.gx) P::store(p.gx, at, x[q]);
+            if (p.ggate) P::store(p.ggate, at, gate[q]);
+          }
+        }
+      }
+    if constexpr (kSums) {
+      float* out = p.part + ((size_t)k.n * m.nsplit + k.split) * 2 * a.C + k.c0 + c;
+      for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) red[threadIdx.x * V + i] = which ? db[i] : dw[i];
+        __syncthreads();
+        if (mine && rt == 0)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float s = 0.0f;
+            for (int q = 0; q < m.rt; ++q) s += red[(threadIdx.x + q * m.ct) * V + i];
+            out[(size_t)which * a.C + i] = s;
+          }
+      }
+    }
+  }
+}
+
+// A block a map and group: the slabs' sums of each channel, and from them the group's means.
+__global__ void __launch_bounds__(256) map_means_kernel(MapArgs p) {
+  const Norm& a = p.a;
+  const int W = a.C / a.groups, g = blockIdx.x % a.groups, n = blockIdx.x / a.groups;
+  __shared__ float red[4];
+  float s[2] = {0.0f, 0.0f};
+  for (int c = g * W + threadIdx.x; c < (g + 1) * W; c += 256)
+    for (int which = 0; which < 2; ++which) {
+      const float* q = p.part + ((size_t)n * p.m.nsplit * 2 + which) * a.C + c;
+      float v = 0.0f;
+      for (int i = 0; i < p.m.nsplit; ++i) v += q[(size_t)i * 2 * a.C];
+      p.chan[((size_t)n * 2 + which) * a.C + c] = v;
+      s[which] += a.weight ? v * a.weight[c] : v;
+    }
+  const float inv = 1.0f / fmaxf((float)row_len(a.lens, n, a.L) * W, 1.0f);
+  const float m2 = block_sum(s[0], red) * inv, m1 = block_sum(s[1], red) * inv;
+  if (threadIdx.x == 0) p.means[blockIdx.x] = make_float2(m2, m1);
+}
+
+// ---- launches --------------------------------------------------------------------------------
+bool all_aligned(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if ((uintptr_t)p % 16) return false;
+  return true;
+}
+
+// The plan a call takes goes by sizes alone, so that a workspace is enough whatever the pointers: a
+// misaligned call is the single-element form of the same plan's layout.
+int vec_of(const Norm& a) { return a.bf16 ? 8 : 4; }
+
+int token_blocks(const Norm& a, const TokenPlan& t, int per_cu) {
+  const int by = (a.groups + t.gb - 1) / t.gb;
+  const int64_t need = ((int64_t)a.N + t.nb - 1) / t.nb;
+  int64_t bx = 256 * per_cu / by;
+  if (bx < 64) bx = 64;
+  return (int)(need < bx ? need : bx);
+}
+
+template <bool kBf16, bool kVec>
+hipError_t run_tokens(const TokenArgs& p, bool grad, int bx, hipStream_t st) {
+  const dim3 grid(bx, (p.a.groups + p.t.gb - 1) / p.t.gb);
+  auto go = [&](auto ppl) {
+    constexpr int K = decltype(ppl)::value;
+    if (grad)
+      token_grad_kernel<kBf16, kVec, K><<<grid, 256, 0, st>>>(p);
+    else
+      token_kernel<kBf16, kVec, K><<<grid, 256, 0, st>>>(p);
+  };
+  if (p.t.ppl == 1) go(std::integral_constant<int, 1>{});
+  else if (p.t.ppl == 2) go(std::integral_constant<int, 2>{});
+  else if (p.t.ppl == 4) go(std::integral_constant<int, 4>{});
+  else go(std::integral_constant<int, 8>{});
   return hipGetLastError();
 }
 
-size_t groupnorm_workspace_backward(const Norm&) { return 0; }
+hipError_t run_tokens(const TokenArgs& p, bool vec, bool grad, int bx, hipStream_t st) {
+  if (p.a.bf16) return vec ? run_tokens<true, true>(p, grad, bx, st) : run_tokens<true, false>(p, grad, bx, st);
+  return vec ? run_tokens<false, true>(p, grad, bx, st) : run_tokens<false, false>(p, grad, bx, st);
+}
+
+template <class F>
+void with_types(bool bf16, bool vec, F f) {
+  if (bf16)
+    vec ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  else
+    vec ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Slabs for either access form, so that a workspace does not depend on alignment.
+int most_splits(const Norm& a) {
+  const int s1 = map_plan(a, 1).nsplit;
+  const int sv = map_vec(a, vec_of(a)) ? map_plan(a, vec_of(a)).nsplit : 1;
+  return s1 > sv ? s1 : sv;
+}
+
+struct TokenChoice {
+  TokenPlan t;
+  bool vec;
+};
+TokenChoice choose_tokens(const Norm& a, bool ok) {
+  const int W = a.C / a.groups, V = vec_of(a);
+  if (a.L != 1) return {{}, false};
+  if (ok) {
+    const TokenPlan t = token_plan(W, a.groups, V);
+    if (t.ppl) return {t, true};
+  }
+  return {token_plan(W, a.groups, 1), false};
+}
+constexpr int kGradBlocksPerCu = 3;      // bounds the partial sums of dw and db
+
+}  // namespace
+
+size_t groupnorm_workspace(const Norm& a) {
+  return align256((size_t)a.N * most_splits(a) * a.groups * sizeof(float2));
+}
+
+hipError_t launch_groupnorm(const Norm& a, void* y, float* mean, float* rstd, char* ws, hipStream_t st) {
+  const bool ok = all_aligned({a.x, a.gate, y});
+  const TokenChoice tc = choose_tokens(a, ok);
+  if (tc.t.ppl) {
+    TokenArgs p{};
+    p.a = a, p.t = tc.t, p.y = y, p.mean = mean, p.rstd = rstd;
+    return run_tokens(p, tc.vec, false, token_blocks(a, tc.t, 8), st);
+  }
+  const bool vec = ok && map_vec(a, vec_of(a));
+  MapArgs p{};
+  p.a = a, p.m = map_plan(a, vec ? vec_of(a) : 1), p.stats = (float2*)ws, p.y = y, p.mean = mean, p.rstd = rstd;
+  const unsigned grid = (unsigned)a.N * p.m.ctiles * p.m.nsplit;
+  with_types(a.bf16, vec, [&](auto b, auto v) {
+    map_stats_kernel<decltype(b)::value, decltype(v)::value><<<grid, 256, 0, st>>>(p);
+    map_norm_kernel<decltype(b)::value, decltype(v)::value><<<grid, 256, 0, st>>>(p);
+  });
+  return hipGetLastError();
+}
+
+namespace {
+struct GradLayout {
+  size_t part = 0, chan = 0, means = 0, total = 0;
+};
+GradLayout grad_layout(const Norm& a) {
+  GradLayout l;
+  if (a.L == 1) l.chan = align256((size_t)256 * kGradBlocksPerCu * 2 * a.C * 4);   // token form: partial sums
+  const size_t maps = align256((size_t)a.N * most_splits(a) * 2 * a.C * 4);
+  const bool tokens = choose_tokens(a, true).t.ppl && choose_tokens(a, false).t.ppl;
+  if (!tokens) {
+    l.chan = l.chan > maps ? l.chan : maps;
+    l.means = l.chan + align256((size_t)a.N * 2 * a.C * 4);
+    l.total = l.means + align256((size_t)a.N * a.groups * sizeof(float2));
+  } else {
+    l.total = l.chan;
+  }
+  return l;
+}
+}  // namespace
+
+size_t groupnorm_workspace_backward(const Norm& a) { return grad_layout(a).total; }
 
 hipError_t launch_groupnorm_backward(const Norm& a, const void* gy, const float* mean, const float* rstd, void* gx,
-                                     float* gw, float* gb, void* ggate, char*, hipStream_t st) {
-  const unsigned grid = (unsigned)a.N * a.groups < 65536u ? (unsigned)a.N * a.groups : 65536u;
-  if (a.bf16) {
-    if (gx || ggate) norm_grad_kernel<true><<<grid, 256, 0, st>>>(a, gy, mean, rstd, gx, ggate);
-    if (gw || gb) norm_param_kernel<true><<<a.C, 256, 0, st>>>(a, gy, mean, rstd, gw, gb);
-  } else {
-    if (gx || ggate) norm_grad_kernel<false><<<grid, 256, 0, st>>>(a, gy, mean, rstd, gx, ggate);
-    if (gw || gb) norm_param_kernel<false><<<a.C, 256, 0, st>>>(a, gy, mean, rstd, gw, gb);
+                                     float* gw, float* gb, void* ggate, char* ws, hipStream_t st) {
+  const GradLayout l = grad_layout(a);
+  const bool ok = all_aligned({a.x, a.gate, gy, gx, ggate}), params = gw || gb;
+  const TokenChoice tc = choose_tokens(a, ok);
+  const unsigned sum_blocks = (2 * (unsigned)a.C + 31) / 32;
+  if (tc.t.ppl) {
+    TokenArgs p{};
+    p.a = a, p.t = tc.t, p.gy = gy, p.mean_in = mean, p.rstd_in = rstd, p.gx = gx, p.ggate = ggate;
+    if (params) p.part = (float*)ws;
+    const int bx = token_blocks(a, tc.t, kGradBlocksPerCu);
+    hipError_t e = run_tokens(p, tc.vec, true, bx, st);
+    if (e != hipSuccess || !params) return e;
+    param_sum_kernel<<<sum_blocks, 256, 0, st>>>(p.part, bx, a.C, gw, gb);
+    return hipGetLastError();
   }
+  const bool vec = ok && map_vec(a, vec_of(a));
+  MapArgs p{};
+  p.a = a, p.m = map_plan(a, vec ? vec_of(a) : 1), p.gy = gy, p.mean_in = mean, p.rstd_in = rstd;
+  p.part = (float*)ws, p.chan = (float*)(ws + l.chan), p.means = (float2*)(ws + l.means);
+  p.gx = gx, p.ggate = ggate;
+  const unsigned grid = (unsigned)a.N * p.m.ctiles * p.m.nsplit;
+  with_types(a.bf16, vec, [&](auto b, auto v) {
+    constexpr bool kB = decltype(b)::value, kV = decltype(v)::value;
+    map_grad_kernel<kB, kV, true><<<grid, 256, 0, st>>>(p);
+    map_means_kernel<<<(unsigned)a.N * a.groups, 256, 0, st>>>(p);
+    if (gx || ggate) map_grad_kernel<kB, kV, false><<<grid, 256, 0, st>>>(p);
+  });
+  if (params) param_sum_kernel<<<sum_blocks, 256, 0, st>>>(p.chan, a.N, a.C, gw, gb);
   return hipGetLastError();
 }
 
