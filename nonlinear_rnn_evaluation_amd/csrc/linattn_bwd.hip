@@ -123,7 +123,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
   RoleArgs base{};
   base.a = a;
   base.vec = rows_vec(a.q, a.Dk, a.bf16) && rows_vec(a.k, a.Dk, a.bf16) && rows_vec(a.v, a.Dv, a.bf16) &&
-             rows_vec(d.go, a.Dv, a.bf16);
+             rows_vec(d.go, a.Dv, a.bf16) && ((uintptr_t)d.gq | (uintptr_t)d.gk | (uintptr_t)d.gv) % 16 == 0;
   base.seg_chunks = l.plan.seg_chunks, base.nseg = nseg;
   base.p_scale = a.scale;
   // forward in time: keys k, values v; backward: keys q, values do, times the scale
@@ -160,7 +160,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     RoleArgs p = fwd;
     p.x = d.go, p.y = a.v, p.z = a.k, p.e = a.q;
     p.dk = a.Dv, p.dv = a.Dk, p.transposed = 1;
-    p.o = d.gq, p.vec_out = a.Dk % 4 == 0 && (uintptr_t)d.gq % 16 == 0;
+    p.o = d.gq;
     p.u = u, p.b = b;
     if (nseg == 1) p.s_out = last;
     if ((e = run_role<false, kDotQ>(p, st)) != hipSuccess) return e;
@@ -170,7 +170,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     RoleArgs p = rev;
     p.x = a.v, p.y = d.go, p.z = a.q, p.e = a.k;
     p.dk = a.Dv, p.dv = a.Dk, p.transposed = 1;
-    p.o = d.gk, p.vec_out = a.Dk % 4 == 0 && (uintptr_t)d.gk % 16 == 0;
+    p.o = d.gk;
     p.c = c;
     if (d.gg && (d.gstate_out || nseg > 1)) p.x_end = (float*)(ws + l.x_end), p.s_entry = S, p.s_last = last;
     if (nseg == 1) p.s_out = d.gstate_in;
@@ -180,7 +180,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     RoleArgs p = rev;
     p.x = a.k, p.y = a.q, p.z = d.go;
     p.dk = a.Dk, p.dv = a.Dv;
-    p.o = d.gv, p.vec_out = a.Dv % 4 == 0 && (uintptr_t)d.gv % 16 == 0;
+    p.o = d.gv;
     if ((e = run_role<true, kOut>(p, st)) != hipSuccess) return e;
   }
   if (d.gg) {

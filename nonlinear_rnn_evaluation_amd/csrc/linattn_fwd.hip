@@ -70,8 +70,8 @@ hipError_t launch_linattn_forward(const LinAttn& a, const float* state_in, void*
   p.a = a;
   p.x = a.q, p.y = a.k, p.z = a.v;
   p.nq = a.H / a.Hkv, p.nkv = 1, p.dk = a.Dk, p.dv = a.Dv;
-  p.vec = rows_vec(a.q, a.Dk, a.bf16) && rows_vec(a.k, a.Dk, a.bf16) && rows_vec(a.v, a.Dv, a.bf16);
-  p.vec_out = a.Dv % 4 == 0 && (uintptr_t)o % 16 == 0;
+  p.vec = rows_vec(a.q, a.Dk, a.bf16) && rows_vec(a.k, a.Dk, a.bf16) && rows_vec(a.v, a.Dv, a.bf16) &&
+          (uintptr_t)o % 16 == 0;
   p.p_scale = p.inter_scale = a.scale, p.upd_scale = 1.0f;
   p.o = o;
   p.seg_chunks = l.plan.seg_chunks, p.nseg = l.plan.nseg;

@@ -40,8 +40,7 @@ struct RoleArgs {
   int nq, nkv;           // heads of x, e and the outputs, and of y and z, per state head; one of them is 1
   int dk, dv;            // columns of x and y, and of z, e and the outputs
   int transposed;        // states are stored [dv][dk]
-  int vec;               // rows of x, y, z, e may be read in 16-byte pieces
-  int vec_out;           // outputs may be written four at a time
+  int vec;               // rows of x, y, z, e may be read in 16-byte pieces, outputs written four at a time
   float p_scale, inter_scale, upd_scale;   // on scores, on S^T x, on y z^T
   const float* s_in;     // [B][Hkv][nseg] states at the segments' entry, or nullptr: zeros
   float* s_out;          // [B][Hkv][nseg] states at the segments' exit, or nullptr
@@ -183,32 +182,30 @@ struct Stage {
   uint4 v[kN];
 
   // Rows t0 .. t0 + 63 of batch row b and head h; rows at or past n and columns past `cols` are
-  // zeros.  `vec`: every piece is one aligned load, and 64 rows span less than 2^31 bytes, so an
+  // zeros.  kVec: every piece is one aligned load, and 64 rows span less than 2^31 bytes, so an
   // address is a uniform base and a 32-bit offset.
-  __device__ __forceinline__ void load(const Rows& r, int b, int64_t h, int t0, int n, int cols, bool vec) {
+  template <bool kVec>
+  __device__ __forceinline__ void load(const Rows& r, int b, int h, int t0, int n, int cols) {
     constexpr int kStep = kThreads / kPerRow;            // rows between a thread's pieces
     const Elt* base = (const Elt*)r.p + b * r.sb + h * r.sh + t0 * r.st;
     const int row = threadIdx.x / kPerRow, c = (threadIdx.x % kPerRow) * M::kPiece;
-    const bool in = c < cols;
-    if (vec) {
+    if constexpr (kVec) {
       const uint32_t off = (uint32_t)(row * (int)r.st + c) * (uint32_t)sizeof(Elt);
+      const bool in = c < cols;
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         v[i] = make_uint4(0, 0, 0, 0);
         if (in && t0 + row + i * kStep < n) v[i] = *(const uint4*)((const char*)(base + i * kStep * r.st) + off);
       }
     } else {
+#pragma unroll
       for (int i = 0; i < kN; ++i) {
         Elt e[M::kPiece];
-        const bool live = in && t0 + row + i * kStep < n;
+        const bool live = t0 + row + i * kStep < n;
+        const Elt* src = base + (row + i * kStep) * r.st + c;
 #pragma unroll
-        for (int k = 0; k < M::kPiece; ++k)
-          e[k] = live && c + k < cols ? base[(int64_t)(row + i * kStep) * r.st + c + k] : Elt(0);
-        uint4 w;
-        __builtin_memcpy(&w, e, 16);
-#pragma unroll
-        for (int q = 0; q < kN; ++q)
-          if (q == i) v[q] = w;
+        for (int k = 0; k < M::kPiece; ++k) e[k] = live && c + k < cols ? src[k] : Elt(0);
+        __builtin_memcpy(&v[i], e, 16);
       }
     }
   }
@@ -257,7 +254,7 @@ struct Shared {
 //             where a dot product in fp32 is taken from it
 //   intra     O^T += Z^T P^T
 //   update    S = exp(G_C) S + Y^T (w Z), w Z as three bf16 parts
-template <bool kBf16, int DK, int DV, bool kReverse, Kind kind>
+template <bool kBf16, int DK, int DV, bool kReverse, Kind kind, bool kVec>
 __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs p) {
   using M = Mma<kBf16>;
   using Elt = typename M::Elt;
@@ -320,18 +317,17 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
   Stage<kBf16, DK> sx, sy;
   Stage<kBf16, DV> sz, se;
   float g_next = 0.0f;
-  const bool vec = p.vec;
   auto fetch = [&](int c, int sub) {
     const int t0 = c * kChunk;
     if constexpr (kind != kSum)
       if (p.nq > 1 || sub == 0) {
-        sx.load(p.x, b, (int64_t)h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dk, vec);
-        if constexpr (kDots) se.load(p.e, b, (int64_t)h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dv, vec);
+        sx.template load<kVec>(p.x, b, h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dk);
+        if constexpr (kDots) se.template load<kVec>(p.e, b, h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dv);
       }
     if (p.nkv > 1 || sub == 0) {
-      const int64_t hh = (int64_t)h * p.nkv + (p.nkv > 1 ? sub : 0);
-      sy.load(p.y, b, hh, t0, n, p.dk, vec);
-      sz.load(p.z, b, hh, t0, n, p.dv, vec);
+      const int hh = h * p.nkv + (p.nkv > 1 ? sub : 0);
+      sy.template load<kVec>(p.y, b, hh, t0, n, p.dk);
+      sz.template load<kVec>(p.z, b, hh, t0, n, p.dv);
     }
     if (sub == 0 && wave == 0) {
       const int t = t0 + lane;
@@ -512,19 +508,23 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
       } else {
         // an infinity or a NaN among the values reaches only the outputs that may see its token:
         // a zero score times it would not be zero, so masked products are left out one by one
-        for (int m = 0; m < 4; ++m) {
-          const int i = m * 16 + l15;
+#pragma unroll 1
+        for (int j = 0; j < kChunk; ++j) {
+          float z[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float s = 0.0f;
-              for (int j = kReverse ? i : 0; j < (kReverse ? kChunk : i + 1); ++j)
-                s += Elem<kBf16>::load(sh.p + i * PP + j) * Elem<kBf16>::load(sh.z + j * PV + col0 + nt * 16 + g4 + r);
+            for (int r = 0; r < 4; ++r) z[nt][r] = Elem<kBf16>::load(sh.z + j * PV + col0 + nt * 16 + g4 + r);
 #pragma unroll
-              for (int mm = 0; mm < 4; ++mm)
-                if (mm == m) O[mm][nt][r] += s;
-            }
+          for (int m = 0; m < 4; ++m) {
+            const int i = m * 16 + l15;
+            const float s = Elem<kBf16>::load(sh.p + i * PP + j);
+            if (kReverse ? j >= i : j <= i)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) O[m][nt][r] = fmaf(s, z[nt][r], O[m][nt][r]);
+          }
         }
       }
       if constexpr (kDots) {
@@ -552,13 +552,12 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
         }
       }
       if ((p.nq > 1 || sub == nsub - 1) && p.o) {
-        Elt* out = (Elt*)p.o;
-        const int64_t oh = (int64_t)h * p.nq + (p.nq > 1 ? sub : 0);
+        const int oh = h * p.nq + (p.nq > 1 ? sub : 0), pitch = a.Hkv * p.nq * p.dv;
+        Elt* out = (Elt*)p.o + ((size_t)b * a.T + t0) * pitch + (size_t)oh * p.dv;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const int t = t0 + m * 16 + l15;
-          if (t >= a.T) continue;
-          Elt* row = out + (((size_t)b * a.T + t) * a.Hkv * p.nq + oh) * p.dv;
+          const uint32_t off = (uint32_t)((m * 16 + l15) * pitch + col0 + g4);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const int j = col0 + nt * 16 + g4;
@@ -568,12 +567,12 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
               const float f = t < n ? O[m][nt][r] : 0.0f;
               if constexpr (kBf16) v[r] = f32_to_bf16(f); else v[r] = f;
             }
-            if (p.vec_out) {
-              if (j < p.dv) __builtin_memcpy(__builtin_assume_aligned(row + j, 4 * sizeof(Elt)), v, 4 * sizeof(Elt));
+            if constexpr (kVec) {
+              if (t < a.T && j < p.dv) __builtin_memcpy(__builtin_assume_aligned(out + off + nt * 16, 4 * sizeof(Elt)), v, 4 * sizeof(Elt));
             } else {
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (j + r < p.dv) row[j + r] = v[r];
+                if (t < a.T && j + r < p.dv) out[off + nt * 16 + r] = v[r];
             }
           }
         }
@@ -643,11 +642,11 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
   if (kind == kSum && p.seg_decay && tid == 0) p.seg_decay[blockIdx.x] = __builtin_amdgcn_exp2f((float)seg_log);
 }
 
-template <bool kBf16, int DK, int DV, bool kReverse, Kind kind>
+template <bool kBf16, int DK, int DV, bool kReverse, Kind kind, bool kVec>
 hipError_t launch_chunk(const RoleArgs& p, hipStream_t st) {
   constexpr size_t lds = sizeof(Shared<kBf16, DK, DV, kind>);
   static_assert(lds <= 160 * 1024, "LDS of a block");
-  const auto fn = chunk_kernel<kBf16, DK, DV, kReverse, kind>;
+  const auto fn = chunk_kernel<kBf16, DK, DV, kReverse, kind, kVec>;
   if constexpr (lds > 64 * 1024) {
     static const hipError_t raised = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (raised != hipSuccess) return raised;
@@ -659,13 +658,16 @@ hipError_t launch_chunk(const RoleArgs& p, hipStream_t st) {
 // The narrowest tiles that hold the head sizes: 64 or 128 columns.
 template <bool kReverse, Kind kind>
 hipError_t run_role(const RoleArgs& p, hipStream_t st) {
-  const bool k128 = p.dk > 64, v128 = p.dv > 64;
-  auto go = [&](auto bf) {
-    constexpr bool kB = decltype(bf)::value;
-    if (k128) return v128 ? launch_chunk<kB, 128, 128, kReverse, kind>(p, st) : launch_chunk<kB, 128, 64, kReverse, kind>(p, st);
-    return v128 ? launch_chunk<kB, 64, 128, kReverse, kind>(p, st) : launch_chunk<kB, 64, 64, kReverse, kind>(p, st);
+  auto go = [&](auto bf, auto vec) {
+    constexpr bool kB = decltype(bf)::value, kV = decltype(vec)::value;
+    if (p.dk > 64)
+      return p.dv > 64 ? launch_chunk<kB, 128, 128, kReverse, kind, kV>(p, st) : launch_chunk<kB, 128, 64, kReverse, kind, kV>(p, st);
+    return p.dv > 64 ? launch_chunk<kB, 64, 128, kReverse, kind, kV>(p, st) : launch_chunk<kB, 64, 64, kReverse, kind, kV>(p, st);
   };
-  return p.a.bf16 ? go(std::true_type{}) : go(std::false_type{});
+  const std::true_type yes;
+  const std::false_type no;
+  if (p.a.bf16) return p.vec ? go(yes, yes) : go(yes, no);
+  return p.vec ? go(no, yes) : go(no, no);
 }
 
 inline bool rows_vec(const Rows& r, int cols, int bf16) {
