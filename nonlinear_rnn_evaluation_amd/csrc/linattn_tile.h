@@ -138,6 +138,7 @@ struct Split;
 template <int kParts>
 struct Split<true, kParts> {
   bf16x8 part[kParts];
+  __device__ __forceinline__ Split() {}
   __device__ __forceinline__ explicit Split(float (&v)[8]) {
 #pragma unroll
     for (int k = 0; k < kParts; ++k)
@@ -147,28 +148,23 @@ struct Split<true, kParts> {
         if (k + 1 < kParts) v[e] -= (float)part[k][e];
       }
   }
-  // the smallest part first
-  __device__ __forceinline__ f32x4 mul_a(const bf16x8& b, f32x4 c) const {
-#pragma unroll
-    for (int k = kParts; k--;) c = Mma<true>::mul(part[k], b, c);
-    return c;
-  }
-  __device__ __forceinline__ f32x4 mul_b(const bf16x8& a, f32x4 c) const {
-#pragma unroll
-    for (int k = kParts; k--;) c = Mma<true>::mul(a, part[k], c);
-    return c;
-  }
 };
 template <int kParts>
 struct Split<false, kParts> {
-  Mma<false>::Frag f;
+  Mma<false>::Frag part[1];
+  __device__ __forceinline__ Split() {}
   __device__ __forceinline__ explicit Split(float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = v[e];
+    for (int e = 0; e < 8; ++e) part[0].v[e] = v[e];
   }
-  __device__ __forceinline__ f32x4 mul_a(const Mma<false>::Frag& b, f32x4 c) const { return Mma<false>::mul(f, b, c); }
-  __device__ __forceinline__ f32x4 mul_b(const Mma<false>::Frag& a, f32x4 c) const { return Mma<false>::mul(a, f, c); }
 };
+
+// The same number, as far as the compiler can tell computed anew: addresses made from it stay where
+// they are used instead of being kept in registers over the whole loop.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 // ---- tiles ---------------------------------------------------------------------------------
 // 64 rows x kCols of one operand on its way from memory to LDS: 16-byte pieces in registers.
@@ -182,21 +178,23 @@ struct Stage {
   uint4 v[kN];
 
   // Rows t0 .. t0 + 63 of batch row b and head h; rows at or past n and columns past `cols` are
-  // zeros.  kVec: every piece is one aligned load, and 64 rows span less than 2^31 bytes, so an
-  // address is a uniform base and a 32-bit offset.
+  // zeros.  kVec: every piece is one aligned buffer load from a uniform base, and 64 rows span
+  // less than 2^31 bytes; a piece that is not there gets an offset past the buffer's end, which
+  // reads as zeros without a branch.
   template <bool kVec>
   __device__ __forceinline__ void load(const Rows& r, int b, int h, int t0, int n, int cols) {
     constexpr int kStep = kThreads / kPerRow;            // rows between a thread's pieces
     const Elt* base = (const Elt*)r.p + b * r.sb + h * r.sh + t0 * r.st;
-    const int row = threadIdx.x / kPerRow, c = (threadIdx.x % kPerRow) * M::kPiece;
+    const int tid = fresh(threadIdx.x), row = tid / kPerRow, c = (tid % kPerRow) * M::kPiece;
     if constexpr (kVec) {
-      const uint32_t off = (uint32_t)(row * (int)r.st + c) * (uint32_t)sizeof(Elt);
-      const bool in = c < cols;
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7fffffff, 0x00027000);
+      const uint32_t pitch = (uint32_t)r.st * (uint32_t)sizeof(Elt);
+      const uint32_t off = row * pitch + c * (uint32_t)sizeof(Elt);
+      const int left = c < cols ? n - t0 - row : 0;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (in && t0 + row + i * kStep < n) v[i] = *(const uint4*)((const char*)(base + i * kStep * r.st) + off);
-      }
+      for (int i = 0; i < kN; ++i)
+        v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rsrc, left > i * kStep ? off + i * kStep * pitch : 0x80000000u, 0, 0));
     } else {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
@@ -210,13 +208,31 @@ struct Stage {
     }
   }
   __device__ __forceinline__ void store(Elt* tile) const {
+    const int tid = fresh(threadIdx.x);
+    Elt* at = tile + (tid / kPerRow) * kPitch + (tid % kPerRow) * M::kPiece;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int p = threadIdx.x + i * kThreads;
-      *(uint4*)(tile + (p / kPerRow) * kPitch + (p % kPerRow) * M::kPiece) = v[i];
-    }
+    for (int i = 0; i < kN; ++i) *(uint4*)(at + i * (kThreads / kPerRow) * kPitch) = v[i];
   }
 };
+
+// x of the lanes that a DPP move brings together, 0 where it brings nothing
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double dpp_move(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, kRows, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRows, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// inclusive scan over the wave: within rows of 16 lanes, then across them
+__device__ __forceinline__ double wave_scan(double x) {
+  x += dpp_move<0x111, 0xf>(x);      // row_shr:1
+  x += dpp_move<0x112, 0xf>(x);
+  x += dpp_move<0x114, 0xf>(x);
+  x += dpp_move<0x118, 0xf>(x);
+  x += dpp_move<0x142, 0xa>(x);      // row_bcast:15 to rows 1 and 3
+  x += dpp_move<0x143, 0xc>(x);      // row_bcast:31 to rows 2 and 3
+  return x;
+}
 
 __device__ __forceinline__ float row16_sum(float v) {      // over the 16 lanes of a group
   v += __shfl_xor(v, 1);
@@ -229,6 +245,19 @@ __device__ __forceinline__ float group_sum(float v) {      // over the four grou
   return v + __shfl_xor(v, 32);
 }
 
+// Where the scores of row i from column j on stand, j a multiple of 4: rows of 64 without padding,
+// their 16-byte pieces permuted by the row so that 16 rows of one column spread over the banks.
+template <bool kBf16>
+__device__ __forceinline__ int score_at(int i, int j) {
+  constexpr int kPiece = Mma<kBf16>::kPiece;
+  return i * kChunk + (((j / kPiece) ^ (i & (64 / kPiece - 1))) * kPiece) + j % kPiece;
+}
+template <bool kBf16>
+__device__ __forceinline__ typename Mma<kBf16>::Frag score_rows(const typename Mma<kBf16>::Elt* p, int i, int j) {
+  if constexpr (kBf16) return Mma<true>::rows(p + score_at<true>(i, j));
+  else return Mma<false>::two(p + score_at<false>(i, j), p + score_at<false>(i, j + 4));
+}
+
 // LDS of one block.
 template <bool kBf16, int DK, int DV, Kind kind>
 struct Shared {
@@ -238,10 +267,12 @@ struct Shared {
   alignas(16) Elt y[kChunk * Stage<kBf16, DK>::kPitch];
   alignas(16) Elt z[kChunk * Stage<kBf16, DV>::kPitch];
   alignas(16) Elt e[kind == kDotQ || kind == kDotK ? kChunk * Stage<kBf16, DV>::kPitch : 1];
-  alignas(16) Elt p[kSumOnly ? 1 : kChunk * Stage<kBf16, kChunk>::kPitch];   // scores [i][j]
-  alignas(16) float ghi[kChunk], glo[kChunk];   // G in units of log2, as a sum of two floats
-  float inter[kChunk], upd[kChunk];             // the weights of S^T x and of y z^T
-  float total;                                  // exp(G_C)
+  alignas(16) Elt p[kSumOnly ? 1 : kChunk * kChunk];   // scores [i][j], see score_at
+  struct alignas(16) Weights {
+    float ghi[kChunk], glo[kChunk];             // G in units of log2, as a sum of two floats
+    float inter[kChunk], upd[kChunk];           // the weights of S^T x and of y z^T
+    float total;                                // exp(G_C)
+  } w[2];                                       // this chunk's and the next one's
   float dot[kind == kDotQ || kind == kDotK ? 4 : 1][kChunk];
   float row[kind == kDotQ ? kChunk : 1], col[kind == kDotQ ? 10 : 1][16];
 };
@@ -262,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
   constexpr int NT = DV / 64;               // column tiles of 16 of a wave
   constexpr int KT = DK / 16;               // row tiles of S
   constexpr int NW = NT * 16;
-  constexpr int PK = Stage<kBf16, DK>::kPitch, PV = Stage<kBf16, DV>::kPitch, PP = Stage<kBf16, kChunk>::kPitch;
+  constexpr int PK = Stage<kBf16, DK>::kPitch, PV = Stage<kBf16, DV>::kPitch;
   constexpr bool kDots = kind == kDotQ || kind == kDotK;
   constexpr int kParts = kDots ? 3 : 1;
   using Sh = Shared<kBf16, DK, DV, kind>;
@@ -270,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
   Sh& sh = *(Sh*)smem;
 
   const LinAttn& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l15 = lane & 15, g4 = (lane >> 4) * 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l15 = lane & 15, g4 = (lane >> 4) * 4;
   const int seg = blockIdx.x % p.nseg;
   const int h = blockIdx.x / p.nseg % a.Hkv, b = blockIdx.x / p.nseg / a.Hkv;
   const int n = row_len(a.lens, b, a.T);
@@ -294,6 +325,12 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         S[kt][nt][r] = (kind != kSum && p.s_in && s_in_range(kt, nt, r)) ? p.s_in[s_at(kt, nt, r)] : 0.0f;
+
+  // the loads of S end here: a wait for them inside the loop would wait for the tiles behind them
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(S[kt][nt]));
 
   if constexpr (kind == kDotK) {
     if (p.x_end) {
@@ -336,13 +373,35 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
   };
 
   double seg_log = 0.0;                       // wave 0: log2 of the segment's decay
+  // Wave 0 turns the log decays that it fetched into a chunk's weights.  G is an inclusive scan in
+  // 64 bits, because differences of sums of log decays (each down to -104) are what counts.
+  auto weigh = [&](int slot) {
+    const double x = wave_scan((double)g_next * 1.4426950408889634);
+    const uint64_t last = __builtin_bit_cast(uint64_t, x);
+    const double end = __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(last >> 32), 63) << 32 |
+                                                      (uint32_t)__builtin_amdgcn_readlane((uint32_t)last, 63));
+    const float hi = (float)x;
+    const float from_start = __builtin_amdgcn_exp2f(hi), to_end = __builtin_amdgcn_exp2f((float)(end - x));
+    auto& w = sh.w[slot];
+    w.ghi[lane] = hi;
+    w.glo[lane] = (float)(x - (double)hi);
+    w.inter[lane] = (kReverse ? to_end : from_start) * p.inter_scale;
+    w.upd[lane] = (kReverse ? from_start : to_end) * p.upd_scale;
+    if (lane == 0) w.total = __builtin_amdgcn_exp2f((float)end);
+    seg_log += end;
+  };
   const int count = live > c_lo ? (live - c_lo) * nsub : 0;
-  if (count > 0) fetch(kReverse ? live - 1 : c_lo, 0);
+  if (count > 0) {
+    fetch(kReverse ? live - 1 : c_lo, 0);
+    if (wave == 0) weigh(0);
+  }
   float u_acc = 0.0f, b_acc = 0.0f;           // threads 0..63 (kDots): sums over the query heads
   f32x4 O[4][NT];
 
   for (int it = 0; it < count; ++it) {
-    const int c = kReverse ? live - 1 - it / nsub : c_lo + it / nsub, sub = it % nsub, t0 = c * kChunk;
+    const int step = it / nsub, sub = it % nsub, c = kReverse ? live - 1 - step : c_lo + step, t0 = c * kChunk;
+    const auto& wt = sh.w[step & 1];
+    const bool last_sub = sub == nsub - 1;
     const bool new_x = p.nq > 1 || sub == 0, new_yz = p.nkv > 1 || sub == 0;
     __syncthreads();
     if constexpr (kind != kSum)
@@ -354,25 +413,6 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
       sy.store(sh.y);
       sz.store(sh.z);
     }
-    if (sub == 0 && wave == 0) {
-      // G: an inclusive scan over the chunk in 64 bits, because differences of sums of log
-      // decays (each down to -104) are what counts
-      double x = (double)g_next * 1.4426950408889634;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-      }
-      const double end = __shfl(x, 63);
-      const float hi = (float)x;
-      sh.ghi[lane] = hi;
-      sh.glo[lane] = (float)(x - (double)hi);
-      const float from_start = __builtin_amdgcn_exp2f((float)x), to_end = __builtin_amdgcn_exp2f((float)(end - x));
-      sh.inter[lane] = (kReverse ? to_end : from_start) * p.inter_scale;
-      sh.upd[lane] = (kReverse ? from_start : to_end) * p.upd_scale;
-      if (lane == 0) sh.total = __builtin_amdgcn_exp2f((float)end);
-      seg_log += end;
-    }
     auto fetch_next = [&] {
       if (it + 1 < count) fetch(kReverse ? live - 1 - (it + 1) / nsub : c_lo + (it + 1) / nsub, (it + 1) % nsub);
     };
@@ -381,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
 
     if constexpr (kind != kSum) {
       // ---- scores of the wave's 16 queries: lane column i, four rows j a register block
+      const int ln = fresh(lane), l15 = ln & 15, g4 = (ln >> 4) * 4;
       const int i = wave * 16 + l15;
       f32x4 P[4], A[4];
 #pragma unroll
@@ -402,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
             if (jt <= wave) A[jt] = M::mul(M::rows(sh.z + (jt * 16 + l15) * PV + k * 32 + g4 * 2), ef, A[jt]);
         }
       }
-      const float gi = sh.ghi[i], gi_lo = sh.glo[i];
+      const float gi = wt.ghi[i], gi_lo = wt.glo[i];
       float row = 0.0f;
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         Elt pe[4];
         if (kReverse ? jt >= wave : jt <= wave) {
-          const float4 gh = *(const float4*)&sh.ghi[jt * 16 + g4], gl = *(const float4*)&sh.glo[jt * 16 + g4];
+          const float4 gh = *(const float4*)&wt.ghi[jt * 16 + g4], gl = *(const float4*)&wt.glo[jt * 16 + g4];
           const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w};
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -428,17 +469,12 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
         } else {
           pe[0] = pe[1] = pe[2] = pe[3] = Elt(0);
         }
-        __builtin_memcpy(__builtin_assume_aligned(sh.p + i * PP + jt * 16 + g4, 4 * sizeof(Elt)), pe, 4 * sizeof(Elt));
+        __builtin_memcpy(__builtin_assume_aligned(sh.p + score_at<kBf16>(i, jt * 16 + g4), 4 * sizeof(Elt)), pe, 4 * sizeof(Elt));
       }
       if constexpr (kind == kDotQ) {
         row = group_sum(row);
         if (lane < 16) sh.row[i] = row;
       }
-      // the next tiles are on their way during what follows (asked for any earlier, they would
-      // share the registers with the scores)
-      __builtin_amdgcn_sched_barrier(0);
-      fetch_next();
-      __builtin_amdgcn_sched_barrier(0);
       // ---- what the state gives: O^T = S^T X^T
       if (new_x) {
 #pragma unroll
@@ -450,19 +486,25 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
           Frag xf[4];
 #pragma unroll
           for (int m = 0; m < 4; ++m) xf[m] = M::rows_split(sh.x + (m * 16 + l15) * PK + k * 32 + g4);
+          Split<kBf16, kParts> sf[NT];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float v[8];
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] = S[2 * k][nt][r], v[4 + r] = S[2 * k + 1][nt][r];
-            const Split<kBf16, kParts> sf(v);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) O[m][nt] = sf.mul_a(xf[m], O[m][nt]);
+            sf[nt] = Split<kBf16, kParts>(v);
           }
+          // the smallest part first; products into one accumulator stand apart
+#pragma unroll
+          for (int q = (kBf16 ? kParts : 1); q--;)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) O[m][nt] = M::mul(sf[nt].part[q], xf[m], O[m][nt]);
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const float w = sh.inter[m * 16 + l15];
+          const float w = wt.inter[m * 16 + l15];
           float d = 0.0f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -479,15 +521,20 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
           }
         }
       }
+      // the next tiles are on their way during the rest of the chunk (asked for any earlier, they
+      // would share the registers with the products above and spill)
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_next();
       __syncthreads();
     }
 
     // ---- the wave's columns of Z, all 64 rows
+    const int lane2 = fresh(lane), l15 = lane2 & 15, g4 = (lane2 >> 4) * 4;
     Frag zf[2][NT];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) zf[k][nt] = M::cols(sh.z, PV, k * 32, col0 + nt * 16, lane);
+      for (int nt = 0; nt < NT; ++nt) zf[k][nt] = M::cols(sh.z, PV, k * 32, col0 + nt * 16, lane2);
 
     if constexpr (kind != kSum) {
       bool fine = true;
@@ -501,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (kReverse ? (k == 1 || m < 2) : (k == 0 || m >= 2)) {
-              const Frag pf = M::rows(sh.p + (m * 16 + l15) * PP + k * 32 + g4 * 2);
+              const Frag pf = score_rows<kBf16>(sh.p, m * 16 + l15, k * 32 + g4 * 2);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) O[m][nt] = M::mul(zf[k][nt], pf, O[m][nt]);
             }
@@ -518,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int i = m * 16 + l15;
-            const float s = Elem<kBf16>::load(sh.p + i * PP + j);
+            const float s = Elem<kBf16>::load(sh.p + score_at<kBf16>(i, j & ~3) + (j & 3));
             if (kReverse ? j >= i : j <= i)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
@@ -536,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
             for (int w = jt; w < 4; ++w) s += sh.col[w * (w + 1) / 2 + jt][tid & 15];
             u_acc += sh.row[tid] - s;
           }
-          if (sub == nsub - 1) {
+          if (last_sub) {
             const int t = t0 + tid;
             if (t < a.T) {
               const size_t at = ((size_t)b * a.Hkv + h) * a.T + t;
@@ -551,28 +598,38 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
           }
         }
       }
-      if ((p.nq > 1 || sub == nsub - 1) && p.o) {
+      if ((p.nq > 1 || last_sub) && p.o) {
         const int oh = h * p.nq + (p.nq > 1 ? sub : 0), pitch = a.Hkv * p.nq * p.dv;
         Elt* out = (Elt*)p.o + ((size_t)b * a.T + t0) * pitch + (size_t)oh * p.dv;
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)out, 0, 0x7fffffff, 0x00027000);
+        const int ln = fresh(lane2), l15 = ln & 15, g4 = (ln >> 4) * 4;
+        const uint32_t off = (uint32_t)(l15 * pitch + col0 + g4) * (uint32_t)sizeof(Elt);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const int t = t0 + m * 16 + l15;
-          const uint32_t off = (uint32_t)((m * 16 + l15) * pitch + col0 + g4);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const int j = col0 + nt * 16 + g4;
+            const int left = t < a.T ? p.dv - (col0 + nt * 16 + g4) : 0;
             Elt v[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float f = t < n ? O[m][nt][r] : 0.0f;
               if constexpr (kBf16) v[r] = f32_to_bf16(f); else v[r] = f;
             }
+            // what is not there goes past the buffer's end, where stores are dropped
             if constexpr (kVec) {
-              if (t < a.T && j < p.dv) __builtin_memcpy(__builtin_assume_aligned(out + off + nt * 16, 4 * sizeof(Elt)), v, 4 * sizeof(Elt));
+              const uint32_t at = left > 0 ? off + (uint32_t)(m * 16 * pitch + nt * 16) * (uint32_t)sizeof(Elt) : 0x80000000u;
+              if constexpr (kBf16) {
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), rsrc, at, 0, 0);
+              } else {
+                typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, at, 0, 0);
+              }
             } else {
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (t < a.T && j + r < p.dv) out[off + nt * 16 + r] = v[r];
+                if (r < left) out[(m * 16 + l15) * pitch + col0 + g4 + nt * 16 + r] = v[r];
             }
           }
         }
@@ -580,9 +637,9 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
     }
 
     // ---- the state's update, once for each pair of keys and values
-    if (p.nkv > 1 || sub == nsub - 1) {
+    if (p.nkv > 1 || last_sub) {
       if (p.nkv == 1 || sub == 0) {
-        const float total = sh.total;
+        const float total = wt.total;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -590,10 +647,11 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float* wp = sh.upd + k * 32 + g4 * 2;
+        const float* wp = wt.upd + k * 32 + g4 * 2;
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = wp[e];
+        Split<kBf16, 3> wz[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float v[8];
@@ -601,15 +659,25 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
           for (int e = 0; e < 8; ++e) {
             if constexpr (kBf16) v[e] = w[e] * (float)zf[k][nt][e]; else v[e] = w[e] * zf[k][nt].v[e];
           }
-          const Split<kBf16, 3> wz(v);
+          wz[nt] = Split<kBf16, 3>(v);
+        }
+        constexpr int KG = kBf16 ? 4 : 2;     // row tiles at a time
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            const Frag yf = M::cols(sh.y, PK, k * 32, kt * 16, lane);
-            S[kt][nt] = wz.mul_b(yf, S[kt][nt]);
-          }
+        for (int kt = 0; kt < KT; kt += KG) {
+          Frag yf[KG];
+#pragma unroll
+          for (int q = 0; q < KG; ++q) yf[q] = M::cols(sh.y, PK, k * 32, (kt + q) * 16, lane2);
+#pragma unroll
+          for (int part = (kBf16 ? 3 : 1); part--;)
+#pragma unroll
+            for (int q = 0; q < KG; ++q)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) S[kt + q][nt] = M::mul(yf[q], wz[nt].part[part], S[kt + q][nt]);
         }
       }
     }
+    // the next chunk's weights, where no other wave waits for them
+    if (last_sub && it + 1 < count && wave == 0) weigh(~step & 1);
   }
 
   // ---- chunks without tokens: zeros
