@@ -23,7 +23,8 @@ namespace {
 
 struct DecayArgs {
   LinAttn a;
-  const float *u, *b, *c;    // [B][Hkv][T]; u = sum_j W_tj - sum_i W_it
+  const float *u, *c;        // [B][Hkv][T]; u_t = b_t + sum_j W_tj - sum_i W_it
+  const float* b;            // [B][Hkv][chunks]: sum b
   const float* x_end;        // [B][Hkv][nseg], or nullptr: zeros
   int seg_chunks, nseg;
   float* gg;                 // [B][T][Hkv] (per token), or
@@ -48,19 +49,19 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs p) {
   const int seg = w % p.nseg, h = w / p.nseg % a.Hkv, b = w / p.nseg / a.Hkv;
   const int n = row_len(a.lens, b, a.T);
   const size_t base = ((size_t)b * a.Hkv + h) * a.T;
-  const int c_lo = seg * p.seg_chunks, c_hi = min(c_lo + p.seg_chunks, (a.T + kChunk - 1) / kChunk);
+  const int chunks = (a.T + kChunk - 1) / kChunk, c_lo = seg * p.seg_chunks, c_hi = min(c_lo + p.seg_chunks, chunks);
   float x = p.x_end ? p.x_end[w] : 0.0f;
   double sum = 0.0;
   for (int ch = c_hi - 1; ch >= c_lo; --ch) {
     const int t = ch * kChunk + lane;
     const bool in = t < a.T;
-    const float u = in ? p.u[base + t] : 0.0f, bb = in ? p.b[base + t] : 0.0f, cc = in ? p.c[base + t] : 0.0f;
-    const float ub = wave_suffix_sum(u + bb, lane), cs = wave_suffix_sum(cc, lane);
-    const float b_all = __shfl(wave_suffix_sum(bb, lane), 0), c_all = __shfl(cs, 0);
+    const float u = in ? p.u[base + t] : 0.0f, cc = in ? p.c[base + t] : 0.0f;
+    const float b_all = p.b[((size_t)b * a.Hkv + h) * chunks + ch];
+    const float us = wave_suffix_sum(u, lane), cs = wave_suffix_sum(cc, lane), c_all = __shfl(cs, 0);
     const float g = a.g[a.decay_token ? ((size_t)b * a.T + (in ? t : 0)) * a.Hkv + h : (size_t)h];
     x -= c_all;                                   // exp(G_C) <S, E>
     // a decay that forgets everything passes no gradient
-    const float d = t < n && !(g <= kLogDecayMin) ? ub + (c_all - cs) + x : 0.0f;
+    const float d = t < n && !(g <= kLogDecayMin) ? us + (c_all - cs) + x : 0.0f;
     if (p.gg && in) p.gg[((size_t)b * a.T + t) * a.Hkv + h] = d;
     sum += d;
     x += b_all;
@@ -97,7 +98,8 @@ BackwardLayout backward_layout(const LinAttn& a) {
   const size_t rows = (size_t)a.B * a.Hkv, segs = rows * l.plan.nseg, tokens = rows * a.T * 4;
   if (l.plan.nseg > 1) l.s = take(l.plan.states), l.e = take(l.plan.states), l.decay = take(segs * 4);
   l.last = take(rows * a.Dk * a.Dv * 4);
-  l.u = take(tokens), l.b = take(tokens), l.c = take(tokens);
+  l.u = take(tokens), l.c = take(tokens);
+  l.b = take(rows * ((a.T + kChunk - 1) / kChunk) * 4);
   l.x_end = take(segs * 4);
   l.seg_sum = take(segs * 8);
   l.total = off;
@@ -171,7 +173,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     p.x = a.v, p.y = d.go, p.z = a.q, p.e = a.k;
     p.dk = a.Dv, p.dv = a.Dk, p.transposed = 1;
     p.o = d.gk;
-    p.c = c;
+    p.u = c;
     if (d.gg && (d.gstate_out || nseg > 1)) p.x_end = (float*)(ws + l.x_end), p.s_entry = S, p.s_last = last;
     if (nseg == 1) p.s_out = d.gstate_in;
     if ((e = run_role<true, kDotK>(p, st)) != hipSuccess) return e;
@@ -184,7 +186,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     if ((e = run_role<true, kOut>(p, st)) != hipSuccess) return e;
   }
   if (d.gg) {
-    DecayArgs p{a, u, b, c, nullptr, l.plan.seg_chunks, nseg, nullptr, nullptr};
+    DecayArgs p{a, u, c, b, nullptr, l.plan.seg_chunks, nseg, nullptr, nullptr};
     if (a.decay_token) p.gg = d.gg; else p.seg_sum = (double*)(ws + l.seg_sum);
     if (d.gstate_out || nseg > 1) p.x_end = (float*)(ws + l.x_end);
     const int64_t waves = rows * nseg;

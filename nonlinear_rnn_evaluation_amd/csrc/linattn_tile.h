@@ -21,7 +21,6 @@ namespace pnr {
 namespace linattn {
 
 constexpr int kChunk = 64;
-constexpr int kThreads = 256;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -46,7 +45,8 @@ struct RoleArgs {
   float* s_out;          // [B][Hkv][nseg] states at the segments' exit, or nullptr
   float* seg_decay;      // kSum: [B][Hkv][nseg] the segment's whole decay, or nullptr
   void* o;
-  float *u, *b, *c;      // [B][Hkv][T] (kDotQ: u and b, kDotK: c)
+  float* u;              // [B][Hkv][T]: u + b (kDotQ), c (kDotK) of the decay's gradient
+  float* b;              // [B][Hkv][chunks]: sums of b (kDotQ)
   float* x_end;          // kDotK: [B][Hkv][nseg] <state after the segment's last token, s_in>, or nullptr
   const float* s_entry;  // ... that state, for all but the last segment: the next one's entry, [B][Hkv][nseg]
   const float* s_last;   // ... and after the last, [B][Hkv]
@@ -141,12 +141,18 @@ struct Split<true, kParts> {
   __device__ __forceinline__ Split() {}
   __device__ __forceinline__ explicit Split(float (&v)[8]) {
 #pragma unroll
-    for (int k = 0; k < kParts; ++k)
+    for (int k = 0; k < kParts; ++k) {
+      uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        part[k][e] = (__bf16)v[e];
-        if (k + 1 < kParts) v[e] -= (float)part[k][e];
+      for (int e = 0; e < 8; e += 2) {
+        w[e / 2] = pack_bf16(v[e], v[e + 1]);
+        if (k + 1 < kParts) {
+          v[e] -= __uint_as_float(w[e / 2] << 16);
+          v[e + 1] -= __uint_as_float(w[e / 2] & 0xffff0000u);
+        }
       }
+      __builtin_memcpy(&part[k], w, 16);
+    }
   }
 };
 template <int kParts>
@@ -167,14 +173,17 @@ __device__ __forceinline__ int fresh(int v) {
 }
 
 // ---- tiles ---------------------------------------------------------------------------------
+template <bool kBf16>
+constexpr int pitch_of(int cols) { return cols + Mma<kBf16>::kPad; }
+
 // 64 rows x kCols of one operand on its way from memory to LDS: 16-byte pieces in registers.
-template <bool kBf16, int kCols>
+template <bool kBf16, int kCols, int kThreads>
 struct Stage {
   using M = Mma<kBf16>;
   using Elt = typename M::Elt;
   static constexpr int kPerRow = kCols / M::kPiece;
   static constexpr int kN = kChunk * kPerRow / kThreads;
-  static constexpr int kPitch = kCols + M::kPad;
+  static constexpr int kPitch = pitch_of<kBf16>(kCols);
   uint4 v[kN];
 
   // Rows t0 .. t0 + 63 of batch row b and head h; rows at or past n and columns past `cols` are
@@ -258,42 +267,47 @@ __device__ __forceinline__ typename Mma<kBf16>::Frag score_rows(const typename M
   else return Mma<false>::two(p + score_at<false>(i, j), p + score_at<false>(i, j + 4));
 }
 
-// LDS of one block.
+// LDS of one block (bf16, 128 x 128: two blocks a CU, also with the dot products' arrays).
 template <bool kBf16, int DK, int DV, Kind kind>
 struct Shared {
   using Elt = typename Mma<kBf16>::Elt;
-  static constexpr bool kSumOnly = kind == kSum;
-  alignas(16) Elt x[kSumOnly ? 1 : kChunk * Stage<kBf16, DK>::kPitch];
-  alignas(16) Elt y[kChunk * Stage<kBf16, DK>::kPitch];
-  alignas(16) Elt z[kChunk * Stage<kBf16, DV>::kPitch];
-  alignas(16) Elt e[kind == kDotQ || kind == kDotK ? kChunk * Stage<kBf16, DV>::kPitch : 1];
+  static constexpr bool kSumOnly = kind == kSum, kDots = kind == kDotQ || kind == kDotK;
+  alignas(16) Elt x[kSumOnly ? 1 : kChunk * pitch_of<kBf16>(DK)];
+  alignas(16) Elt y[kChunk * pitch_of<kBf16>(DK)];
+  alignas(16) Elt z[kChunk * pitch_of<kBf16>(DV)];
+  alignas(16) Elt e[kDots ? kChunk * pitch_of<kBf16>(DV) : 1];
   alignas(16) Elt p[kSumOnly ? 1 : kChunk * kChunk];   // scores [i][j], see score_at
   struct alignas(16) Weights {
-    float ghi[kChunk], glo[kChunk];             // G in units of log2, as a sum of two floats
-    float inter[kChunk], upd[kChunk];           // the weights of S^T x and of y z^T
-    float total;                                // exp(G_C)
-  } w[2];                                       // this chunk's and the next one's
-  float dot[kind == kDotQ || kind == kDotK ? 4 : 1][kChunk];
-  float row[kind == kDotQ ? kChunk : 1], col[kind == kDotQ ? 10 : 1][16];
+    float ghi[kChunk];                 // G in units of log2, as the sum of a float
+    uint16_t glo[kChunk];              // ... and a bf16
+    float upd[kChunk];                 // the weights of y z^T
+    float total;                       // exp(G_C)
+    float end_hi, end_lo;              // G_C
+  } w[2];                              // this chunk's and the next one's
+  float dot[kDots ? DV / 16 : 1][kChunk];      // the waves' parts of dot products and row sums
+  float bsum[kDots ? DV / 16 : 1];
+  float col[kind == kDotQ ? 10 : 1][16];       // column sums of the score tiles on and below the diagonal
 };
 
-// A block walks the chunks of one segment of one state head, with the state in accumulators:
-// wave w holds the columns w DV / 4 .. of S, all DK rows.  A chunk:
-//   scores    each wave 16 query rows: P^T = Y X^T, weighted, to LDS           (P is rounded to the
+// A block walks the chunks of one segment of one state head, with the state in accumulators: a
+// wave holds 16 columns of S, all DK rows.  (With 32 columns a wave, half the waves and half the
+// reads of X and Y from LDS, 256 registers leave two waves a SIMD: 161 us where this takes
+// KOUT_US us, 16 heads of 128 x 128 over 32768 tokens.)  A chunk:
+//   scores    each wave one or two 16 x 16 tiles a query row tile: P^T = Y X^T, weighted, to LDS           (P is rounded to the
 //             element type: one rounding of each score before a sum over up to 64 of them)
 //   inter     O^T = S^T X^T, weighted; S enters as bf16 (one rounding), or as three bf16 parts
 //             where a dot product in fp32 is taken from it
 //   intra     O^T += Z^T P^T
 //   update    S = exp(G_C) S + Y^T (w Z), w Z as three bf16 parts
 template <bool kBf16, int DK, int DV, bool kReverse, Kind kind, bool kVec>
-__global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs p) {
+__global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(RoleArgs p) {
   using M = Mma<kBf16>;
   using Elt = typename M::Elt;
   using Frag = typename M::Frag;
-  constexpr int NT = DV / 64;               // column tiles of 16 of a wave
+  constexpr int kWaves = DV / 16, kThreads = kWaves * 64;
   constexpr int KT = DK / 16;               // row tiles of S
-  constexpr int NW = NT * 16;
-  constexpr int PK = Stage<kBf16, DK>::kPitch, PV = Stage<kBf16, DV>::kPitch;
+  constexpr int JT = 16 / kWaves;           // score tiles a wave takes of its query row tile
+  constexpr int PK = pitch_of<kBf16>(DK), PV = pitch_of<kBf16>(DV);
   constexpr bool kDots = kind == kDotQ || kind == kDotK;
   constexpr int kParts = kDots ? 3 : 1;
   using Sh = Shared<kBf16, DK, DV, kind>;
@@ -310,27 +324,25 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
   const int live = min(c_hi, (n + kChunk - 1) / kChunk);       // chunks c_lo .. live - 1 hold tokens
   const int nsub = p.nq > p.nkv ? p.nq : p.nkv;
   const size_t sbase = (size_t)blockIdx.x * p.dk * p.dv;
-  const int col0 = wave * NW;                                  // the wave's first column
+  const int col0 = wave * 16;                                  // the wave's first column
+  const int it0 = wave / (kWaves / 4), jt0 = wave % (kWaves / 4) * JT;   // its score tiles
 
-  f32x4 S[KT][NT];
-  auto s_at = [&](int kt, int nt, int r) {     // element (row, column) of accumulator register r
-    const int i = kt * 16 + g4 + r, j = col0 + nt * 16 + l15;
+  f32x4 S[KT];
+  auto s_at = [&](int kt, int r) {     // element (row, column) of accumulator register r
+    const int i = kt * 16 + g4 + r, j = col0 + l15;
     return sbase + (p.transposed ? (size_t)j * p.dk + i : (size_t)i * p.dv + j);
   };
-  auto s_in_range = [&](int kt, int nt, int r) { return kt * 16 + g4 + r < p.dk && col0 + nt * 16 + l15 < p.dv; };
+  auto s_in_range = [&](int kt, int r) { return kt * 16 + g4 + r < p.dk && col0 + l15 < p.dv; };
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
       for (int r = 0; r < 4; ++r)
-        S[kt][nt][r] = (kind != kSum && p.s_in && s_in_range(kt, nt, r)) ? p.s_in[s_at(kt, nt, r)] : 0.0f;
+        S[kt][r] = (kind != kSum && p.s_in && s_in_range(kt, r)) ? p.s_in[s_at(kt, r)] : 0.0f;
 
   // the loads of S end here: a wait for them inside the loop would wait for the tiles behind them
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(S[kt][nt]));
+    asm volatile("" : "+v"(S[kt]));
 
   if constexpr (kind == kDotK) {
     if (p.x_end) {
@@ -340,19 +352,22 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (s_in_range(kt, nt, r)) s += S[kt][nt][r] * after[s_at(kt, nt, r)];
+            if (s_in_range(kt, r)) s += S[kt][r] * after[s_at(kt, r)];
       s = row16_sum(group_sum(s));
-      if (lane == 0) sh.dot[0][wave] = s;
+      if (lane == 0) sh.bsum[wave] = s;
       __syncthreads();
-      if (tid == 0) p.x_end[blockIdx.x] = sh.dot[0][0] + sh.dot[0][1] + sh.dot[0][2] + sh.dot[0][3];
+      if (tid == 0) {
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) s += sh.bsum[w];
+        p.x_end[blockIdx.x] = s;
+      }
     }
   }
 
-  Stage<kBf16, DK> sx, sy;
-  Stage<kBf16, DV> sz, se;
+  Stage<kBf16, DK, kThreads> sx, sy;
+  Stage<kBf16, DV, kThreads> sz, se;
   float g_next = 0.0f;
   auto fetch = [&](int c, int sub) {
     const int t0 = c * kChunk;
@@ -380,14 +395,15 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
     const uint64_t last = __builtin_bit_cast(uint64_t, x);
     const double end = __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(last >> 32), 63) << 32 |
                                                       (uint32_t)__builtin_amdgcn_readlane((uint32_t)last, 63));
-    const float hi = (float)x;
-    const float from_start = __builtin_amdgcn_exp2f(hi), to_end = __builtin_amdgcn_exp2f((float)(end - x));
+    const float hi = (float)x, end_hi = (float)end;
     auto& w = sh.w[slot];
     w.ghi[lane] = hi;
-    w.glo[lane] = (float)(x - (double)hi);
-    w.inter[lane] = (kReverse ? to_end : from_start) * p.inter_scale;
-    w.upd[lane] = (kReverse ? from_start : to_end) * p.upd_scale;
-    if (lane == 0) w.total = __builtin_amdgcn_exp2f((float)end);
+    w.glo[lane] = f32_to_bf16((float)(x - (double)hi));
+    w.upd[lane] = __builtin_amdgcn_exp2f(kReverse ? hi : (float)(end - x)) * p.upd_scale;
+    if (lane == 0) {
+      w.total = __builtin_amdgcn_exp2f(end_hi);
+      w.end_hi = end_hi, w.end_lo = (float)(end - (double)end_hi);
+    }
     seg_log += end;
   };
   const int count = live > c_lo ? (live - c_lo) * nsub : 0;
@@ -396,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
     if (wave == 0) weigh(0);
   }
   float u_acc = 0.0f, b_acc = 0.0f;           // threads 0..63 (kDots): sums over the query heads
-  f32x4 O[4][NT];
+  f32x4 O[4];
 
   for (int it = 0; it < count; ++it) {
     const int step = it / nsub, sub = it % nsub, c = kReverse ? live - 1 - step : c_lo + step, t0 = c * kChunk;
@@ -420,105 +436,107 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
     __syncthreads();
 
     if constexpr (kind != kSum) {
-      // ---- scores of the wave's 16 queries: lane column i, four rows j a register block
+      // ---- scores: lane column i, four rows j a register block
       const int ln = fresh(lane), l15 = ln & 15, g4 = (ln >> 4) * 4;
-      const int i = wave * 16 + l15;
-      f32x4 P[4], A[4];
-#pragma unroll
-      for (int jt = 0; jt < 4; ++jt) P[jt] = A[jt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int k = 0; k < DK / 32; ++k) {
-        const Frag xf = M::rows(sh.x + i * PK + k * 32 + g4 * 2);
-#pragma unroll
-        for (int jt = 0; jt < 4; ++jt)
-          if (kReverse ? jt >= wave : jt <= wave)
-            P[jt] = M::mul(M::rows(sh.y + (jt * 16 + l15) * PK + k * 32 + g4 * 2), xf, P[jt]);
-      }
-      if constexpr (kind == kDotQ) {
-#pragma unroll
-        for (int k = 0; k < DV / 32; ++k) {
-          const Frag ef = M::rows(sh.e + i * PV + k * 32 + g4 * 2);
-#pragma unroll
-          for (int jt = 0; jt < 4; ++jt)
-            if (jt <= wave) A[jt] = M::mul(M::rows(sh.z + (jt * 16 + l15) * PV + k * 32 + g4 * 2), ef, A[jt]);
-        }
-      }
-      const float gi = wt.ghi[i], gi_lo = wt.glo[i];
+      const int i = it0 * 16 + l15;
       float row = 0.0f;
+      if (kReverse ? jt0 + JT > it0 : jt0 <= it0) {       // some of the wave's tiles may see their keys
+        f32x4 P[JT], A[JT];
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        Elt pe[4];
-        if (kReverse ? jt >= wave : jt <= wave) {
-          const float4 gh = *(const float4*)&wt.ghi[jt * 16 + g4], gl = *(const float4*)&wt.glo[jt * 16 + g4];
-          const float ghv[4] = {gh.x, gh.y, gh.z, gh.w}, glv[4] = {gl.x, gl.y, gl.z, gl.w};
+        for (int q = 0; q < JT; ++q) P[q] = A[q] = f32x4{0, 0, 0, 0};
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = jt * 16 + g4 + r;
-            const float d = (gi - ghv[r]) + (gi_lo - glv[r]);
-            const float w = __builtin_amdgcn_exp2f(kReverse ? -d : d) * p.p_scale;
-            const bool in = kReverse ? j >= i : j <= i;
-            const float s = in ? P[jt][r] * w : 0.0f;
-            if constexpr (kind == kDotQ) {
-              const float t = j < i ? s * A[jt][r] : 0.0f;
-              row += t;
-              const float cs = row16_sum(t);
-              if (l15 == 0) sh.col[wave * (wave + 1) / 2 + jt][g4 + r] = cs;
-            }
-            if constexpr (kBf16) pe[r] = f32_to_bf16(s); else pe[r] = s;
-          }
-        } else {
-          pe[0] = pe[1] = pe[2] = pe[3] = Elt(0);
+        for (int k = 0; k < DK / 32; ++k) {
+          const Frag xf = M::rows(sh.x + i * PK + k * 32 + g4 * 2);
+#pragma unroll
+          for (int q = 0; q < JT; ++q) P[q] = M::mul(M::rows(sh.y + ((jt0 + q) * 16 + l15) * PK + k * 32 + g4 * 2), xf, P[q]);
         }
-        __builtin_memcpy(__builtin_assume_aligned(sh.p + score_at<kBf16>(i, jt * 16 + g4), 4 * sizeof(Elt)), pe, 4 * sizeof(Elt));
-      }
-      if constexpr (kind == kDotQ) {
-        row = group_sum(row);
-        if (lane < 16) sh.row[i] = row;
+        if constexpr (kind == kDotQ) {
+#pragma unroll
+          for (int k = 0; k < DV / 32; ++k) {
+            const Frag ef = M::rows(sh.e + i * PV + k * 32 + g4 * 2);
+#pragma unroll
+            for (int q = 0; q < JT; ++q) A[q] = M::mul(M::rows(sh.z + ((jt0 + q) * 16 + l15) * PV + k * 32 + g4 * 2), ef, A[q]);
+          }
+        }
+        const float gi = wt.ghi[i], gi_lo = bf16_to_f32(wt.glo[i]);
+#pragma unroll
+        for (int q = 0; q < JT; ++q) {
+          const int jt = jt0 + q, j0 = jt * 16 + g4;
+          float s[4] = {0, 0, 0, 0};
+          if (kReverse ? jt >= it0 : jt <= it0) {
+            const float4 gh = *(const float4*)&wt.ghi[j0];
+            const uint2 gl = *(const uint2*)&wt.glo[j0];
+            const float ghv[4] = {gh.x, gh.y, gh.z, gh.w};
+            const float glv[4] = {__uint_as_float(gl.x << 16), __uint_as_float(gl.x & 0xffff0000u),
+                                  __uint_as_float(gl.y << 16), __uint_as_float(gl.y & 0xffff0000u)};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float d = kReverse ? (ghv[r] - gi) + (glv[r] - gi_lo) : (gi - ghv[r]) + (gi_lo - glv[r]);
+              s[r] = P[q][r] * (__builtin_amdgcn_exp2f(d) * p.p_scale);
+            }
+            if (jt == it0)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) s[r] = (kReverse ? j0 + r >= i : j0 + r <= i) ? s[r] : 0.0f;
+            if constexpr (kind == kDotQ) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float t = j0 + r < i ? s[r] * A[q][r] : 0.0f;
+                row += t;
+                const float cs = row16_sum(t);
+                if (l15 == 0) sh.col[it0 * (it0 + 1) / 2 + jt][g4 + r] = cs;
+              }
+            }
+          }
+          if constexpr (kBf16)
+            *(uint2*)(sh.p + score_at<true>(i, j0)) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+          else
+            *(float4*)(sh.p + score_at<false>(i, j0)) = make_float4(s[0], s[1], s[2], s[3]);
+        }
+        if constexpr (kind == kDotQ) row = group_sum(row);
       }
       // ---- what the state gives: O^T = S^T X^T
       if (new_x) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) O[m][nt] = f32x4{0, 0, 0, 0};
+        for (int m = 0; m < 4; ++m) O[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < DK / 32; ++k) {
-          Frag xf[4];
+          float v[8];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) xf[m] = M::rows_split(sh.x + (m * 16 + l15) * PK + k * 32 + g4);
-          Split<kBf16, kParts> sf[NT];
+          for (int r = 0; r < 4; ++r) v[r] = S[2 * k][r], v[4 + r] = S[2 * k + 1][r];
+          const Split<kBf16, kParts> sf(v);
+          constexpr int MG = kDots ? 2 : 4;     // row tiles at a time: three parts leave room for two
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float v[8];
+          for (int m0 = 0; m0 < 4; m0 += MG) {
+            Frag xf[MG];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = S[2 * k][nt][r], v[4 + r] = S[2 * k + 1][nt][r];
-            sf[nt] = Split<kBf16, kParts>(v);
+            for (int m = 0; m < MG; ++m) xf[m] = M::rows_split(sh.x + ((m0 + m) * 16 + l15) * PK + k * 32 + g4);
+            // the smallest part first; products into one accumulator stand apart
+#pragma unroll
+            for (int q = (kBf16 ? kParts : 1); q--;)
+#pragma unroll
+              for (int m = 0; m < MG; ++m) O[m0 + m] = M::mul(sf.part[q], xf[m], O[m0 + m]);
           }
-          // the smallest part first; products into one accumulator stand apart
-#pragma unroll
-          for (int q = (kBf16 ? kParts : 1); q--;)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int m = 0; m < 4; ++m) O[m][nt] = M::mul(sf[nt].part[q], xf[m], O[m][nt]);
         }
+        float sum = 0.0f;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const float w = wt.inter[m * 16 + l15];
-          float d = 0.0f;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            O[m][nt] *= w;
-            if constexpr (kDots) {
-              const Elt* er = sh.e + (m * 16 + l15) * PV + col0 + nt * 16 + g4;
-#pragma unroll
-              for (int r = 0; r < 4; ++r) d += O[m][nt][r] * Elem<kBf16>::load(er + r);
-            }
-          }
+          const int t = m * 16 + l15;
+          const float g = kReverse ? (wt.end_hi - wt.ghi[t]) + (wt.end_lo - bf16_to_f32(wt.glo[t])) : wt.ghi[t];
+          O[m] *= __builtin_amdgcn_exp2f(g) * p.inter_scale;
           if constexpr (kDots) {
+            float d = 0.0f;
+            const Elt* er = sh.e + t * PV + col0 + g4;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d += O[m][r] * Elem<kBf16>::load(er + r);
             d = group_sum(d);
-            if (lane < 16) sh.dot[wave][m * 16 + l15] = d;
+            sum += d;
+            if constexpr (kind == kDotQ) d += m == it0 ? row : 0.0f;
+            if (lane < 16) sh.dot[wave][t] = d;
           }
+        }
+        if constexpr (kind == kDotQ) {
+          sum = row16_sum(sum);
+          if (lane == 0) sh.bsum[wave] = sum;
         }
       }
       // the next tiles are on their way during the rest of the chunk (asked for any earlier, they
@@ -530,70 +548,56 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
 
     // ---- the wave's columns of Z, all 64 rows
     const int lane2 = fresh(lane), l15 = lane2 & 15, g4 = (lane2 >> 4) * 4;
-    Frag zf[2][NT];
+    Frag zf[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) zf[k][nt] = M::cols(sh.z, PV, k * 32, col0 + nt * 16, lane2);
+    for (int k = 0; k < 2; ++k) zf[k] = M::cols(sh.z, PV, k * 32, col0, lane2);
 
     if constexpr (kind != kSum) {
-      bool fine = true;
+      if (__all(M::finite(zf[0]) && M::finite(zf[1]))) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) fine = fine && M::finite(zf[k][nt]);
-      if (__all(fine)) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (kReverse ? (k == 1 || m < 2) : (k == 0 || m >= 2)) {
-              const Frag pf = score_rows<kBf16>(sh.p, m * 16 + l15, k * 32 + g4 * 2);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) O[m][nt] = M::mul(zf[k][nt], pf, O[m][nt]);
-            }
+          for (int m = 0; m < 4; ++m)
+            if (kReverse ? (k == 1 || m < 2) : (k == 0 || m >= 2))
+              O[m] = M::mul(zf[k], score_rows<kBf16>(sh.p, m * 16 + l15, k * 32 + g4 * 2), O[m]);
       } else {
         // an infinity or a NaN among the values reaches only the outputs that may see its token:
         // a zero score times it would not be zero, so masked products are left out one by one
 #pragma unroll 1
         for (int j = 0; j < kChunk; ++j) {
-          float z[NT][4];
+          float z[4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) z[nt][r] = Elem<kBf16>::load(sh.z + j * PV + col0 + nt * 16 + g4 + r);
+          for (int r = 0; r < 4; ++r) z[r] = Elem<kBf16>::load(sh.z + j * PV + col0 + g4 + r);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int i = m * 16 + l15;
-            const float s = Elem<kBf16>::load(sh.p + score_at<kBf16>(i, j & ~3) + (j & 3));
-            if (kReverse ? j >= i : j <= i)
+            if (kReverse ? j >= i : j <= i) {
+              const float s = Elem<kBf16>::load(sh.p + score_at<kBf16>(i, j & ~3) + (j & 3));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) O[m][nt][r] = fmaf(s, z[nt][r], O[m][nt][r]);
+              for (int r = 0; r < 4; ++r) O[m][r] = fmaf(s, z[r], O[m][r]);
+            }
           }
         }
       }
       if constexpr (kDots) {
         if (tid < kChunk) {
-          if (new_x) b_acc += sh.dot[0][tid] + sh.dot[1][tid] + sh.dot[2][tid] + sh.dot[3][tid];
-          if constexpr (kind == kDotQ) {
-            const int jt = tid >> 4;
-            float s = 0.0f;
-            for (int w = jt; w < 4; ++w) s += sh.col[w * (w + 1) / 2 + jt][tid & 15];
-            u_acc += sh.row[tid] - s;
+          if (new_x) {
+            float d = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) d += sh.dot[w][tid];
+            if constexpr (kind == kDotQ) {
+              const int jt = tid >> 4;
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                if (w >= jt) d -= sh.col[w * (w + 1) / 2 + jt][tid & 15];
+#pragma unroll
+              for (int w = 0; w < kWaves; ++w) b_acc += sh.bsum[w];
+            }
+            u_acc += d;
           }
           if (last_sub) {
-            const int t = t0 + tid;
-            if (t < a.T) {
-              const size_t at = ((size_t)b * a.Hkv + h) * a.T + t;
-              if constexpr (kind == kDotQ) {
-                p.u[at] = u_acc;
-                p.b[at] = b_acc;
-              } else {
-                p.c[at] = b_acc;
-              }
-            }
+            if (t0 + tid < a.T) p.u[((size_t)b * a.Hkv + h) * a.T + t0 + tid] = u_acc;
+            if (kind == kDotQ && tid == 0) p.b[((size_t)b * a.Hkv + h) * c_all + c] = b_acc;
             u_acc = b_acc = 0.0f;
           }
         }
@@ -604,33 +608,27 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
         const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)out, 0, 0x7fffffff, 0x00027000);
         const int ln = fresh(lane2), l15 = ln & 15, g4 = (ln >> 4) * 4;
         const uint32_t off = (uint32_t)(l15 * pitch + col0 + g4) * (uint32_t)sizeof(Elt);
+        if (t0 + kChunk > n)                    // tokens behind the row's end
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (t0 + m * 16 + l15 >= n) O[m] = f32x4{0, 0, 0, 0};
+        const int cols = p.dv - (col0 + g4);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const int t = t0 + m * 16 + l15;
+          const int left = t0 + m * 16 + l15 < a.T ? cols : 0;
+          // what is not there goes past the buffer's end, where stores are dropped
+          if constexpr (kVec) {
+            const uint32_t at = left > 0 ? off + (uint32_t)(m * 16 * pitch) * (uint32_t)sizeof(Elt) : 0x80000000u;
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+            if constexpr (kBf16)
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(O[m][0], O[m][1]), pack_bf16(O[m][2], O[m][3])}, rsrc, at, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[m]), rsrc, at, 0, 0);
+          } else {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int left = t < a.T ? p.dv - (col0 + nt * 16 + g4) : 0;
-            Elt v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float f = t < n ? O[m][nt][r] : 0.0f;
-              if constexpr (kBf16) v[r] = f32_to_bf16(f); else v[r] = f;
-            }
-            // what is not there goes past the buffer's end, where stores are dropped
-            if constexpr (kVec) {
-              const uint32_t at = left > 0 ? off + (uint32_t)(m * 16 * pitch + nt * 16) * (uint32_t)sizeof(Elt) : 0x80000000u;
-              if constexpr (kBf16) {
-                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), rsrc, at, 0, 0);
-              } else {
-                typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, at, 0, 0);
-              }
-            } else {
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (r < left) out[(m * 16 + l15) * pitch + col0 + g4 + nt * 16 + r] = v[r];
-            }
+            for (int r = 0; r < 4; ++r)
+              if (r < left) Elem<kBf16>::store(out + (m * 16 + l15) * pitch + col0 + g4 + r, O[m][r]);
           }
         }
       }
@@ -641,27 +639,18 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
       if (p.nkv == 1 || sub == 0) {
         const float total = wt.total;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) S[kt][nt] *= total;
+        for (int kt = 0; kt < KT; ++kt) S[kt] *= total;
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float* wp = wt.upd + k * 32 + g4 * 2;
-        float w[8];
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = wp[e];
-        Split<kBf16, 3> wz[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if constexpr (kBf16) v[e] = w[e] * (float)zf[k][nt][e]; else v[e] = w[e] * zf[k][nt].v[e];
-          }
-          wz[nt] = Split<kBf16, 3>(v);
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (kBf16) v[e] = wp[e] * (float)zf[k][e]; else v[e] = wp[e] * zf[k].v[e];
         }
-        constexpr int KG = kBf16 ? 4 : 2;     // row tiles at a time
+        const Split<kBf16, 3> wz(v);
+        constexpr int KG = kDots ? 2 : 4;     // row tiles at a time
 #pragma unroll
         for (int kt = 0; kt < KT; kt += KG) {
           Frag yf[KG];
@@ -670,9 +659,7 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
 #pragma unroll
           for (int part = (kBf16 ? 3 : 1); part--;)
 #pragma unroll
-            for (int q = 0; q < KG; ++q)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) S[kt + q][nt] = M::mul(yf[q], wz[nt].part[part], S[kt + q][nt]);
+            for (int q = 0; q < KG; ++q) S[kt + q] = M::mul(yf[q], wz.part[part], S[kt + q]);
         }
       }
     }
@@ -690,23 +677,16 @@ __global__ void __launch_bounds__(kThreads, kBf16 ? 2 : 1) chunk_kernel(RoleArgs
           ((Elt*)p.o)[(((size_t)b * a.T + t) * a.Hkv + h) * p.nq * p.dv + j] = Elt(0);
         }
       if constexpr (kDots)
-        for (int t = tid; t < rows; t += kThreads) {
-          const size_t at = ((size_t)b * a.Hkv + h) * a.T + t0 + t;
-          if constexpr (kind == kDotQ)
-            p.u[at] = p.b[at] = 0.0f;
-          else
-            p.c[at] = 0.0f;
-        }
+        for (int t = tid; t < rows; t += kThreads) p.u[((size_t)b * a.Hkv + h) * a.T + t0 + t] = 0.0f;
+      if (kind == kDotQ && tid == 0) p.b[((size_t)b * a.Hkv + h) * c_all + c] = 0.0f;
     }
   }
   if (p.s_out)
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (s_in_range(kt, nt, r)) p.s_out[s_at(kt, nt, r)] = S[kt][nt][r];
+          if (s_in_range(kt, r)) p.s_out[s_at(kt, r)] = S[kt][r];
   if (kind == kSum && p.seg_decay && tid == 0) p.seg_decay[blockIdx.x] = __builtin_amdgcn_exp2f((float)seg_log);
 }
 
@@ -719,7 +699,7 @@ hipError_t launch_chunk(const RoleArgs& p, hipStream_t st) {
     static const hipError_t raised = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (raised != hipSuccess) return raised;
   }
-  fn<<<(unsigned)p.a.B * p.a.Hkv * p.nseg, kThreads, lds, st>>>(p);
+  fn<<<(unsigned)p.a.B * p.a.Hkv * p.nseg, DV * 4, lds, st>>>(p);
   return hipGetLastError();
 }
 
