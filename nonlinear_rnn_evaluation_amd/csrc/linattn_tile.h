@@ -173,6 +173,9 @@ __device__ __forceinline__ int fresh(int v) {
 }
 
 // ---- tiles ---------------------------------------------------------------------------------
+template <bool kBf16, int kCols, int kThreads>
+struct Direct;
+
 template <bool kBf16>
 constexpr int pitch_of(int cols) { return cols + Mma<kBf16>::kPad; }
 
@@ -222,6 +225,52 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < kN; ++i) *(uint4*)(at + i * (kThreads / kPerRow) * kPitch) = v[i];
   }
+  __device__ __forceinline__ void store_permuted(Elt* tile) const {      // as a Direct tile
+    const int tid = fresh(threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      *(uint4*)(tile + Direct<kBf16, kCols, kThreads>::at(tid / kPerRow + i * (kThreads / kPerRow), tid % kPerRow)) = v[i];
+  }
+};
+
+// 64 rows x kCols without padding, the 16-byte pieces of a row permuted by the row so that 16 rows of
+// one piece spread over the banks: the form that loads can fill without passing through
+// registers, whose lanes write to consecutive addresses.
+template <bool kBf16, int kCols, int kThreads>
+struct Direct {
+  using M = Mma<kBf16>;
+  using Elt = typename M::Elt;
+  static constexpr int kPerRow = kCols / M::kPiece;
+  static __device__ __forceinline__ int permute(int row) { return kPerRow >= 16 ? row & 15 : row >> 1 & 7; }
+  // first element of a row's piece
+  static __device__ __forceinline__ int at(int row, int piece) { return (row * kPerRow + (piece ^ permute(row))) * M::kPiece; }
+  static __device__ __forceinline__ typename M::Frag rows(const Elt* t, int row, int k, int g) {       // natural order
+    if constexpr (kBf16) return M::rows(t + at(row, k * 4 + g));
+    else return M::two(t + at(row, k * 8 + g * 2), t + at(row, k * 8 + g * 2 + 1));
+  }
+  static __device__ __forceinline__ typename M::Frag rows_split(const Elt* t, int row, int k, int g) {
+    if constexpr (kBf16) {
+      struct { uint2 a, b; } w{*(const uint2*)(t + at(row, k * 4 + g / 2) + g % 2 * 4),
+                               *(const uint2*)(t + at(row, k * 4 + 2 + g / 2) + g % 2 * 4)};
+      return __builtin_bit_cast(typename M::Frag, w);
+    } else {
+      return M::two(t + at(row, k * 8 + g), t + at(row, k * 8 + 4 + g));
+    }
+  }
+  // rows t0 .. t0 + 63 as Stage::load takes them, straight to LDS; complete once vmcnt says so
+  static __device__ __forceinline__ void load(const Rows& r, int b, int h, int t0, int n, int cols, Elt* tile, int wave) {
+    const Elt* base = (const Elt*)r.p + b * r.sb + h * r.sh + t0 * r.st;
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7fffffff, 0x00027000);
+    const uint32_t pitch = (uint32_t)r.st * (uint32_t)sizeof(Elt);
+    const int tid = fresh(threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < kChunk * kPerRow / kThreads; ++i) {
+      const int q = i * kThreads + tid, row = q / kPerRow, c = ((q % kPerRow) ^ permute(row)) * M::kPiece;
+      const bool in = t0 + row < n && c < cols;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(tile + (i * kThreads + wave * 64) * M::kPiece),
+                                               16, in ? row * pitch + c * (uint32_t)sizeof(Elt) : 0x80000000u, 0, 0, 0);
+    }
+  }
 };
 
 // x of the lanes that a DPP move brings together, 0 where it brings nothing
@@ -267,26 +316,13 @@ __device__ __forceinline__ typename Mma<kBf16>::Frag score_rows(const typename M
   else return Mma<false>::two(p + score_at<false>(i, j), p + score_at<false>(i, j + 4));
 }
 
-// LDS of one block (bf16, 128 x 128: two blocks a CU, also with the dot products' arrays).
-template <bool kBf16, int DK, int DV, Kind kind>
-struct Shared {
-  using Elt = typename Mma<kBf16>::Elt;
-  static constexpr bool kSumOnly = kind == kSum, kDots = kind == kDotQ || kind == kDotK;
-  alignas(16) Elt x[kSumOnly ? 1 : kChunk * pitch_of<kBf16>(DK)];
-  alignas(16) Elt y[kChunk * pitch_of<kBf16>(DK)];
-  alignas(16) Elt z[kChunk * pitch_of<kBf16>(DV)];
-  alignas(16) Elt e[kDots ? kChunk * pitch_of<kBf16>(DV) : 1];
-  alignas(16) Elt p[kSumOnly ? 1 : kChunk * kChunk];   // scores [i][j], see score_at
-  struct alignas(16) Weights {
-    float ghi[kChunk];                 // G in units of log2, as the sum of a float
-    uint16_t glo[kChunk];              // ... and a bf16
-    float upd[kChunk];                 // the weights of y z^T
-    float total;                       // exp(G_C)
-    float end_hi, end_lo;              // G_C
-  } w[2];                              // this chunk's and the next one's
-  float dot[kDots ? DV / 16 : 1][kChunk];      // the waves' parts of dot products and row sums
-  float bsum[kDots ? DV / 16 : 1];
-  float col[kind == kDotQ ? 10 : 1][16];       // column sums of the score tiles on and below the diagonal
+// A chunk's weights.
+struct alignas(16) Weights {
+  float ghi[kChunk];                 // G in units of log2, as the sum of a float
+  uint16_t glo[kChunk];              // ... and a bf16
+  float upd[kChunk];                 // the weights of y z^T
+  float total;                       // exp(G_C)
+  float end_hi, end_lo;              // G_C
 };
 
 // A block walks the chunks of one segment of one state head, with the state in accumulators: a
@@ -310,9 +346,18 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   constexpr int PK = pitch_of<kBf16>(DK), PV = pitch_of<kBf16>(DV);
   constexpr bool kDots = kind == kDotQ || kind == kDotK;
   constexpr int kParts = kDots ? 3 : 1;
-  using Sh = Shared<kBf16, DK, DV, kind>;
-  extern __shared__ __align__(16) char smem[];
-  Sh& sh = *(Sh*)smem;
+  constexpr bool kAll = kind != kSum;
+  // LDS (bf16, 128 x 128: two blocks a CU, also with the dot products' arrays).  Arrays of their own,
+  // so that a read of one need not wait for loads on their way to another.
+  __shared__ alignas(16) Elt lds_x[kAll ? kChunk * DK : 1];           // Direct
+  __shared__ alignas(16) Elt lds_y[kChunk * PK];
+  __shared__ alignas(16) Elt lds_z[kChunk * PV];
+  __shared__ alignas(16) Elt lds_e[kDots ? kChunk * DV : 1];          // Direct
+  __shared__ alignas(16) Elt lds_p[kAll ? kChunk * kChunk : 1];       // scores [i][j], see score_at
+  __shared__ Weights lds_w[2];                                        // this chunk's and the next one's
+  __shared__ float lds_dot[kDots ? kWaves : 1][kChunk];               // the waves' parts of dot products and row sums
+  __shared__ float lds_bsum[kDots ? kWaves : 1];
+  __shared__ float lds_col[kind == kDotQ ? 10 : 1][16];               // column sums of the score tiles up to the diagonal
 
   const LinAttn& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l15 = lane & 15, g4 = (lane >> 4) * 4;
@@ -355,23 +400,29 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
           for (int r = 0; r < 4; ++r)
             if (s_in_range(kt, r)) s += S[kt][r] * after[s_at(kt, r)];
       s = row16_sum(group_sum(s));
-      if (lane == 0) sh.bsum[wave] = s;
+      if (lane == 0) lds_bsum[wave] = s;
       __syncthreads();
       if (tid == 0) {
         s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) s += sh.bsum[w];
+        for (int w = 0; w < kWaves; ++w) s += lds_bsum[w];
         p.x_end[blockIdx.x] = s;
       }
     }
   }
 
+  using TX = Direct<kBf16, DK, kThreads>;
+  using TE = Direct<kBf16, DV, kThreads>;
   Stage<kBf16, DK, kThreads> sx, sy;
   Stage<kBf16, DV, kThreads> sz, se;
   float g_next = 0.0f;
   auto fetch = [&](int c, int sub) {
     const int t0 = c * kChunk;
-    if constexpr (kind != kSum)
+    if (sub == 0 && wave == 0) {
+      const int t = min(t0 + lane, n - 1);
+      g_next = a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h];
+    }
+    if constexpr (kind != kSum && !kVec)
       if (p.nq > 1 || sub == 0) {
         sx.template load<kVec>(p.x, b, h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dk);
         if constexpr (kDots) se.template load<kVec>(p.e, b, h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dv);
@@ -381,22 +432,28 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       sy.template load<kVec>(p.y, b, hh, t0, n, p.dk);
       sz.template load<kVec>(p.z, b, hh, t0, n, p.dv);
     }
-    if (sub == 0 && wave == 0) {
-      const int t = t0 + lane;
-      g_next = t < n ? clamp_log_decay(a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h]) : 0.0f;
-    }
   };
 
   double seg_log = 0.0;                       // wave 0: log2 of the segment's decay
+  // X and E are done with once the first half of a chunk is: aligned rows go straight to them then
+  auto fetch_direct = [&](int c, int sub) {
+    if constexpr (kind != kSum && kVec)
+      if (p.nq > 1 || sub == 0) {
+        const int hh = h * p.nq + (p.nq > 1 ? sub : 0), t0 = c * kChunk;
+        TX::load(p.x, b, hh, t0, n, p.dk, lds_x, wave);
+        if constexpr (kDots) TE::load(p.e, b, hh, t0, n, p.dv, lds_e, wave);
+      }
+  };
   // Wave 0 turns the log decays that it fetched into a chunk's weights.  G is an inclusive scan in
   // 64 bits, because differences of sums of log decays (each down to -104) are what counts.
-  auto weigh = [&](int slot) {
-    const double x = wave_scan((double)g_next * 1.4426950408889634);
+  auto weigh = [&](int c, int slot) {
+    const float g = c * kChunk + lane < n ? clamp_log_decay(g_next) : 0.0f;
+    const double x = wave_scan((double)g * 1.4426950408889634);
     const uint64_t last = __builtin_bit_cast(uint64_t, x);
     const double end = __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(last >> 32), 63) << 32 |
                                                       (uint32_t)__builtin_amdgcn_readlane((uint32_t)last, 63));
     const float hi = (float)x, end_hi = (float)end;
-    auto& w = sh.w[slot];
+    auto& w = lds_w[slot];
     w.ghi[lane] = hi;
     w.glo[lane] = f32_to_bf16((float)(x - (double)hi));
     w.upd[lane] = __builtin_amdgcn_exp2f(kReverse ? hi : (float)(end - x)) * p.upd_scale;
@@ -408,31 +465,37 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   };
   const int count = live > c_lo ? (live - c_lo) * nsub : 0;
   if (count > 0) {
+    fetch_direct(kReverse ? live - 1 : c_lo, 0);
     fetch(kReverse ? live - 1 : c_lo, 0);
-    if (wave == 0) weigh(0);
+    if (wave == 0) weigh(kReverse ? live - 1 : c_lo, 0);
   }
   float u_acc = 0.0f, b_acc = 0.0f;           // threads 0..63 (kDots): sums over the query heads
   f32x4 O[4];
 
   for (int it = 0; it < count; ++it) {
     const int step = it / nsub, sub = it % nsub, c = kReverse ? live - 1 - step : c_lo + step, t0 = c * kChunk;
-    const auto& wt = sh.w[step & 1];
+    const auto& wt = lds_w[step & 1];
     const bool last_sub = sub == nsub - 1;
     const bool new_x = p.nq > 1 || sub == 0, new_yz = p.nkv > 1 || sub == 0;
     __syncthreads();
-    if constexpr (kind != kSum)
+    if constexpr (kind != kSum && !kVec)
       if (new_x) {
-        sx.store(sh.x);
-        if constexpr (kDots) se.store(sh.e);
+        sx.store_permuted(lds_x);
+        if constexpr (kDots) se.store_permuted(lds_e);
       }
     if (new_yz) {
-      sy.store(sh.y);
-      sz.store(sh.z);
+      sy.store(lds_y);
+      sz.store(lds_z);
     }
-    auto fetch_next = [&] {
-      if (it + 1 < count) fetch(kReverse ? live - 1 - (it + 1) / nsub : c_lo + (it + 1) / nsub, (it + 1) % nsub);
-    };
-    if constexpr (kind == kSum) fetch_next();
+    const int next_sub = last_sub ? 0 : sub + 1, next_c = last_sub ? (kReverse ? c - 1 : c + 1) : c;
+    if constexpr (kind == kSum)
+      if (it + 1 < count) fetch(next_c, next_sub);
+    if constexpr (kind != kSum && kVec) {
+      // this thread's loads to LDS have landed; after the barrier, everyone's
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_s_waitcnt(0x0F70);
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    }
     __syncthreads();
 
     if constexpr (kind != kSum) {
@@ -446,16 +509,16 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         for (int q = 0; q < JT; ++q) P[q] = A[q] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < DK / 32; ++k) {
-          const Frag xf = M::rows(sh.x + i * PK + k * 32 + g4 * 2);
+          const Frag xf = TX::rows(lds_x, i, k, g4 / 4);
 #pragma unroll
-          for (int q = 0; q < JT; ++q) P[q] = M::mul(M::rows(sh.y + ((jt0 + q) * 16 + l15) * PK + k * 32 + g4 * 2), xf, P[q]);
+          for (int q = 0; q < JT; ++q) P[q] = M::mul(M::rows(lds_y + ((jt0 + q) * 16 + l15) * PK + k * 32 + g4 * 2), xf, P[q]);
         }
         if constexpr (kind == kDotQ) {
 #pragma unroll
           for (int k = 0; k < DV / 32; ++k) {
-            const Frag ef = M::rows(sh.e + i * PV + k * 32 + g4 * 2);
+            const Frag ef = TE::rows(lds_e, i, k, g4 / 4);
 #pragma unroll
-            for (int q = 0; q < JT; ++q) A[q] = M::mul(M::rows(sh.z + ((jt0 + q) * 16 + l15) * PV + k * 32 + g4 * 2), ef, A[q]);
+            for (int q = 0; q < JT; ++q) A[q] = M::mul(M::rows(lds_z + ((jt0 + q) * 16 + l15) * PV + k * 32 + g4 * 2), ef, A[q]);
           }
         }
         const float gi = wt.ghi[i], gi_lo = bf16_to_f32(wt.glo[i]);
@@ -483,14 +546,14 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
                 const float t = j0 + r < i ? s[r] * A[q][r] : 0.0f;
                 row += t;
                 const float cs = row16_sum(t);
-                if (l15 == 0) sh.col[it0 * (it0 + 1) / 2 + jt][g4 + r] = cs;
+                if (l15 == 0) lds_col[it0 * (it0 + 1) / 2 + jt][g4 + r] = cs;
               }
             }
           }
           if constexpr (kBf16)
-            *(uint2*)(sh.p + score_at<true>(i, j0)) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+            *(uint2*)(lds_p + score_at<true>(i, j0)) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
           else
-            *(float4*)(sh.p + score_at<false>(i, j0)) = make_float4(s[0], s[1], s[2], s[3]);
+            *(float4*)(lds_p + score_at<false>(i, j0)) = make_float4(s[0], s[1], s[2], s[3]);
         }
         if constexpr (kind == kDotQ) row = group_sum(row);
       }
@@ -509,7 +572,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
           for (int m0 = 0; m0 < 4; m0 += MG) {
             Frag xf[MG];
 #pragma unroll
-            for (int m = 0; m < MG; ++m) xf[m] = M::rows_split(sh.x + ((m0 + m) * 16 + l15) * PK + k * 32 + g4);
+            for (int m = 0; m < MG; ++m) xf[m] = TX::rows_split(lds_x, (m0 + m) * 16 + l15, k, g4 / 4);
             // the smallest part first; products into one accumulator stand apart
 #pragma unroll
             for (int q = (kBf16 ? kParts : 1); q--;)
@@ -525,32 +588,33 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
           O[m] *= __builtin_amdgcn_exp2f(g) * p.inter_scale;
           if constexpr (kDots) {
             float d = 0.0f;
-            const Elt* er = sh.e + t * PV + col0 + g4;
+            const Elt* er = lds_e + TE::at(t, (col0 + g4) / M::kPiece) + (col0 + g4) % M::kPiece;
 #pragma unroll
             for (int r = 0; r < 4; ++r) d += O[m][r] * Elem<kBf16>::load(er + r);
             d = group_sum(d);
             sum += d;
             if constexpr (kind == kDotQ) d += m == it0 ? row : 0.0f;
-            if (lane < 16) sh.dot[wave][t] = d;
+            if (lane < 16) lds_dot[wave][t] = d;
           }
         }
         if constexpr (kind == kDotQ) {
           sum = row16_sum(sum);
-          if (lane == 0) sh.bsum[wave] = sum;
+          if (lane == 0) lds_bsum[wave] = sum;
         }
       }
       // the next tiles are on their way during the rest of the chunk (asked for any earlier, they
       // would share the registers with the products above and spill)
       __builtin_amdgcn_sched_barrier(0);
-      fetch_next();
+      if (it + 1 < count) fetch(next_c, next_sub);
       __syncthreads();
+      if (it + 1 < count) fetch_direct(next_c, next_sub);
     }
 
     // ---- the wave's columns of Z, all 64 rows
     const int lane2 = fresh(lane), l15 = lane2 & 15, g4 = (lane2 >> 4) * 4;
     Frag zf[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) zf[k] = M::cols(sh.z, PV, k * 32, col0, lane2);
+    for (int k = 0; k < 2; ++k) zf[k] = M::cols(lds_z, PV, k * 32, col0, lane2);
 
     if constexpr (kind != kSum) {
       if (__all(M::finite(zf[0]) && M::finite(zf[1]))) {
@@ -559,7 +623,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 #pragma unroll
           for (int m = 0; m < 4; ++m)
             if (kReverse ? (k == 1 || m < 2) : (k == 0 || m >= 2))
-              O[m] = M::mul(zf[k], score_rows<kBf16>(sh.p, m * 16 + l15, k * 32 + g4 * 2), O[m]);
+              O[m] = M::mul(zf[k], score_rows<kBf16>(lds_p, m * 16 + l15, k * 32 + g4 * 2), O[m]);
       } else {
         // an infinity or a NaN among the values reaches only the outputs that may see its token:
         // a zero score times it would not be zero, so masked products are left out one by one
@@ -567,12 +631,12 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         for (int j = 0; j < kChunk; ++j) {
           float z[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) z[r] = Elem<kBf16>::load(sh.z + j * PV + col0 + g4 + r);
+          for (int r = 0; r < 4; ++r) z[r] = Elem<kBf16>::load(lds_z + j * PV + col0 + g4 + r);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int i = m * 16 + l15;
             if (kReverse ? j >= i : j <= i) {
-              const float s = Elem<kBf16>::load(sh.p + score_at<kBf16>(i, j & ~3) + (j & 3));
+              const float s = Elem<kBf16>::load(lds_p + score_at<kBf16>(i, j & ~3) + (j & 3));
 #pragma unroll
               for (int r = 0; r < 4; ++r) O[m][r] = fmaf(s, z[r], O[m][r]);
             }
@@ -584,14 +648,14 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
           if (new_x) {
             float d = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) d += sh.dot[w][tid];
+            for (int w = 0; w < kWaves; ++w) d += lds_dot[w][tid];
             if constexpr (kind == kDotQ) {
               const int jt = tid >> 4;
 #pragma unroll
               for (int w = 0; w < 4; ++w)
-                if (w >= jt) d -= sh.col[w * (w + 1) / 2 + jt][tid & 15];
+                if (w >= jt) d -= lds_col[w * (w + 1) / 2 + jt][tid & 15];
 #pragma unroll
-              for (int w = 0; w < kWaves; ++w) b_acc += sh.bsum[w];
+              for (int w = 0; w < kWaves; ++w) b_acc += lds_bsum[w];
             }
             u_acc += d;
           }
@@ -655,7 +719,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         for (int kt = 0; kt < KT; kt += KG) {
           Frag yf[KG];
 #pragma unroll
-          for (int q = 0; q < KG; ++q) yf[q] = M::cols(sh.y, PK, k * 32, (kt + q) * 16, lane2);
+          for (int q = 0; q < KG; ++q) yf[q] = M::cols(lds_y, PK, k * 32, (kt + q) * 16, lane2);
 #pragma unroll
           for (int part = (kBf16 ? 3 : 1); part--;)
 #pragma unroll
@@ -664,7 +728,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       }
     }
     // the next chunk's weights, where no other wave waits for them
-    if (last_sub && it + 1 < count && wave == 0) weigh(~step & 1);
+    if (last_sub && it + 1 < count && wave == 0) weigh(next_c, ~step & 1);
   }
 
   // ---- chunks without tokens: zeros
@@ -692,14 +756,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 
 template <bool kBf16, int DK, int DV, bool kReverse, Kind kind, bool kVec>
 hipError_t launch_chunk(const RoleArgs& p, hipStream_t st) {
-  constexpr size_t lds = sizeof(Shared<kBf16, DK, DV, kind>);
-  static_assert(lds <= 160 * 1024, "LDS of a block");
-  const auto fn = chunk_kernel<kBf16, DK, DV, kReverse, kind, kVec>;
-  if constexpr (lds > 64 * 1024) {
-    static const hipError_t raised = hipFuncSetAttribute((const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (raised != hipSuccess) return raised;
-  }
-  fn<<<(unsigned)p.a.B * p.a.Hkv * p.nseg, DV * 4, lds, st>>>(p);
+  chunk_kernel<kBf16, DK, DV, kReverse, kind, kVec><<<(unsigned)p.a.B * p.a.Hkv * p.nseg, DV * 4, 0, st>>>(p);
   return hipGetLastError();
 }
 
