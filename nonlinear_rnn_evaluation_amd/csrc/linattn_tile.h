@@ -54,11 +54,13 @@ struct RoleArgs {
 };
 
 // ---- fragments ---------------------------------------------------------------------------
-// An MFMA operand covers 16 rows (or columns) x 32 of the summed index: lane l holds row
-// l & 15 and eight summed indexes, those of its group g = l >> 4.  Which eight is free as long
-// as both operands agree: "natural" is 8 g + e; "split" is 4 g + e (e < 4) and 16 + 4 g + e - 4, the
-// order in which two stacked accumulator tiles hold their rows, so that a state in
-// accumulators is an operand without leaving its registers.
+// An MFMA operand covers 16 rows (or columns) x 32 of the summed index: lane l holds row l & 15 and
+// the eight summed indexes 8 g + e of its group g = l >> 4.  An accumulator tile holds rows
+// 4 g + r.  So that the state, kept in accumulators, is an operand without leaving its registers,
+// row m of its tile kt stands for row state_row(kt, m) of S: the eight values that a
+// lane holds in tiles 2 k and 2 k + 1 are then rows 32 k + 8 g + 0 .. 7.
+__device__ __forceinline__ int state_row(int kt, int m) { return kt / 2 * 32 + m / 4 * 8 + kt % 2 * 4 + m % 4; }
+
 template <bool kBf16>
 struct Mma;
 
@@ -67,31 +69,23 @@ struct Mma<true> {
   using Elt = uint16_t;
   using Frag = bf16x8;
   static constexpr int kPiece = 8;     // elements of a 16-byte piece
-  static constexpr int kPad = 8;       // elements of padding a row: rows start 4 banks apart
+  static constexpr int kPadY = 24, kPadZ = 8;   // elements of padding a row: rows start 12 and 4 banks apart
   static __device__ __forceinline__ f32x4 mul(Frag a, Frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
   static __device__ __forceinline__ Frag rows(const Elt* p) { return *(const Frag*)p; }
-  static __device__ __forceinline__ Frag rows_split(const Elt* p) {
-    struct { uint2 a, b; } w{*(const uint2*)p, *(const uint2*)(p + 16)};
-    return __builtin_bit_cast(Frag, w);
-  }
-  // eight rows (natural order) of one column: two transposing reads of 4 rows x 16 columns, for
-  // which lane i of a group points at row i / 4, columns 4 (i % 4) .. + 3
+  // Eight rows of one column: two transposing reads of 4 rows x 16 columns, for which lane i of a
+  // group points at row i / 4 and the four columns from col0 + kStride (i % 4) on; lane l receives
+  // column l of the 16.
+  template <int kStride>
   static __device__ __forceinline__ Frag cols(const Elt* tile, int pitch, int row0, int col0, int lane) {
-    const Elt* p = tile + (row0 + (lane >> 4) * 8 + ((lane >> 2) & 3)) * pitch + col0 + (lane & 3) * 4;
+    const Elt* p = tile + (row0 + (lane >> 4) * 8 + ((lane >> 2) & 3)) * pitch + col0 + (lane & 3) * kStride;
     using L = __attribute__((address_space(3))) s16x4;
     struct { s16x4 a, b; } w{__builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)p),
                              __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + 4 * pitch))};
     return __builtin_bit_cast(Frag, w);
   }
-  static __device__ __forceinline__ bool finite(Frag f) {
-    struct W { uint32_t w[4]; } w = __builtin_bit_cast(W, f);
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m |= (w.w[i] & 0x7f807f80u) + 0x00800080u;
-    return (m & 0x80008000u) == 0;
-  }
+  static __device__ __forceinline__ Frag none() { return Frag{}; }
 };
 
 template <>
@@ -99,7 +93,7 @@ struct Mma<false> {
   using Elt = float;
   struct Frag { float v[8]; };
   static constexpr int kPiece = 4;
-  static constexpr int kPad = 4;
+  static constexpr int kPadY = 4, kPadZ = 4;
   static __device__ __forceinline__ f32x4 mul(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
@@ -113,20 +107,15 @@ struct Mma<false> {
     return f;
   }
   static __device__ __forceinline__ Frag rows(const Elt* p) { return two(p, p + 4); }
-  static __device__ __forceinline__ Frag rows_split(const Elt* p) { return two(p, p + 16); }
+  template <int kStride>
   static __device__ __forceinline__ Frag cols(const Elt* tile, int pitch, int row0, int col0, int lane) {
     Frag f;
-    const Elt* p = tile + (row0 + (lane >> 4) * 8) * pitch + col0 + (lane & 15);
+    const Elt* p = tile + (row0 + (lane >> 4) * 8) * pitch + col0 + ((lane >> 2) & 3) * kStride + (lane & 3);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f.v[e] = p[e * pitch];
     return f;
   }
-  static __device__ __forceinline__ bool finite(const Frag& f) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m |= (__float_as_uint(f.v[e]) & 0x7f800000u) + 0x00800000u;
-    return (m & 0x80000000u) == 0;
-  }
+  static __device__ __forceinline__ Frag none() { return Frag{}; }
 };
 
 // Eight fp32 values as an operand: in fp32 as they are; in bf16 as the sum of kParts bf16 values,
@@ -176,48 +165,70 @@ __device__ __forceinline__ int fresh(int v) {
 template <bool kBf16, int kCols, int kThreads>
 struct Direct;
 
+// A buffer from p on, of any length: offsets from kNowhere on lie behind its end, where loads give
+// zeros and stores are dropped.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, 0x7fffffff, 0x00027000);
+}
+
+// The rows of one batch row and head.
 template <bool kBf16>
-constexpr int pitch_of(int cols) { return cols + Mma<kBf16>::kPad; }
+struct Source {
+  using Elt = typename Mma<kBf16>::Elt;
+  const Elt* p;
+  int64_t st;
+  uint32_t pitch;        // st in bytes, where 64 rows span less than 2^31 of them
+  __device__ __forceinline__ Source(const Rows& r, int b, int h)
+      : p((const Elt*)r.p + b * r.sb + h * r.sh), st(r.st), pitch((uint32_t)r.st * (uint32_t)sizeof(Elt)) {}
+  __device__ __forceinline__ const Elt* at(int t) const { return p + t * st; }
+};
 
 // 64 rows x kCols of one operand on its way from memory to LDS: 16-byte pieces in registers.
-template <bool kBf16, int kCols, int kThreads>
+template <bool kBf16, int kCols, int kThreads, int kPitch>
 struct Stage {
   using M = Mma<kBf16>;
   using Elt = typename M::Elt;
   static constexpr int kPerRow = kCols / M::kPiece;
   static constexpr int kN = kChunk * kPerRow / kThreads;
-  static constexpr int kPitch = pitch_of<kBf16>(kCols);
   uint4 v[kN];
 
-  // Rows t0 .. t0 + 63 of batch row b and head h; rows at or past n and columns past `cols` are
-  // zeros.  kVec: every piece is one aligned buffer load from a uniform base, and 64 rows span
-  // less than 2^31 bytes; a piece that is not there gets an offset past the buffer's end, which
-  // reads as zeros without a branch.
+  // Rows t0 .. t0 + 63; rows at or past n and columns past `cols` are zeros.  kVec: every piece is
+  // one aligned buffer load from a uniform base, and 64 rows span less than 2^31 bytes; a piece
+  // that is not there gets an offset past the buffer's end, which reads as zeros without a branch.
   template <bool kVec>
-  __device__ __forceinline__ void load(const Rows& r, int b, int h, int t0, int n, int cols) {
+  __device__ __forceinline__ void load(const Source<kBf16>& src, uint32_t off, int t0, int n, int cols) {
     constexpr int kStep = kThreads / kPerRow;            // rows between a thread's pieces
-    const Elt* base = (const Elt*)r.p + b * r.sb + h * r.sh + t0 * r.st;
-    const int tid = fresh(threadIdx.x), row = tid / kPerRow, c = (tid % kPerRow) * M::kPiece;
+    const Elt* base = src.at(t0);
     if constexpr (kVec) {
-      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7fffffff, 0x00027000);
-      const uint32_t pitch = (uint32_t)r.st * (uint32_t)sizeof(Elt);
-      const uint32_t off = row * pitch + c * (uint32_t)sizeof(Elt);
-      const int left = c < cols ? n - t0 - row : 0;
+      const __amdgpu_buffer_rsrc_t rsrc = buffer_at(base);
+      if (t0 + kChunk <= n) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             rsrc, left > i * kStep ? off + i * kStep * pitch : 0x80000000u, 0, 0));
+        for (int i = 0; i < kN; ++i)
+          v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, i * kStep * src.pitch, 0));
+      } else {
+        const int left = n - t0 - (int)fresh(threadIdx.x) / kPerRow;
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          v[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, left > i * kStep ? off : kNowhere, i * kStep * src.pitch, 0));
+      }
     } else {
+      const int tid = fresh(threadIdx.x), row = tid / kPerRow, c = (tid % kPerRow) * M::kPiece;
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         Elt e[M::kPiece];
         const bool live = t0 + row + i * kStep < n;
-        const Elt* src = base + (row + i * kStep) * r.st + c;
+        const Elt* from = base + (row + i * kStep) * src.st + c;
 #pragma unroll
-        for (int k = 0; k < M::kPiece; ++k) e[k] = live && c + k < cols ? src[k] : Elt(0);
+        for (int k = 0; k < M::kPiece; ++k) e[k] = live && c + k < cols ? from[k] : Elt(0);
         __builtin_memcpy(&v[i], e, 16);
       }
     }
+  }
+  // byte offset of a thread's first piece from its chunk's base
+  static __device__ __forceinline__ uint32_t offset(uint32_t pitch, int cols) {
+    const int tid = threadIdx.x, c = (tid % kPerRow) * M::kPiece;
+    return c < cols ? tid / kPerRow * pitch + c * (uint32_t)sizeof(Elt) : kNowhere;
   }
   __device__ __forceinline__ void store(Elt* tile) const {
     const int tid = fresh(threadIdx.x);
@@ -241,35 +252,27 @@ struct Direct {
   using M = Mma<kBf16>;
   using Elt = typename M::Elt;
   static constexpr int kPerRow = kCols / M::kPiece;
-  static __device__ __forceinline__ int permute(int row) { return kPerRow >= 16 ? row & 15 : row >> 1 & 7; }
+  static constexpr int kStep = kThreads / kPerRow;       // rows between a thread's pieces, which one permutation serves
+  static __device__ __forceinline__ int permute(int row) { return kPerRow >= 16 ? row & (kStep >= 16 ? 15 : 7) : row >> 1 & 7; }
+  static_assert(kStep % (kPerRow < 16 || kStep >= 16 ? 16 : 8) == 0, "one permutation for all of a thread's rows");
   // first element of a row's piece
   static __device__ __forceinline__ int at(int row, int piece) { return (row * kPerRow + (piece ^ permute(row))) * M::kPiece; }
-  static __device__ __forceinline__ typename M::Frag rows(const Elt* t, int row, int k, int g) {       // natural order
+  static __device__ __forceinline__ typename M::Frag rows(const Elt* t, int row, int k, int g) {
     if constexpr (kBf16) return M::rows(t + at(row, k * 4 + g));
     else return M::two(t + at(row, k * 8 + g * 2), t + at(row, k * 8 + g * 2 + 1));
   }
-  static __device__ __forceinline__ typename M::Frag rows_split(const Elt* t, int row, int k, int g) {
-    if constexpr (kBf16) {
-      struct { uint2 a, b; } w{*(const uint2*)(t + at(row, k * 4 + g / 2) + g % 2 * 4),
-                               *(const uint2*)(t + at(row, k * 4 + 2 + g / 2) + g % 2 * 4)};
-      return __builtin_bit_cast(typename M::Frag, w);
-    } else {
-      return M::two(t + at(row, k * 8 + g), t + at(row, k * 8 + 4 + g));
-    }
-  }
   // rows t0 .. t0 + 63 as Stage::load takes them, straight to LDS; complete once vmcnt says so
-  static __device__ __forceinline__ void load(const Rows& r, int b, int h, int t0, int n, int cols, Elt* tile, int wave) {
-    const Elt* base = (const Elt*)r.p + b * r.sb + h * r.sh + t0 * r.st;
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0x7fffffff, 0x00027000);
-    const uint32_t pitch = (uint32_t)r.st * (uint32_t)sizeof(Elt);
-    const int tid = fresh(threadIdx.x);
+  static __device__ __forceinline__ void load(const Source<kBf16>& src, uint32_t off, int t0, int n, Elt* tile, int wave) {
+    const __amdgpu_buffer_rsrc_t rsrc = buffer_at(src.at(t0));
+    const int left = t0 + kChunk <= n ? kChunk : n - t0 - (int)fresh(threadIdx.x) / kPerRow;
 #pragma unroll
-    for (int i = 0; i < kChunk * kPerRow / kThreads; ++i) {
-      const int q = i * kThreads + tid, row = q / kPerRow, c = ((q % kPerRow) ^ permute(row)) * M::kPiece;
-      const bool in = t0 + row < n && c < cols;
+    for (int i = 0; i < kChunk / kStep; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(tile + (i * kThreads + wave * 64) * M::kPiece),
-                                               16, in ? row * pitch + c * (uint32_t)sizeof(Elt) : 0x80000000u, 0, 0, 0);
-    }
+                                               16, left > i * kStep ? off : kNowhere, i * kStep * src.pitch, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t offset(uint32_t pitch, int cols) {
+    const int tid = threadIdx.x, row = tid / kPerRow, c = ((tid % kPerRow) ^ permute(row)) * M::kPiece;
+    return c < cols ? row * pitch + c * (uint32_t)sizeof(Elt) : kNowhere;
   }
 };
 
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   constexpr int kWaves = DV / 16, kThreads = kWaves * 64;
   constexpr int KT = DK / 16;               // row tiles of S
   constexpr int JT = 16 / kWaves;           // score tiles a wave takes of its query row tile
-  constexpr int PK = pitch_of<kBf16>(DK), PV = pitch_of<kBf16>(DV);
+  constexpr int PK = DK + M::kPadY, PV = DV + M::kPadZ;     // rows of Y and Z in LDS
   constexpr bool kDots = kind == kDotQ || kind == kDotK;
   constexpr int kParts = kDots ? 3 : 1;
   constexpr bool kAll = kind != kSum;
@@ -374,10 +377,10 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 
   f32x4 S[KT];
   auto s_at = [&](int kt, int r) {     // element (row, column) of accumulator register r
-    const int i = kt * 16 + g4 + r, j = col0 + l15;
+    const int i = state_row(kt, g4) + r, j = col0 + l15;
     return sbase + (p.transposed ? (size_t)j * p.dk + i : (size_t)i * p.dv + j);
   };
-  auto s_in_range = [&](int kt, int r) { return kt * 16 + g4 + r < p.dk && col0 + l15 < p.dv; };
+  auto s_in_range = [&](int kt, int r) { return state_row(kt, g4) + r < p.dk && col0 + l15 < p.dv; };
 #pragma unroll
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -413,8 +416,11 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 
   using TX = Direct<kBf16, DK, kThreads>;
   using TE = Direct<kBf16, DV, kThreads>;
-  Stage<kBf16, DK, kThreads> sx, sy;
-  Stage<kBf16, DV, kThreads> sz, se;
+  Stage<kBf16, DK, kThreads, PK> sx, sy;
+  Stage<kBf16, DV, kThreads, PV> sz, se;
+  const uint32_t es = sizeof(Elt);
+  const uint32_t off_x = kVec && kAll ? TX::offset((uint32_t)p.x.st * es, p.dk) : 0, off_e = kVec && kDots ? TE::offset((uint32_t)p.e.st * es, p.dv) : 0;
+  const uint32_t off_y = kVec ? decltype(sy)::offset((uint32_t)p.y.st * es, p.dk) : 0, off_z = kVec ? decltype(sz)::offset((uint32_t)p.z.st * es, p.dv) : 0;
   float g_next = 0.0f;
   auto fetch = [&](int c, int sub) {
     const int t0 = c * kChunk;
@@ -422,26 +428,27 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       const int t = min(t0 + lane, n - 1);
       g_next = a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h];
     }
-    if constexpr (kind != kSum && !kVec)
+    if constexpr (kAll && !kVec)
       if (p.nq > 1 || sub == 0) {
-        sx.template load<kVec>(p.x, b, h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dk);
-        if constexpr (kDots) se.template load<kVec>(p.e, b, h * p.nq + (p.nq > 1 ? sub : 0), t0, n, p.dv);
+        const int hh = h * p.nq + (p.nq > 1 ? sub : 0);
+        sx.template load<kVec>(Source<kBf16>(p.x, b, hh), 0, t0, n, p.dk);
+        if constexpr (kDots) se.template load<kVec>(Source<kBf16>(p.e, b, hh), 0, t0, n, p.dv);
       }
     if (p.nkv > 1 || sub == 0) {
       const int hh = h * p.nkv + (p.nkv > 1 ? sub : 0);
-      sy.template load<kVec>(p.y, b, hh, t0, n, p.dk);
-      sz.template load<kVec>(p.z, b, hh, t0, n, p.dv);
+      sy.template load<kVec>(Source<kBf16>(p.y, b, hh), off_y, t0, n, p.dk);
+      sz.template load<kVec>(Source<kBf16>(p.z, b, hh), off_z, t0, n, p.dv);
     }
   };
 
   double seg_log = 0.0;                       // wave 0: log2 of the segment's decay
   // X and E are done with once the first half of a chunk is: aligned rows go straight to them then
   auto fetch_direct = [&](int c, int sub) {
-    if constexpr (kind != kSum && kVec)
+    if constexpr (kAll && kVec)
       if (p.nq > 1 || sub == 0) {
         const int hh = h * p.nq + (p.nq > 1 ? sub : 0), t0 = c * kChunk;
-        TX::load(p.x, b, hh, t0, n, p.dk, lds_x, wave);
-        if constexpr (kDots) TE::load(p.e, b, hh, t0, n, p.dv, lds_e, wave);
+        TX::load(Source<kBf16>(p.x, b, hh), off_x, t0, n, lds_x, wave);
+        if constexpr (kDots) TE::load(Source<kBf16>(p.e, b, hh), off_e, t0, n, lds_e, wave);
       }
   };
   // Wave 0 turns the log decays that it fetched into a chunk's weights.  G is an inclusive scan in
@@ -471,6 +478,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   }
   float u_acc = 0.0f, b_acc = 0.0f;           // threads 0..63 (kDots): sums over the query heads
   f32x4 O[4];
+  const f32x4 zero = {0, 0, 0, 0};
 
   for (int it = 0; it < count; ++it) {
     const int step = it / nsub, sub = it % nsub, c = kReverse ? live - 1 - step : c_lo + step, t0 = c * kChunk;
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     const bool last_sub = sub == nsub - 1;
     const bool new_x = p.nq > 1 || sub == 0, new_yz = p.nkv > 1 || sub == 0;
     __syncthreads();
-    if constexpr (kind != kSum && !kVec)
+    if constexpr (kAll && !kVec)
       if (new_x) {
         sx.store_permuted(lds_x);
         if constexpr (kDots) se.store_permuted(lds_e);
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     const int next_sub = last_sub ? 0 : sub + 1, next_c = last_sub ? (kReverse ? c - 1 : c + 1) : c;
     if constexpr (kind == kSum)
       if (it + 1 < count) fetch(next_c, next_sub);
-    if constexpr (kind != kSum && kVec) {
+    if constexpr (kAll && kVec) {
       // this thread's loads to LDS have landed; after the barrier, everyone's
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
       __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     }
     __syncthreads();
 
-    if constexpr (kind != kSum) {
+    if constexpr (kAll) {
       // ---- scores: lane column i, four rows j a register block
       const int ln = fresh(lane), l15 = ln & 15, g4 = (ln >> 4) * 4;
       const int i = it0 * 16 + l15;
@@ -506,19 +514,17 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       if (kReverse ? jt0 + JT > it0 : jt0 <= it0) {       // some of the wave's tiles may see their keys
         f32x4 P[JT], A[JT];
 #pragma unroll
-        for (int q = 0; q < JT; ++q) P[q] = A[q] = f32x4{0, 0, 0, 0};
-#pragma unroll
         for (int k = 0; k < DK / 32; ++k) {
           const Frag xf = TX::rows(lds_x, i, k, g4 / 4);
 #pragma unroll
-          for (int q = 0; q < JT; ++q) P[q] = M::mul(M::rows(lds_y + ((jt0 + q) * 16 + l15) * PK + k * 32 + g4 * 2), xf, P[q]);
+          for (int q = 0; q < JT; ++q) P[q] = M::mul(M::rows(lds_y + ((jt0 + q) * 16 + l15) * PK + k * 32 + g4 * 2), xf, k ? P[q] : zero);
         }
         if constexpr (kind == kDotQ) {
 #pragma unroll
           for (int k = 0; k < DV / 32; ++k) {
             const Frag ef = TE::rows(lds_e, i, k, g4 / 4);
 #pragma unroll
-            for (int q = 0; q < JT; ++q) A[q] = M::mul(M::rows(lds_z + ((jt0 + q) * 16 + l15) * PV + k * 32 + g4 * 2), ef, A[q]);
+            for (int q = 0; q < JT; ++q) A[q] = M::mul(M::rows(lds_z + ((jt0 + q) * 16 + l15) * PV + k * 32 + g4 * 2), ef, k ? A[q] : zero);
           }
         }
         const float gi = wt.ghi[i], gi_lo = bf16_to_f32(wt.glo[i]);
@@ -560,8 +566,6 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       // ---- what the state gives: O^T = S^T X^T
       if (new_x) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) O[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
         for (int k = 0; k < DK / 32; ++k) {
           float v[8];
 #pragma unroll
@@ -572,12 +576,12 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
           for (int m0 = 0; m0 < 4; m0 += MG) {
             Frag xf[MG];
 #pragma unroll
-            for (int m = 0; m < MG; ++m) xf[m] = TX::rows_split(lds_x, (m0 + m) * 16 + l15, k, g4 / 4);
+            for (int m = 0; m < MG; ++m) xf[m] = TX::rows(lds_x, (m0 + m) * 16 + l15, k, g4 / 4);
             // the smallest part first; products into one accumulator stand apart
 #pragma unroll
             for (int q = (kBf16 ? kParts : 1); q--;)
 #pragma unroll
-              for (int m = 0; m < MG; ++m) O[m0 + m] = M::mul(sf.part[q], xf[m], O[m0 + m]);
+              for (int m = 0; m < MG; ++m) O[m0 + m] = M::mul(sf.part[q], xf[m], k || q + 1 < (kBf16 ? kParts : 1) ? O[m0 + m] : zero);
           }
         }
         float sum = 0.0f;
@@ -614,10 +618,13 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     const int lane2 = fresh(lane), l15 = lane2 & 15, g4 = (lane2 >> 4) * 4;
     Frag zf[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) zf[k] = M::cols(lds_z, PV, k * 32, col0, lane2);
+    for (int k = 0; k < 2; ++k) zf[k] = M::template cols<4>(lds_z, PV, k * 32, col0, lane2);
 
-    if constexpr (kind != kSum) {
-      if (__all(M::finite(zf[0]) && M::finite(zf[1]))) {
+    if constexpr (kAll) {
+      // zero times every value: a NaN where one of them is none or infinite
+      const f32x4 odd = M::mul(zf[1], M::none(), M::mul(zf[0], M::none(), zero));
+      const float sum = (odd[0] + odd[1]) + (odd[2] + odd[3]);
+      if (__all(sum == sum)) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -669,26 +676,25 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       if ((p.nq > 1 || last_sub) && p.o) {
         const int oh = h * p.nq + (p.nq > 1 ? sub : 0), pitch = a.Hkv * p.nq * p.dv;
         Elt* out = (Elt*)p.o + ((size_t)b * a.T + t0) * pitch + (size_t)oh * p.dv;
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)out, 0, 0x7fffffff, 0x00027000);
+        const __amdgpu_buffer_rsrc_t rsrc = buffer_at(out);
         const int ln = fresh(lane2), l15 = ln & 15, g4 = (ln >> 4) * 4;
         const uint32_t off = (uint32_t)(l15 * pitch + col0 + g4) * (uint32_t)sizeof(Elt);
         if (t0 + kChunk > n)                    // tokens behind the row's end
 #pragma unroll
           for (int m = 0; m < 4; ++m)
             if (t0 + m * 16 + l15 >= n) O[m] = f32x4{0, 0, 0, 0};
-        const int cols = p.dv - (col0 + g4);
+        const int cols = p.dv - (col0 + g4), rows = a.T - t0 - l15;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const int left = t0 + m * 16 + l15 < a.T ? cols : 0;
-          // what is not there goes past the buffer's end, where stores are dropped
+          const int left = m * 16 < rows ? cols : 0;
           if constexpr (kVec) {
-            const uint32_t at = left > 0 ? off + (uint32_t)(m * 16 * pitch) * (uint32_t)sizeof(Elt) : 0x80000000u;
+            const uint32_t at = left > 0 ? off : kNowhere, step = (uint32_t)(m * 16 * pitch) * es;
             typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
             typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
             if constexpr (kBf16)
-              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(O[m][0], O[m][1]), pack_bf16(O[m][2], O[m][3])}, rsrc, at, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(O[m][0], O[m][1]), pack_bf16(O[m][2], O[m][3])}, rsrc, at, step, 0);
             else
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[m]), rsrc, at, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[m]), rsrc, at, step, 0);
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -719,7 +725,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         for (int kt = 0; kt < KT; kt += KG) {
           Frag yf[KG];
 #pragma unroll
-          for (int q = 0; q < KG; ++q) yf[q] = M::cols(lds_y, PK, k * 32, (kt + q) * 16, lane2);
+          for (int q = 0; q < KG; ++q) yf[q] = M::template cols<8>(lds_y, PK, k * 32, state_row(kt + q, 0), lane2);
 #pragma unroll
           for (int part = (kBf16 ? 3 : 1); part--;)
 #pragma unroll
@@ -732,7 +738,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   }
 
   // ---- chunks without tokens: zeros
-  if constexpr (kind != kSum) {
+  if constexpr (kAll) {
     for (int c = max(live, c_lo); c < c_hi; ++c) {
       const int t0 = c * kChunk, rows = min(kChunk, a.T - t0);
       if (p.o)
