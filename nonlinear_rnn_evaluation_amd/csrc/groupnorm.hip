@@ -139,7 +139,7 @@ struct TokenPlan {
   int ppl;         // pieces a lane: 1, 2, 4 or 8; 0: the group is too wide
   int gb, nb;      // groups, and tokens, a block holds at a time
 };
-TokenPlan token_plan(int W, int groups, int V) {
+TokenPlan token_plan(int W, int groups, int V, int threads) {
   TokenPlan t{};
   const int pieces = (W + V - 1) / V;
   if (W % V || pieces > 512) return t;
@@ -147,8 +147,8 @@ TokenPlan token_plan(int W, int groups, int V) {
   while (t.lanes < pieces && t.lanes < 64) t.lanes *= 2;
   t.ppl = 1;
   while (t.ppl * t.lanes < pieces) t.ppl *= 2;
-  t.gb = groups < 256 / t.lanes ? groups : 256 / t.lanes;
-  t.nb = 256 / (t.lanes * t.gb);
+  t.gb = groups < threads / t.lanes ? groups : threads / t.lanes;
+  t.nb = threads / (t.lanes * t.gb);
   return t;
 }
 
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(256) token_kernel(TokenArgs p) {
   }
 }
 
-template <bool kBf16, bool kVec, int PPL>
-__global__ void __launch_bounds__(256) token_grad_kernel(TokenArgs p) {
+template <bool kBf16, bool kVec, int PPL, int kThreads>
+__global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenArgs p) {
   using P = Piece<kBf16, kVec>;
   constexpr int V = P::V;
   const Norm& a = p.a;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(256) token_grad_kernel(TokenArgs p) {
   }
   if (!p.part) return;
   // the block's tokens of a channel meet in LDS, in the order of their slots
-  __shared__ float red[256 * V];
+  __shared__ float red[kThreads * V];
   float* out = p.part + (size_t)blockIdx.x * 2 * a.C;
   const int width = p.t.gb * lanes;            // threads that hold one token
 #pragma unroll
@@ -325,18 +325,19 @@ __global__ void __launch_bounds__(256) token_grad_kernel(TokenArgs p) {
     }
 }
 
-// dw, db: sums of [rows][2][C] over the rows; 32 channels a block, 8 runs of rows joined in order
-__global__ void __launch_bounds__(256) param_sum_kernel(const float* part, int64_t rows, int C, float* gw, float* gb) {
-  __shared__ float red[8][32];
+// dw, db: sums of [rows][2][C] over the rows; 32 channels a block, 32 runs of rows joined in order
+__global__ void __launch_bounds__(1024) param_sum_kernel(const float* part, int64_t rows, int C, float* gw, float* gb) {
+  __shared__ float red[32][32];
   const int i = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
   float s = 0.0f;
   if (i < 2 * C)
-    for (int64_t r = run; r < rows; r += 8) s += part[r * 2 * C + i];
+#pragma unroll 8
+    for (int64_t r = run; r < rows; r += 32) s += part[r * 2 * C + i];
   red[run][threadIdx.x & 31] = s;
   __syncthreads();
   if (run == 0 && i < 2 * C) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += red[k][threadIdx.x];
+    for (int k = 1; k < 32; ++k) s += red[k][threadIdx.x];
     float* out = i < C ? gw : gb;
     if (out) out[i < C ? i : i - C] = s;
   }
@@ -411,6 +412,11 @@ __device__ __forceinline__ MapBlock map_block(const Norm& a, const MapPlan& m) {
   k.r0 = k.split * m.rows;
   k.r1 = min(k.r0 + m.rows, a.L);
   return k;
+}
+
+// rows of slab q that belong to the map
+__device__ __forceinline__ float slab_rows(const MapBlock& k, const MapPlan& m, int q) {
+  return (float)max(min((q + 1) * m.rows, k.len) - q * m.rows, 0);
 }
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -517,27 +523,33 @@ __global__ void __launch_bounds__(256) map_norm_kernel(MapArgs p) {
   const Norm& a = p.a;
   const MapPlan& m = p.m;
   const MapBlock k = map_block(a, m);
-  const int W = a.C / a.groups, g0 = k.c0 / W, ng = k.cols / W;
+  const int W = a.C / a.groups, ng = k.cols / W;
   __shared__ float2 group[256 * V];            // mean and rstd
-  for (int g = threadIdx.x; g < ng; g += 256) {
-    // the slabs' means and deviations, joined by their counts
-    const float2* s = p.stats + (size_t)k.n * m.nsplit * a.groups + g0 + g;
-    float count = 0.0f, mean = 0.0f, dev = 0.0f;
-    for (int q = 0; q < m.nsplit; ++q) {
-      const int rows = min((q + 1) * m.rows, k.len) - q * m.rows;
-      if (rows <= 0) break;
-      const float c = (float)rows * W, total = count + c, f = c / total;
+  // the slabs' means and deviations joined by their counts, several lanes a group
+  int lanes = 64;
+  while (lanes > 1 && (lanes / 2 >= m.nsplit || lanes * ng > 256)) lanes /= 2;
+  const int sub = threadIdx.x % lanes;
+  const float total = (float)k.len * W, inv = 1.0f / fmaxf(total, 1.0f);
+  for (int g0 = 0; g0 < ng; g0 += 256 / lanes) {
+    const int g = g0 + threadIdx.x / lanes;
+    const float2* s = p.stats + (size_t)k.n * m.nsplit * a.groups + k.c0 / W + min(g, ng - 1);
+    float mean = 0.0f, dev = 0.0f;
+#pragma unroll 4
+    for (int q = sub; q < m.nsplit; q += lanes) mean += slab_rows(k, m, q) * s[(size_t)q * a.groups].x;
+    mean = lanes_sum(mean, lanes) * W * inv;
+#pragma unroll 4
+    for (int q = sub; q < m.nsplit; q += lanes) {
       const float2 e = s[(size_t)q * a.groups];
-      const float d = e.x - mean;
-      dev += e.y + d * d * count * f;
-      mean = fmaf(d, f, mean);
-      count = total;
+      const float rows = slab_rows(k, m, q), d = e.x - mean;
+      dev += rows > 0.0f ? e.y + rows * W * d * d : 0.0f;
     }
-    const float rstd = 1.0f / sqrtf(dev / fmaxf(count, 1.0f) + a.eps);
-    group[g] = make_float2(mean, rstd);
-    if (k.split == 0) {
-      if (p.mean) p.mean[(size_t)k.n * a.groups + g0 + g] = mean;
-      if (p.rstd) p.rstd[(size_t)k.n * a.groups + g0 + g] = rstd;
+    const float rstd = 1.0f / sqrtf(fmaf(lanes_sum(dev, lanes), inv, a.eps));
+    if (g < ng && sub == 0) {
+      group[g] = make_float2(mean, rstd);
+      if (k.split == 0) {
+        if (p.mean) p.mean[(size_t)k.n * a.groups + k.c0 / W + g] = mean;
+        if (p.rstd) p.rstd[(size_t)k.n * a.groups + k.c0 / W + g] = rstd;
+      }
     }
   }
   __syncthreads();
@@ -679,23 +691,43 @@ __global__ void __launch_bounds__(256) map_grad_kernel(MapArgs p) {
   }
 }
 
-// A block a map and group: the slabs' sums of each channel, and from them the group's means.
+// A block a map and group: the slabs' sums of each channel, and from them the group's means.  32
+// channels at a time, 8 runs of slabs joined in order.
 __global__ void __launch_bounds__(256) map_means_kernel(MapArgs p) {
   const Norm& a = p.a;
   const int W = a.C / a.groups, g = blockIdx.x % a.groups, n = blockIdx.x / a.groups;
-  __shared__ float red[4];
-  float s[2] = {0.0f, 0.0f};
-  for (int c = g * W + threadIdx.x; c < (g + 1) * W; c += 256)
-    for (int which = 0; which < 2; ++which) {
-      const float* q = p.part + ((size_t)n * p.m.nsplit * 2 + which) * a.C + c;
-      float v = 0.0f;
-      for (int i = 0; i < p.m.nsplit; ++i) v += q[(size_t)i * 2 * a.C];
-      p.chan[((size_t)n * 2 + which) * a.C + c] = v;
-      s[which] += a.weight ? v * a.weight[c] : v;
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
+  __shared__ float2 red[8][32];
+  float2 group = make_float2(0.0f, 0.0f);
+  for (int c0 = 0; c0 < W; c0 += 32) {
+    const int c = g * W + c0 + lane;
+    const bool in = c0 + lane < W;
+    float2 s = make_float2(0.0f, 0.0f);
+    if (in)
+#pragma unroll 8
+      for (int i = run; i < p.m.nsplit; i += 8) {
+        const float* q = p.part + ((size_t)n * p.m.nsplit + i) * 2 * a.C + c;
+        s.x += q[0];
+        s.y += q[a.C];
+      }
+    __syncthreads();
+    red[run][lane] = s;
+    __syncthreads();
+    if (run == 0 && in) {
+#pragma unroll
+      for (int k = 1; k < 8; ++k) s.x += red[k][lane].x, s.y += red[k][lane].y;
+      p.chan[(size_t)n * 2 * a.C + c] = s.x;
+      p.chan[(size_t)n * 2 * a.C + a.C + c] = s.y;
+      const float w = a.weight ? a.weight[c] : 1.0f;
+      group.x = fmaf(s.x, w, group.x);
+      group.y = fmaf(s.y, w, group.y);
     }
-  const float inv = 1.0f / fmaxf((float)row_len(a.lens, n, a.L) * W, 1.0f);
-  const float m2 = block_sum(s[0], red) * inv, m1 = block_sum(s[1], red) * inv;
-  if (threadIdx.x == 0) p.means[blockIdx.x] = make_float2(m2, m1);
+  }
+  if (threadIdx.x < 64) {
+    const float inv = 1.0f / fmaxf((float)row_len(a.lens, n, a.L) * W, 1.0f);
+    const float m2 = lanes_sum(group.x, 32) * inv, m1 = lanes_sum(group.y, 32) * inv;
+    if (threadIdx.x == 0) p.means[blockIdx.x] = make_float2(m2, m1);
+  }
 }
 
 // ---- launches --------------------------------------------------------------------------------
@@ -708,6 +740,12 @@ bool all_aligned(std::initializer_list<const void*> ps) {
 // The plan a call takes goes by sizes alone, so that a workspace is enough whatever the pointers: a
 // misaligned call is the single-element form of the same plan's layout.
 int vec_of(const Norm& a) { return a.bf16 ? 8 : 4; }
+
+// Threads of a token gradient block of ppl pieces a lane: wide blocks leave fewer partial sums of dw
+// and db (256 rows of them instead of 768: 5 us instead of 27 for 2048 channels); above two
+// pieces a lane they do not have the registers.
+constexpr int kGradThreads = 1024;
+int grad_threads(int ppl) { return ppl <= 2 ? kGradThreads : 256; }
 
 int token_blocks(const Norm& a, const TokenPlan& t, int per_cu) {
   const int by = (a.groups + t.gb - 1) / t.gb;
@@ -722,8 +760,9 @@ hipError_t run_tokens(const TokenArgs& p, bool grad, int bx, hipStream_t st) {
   const dim3 grid(bx, (p.a.groups + p.t.gb - 1) / p.t.gb);
   auto go = [&](auto ppl) {
     constexpr int K = decltype(ppl)::value;
+    constexpr int kWide = K <= 2 ? kGradThreads : 256;
     if (grad)
-      token_grad_kernel<kBf16, kVec, K><<<grid, 256, 0, st>>>(p);
+      token_grad_kernel<kBf16, kVec, K, kWide><<<grid, kWide, 0, st>>>(p);
     else
       token_kernel<kBf16, kVec, K><<<grid, 256, 0, st>>>(p);
   };
@@ -760,16 +799,22 @@ struct TokenChoice {
   TokenPlan t;
   bool vec;
 };
-TokenChoice choose_tokens(const Norm& a, bool ok) {
+TokenChoice choose_tokens(const Norm& a, bool ok, bool grad) {
   const int W = a.C / a.groups, V = vec_of(a);
   if (a.L != 1) return {{}, false};
+  auto plan = [&](int v) {
+    const TokenPlan t = token_plan(W, a.groups, v, 256);
+    return grad && t.ppl ? token_plan(W, a.groups, v, grad_threads(t.ppl)) : t;
+  };
   if (ok) {
-    const TokenPlan t = token_plan(W, a.groups, V);
+    const TokenPlan t = plan(V);
     if (t.ppl) return {t, true};
   }
-  return {token_plan(W, a.groups, 1), false};
+  return {plan(1), false};
 }
-constexpr int kGradBlocksPerCu = 3;      // bounds the partial sums of dw and db
+// blocks a CU of the token gradient: they bound the partial sums of dw and db
+int grad_blocks_per_cu(int ppl) { return ppl <= 2 ? 1 : 3; }
+constexpr int kMostGradBlocksPerCu = 3;
 
 }  // namespace
 
@@ -779,7 +824,7 @@ size_t groupnorm_workspace(const Norm& a) {
 
 hipError_t launch_groupnorm(const Norm& a, void* y, float* mean, float* rstd, char* ws, hipStream_t st) {
   const bool ok = all_aligned({a.x, a.gate, y});
-  const TokenChoice tc = choose_tokens(a, ok);
+  const TokenChoice tc = choose_tokens(a, ok, false);
   if (tc.t.ppl) {
     TokenArgs p{};
     p.a = a, p.t = tc.t, p.y = y, p.mean = mean, p.rstd = rstd;
@@ -802,9 +847,9 @@ struct GradLayout {
 };
 GradLayout grad_layout(const Norm& a) {
   GradLayout l;
-  if (a.L == 1) l.chan = align256((size_t)256 * kGradBlocksPerCu * 2 * a.C * 4);   // token form: partial sums
+  if (a.L == 1) l.chan = align256((size_t)256 * kMostGradBlocksPerCu * 2 * a.C * 4);   // token form: partial sums
   const size_t maps = align256((size_t)a.N * most_splits(a) * 2 * a.C * 4);
-  const bool tokens = choose_tokens(a, true).t.ppl && choose_tokens(a, false).t.ppl;
+  const bool tokens = choose_tokens(a, true, true).t.ppl && choose_tokens(a, false, true).t.ppl;
   if (!tokens) {
     l.chan = l.chan > maps ? l.chan : maps;
     l.means = l.chan + align256((size_t)a.N * 2 * a.C * 4);
@@ -822,16 +867,16 @@ hipError_t launch_groupnorm_backward(const Norm& a, const void* gy, const float*
                                      float* gw, float* gb, void* ggate, char* ws, hipStream_t st) {
   const GradLayout l = grad_layout(a);
   const bool ok = all_aligned({a.x, a.gate, gy, gx, ggate}), params = gw || gb;
-  const TokenChoice tc = choose_tokens(a, ok);
+  const TokenChoice tc = choose_tokens(a, ok, true);
   const unsigned sum_blocks = (2 * (unsigned)a.C + 31) / 32;
   if (tc.t.ppl) {
     TokenArgs p{};
     p.a = a, p.t = tc.t, p.gy = gy, p.mean_in = mean, p.rstd_in = rstd, p.gx = gx, p.ggate = ggate;
     if (params) p.part = (float*)ws;
-    const int bx = token_blocks(a, tc.t, kGradBlocksPerCu);
+    const int bx = token_blocks(a, tc.t, grad_blocks_per_cu(tc.t.ppl));
     hipError_t e = run_tokens(p, tc.vec, true, bx, st);
     if (e != hipSuccess || !params) return e;
-    param_sum_kernel<<<sum_blocks, 256, 0, st>>>(p.part, bx, a.C, gw, gb);
+    param_sum_kernel<<<sum_blocks, 1024, 0, st>>>(p.part, bx, a.C, gw, gb);
     return hipGetLastError();
   }
   const bool vec = ok && map_vec(a, vec_of(a));
@@ -846,7 +891,7 @@ hipError_t launch_groupnorm_backward(const Norm& a, const void* gy, const float*
     map_means_kernel<<<(unsigned)a.N * a.groups, 256, 0, st>>>(p);
     if (gx || ggate) map_grad_kernel<kB, kV, false><<<grid, 256, 0, st>>>(p);
   });
-  if (params) param_sum_kernel<<<sum_blocks, 256, 0, st>>>(p.chan, a.N, a.C, gw, gb);
+  if (params) param_sum_kernel<<<sum_blocks, 1024, 0, st>>>(p.chan, a.N, a.C, gw, gb);
   return hipGetLastError();
 }
 
