@@ -68,12 +68,13 @@ struct Piece {
   using E = Elem<kBf16>;
   using T = typename E::type;
   static constexpr int V = kVec ? (kBf16 ? 8 : 4) : 1;
-  static __device__ __forceinline__ void load(const void* p, size_t at, float (&f)[V]) {
-    const T* s = (const T*)p + at;
+  using Raw = typename std::conditional<kVec, uint4, T>::type;
+  static __device__ __forceinline__ Raw raw(const void* p, size_t at) { return *(const Raw*)((const T*)p + at); }
+  static __device__ __forceinline__ void load(const void* p, size_t at, float (&f)[V]) { unpack(raw(p, at), f); }
+  static __device__ __forceinline__ void unpack(const Raw& w, float (&f)[V]) {
     if constexpr (!kVec) {
-      f[0] = E::load(s);
+      f[0] = E::load(&w);
     } else {
-      const uint4 w = *(const uint4*)s;
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -448,21 +449,22 @@ __global__ void __launch_bounds__(256) map_stats_kernel(MapArgs p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) mean[i] = dev[i] = 0.0f;
     if (rt < m.rt)
-      for (int r = k.r0 + rt; r < r1; r += 4 * m.rt) {
-        float f[4][V];
+      for (int r = k.r0 + rt; r < r1; r += 8 * m.rt) {
+        typename P::Raw w[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (r + q * m.rt < r1) P::load(x, base + (size_t)(r + q * m.rt) * a.C + c, f[q]);
+        for (int q = 0; q < 8; ++q) w[q] = P::raw(x, base + (size_t)min(r + q * m.rt, r1 - 1) * a.C + c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 8; ++q)
           if (r + q * m.rt < r1) {
+            float f[V];
+            P::unpack(w[q], f);
             count += 1.0f;
             const float inv = __builtin_amdgcn_rcpf(count);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              const float d = f[q][i] - mean[i];
+              const float d = f[i] - mean[i];
               mean[i] = fmaf(d, inv, mean[i]);
-              dev[i] = fmaf(d, f[q][i] - mean[i], dev[i]);
+              dev[i] = fmaf(d, f[i] - mean[i], dev[i]);
             }
           }
       }
@@ -489,28 +491,36 @@ __global__ void __launch_bounds__(256) map_stats_kernel(MapArgs p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) part[rt * m.tile + ct * V + i] = make_float2(mean[i], dev[i]);
   __syncthreads();
-  // groups: `lanes` lanes each over rt x W pairs, weighted by their counts of rows
+  // a channel's threads, joined by their counts of rows
+  const int rows = r1 > k.r0 ? r1 - k.r0 : 0, ng = k.cols / W;
+  for (int c = threadIdx.x; c < k.cols; c += 256) {
+    float2 all = part[c];
+    float count = (float)((rows + m.rt - 1) / m.rt);
+    for (int r = 1; r < m.rt && r < rows; ++r) {
+      const float more = (float)((rows - r + m.rt - 1) / m.rt), f = more / (count + more);
+      const float2 e = part[r * m.tile + c];
+      const float d = e.x - all.x;
+      all.y += e.y + d * d * count * f;
+      all.x = fmaf(d, f, all.x);
+      count += more;
+    }
+    part[c] = all;
+  }
+  __syncthreads();
+  // a group's channels, all of the same count
   int lanes = 64;
-  while (lanes > 1 && lanes / 2 >= m.rt * W) lanes /= 2;
-  const int rows = r1 > k.r0 ? r1 - k.r0 : 0, sub = threadIdx.x % lanes, ng = k.cols / W;
+  while (lanes > 1 && lanes / 2 >= W) lanes /= 2;
+  const int sub = threadIdx.x % lanes;
   for (int g0 = 0; g0 < ng; g0 += 256 / lanes) {
-    const int g = g0 + threadIdx.x / lanes;
+    const int g = g0 + threadIdx.x / lanes, at = min(g, ng - 1) * W;
     float s = 0.0f;
-    if (g < ng)
-      for (int q = sub; q < m.rt * W; q += lanes) {
-        const int r = q / W;
-        const float c = (float)((rows - r + m.rt - 1) / m.rt);
-        if (rows > r) s += c * part[r * m.tile + g * W + q % W].x;
-      }
-    const float gm = lanes_sum(s, lanes) / fmaxf((float)rows * W, 1.0f);
+    for (int q = sub; q < W; q += lanes) s += part[at + q].x;
+    const float gm = lanes_sum(s, lanes) / W;
     s = 0.0f;
-    if (g < ng)
-      for (int q = sub; q < m.rt * W; q += lanes) {
-        const int r = q / W;
-        const float c = (float)((rows - r + m.rt - 1) / m.rt);
-        const float2 e = part[r * m.tile + g * W + q % W];
-        if (rows > r) s += e.y + c * (e.x - gm) * (e.x - gm);
-      }
+    for (int q = sub; q < W; q += lanes) {
+      const float2 e = part[at + q];
+      s += e.y + rows * (e.x - gm) * (e.x - gm);
+    }
     const float gd = lanes_sum(s, lanes);
     if (g < ng && sub == 0) out[g] = make_float2(gm, gd);
   }
@@ -566,35 +576,38 @@ __global__ void __launch_bounds__(256) map_norm_kernel(MapArgs p) {
       mean[i] = e.x;
       w[i] *= e.y;
     }
-    for (int r = k.r0 + rt; r < k.r1; r += 4 * m.rt) {
-      float f[4][V], gate[4][V];
+    constexpr int U = 4;                       // rows in flight
+    for (int r = k.r0 + rt; r < k.r1; r += U * m.rt) {
+      typename P::Raw w_x[U], w_g[U];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (r + q * m.rt < k.r1) {
+      for (int q = 0; q < U; ++q)
+        if (r + q * m.rt < min(k.r1, k.len)) {
           const size_t at = base + (size_t)(r + q * m.rt) * a.C + c;
-          if (r + q * m.rt < k.len) {
-            P::load(a.x, at, f[q]);
-            if (a.gate) P::load(a.gate, at, gate[q]);
-          }
+          w_x[q] = P::raw(a.x, at);
+          if (a.gate) w_g[q] = P::raw(a.gate, at);
         }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < U; ++q) {
         if (r + q * m.rt >= k.r1) continue;
+        float f[V];
         if (r + q * m.rt < k.len) {
+          P::unpack(w_x[q], f);
 #pragma unroll
-          for (int i = 0; i < V; ++i) f[q][i] = fmaf(f[q][i] - mean[i], w[i], b[i]);
+          for (int i = 0; i < V; ++i) f[i] = fmaf(f[i] - mean[i], w[i], b[i]);
           if (a.gate) {
-            act_values(a.act, gate[q]);
+            float gate[V];
+            P::unpack(w_g[q], gate);
+            act_values(a.act, gate);
 #pragma unroll
-            for (int i = 0; i < V; ++i) f[q][i] *= gate[q][i];
+            for (int i = 0; i < V; ++i) f[i] *= gate[i];
           } else {
-            act_values(a.act, f[q]);
+            act_values(a.act, f);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) f[q][i] = 0.0f;
+          for (int i = 0; i < V; ++i) f[i] = 0.0f;
         }
-        P::store(p.y, base + (size_t)(r + q * m.rt) * a.C + c, f[q]);
+        P::store(p.y, base + (size_t)(r + q * m.rt) * a.C + c, f);
       }
     }
   }
