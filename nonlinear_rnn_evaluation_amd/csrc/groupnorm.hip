@@ -832,6 +832,7 @@ constexpr int kMostGradBlocksPerCu = 3;
 }  // namespace
 
 size_t groupnorm_workspace(const Norm& a) {
+  if (choose_tokens(a, true, false).t.ppl && choose_tokens(a, false, false).t.ppl) return 0;
   return align256((size_t)a.N * most_splits(a) * a.groups * sizeof(float2));
 }
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Optional
 
 import torch
@@ -519,58 +520,79 @@ def scan(kind: int, A: torch.Tensor, b: torch.Tensor, tile_len: int = 0) -> torc
 
 
 # ---- sequence mixing: linear attention with per-head decay, group norm with an activation ------
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
-    """A strided [..., D] operand: the last axis contiguous, the others as they are."""
+# A decoded token costs little more than its call, so the checks below are one expression each
+# where everything is right, and the descriptors are packed in one go.
+_SEQ_DT = {torch.float32: F32, torch.bfloat16: BF16}
+_LINATTN = struct.Struct("8i d 9q 3P N")      # the layouts of pnr_linattn and pnr_norm
+_NORM = struct.Struct("6i d 3P N")
+
+
+def _raw_stream(device: int) -> int:
+    """torch's current stream of a device, as a hipStream_t."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _on(device: int, t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple) -> Optional[int]:
+    """The pointer of a contiguous tensor on the call's device."""
+    if t is None:
+        return None
+    if not (t.dtype == dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()):
+        _arg(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
+    """Names what is wrong with a strided [..., D] operand."""
     _check(t, name, dtype, shape)
     if not t.is_cuda:
         raise ValueError("libpnr takes device tensors")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return t
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-
-
-def _workspace(need: int, workspace: Optional[torch.Tensor], device: torch.device, desc) -> Optional[torch.Tensor]:
+def _workspace(need: int, workspace: Optional[torch.Tensor], device: int, desc) -> Optional[torch.Tensor]:
     """Points the descriptor at `workspace`, or at a new one where that is missing or too small."""
     if need:
         if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        _same_device(device, workspace=workspace)
+            workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", device))
+        elif workspace.get_device() != device:
+            raise ValueError(f"workspace is on {workspace.device}, not on cuda:{device}")
         desc.workspace = _ptr(workspace)
         desc.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
 
 
 def _raise(what: str, rc: int) -> None:
-    if rc < 0:
-        raise PnrError(f"{what} returned {rc}: {pnr_last_error()}")
+    raise PnrError(f"{what} returned {rc}: {pnr_last_error()}")
 
 
 def _linattn(q, k, v, log_decay, scale, lens, step: bool) -> tuple:
-    """The descriptor of a linear-attention call and the four inputs' pointers."""
-    if q.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"linear attention takes float32 or bfloat16 (got {q.dtype})")
-    if q.dim() != (3 if step else 4) or k.dim() != q.dim() or v.dim() != q.dim():
+    """The descriptor of a linear-attention call, the four inputs' pointers, the sizes, the device."""
+    dt = q.dtype
+    code = _SEQ_DT.get(dt)
+    if code is None:
+        raise TypeError(f"linear attention takes float32 or bfloat16 (got {dt})")
+    qs, ks, vs, dims = q.shape, k.shape, v.shape, 3 if step else 4
+    if not len(qs) == len(ks) == len(vs) == dims:
         raise ValueError("q, k, v must be " + ("[B, heads, D]" if step else "[B, T, heads, D]"))
-    lead = tuple(q.shape[:-2])
-    H, Dk = q.shape[-2:]
-    Hkv, Dv = v.shape[-2:]
-    _rows(q, "q", q.dtype, (*lead, H, Dk))
-    _rows(k, "k", q.dtype, (*lead, Hkv, Dk))
-    _rows(v, "v", q.dtype, (*lead, Hkv, Dv))
+    lead, (H, Dk), (Hkv, Dv) = qs[:-2], qs[-2:], vs[-2:]
+    a, b, c, dev = q.stride(), k.stride(), v.stride(), q.get_device()
+    if not (k.dtype == dt == v.dtype and dev >= 0 and k.get_device() == dev == v.get_device() and vs[:-2] == lead
+            and ks == (*lead, Hkv, Dk) and (a[-1] == 1 or Dk == 1) and (b[-1] == 1 or Dk == 1) and (c[-1] == 1 or Dv == 1)):
+        _rows(q, "q", dt, qs, dev)
+        _rows(k, "k", dt, (*lead, Hkv, Dk), dev)
+        _rows(v, "v", dt, (*lead, Hkv, Dv), dev)
     token = log_decay.dim() != 1
-    g = _arg(log_decay, "log_decay", torch.float32, (*lead, Hkv) if token else (Hkv,))
-    _same_device(q.device, k=k, v=v, log_decay=log_decay, lens=lens)
-    strides = [(t.stride(0), 0 if step else t.stride(1), t.stride(-2)) for t in (q, k, v)]
-    desc = PnrLinattn(lead[0], 1 if step else lead[1], H, Hkv, Dk, Dv, _DT[q.dtype], DECAY_TOKEN if token else DECAY_HEAD,
-                      Dk ** -0.5 if scale is None else scale, *[(ctypes.c_int64 * 3)(*x) for x in strides],
-                      _arg(lens, "lens", torch.int32, lead[:1]), _stream())
-    return desc, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g)
+    g = _on(dev, log_decay, "log_decay", torch.float32, (*lead, Hkv) if token else (Hkv,))
+    T, qt, kt, vt = (1, 0, 0, 0) if step else (lead[1], a[1], b[1], c[1])
+    desc = PnrLinattn.from_buffer_copy(_LINATTN.pack(
+        lead[0], T, H, Hkv, Dk, Dv, code, DECAY_TOKEN if token else DECAY_HEAD, Dk ** -0.5 if scale is None else scale,
+        a[0], qt, a[-2], b[0], kt, b[-2], c[0], vt, c[-2], _on(dev, lens, "lens", torch.int32, lead[:1]) or 0,
+        _raw_stream(dev), 0, 0))
+    return desc, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g), (lead[0], T, H, Hkv, Dk, Dv), dev
 
 
 def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
@@ -583,19 +605,18 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     before the first token, zeros if None) float32 [B,H_kv,D_k,D_v], lens int32 [B] (tokens of
     each row, T if None); scale None is D_k ** -0.5.  Returns dict(o=[B,T,H,D_v], state=the state
     after each row's last token, workspace)."""
-    desc, ptrs = _linattn(q, k, v, log_decay, scale, lens, False)
-    B, T, H, Dk = q.shape
-    Hkv, Dv = v.shape[-2:]
+    desc, ptrs, (B, T, H, Hkv, Dk, Dv), dev = _linattn(q, k, v, log_decay, scale, lens, False)
     if o is None:
         o = torch.empty(B, T, H, Dv, dtype=q.dtype, device=q.device)
-    if state_out is None:
-        state_out = torch.empty(B, Hkv, Dk, Dv, dtype=torch.float32, device=q.device)
-    _same_device(q.device, state=state, o=o, state_out=state_out)
     shape = (B, Hkv, Dk, Dv)
-    workspace = _workspace(pnr_linattn_workspace_bytes(desc), workspace, q.device, desc)
-    rc = pnr_linattn_forward(desc, *ptrs, _arg(state, "state", torch.float32, shape),
-                             _arg(o, "o", q.dtype, (B, T, H, Dv)), _arg(state_out, "state_out", torch.float32, shape))
-    _raise("pnr_linattn_forward", rc)
+    if state_out is None:
+        state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    args = (_on(dev, state, "state", torch.float32, shape), _on(dev, o, "o", q.dtype, (B, T, H, Dv)),
+            _on(dev, state_out, "state_out", torch.float32, shape))
+    workspace = _workspace(pnr_linattn_workspace_bytes(desc), workspace, dev, desc)
+    rc = pnr_linattn_forward(desc, *ptrs, *args)
+    if rc < 0:
+        _raise("pnr_linattn_forward", rc)
     return {"o": o, "state": state_out, "workspace": workspace}
 
 
@@ -607,19 +628,18 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     pool of running requests' states, of which request b has slot slots[b] (int32 [B]; slot b if
     None; a slot outside the pool marks an idle row).  The pool is updated in place unless
     state_out gives another one of its shape.  Returns dict(o=[B,H,D_v], state=the updated pool)."""
-    desc, ptrs = _linattn(q, k, v, log_decay, scale, None, True)
-    B, H, Dk = q.shape
-    Hkv, Dv = v.shape[-2:]
+    desc, ptrs, (B, _, H, Hkv, Dk, Dv), dev = _linattn(q, k, v, log_decay, scale, None, True)
     if state_out is None:
         state_out = state
     if o is None:
         o = torch.empty(B, H, Dv, dtype=q.dtype, device=q.device)
-    _same_device(q.device, state=state, slots=slots, o=o, state_out=state_out)
-    shape = (state.shape[0], Hkv, Dk, Dv)
-    rc = pnr_linattn_step(desc, *ptrs, _arg(state, "state", torch.float32, shape),
-                          _arg(slots, "slots", torch.int32, (B,)), shape[0], _arg(o, "o", q.dtype, (B, H, Dv)),
-                          _arg(state_out, "state_out", torch.float32, shape))
-    _raise("pnr_linattn_step", rc)
+    n_slots = state.shape[0] if state.dim() else 0
+    shape = (n_slots, Hkv, Dk, Dv)
+    rc = pnr_linattn_step(desc, *ptrs, _on(dev, state, "state", torch.float32, shape),
+                          _on(dev, slots, "slots", torch.int32, (B,)), n_slots, _on(dev, o, "o", q.dtype, (B, H, Dv)),
+                          _on(dev, state_out, "state_out", torch.float32, shape))
+    if rc < 0:
+        _raise("pnr_linattn_step", rc)
     return {"o": o, "state": state_out}
 
 
@@ -633,11 +653,10 @@ def linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     grad_o = dL/do [B,T,H,D_v] and grad_state = dL/d(returned state) (zeros if None).  Returns
     {name: gradient} for the names in `want` (q, k, v in their dtype; log_decay and state in
     float32; "state" only where a state is given) and "workspace"."""
-    desc, ptrs = _linattn(q, k, v, log_decay, scale, lens, False)
-    B, T, H, Dk = q.shape
-    Hkv, Dv = v.shape[-2:]
+    desc, ptrs, (B, T, H, Hkv, Dk, Dv), dev = _linattn(q, k, v, log_decay, scale, lens, False)
     shape = (B, Hkv, Dk, Dv)
-    _same_device(q.device, grad_o=grad_o, state=state, grad_state=grad_state)
+    args = (_on(dev, state, "state", torch.float32, shape), _on(dev, grad_o, "grad_o", q.dtype, (B, T, H, Dv)),
+            _on(dev, grad_state, "grad_state", torch.float32, shape))
     like = dict(q=(q.shape, q.dtype), k=(k.shape, q.dtype), v=(v.shape, q.dtype),
                 log_decay=(log_decay.shape, torch.float32), state=(shape, torch.float32))
     unknown = set(want) - set(like)
@@ -645,28 +664,30 @@ def linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         raise ValueError(f"no gradient named {sorted(unknown)}")
     out = {n: torch.empty(like[n][0], dtype=like[n][1], device=q.device) for n in want
            if n != "state" or state is not None}
-    need = pnr_linattn_workspace_bytes_backward(desc)
-    workspace = _workspace(need, workspace, q.device, desc)
-    rc = pnr_linattn_backward(desc, *ptrs, _arg(state, "state", torch.float32, shape),
-                              _arg(grad_o, "grad_o", q.dtype, (B, T, H, Dv)),
-                              _arg(grad_state, "grad_state", torch.float32, shape),
-                              *[_ptr(out.get(n)) for n in ("q", "k", "v", "log_decay", "state")])
-    _raise("pnr_linattn_backward", rc)
+    workspace = _workspace(pnr_linattn_workspace_bytes_backward(desc), workspace, dev, desc)
+    rc = pnr_linattn_backward(desc, *ptrs, *args, *[_ptr(out.get(n)) for n in ("q", "k", "v", "log_decay", "state")])
+    if rc < 0:
+        _raise("pnr_linattn_backward", rc)
     out["workspace"] = workspace
     return out
 
 
 def _norm(x, groups, weight, bias, gate, act, eps, lens) -> tuple:
-    """The descriptor of a group-norm call and the pointers of x, weight, bias and gate."""
-    if x.dtype not in (torch.float32, torch.bfloat16):
+    """The descriptor of a group-norm call, the pointers of x, weight, bias and gate, the device."""
+    code = _SEQ_DT.get(x.dtype)
+    if code is None:
         raise TypeError(f"group norm takes float32 or bfloat16 (got {x.dtype})")
-    if x.dim() != 3:
-        raise ValueError(f"x must be [N, L, C] (got {tuple(x.shape)})")
-    N, L, C = x.shape
-    _same_device(x.device, weight=weight, bias=bias, gate=gate, lens=lens)
-    ptrs = (_ptr(x), _arg(weight, "weight", torch.float32, (C,)), _arg(bias, "bias", torch.float32, (C,)),
-            _arg(gate, "gate", x.dtype, (N, L, C)))
-    return PnrNorm(N, L, C, groups, _DT[x.dtype], act, eps, _arg(lens, "lens", torch.int32, (N,)), _stream()), ptrs
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x must be [N, L, C] (got {tuple(shape)})")
+    dev, params = x.get_device(), shape[2:]
+    if dev < 0:
+        raise ValueError("libpnr takes device tensors")
+    ptrs = (_on(dev, x, "x", x.dtype, shape), _on(dev, weight, "weight", torch.float32, params),
+            _on(dev, bias, "bias", torch.float32, params), _on(dev, gate, "gate", x.dtype, shape))
+    desc = PnrNorm.from_buffer_copy(_NORM.pack(*shape, groups, code, act, eps,
+                                               _on(dev, lens, "lens", torch.int32, shape[:1]) or 0, _raw_stream(dev), 0, 0))
+    return desc, ptrs, dev
 
 
 def group_norm(x: torch.Tensor, groups: int, *, weight: Optional[torch.Tensor] = None,
@@ -677,14 +698,15 @@ def group_norm(x: torch.Tensor, groups: int, *, weight: Optional[torch.Tensor] =
     over itself and the L positions, scaled by weight and bias (float32 [C], both or neither), then
     y = act(z), or z act(gate) with a gate like x.  lens int32 [N]: the positions of each row.
     L = 1 is the norm of N tokens by heads.  Returns dict(y, mean, rstd [N, groups], workspace)."""
-    desc, ptrs = _norm(x, groups, weight, bias, gate, act, eps, lens)
+    desc, ptrs, dev = _norm(x, groups, weight, bias, gate, act, eps, lens)
     if y is None:
         y = torch.empty_like(x)
-    _same_device(x.device, y=y)
+    out = _on(dev, y, "y", x.dtype, x.shape)
     mean, rstd = torch.empty(2, x.shape[0], max(groups, 1), dtype=torch.float32, device=x.device).unbind(0)
-    workspace = _workspace(pnr_groupnorm_workspace_bytes(desc), workspace, x.device, desc)
-    rc = pnr_groupnorm(desc, *ptrs, _arg(y, "y", x.dtype, tuple(x.shape)), mean.data_ptr(), rstd.data_ptr())
-    _raise("pnr_groupnorm", rc)
+    workspace = _workspace(pnr_groupnorm_workspace_bytes(desc), workspace, dev, desc)
+    rc = pnr_groupnorm(desc, *ptrs, out, mean.data_ptr(), rstd.data_ptr())
+    if rc < 0:
+        _raise("pnr_groupnorm", rc)
     return {"y": y, "mean": mean, "rstd": rstd, "workspace": workspace}
 
 
@@ -696,18 +718,18 @@ def group_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean
     """Run pnr_groupnorm_backward: gradients through group_norm of these arguments, given grad_y and the
     mean and rstd that it returned.  Returns {name: gradient} for the names in `want` whose
     argument is given (x and gate in x's dtype, weight and bias float32) and "workspace"."""
-    desc, ptrs = _norm(x, groups, weight, bias, gate, act, 1e-5, lens)
+    desc, ptrs, dev = _norm(x, groups, weight, bias, gate, act, 1e-5, lens)
     args = dict(x=x, weight=weight, bias=bias, gate=gate)
     unknown = set(want) - set(args)
     if unknown:
         raise ValueError(f"no gradient named {sorted(unknown)}")
-    _same_device(x.device, grad_y=grad_y, mean=mean, rstd=rstd)
-    out = {n: torch.empty_like(args[n]) for n in want if args[n] is not None}
-    workspace = _workspace(pnr_groupnorm_workspace_bytes_backward(desc), workspace, x.device, desc)
     stats = (x.shape[0], groups)
-    rc = pnr_groupnorm_backward(desc, *ptrs, _arg(grad_y, "grad_y", x.dtype, tuple(x.shape)),
-                                _arg(mean, "mean", torch.float32, stats), _arg(rstd, "rstd", torch.float32, stats),
-                                *[_ptr(out.get(n)) for n in ("x", "weight", "bias", "gate")])
-    _raise("pnr_groupnorm_backward", rc)
+    ins = (_on(dev, grad_y, "grad_y", x.dtype, x.shape), _on(dev, mean, "mean", torch.float32, stats),
+           _on(dev, rstd, "rstd", torch.float32, stats))
+    out = {n: torch.empty_like(args[n]) for n in want if args[n] is not None}
+    workspace = _workspace(pnr_groupnorm_workspace_bytes_backward(desc), workspace, dev, desc)
+    rc = pnr_groupnorm_backward(desc, *ptrs, *ins, *[_ptr(out.get(n)) for n in ("x", "weight", "bias", "gate")])
+    if rc < 0:
+        _raise("pnr_groupnorm_backward", rc)
     out["workspace"] = workspace
     return out
