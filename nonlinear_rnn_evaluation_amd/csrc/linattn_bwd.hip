@@ -88,7 +88,7 @@ struct BackwardLayout {
 };
 BackwardLayout backward_layout(const LinAttn& a) {
   BackwardLayout l;
-  l.plan = make_plan(a);
+  l.plan = make_plan(a, true);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;

@@ -52,7 +52,7 @@ struct ForwardLayout {
 };
 ForwardLayout forward_layout(const LinAttn& a) {
   ForwardLayout l;
-  l.plan = make_plan(a);
+  l.plan = make_plan(a, false);
   if (l.plan.nseg > 1) {
     l.decay = l.plan.states;
     l.total = l.decay + (size_t)a.B * a.Hkv * l.plan.nseg * 4;

@@ -794,15 +794,20 @@ struct Plan {
 };
 
 // Few rows and a long axis: the axis is cut into segments that run side by side, at the price of
-// one more pass over the keys and values for the segments' own sums.
-inline Plan make_plan(const LinAttn& a) {
+// one more pass over the keys and values for the segments' own sums, and of the recurrence
+// over the segments.  As many segments as fill the device (256 CUs, two blocks each of the widest
+// bf16 tiles, one of fp32's), from the length on where that pays; one head's pass in us, whole | cut:
+//            forward   128 x 128 bf16          backward  128 x 128 bf16   fp32
+//   192 tokens         17 | 19                           73 | 66          159 | 103
+//   320                25 | 19                           111 | 68         253 | 105
+//   4096              252 | 35                          1141 | 89        2984 | 125
+inline Plan make_plan(const LinAttn& a, bool backward) {
   const int chunks = (a.T + kChunk - 1) / kChunk;
   const int64_t rows = (int64_t)a.B * a.Hkv;
   Plan p{chunks > 0 ? chunks : 1, 1, 0};
-  const int64_t want = 512 / rows;
-  if (want >= 2 && chunks >= 8) {
-    const int seg = (int)((chunks + want - 1) / want);
-    p.seg_chunks = seg < 4 ? 4 : seg;
+  const int64_t want = (a.bf16 ? 512 : 256) / rows;
+  if (want >= 2 && chunks >= (backward || !a.bf16 ? 3 : 5)) {
+    p.seg_chunks = (int)((chunks + want - 1) / want);
     p.nseg = (chunks + p.seg_chunks - 1) / p.seg_chunks;
   }
   p.states = ((size_t)rows * p.nseg * a.Dk * a.Dv * 4 + 255) / 256 * 256;
