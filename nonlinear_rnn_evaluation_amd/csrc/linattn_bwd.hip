@@ -143,7 +143,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
       RoleArgs p = fwd;
       p.y = a.k, p.z = a.v, p.dk = a.Dk, p.dv = a.Dv;
       p.s_out = S, p.seg_decay = decay;
-      if ((e = run_role<false, kSum>(p, st)) != hipSuccess) return e;
+      if ((e = run_sum<false>(p, st)) != hipSuccess) return e;
       sc[count++] = {S, decay, state_in, last, nseg, a.Dk * a.Dv, 0};
       fwd.s_in = S;
     }
@@ -151,7 +151,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
       RoleArgs p = rev;
       p.y = a.q, p.z = d.go, p.dk = a.Dk, p.dv = a.Dv;
       p.s_out = E, p.seg_decay = decay;
-      if ((e = run_role<true, kSum>(p, st)) != hipSuccess) return e;
+      if ((e = run_sum<true>(p, st)) != hipSuccess) return e;
       sc[count++] = {E, decay, d.gstate_out, d.gstate_in, nseg, a.Dk * a.Dv, 1};
       rev.s_in = E;
     }

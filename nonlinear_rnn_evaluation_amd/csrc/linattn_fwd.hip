@@ -83,7 +83,7 @@ hipError_t launch_linattn_forward(const LinAttn& a, const float* state_in, void*
   float* decay = (float*)(ws + l.decay);
   RoleArgs s = p;
   s.s_out = seg, s.seg_decay = decay;
-  hipError_t e = run_role<false, kSum>(s, st);
+  hipError_t e = run_sum<false>(s, st);
   if (e != hipSuccess) return e;
   const ScanArgs sc{seg, decay, state_in, state_out, l.plan.nseg, a.Dk * a.Dv, 0};
   if ((e = launch_scan(&sc, 1, (int64_t)a.B * a.Hkv, st)) != hipSuccess) return e;

@@ -27,10 +27,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 enum Kind {
-  kSum = 0,     // only the state's sum over the segment, from zero
-  kOut = 1,     // outputs
-  kDotQ = 2,    // dq, and from it u and b of the decay's gradient
-  kDotK = 3,    // dk, and from it c of the decay's gradient
+  kOut,         // outputs
+  kDotQ,        // dq, and from it u and b of the decay's gradient
+  kDotK,        // dk, and from it c of the decay's gradient
 };
 
 struct RoleArgs {
@@ -43,7 +42,7 @@ struct RoleArgs {
   float p_scale, inter_scale, upd_scale;   // on scores, on S^T x, on y z^T
   const float* s_in;     // [B][Hkv][nseg] states at the segments' entry, or nullptr: zeros
   float* s_out;          // [B][Hkv][nseg] states at the segments' exit, or nullptr
-  float* seg_decay;      // kSum: [B][Hkv][nseg] the segment's whole decay, or nullptr
+  float* seg_decay;      // sum_kernel: [B][Hkv][nseg] the segment's whole decay
   void* o;
   float* u;              // [B][Hkv][T]: u + b (kDotQ), c (kDotK) of the decay's gradient
   float* b;              // [B][Hkv][chunks]: sums of b (kDotQ)
@@ -153,6 +152,13 @@ struct Split<false, kParts> {
     for (int e = 0; e < 8; ++e) part[0].v[e] = v[e];
   }
 };
+
+// x of lane 63
+__device__ __forceinline__ double wave_last(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  return __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(u >> 32), 63) << 32 |
+                                        (uint32_t)__builtin_amdgcn_readlane((uint32_t)u, 63));
+}
 
 // The same number, as far as the compiler can tell computed anew: addresses made from it stay where
 // they are used instead of being kept in registers over the whole loop.
@@ -328,6 +334,30 @@ struct alignas(16) Weights {
   float end_hi, end_lo;              // G_C
 };
 
+// S += Y^T (w Z) over 32 tokens, for 16 columns of Z held as an operand; kGroup row tiles at a time.
+template <bool kBf16, int DK, int kGroup>
+__device__ __forceinline__ void add_outer(f32x4 (&S)[DK / 16], const typename Mma<kBf16>::Frag& zf, const float* w,
+                                          const typename Mma<kBf16>::Elt* y, int pitch, int lane) {
+  using M = Mma<kBf16>;
+  const float* wp = w + (lane >> 4) * 8;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (kBf16) v[e] = wp[e] * (float)zf[e]; else v[e] = wp[e] * zf.v[e];
+  }
+  const Split<kBf16, 3> wz(v);
+#pragma unroll
+  for (int kt = 0; kt < DK / 16; kt += kGroup) {
+    typename M::Frag yf[kGroup];
+#pragma unroll
+    for (int q = 0; q < kGroup; ++q) yf[q] = M::template cols<8>(y, pitch, 0, state_row(kt + q, 0), lane);
+#pragma unroll
+    for (int part = (kBf16 ? 3 : 1); part--;)
+#pragma unroll
+      for (int q = 0; q < kGroup; ++q) S[kt + q] = M::mul(yf[q], wz.part[part], S[kt + q]);
+  }
+}
+
 // A block walks the chunks of one segment of one state head, with the state in accumulators: a
 // wave holds 16 columns of S, all DK rows.  (With 32 columns a wave, half the waves and half the
 // reads of X and Y from LDS, 256 registers leave two waves a SIMD: 161 us where this takes
@@ -349,14 +379,13 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   constexpr int PK = DK + M::kPadY, PV = DV + M::kPadZ;     // rows of Y and Z in LDS
   constexpr bool kDots = kind == kDotQ || kind == kDotK;
   constexpr int kParts = kDots ? 3 : 1;
-  constexpr bool kAll = kind != kSum;
   // LDS (bf16, 128 x 128: two blocks a CU, also with the dot products' arrays).  Arrays of their own,
   // so that a read of one need not wait for loads on their way to another.
-  __shared__ alignas(16) Elt lds_x[kAll ? kChunk * DK : 1];           // Direct
+  __shared__ alignas(16) Elt lds_x[kChunk * DK];           // Direct
   __shared__ alignas(16) Elt lds_y[kChunk * PK];
   __shared__ alignas(16) Elt lds_z[kChunk * PV];
   __shared__ alignas(16) Elt lds_e[kDots ? kChunk * DV : 1];          // Direct
-  __shared__ alignas(16) Elt lds_p[kAll ? kChunk * kChunk : 1];       // scores [i][j], see score_at
+  __shared__ alignas(16) Elt lds_p[kChunk * kChunk];       // scores [i][j], see score_at
   __shared__ Weights lds_w[2];                                        // this chunk's and the next one's
   __shared__ float lds_dot[kDots ? kWaves : 1][kChunk];               // the waves' parts of dot products and row sums
   __shared__ float lds_bsum[kDots ? kWaves : 1];
@@ -385,7 +414,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        S[kt][r] = (kind != kSum && p.s_in && s_in_range(kt, r)) ? p.s_in[s_at(kt, r)] : 0.0f;
+        S[kt][r] = (p.s_in && s_in_range(kt, r)) ? p.s_in[s_at(kt, r)] : 0.0f;
 
   // the loads of S end here: a wait for them inside the loop would wait for the tiles behind them
 #pragma unroll
@@ -419,7 +448,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   Stage<kBf16, DK, kThreads, PK> sx, sy;
   Stage<kBf16, DV, kThreads, PV> sz, se;
   const uint32_t es = sizeof(Elt);
-  const uint32_t off_x = kVec && kAll ? TX::offset((uint32_t)p.x.st * es, p.dk) : 0, off_e = kVec && kDots ? TE::offset((uint32_t)p.e.st * es, p.dv) : 0;
+  const uint32_t off_x = kVec ? TX::offset((uint32_t)p.x.st * es, p.dk) : 0, off_e = kVec && kDots ? TE::offset((uint32_t)p.e.st * es, p.dv) : 0;
   const uint32_t off_y = kVec ? decltype(sy)::offset((uint32_t)p.y.st * es, p.dk) : 0, off_z = kVec ? decltype(sz)::offset((uint32_t)p.z.st * es, p.dv) : 0;
   float g_next = 0.0f;
   auto fetch = [&](int c, int sub) {
@@ -428,7 +457,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       const int t = min(t0 + lane, n - 1);
       g_next = a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h];
     }
-    if constexpr (kAll && !kVec)
+    if constexpr (!kVec)
       if (p.nq > 1 || sub == 0) {
         const int hh = h * p.nq + (p.nq > 1 ? sub : 0);
         sx.template load<kVec>(Source<kBf16>(p.x, b, hh), 0, t0, n, p.dk);
@@ -441,10 +470,9 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     }
   };
 
-  double seg_log = 0.0;                       // wave 0: log2 of the segment's decay
   // X and E are done with once the first half of a chunk is: aligned rows go straight to them then
   auto fetch_direct = [&](int c, int sub) {
-    if constexpr (kAll && kVec)
+    if constexpr (kVec)
       if (p.nq > 1 || sub == 0) {
         const int hh = h * p.nq + (p.nq > 1 ? sub : 0), t0 = c * kChunk;
         TX::load(Source<kBf16>(p.x, b, hh), off_x, t0, n, lds_x, wave);
@@ -456,9 +484,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   auto weigh = [&](int c, int slot) {
     const float g = c * kChunk + lane < n ? clamp_log_decay(g_next) : 0.0f;
     const double x = wave_scan((double)g * 1.4426950408889634);
-    const uint64_t last = __builtin_bit_cast(uint64_t, x);
-    const double end = __builtin_bit_cast(double, (uint64_t)__builtin_amdgcn_readlane((uint32_t)(last >> 32), 63) << 32 |
-                                                      (uint32_t)__builtin_amdgcn_readlane((uint32_t)last, 63));
+    const double end = wave_last(x);
     const float hi = (float)x, end_hi = (float)end;
     auto& w = lds_w[slot];
     w.ghi[lane] = hi;
@@ -468,7 +494,6 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       w.total = __builtin_amdgcn_exp2f(end_hi);
       w.end_hi = end_hi, w.end_lo = (float)(end - (double)end_hi);
     }
-    seg_log += end;
   };
   const int count = live > c_lo ? (live - c_lo) * nsub : 0;
   if (count > 0) {
@@ -486,7 +511,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     const bool last_sub = sub == nsub - 1;
     const bool new_x = p.nq > 1 || sub == 0, new_yz = p.nkv > 1 || sub == 0;
     __syncthreads();
-    if constexpr (kAll && !kVec)
+    if constexpr (!kVec)
       if (new_x) {
         sx.store_permuted(lds_x);
         if constexpr (kDots) se.store_permuted(lds_e);
@@ -496,9 +521,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       sz.store(lds_z);
     }
     const int next_sub = last_sub ? 0 : sub + 1, next_c = last_sub ? (kReverse ? c - 1 : c + 1) : c;
-    if constexpr (kind == kSum)
-      if (it + 1 < count) fetch(next_c, next_sub);
-    if constexpr (kAll && kVec) {
+    if constexpr (kVec) {
       // this thread's loads to LDS have landed; after the barrier, everyone's
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
       __builtin_amdgcn_s_waitcnt(0x0F70);
@@ -506,7 +529,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     }
     __syncthreads();
 
-    if constexpr (kAll) {
+    {
       // ---- scores: lane column i, four rows j a register block
       const int ln = fresh(lane), l15 = ln & 15, g4 = (ln >> 4) * 4;
       const int i = it0 * 16 + l15;
@@ -620,7 +643,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 #pragma unroll
     for (int k = 0; k < 2; ++k) zf[k] = M::template cols<4>(lds_z, PV, k * 32, col0, lane2);
 
-    if constexpr (kAll) {
+    {
       // zero times every value: a NaN where one of them is none or infinite
       const f32x4 odd = M::mul(zf[1], M::none(), M::mul(zf[0], M::none(), zero));
       const float sum = (odd[0] + odd[1]) + (odd[2] + odd[3]);
@@ -712,33 +735,14 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         for (int kt = 0; kt < KT; ++kt) S[kt] *= total;
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float* wp = wt.upd + k * 32 + g4 * 2;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if constexpr (kBf16) v[e] = wp[e] * (float)zf[k][e]; else v[e] = wp[e] * zf[k].v[e];
-        }
-        const Split<kBf16, 3> wz(v);
-        constexpr int KG = kDots ? 2 : 4;     // row tiles at a time
-#pragma unroll
-        for (int kt = 0; kt < KT; kt += KG) {
-          Frag yf[KG];
-#pragma unroll
-          for (int q = 0; q < KG; ++q) yf[q] = M::template cols<8>(lds_y, PK, k * 32, state_row(kt + q, 0), lane2);
-#pragma unroll
-          for (int part = (kBf16 ? 3 : 1); part--;)
-#pragma unroll
-            for (int q = 0; q < KG; ++q) S[kt + q] = M::mul(yf[q], wz.part[part], S[kt + q]);
-        }
-      }
+      for (int k = 0; k < 2; ++k) add_outer<kBf16, DK, kDots ? 2 : 4>(S, zf[k], wt.upd + k * 32, lds_y + k * 32 * PK, PK, lane2);
     }
     // the next chunk's weights, where no other wave waits for them
     if (last_sub && it + 1 < count && wave == 0) weigh(next_c, ~step & 1);
   }
 
   // ---- chunks without tokens: zeros
-  if constexpr (kAll) {
+  {
     for (int c = max(live, c_lo); c < c_hi; ++c) {
       const int t0 = c * kChunk, rows = min(kChunk, a.T - t0);
       if (p.o)
@@ -757,28 +761,148 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (s_in_range(kt, r)) p.s_out[s_at(kt, r)] = S[kt][r];
-  if (kind == kSum && p.seg_decay && tid == 0) p.seg_decay[blockIdx.x] = __builtin_amdgcn_exp2f((float)seg_log);
 }
 
-template <bool kBf16, int DK, int DV, bool kReverse, Kind kind, bool kVec>
-hipError_t launch_chunk(const RoleArgs& p, hipStream_t st) {
-  chunk_kernel<kBf16, DK, DV, kReverse, kind, kVec><<<(unsigned)p.a.B * p.a.Hkv * p.nseg, DV * 4, 0, st>>>(p);
-  return hipGetLastError();
+// The sum of a segment alone, from a zero state, and the segment's decay: chunk_kernel's update, 128
+// tokens a step (64 in fp32), because keys and values in flight are what bounds it.
+template <bool kBf16, int DK, int DV, bool kReverse, bool kVec>
+__global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleArgs p) {
+  using M = Mma<kBf16>;
+  using Elt = typename M::Elt;
+  using Frag = typename M::Frag;
+  constexpr int kWaves = DV / 16, kThreads = kWaves * 64, KT = DK / 16;
+  constexpr int kHalves = kBf16 ? 2 : 1, kStep = kHalves * kChunk;
+  constexpr int PK = DK + M::kPadY, PV = DV + M::kPadZ;
+  using SY = Stage<kBf16, DK, kThreads, PK>;
+  using SZ = Stage<kBf16, DV, kThreads, PV>;
+  __shared__ alignas(16) Elt lds_y[kStep * PK];
+  __shared__ alignas(16) Elt lds_z[kStep * PV];
+  __shared__ alignas(16) float lds_upd[2][kStep];       // the weights of y z^T, of this step and the next
+  __shared__ float lds_total[2];
+
+  const LinAttn& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l15 = lane & 15, g4 = (lane >> 4) * 4;
+  const int seg = blockIdx.x % p.nseg;
+  const int h = blockIdx.x / p.nseg % a.Hkv, b = blockIdx.x / p.nseg / a.Hkv;
+  const int first = seg * p.seg_chunks * kChunk;        // the segment's tokens: first .. n - 1
+  const int n = min(row_len(a.lens, b, a.T), first + p.seg_chunks * kChunk);
+  const int steps = n > first ? (n - first + kStep - 1) / kStep : 0, count = steps * p.nkv;
+  const int col0 = wave * 16;
+  f32x4 S[KT];
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt) S[kt] = f32x4{0, 0, 0, 0};
+
+  SY sy[kHalves];
+  SZ sz[kHalves];
+  float g_next[kHalves];
+  const uint32_t es = sizeof(Elt);
+  const uint32_t off_y = kVec ? SY::offset((uint32_t)p.y.st * es, p.dk) : 0, off_z = kVec ? SZ::offset((uint32_t)p.z.st * es, p.dv) : 0;
+  auto start = [&](int step) { return first + (kReverse ? steps - 1 - step : step) * kStep; };
+  auto fetch = [&](int step, int sub) {
+    const int t0 = start(step), hh = h * p.nkv + sub;
+    if (sub == 0 && wave == 0)
+#pragma unroll
+      for (int u = 0; u < kHalves; ++u) {
+        const int t = min(t0 + u * kChunk + lane, n - 1);
+        g_next[u] = a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h];
+      }
+    const Source<kBf16> y(p.y, b, hh), z(p.z, b, hh);
+#pragma unroll
+    for (int u = 0; u < kHalves; ++u) {
+      sy[u].template load<kVec>(y, off_y, t0 + u * kChunk, n, p.dk);
+      sz[u].template load<kVec>(z, off_z, t0 + u * kChunk, n, p.dv);
+    }
+  };
+  double seg_log = 0.0;                       // wave 0: log2 of the segment's decay
+  auto weigh = [&](int step) {
+    double x[kHalves], end = 0.0;
+#pragma unroll
+    for (int u = 0; u < kHalves; ++u) {
+      const float g = start(step) + u * kChunk + lane < n ? clamp_log_decay(g_next[u]) : 0.0f;
+      x[u] = end + wave_scan((double)g * 1.4426950408889634);
+      end = wave_last(x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kHalves; ++u)
+      lds_upd[step & 1][u * kChunk + lane] = __builtin_amdgcn_exp2f((float)(kReverse ? x[u] : end - x[u])) * p.upd_scale;
+    if (lane == 0) lds_total[step & 1] = __builtin_amdgcn_exp2f((float)end);
+    seg_log += end;
+  };
+  if (count > 0) {
+    fetch(0, 0);
+    if (wave == 0) weigh(0);
+  }
+  for (int it = 0; it < count; ++it) {
+    const int step = it / p.nkv, sub = it % p.nkv;
+    const bool last_sub = sub == p.nkv - 1;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kHalves; ++u) {
+      sy[u].store(lds_y + u * kChunk * PK);
+      sz[u].store(lds_z + u * kChunk * PV);
+    }
+    if (it + 1 < count) fetch(last_sub ? step + 1 : step, last_sub ? 0 : sub + 1);
+    __syncthreads();
+    if (sub == 0) {
+      const float total = lds_total[step & 1];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) S[kt] *= total;
+    }
+    const int ln = fresh(lane);
+#pragma unroll
+    for (int k = 0; k < kStep / 32; ++k) {
+      const Frag zf = M::template cols<4>(lds_z, PV, k * 32, col0, ln);
+      add_outer<kBf16, DK, 4>(S, zf, lds_upd[step & 1] + k * 32, lds_y + k * 32 * PK, PK, ln);
+    }
+    // the next step's weights, where no other wave waits for them
+    if (last_sub && it + 1 < count && wave == 0) weigh(step + 1);
+  }
+  const size_t base = (size_t)blockIdx.x * p.dk * p.dv;
+#pragma unroll
+  for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = state_row(kt, g4) + r, j = col0 + l15;
+      if (i < p.dk && j < p.dv) p.s_out[base + (size_t)i * p.dv + j] = S[kt][r];
+    }
+  if (tid == 0) p.seg_decay[blockIdx.x] = __builtin_amdgcn_exp2f((float)seg_log);
 }
 
-// The narrowest tiles that hold the head sizes: 64 or 128 columns.
-template <bool kReverse, Kind kind>
-hipError_t run_role(const RoleArgs& p, hipStream_t st) {
-  auto go = [&](auto bf, auto vec) {
-    constexpr bool kB = decltype(bf)::value, kV = decltype(vec)::value;
+// The narrowest tiles that hold the head sizes, 64 or 128 columns, for the call's types.
+template <class F>
+hipError_t with_tiles(const RoleArgs& p, F f) {
+  using std::integral_constant;
+  auto sizes = [&](auto bf, auto vec) {
     if (p.dk > 64)
-      return p.dv > 64 ? launch_chunk<kB, 128, 128, kReverse, kind, kV>(p, st) : launch_chunk<kB, 128, 64, kReverse, kind, kV>(p, st);
-    return p.dv > 64 ? launch_chunk<kB, 64, 128, kReverse, kind, kV>(p, st) : launch_chunk<kB, 64, 64, kReverse, kind, kV>(p, st);
+      return p.dv > 64 ? f(bf, vec, integral_constant<int, 128>{}, integral_constant<int, 128>{})
+                       : f(bf, vec, integral_constant<int, 128>{}, integral_constant<int, 64>{});
+    return p.dv > 64 ? f(bf, vec, integral_constant<int, 64>{}, integral_constant<int, 128>{})
+                     : f(bf, vec, integral_constant<int, 64>{}, integral_constant<int, 64>{});
   };
   const std::true_type yes;
   const std::false_type no;
-  if (p.a.bf16) return p.vec ? go(yes, yes) : go(yes, no);
-  return p.vec ? go(no, yes) : go(no, no);
+  if (p.a.bf16) return p.vec ? sizes(yes, yes) : sizes(yes, no);
+  return p.vec ? sizes(no, yes) : sizes(no, no);
+}
+
+template <bool kReverse, Kind kind>
+hipError_t run_role(const RoleArgs& p, hipStream_t st) {
+  return with_tiles(p, [&](auto bf, auto vec, auto dk, auto dv) {
+    constexpr int DV = decltype(dv)::value;
+    chunk_kernel<decltype(bf)::value, decltype(dk)::value, DV, kReverse, kind, decltype(vec)::value>
+        <<<(unsigned)p.a.B * p.a.Hkv * p.nseg, DV * 4, 0, st>>>(p);
+    return hipGetLastError();
+  });
+}
+
+template <bool kReverse>
+hipError_t run_sum(const RoleArgs& p, hipStream_t st) {
+  return with_tiles(p, [&](auto bf, auto vec, auto dk, auto dv) {
+    constexpr int DV = decltype(dv)::value;
+    sum_kernel<decltype(bf)::value, decltype(dk)::value, DV, kReverse, decltype(vec)::value>
+        <<<(unsigned)p.a.B * p.a.Hkv * p.nseg, DV * 4, 0, st>>>(p);
+    return hipGetLastError();
+  });
 }
 
 inline bool rows_vec(const Rows& r, int cols, int bf16) {
