@@ -433,8 +433,13 @@ int pnr_last_profile(pnr_profile* out);
  *              a row's end is not read (it may hold anything), its outputs and gradients are
  *              zeros, and the state is the one after the row's last token (an empty row hands
  *              state_in on)
- * Supported: dtype PNR_F32 and PNR_BF16, 1 <= D_k, D_v <= 128 (others PNR_E_UNSUPPORTED).
- * Products are accumulated, and states, decays and sums held, in fp32.
+ * Supported: dtype PNR_F32 and PNR_BF16, 1 <= D_k, D_v <= 128 (others PNR_E_UNSUPPORTED),
+ * H <= 32768 and B H <= 8 million.  Products are accumulated, and states, decays and sums held,
+ * in fp32.  With bf16 inputs, states and the decay's gradient are as exact as in fp32; o and the
+ * gradients of q, k and v carry one rounding of each score and of the state to bf16 besides
+ * their own.  A NaN or an infinity in a token reaches that token's and later outputs of its
+ * row and head only (for a gradient, those of earlier tokens).  Outputs do not overlap inputs,
+ * but for the states where it is said.
  *
  * None of these calls waits for the device or allocates: the work is enqueued on
  * desc->stream, so they may be recorded into a HIP graph.  Return PNR_OK or a negative
@@ -509,7 +514,8 @@ int pnr_linattn_backward(const pnr_linattn* desc, const void* q, const void* k, 
  * a whole map or sequence.  weight, bias fp32 [C], or both NULL; gate as x or NULL; lens int32
  * [N] or NULL: only the first min(max(lens[n], 0), L) positions of row n belong to it: the
  * others are not read, and y and the gradients are zeros there (a row with none has mean 0
- * and rstd 1 / sqrt(eps)).  mean, rstd: fp32 [N, groups] outputs, kept for the backward pass
+ * and rstd 1 / sqrt(eps)).  N * groups <= 2e9, or 16 million where L > 1 or a group has more than
+ * 512 channels.  mean, rstd: fp32 [N, groups] outputs, kept for the backward pass
  * (NULL: not wanted).  dtype PNR_F32 or PNR_BF16 (x, gate, y and their gradients).  The calls
  * wait for nothing and allocate nothing.  Workspace sizes: 0 means none needed, or an
  * invalid request, which the call then names.

@@ -47,8 +47,9 @@ int validate(const pnr_linattn* d, bool step) {
   if (d->D_k > kMaxHeadDim || d->D_v > kMaxHeadDim)
     return record_error(PNR_E_UNSUPPORTED, "head sizes up to %d are supported (got D_k=%d D_v=%d)", kMaxHeadDim,
                         d->D_k, d->D_v);
+  // a launch holds 2^32 threads, 512 a row and state head; 64 tokens of outputs span less than 2^31 bytes
   const double rows = (double)d->B * (step ? 1 : d->T);
-  if (d->H > (1 << 15) || (double)d->B * d->H > 1.6e7 || rows * d->H * kMaxHeadDim > 4.0e18 || (!step && d->T > (1 << 30)))
+  if (d->H > (1 << 15) || (double)d->B * d->H > 8.0e6 || rows * d->H * kMaxHeadDim > 4.0e18 || (!step && d->T > (1 << 30)))
     return record_error(PNR_E_INVALID, "problem too large for this library's index range");
   return PNR_OK;
 }
