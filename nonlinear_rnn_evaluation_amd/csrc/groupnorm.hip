@@ -164,7 +164,8 @@ struct TokenArgs {
   float* part;                // [gridDim.x][2][C]: sums of dz n and of dz, or nullptr
 };
 
-// x is read once; C = 2048 in 16 groups, bf16 with a gate: see the table of cases
+// x and the gate are read once: 32768 tokens of 2048 channels in 16 groups, bf16 with a gate, 82 us
+// for 403 MB, 4.9 TB/s (a copy's rate); 8 tokens 4.1 us, the launch and one trip to memory.
 template <bool kBf16, bool kVec, int PPL>
 __global__ void __launch_bounds__(256) token_kernel(TokenArgs p) {
   using P = Piece<kBf16, kVec>;
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(256) token_kernel(TokenArgs p) {
   }
 }
 
+// The same tokens: 127 us for 671 MB, 5.3 TB/s.
 template <bool kBf16, bool kVec, int PPL, int kThreads>
 __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenArgs p) {
   using P = Piece<kBf16, kVec>;
@@ -326,7 +328,8 @@ __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenArgs p) {
     }
 }
 
-// dw, db: sums of [rows][2][C] over the rows; 32 channels a block, 32 runs of rows joined in order
+// dw, db: sums of [rows][2][C] over the rows; 32 channels a block, 32 runs of rows joined in order.
+// 256 rows of 2048 channels: 4.8 us.
 __global__ void __launch_bounds__(1024) param_sum_kernel(const float* part, int64_t rows, int C, float* gw, float* gb) {
   __shared__ float red[32][32];
   const int i = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
@@ -428,6 +431,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return red[0] + red[1] + red[2] + red[3];
 }
 
+// 8 maps of 4096 x 320 in bf16, 32 groups: 11 us for 21 MB; too short to fill memory: two trips to it a
+// thread, then the joins.
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(256) map_stats_kernel(MapArgs p) {
   using P = Piece<kBf16, kVec>;
@@ -526,6 +531,7 @@ __global__ void __launch_bounds__(256) map_stats_kernel(MapArgs p) {
   }
 }
 
+// The same maps: 15 us for 42 MB, x out of the last-level cache.
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(256) map_norm_kernel(MapArgs p) {
   using P = Piece<kBf16, kVec>;
@@ -614,6 +620,8 @@ __global__ void __launch_bounds__(256) map_norm_kernel(MapArgs p) {
 }
 
 // Per channel, over a slab: sums of dz n and of dz (kSums); or the gradients of x and the gate.
+// 3 maps of 1001 x 330 in fp32: 7.3 us and 8.1 us for 8 MB read and 8 read, 4 written, by single elements
+// (rows of 330 are not aligned); launches as short as these are bound by their trips to memory.
 template <bool kBf16, bool kVec, bool kSums>
 __global__ void __launch_bounds__(256) map_grad_kernel(MapArgs p) {
   using P = Piece<kBf16, kVec>;

@@ -13,6 +13,10 @@
 // No term is subtracted from a larger one except within a chunk, in fp32: the global form
 // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t would carry every token's rounding to the first.
 // The last term follows from <S, E> at the segment's end X by X <- X + sum b - sum c per chunk.
+//
+// 4 x 16 heads of 128 x 128 over 4096 tokens in bf16: sums 2 x 45 us, scan 28, dq with u and b 118 to
+// 137, dk with c 123 to 142, dv 72 to 83, dg 13 (the spread is from box to box).  The dot products
+// cost dq and dk their three-part S, a fourth tile of rows and, dq, a second set of scores.
 #include <type_traits>
 
 #include "linattn_tile.h"
@@ -50,7 +54,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs p) {
   const int n = row_len(a.lens, b, a.T);
   const size_t base = ((size_t)b * a.Hkv + h) * a.T;
   const int chunks = (a.T + kChunk - 1) / kChunk, c_lo = seg * p.seg_chunks, c_hi = min(c_lo + p.seg_chunks, chunks);
-  float x = p.x_end ? p.x_end[w] : 0.0f;
+  float x = p.x_end && c_lo * kChunk < n ? p.x_end[w] : 0.0f;
   double sum = 0.0;
   for (int ch = c_hi - 1; ch >= c_lo; --ch) {
     const int t = ch * kChunk + lane;
@@ -144,7 +148,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
       p.y = a.k, p.z = a.v, p.dk = a.Dk, p.dv = a.Dv;
       p.s_out = S, p.seg_decay = decay;
       if ((e = run_sum<false>(p, st)) != hipSuccess) return e;
-      sc[count++] = {S, decay, state_in, last, nseg, a.Dk * a.Dv, 0};
+      sc[count++] = {a, l.plan.seg_chunks, S, decay, state_in, last, nseg, a.Dk * a.Dv, 0};
       fwd.s_in = S;
     }
     if (need_e) {
@@ -152,7 +156,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
       p.y = a.q, p.z = d.go, p.dk = a.Dk, p.dv = a.Dv;
       p.s_out = E, p.seg_decay = decay;
       if ((e = run_sum<true>(p, st)) != hipSuccess) return e;
-      sc[count++] = {E, decay, d.gstate_out, d.gstate_in, nseg, a.Dk * a.Dv, 1};
+      sc[count++] = {a, l.plan.seg_chunks, E, decay, d.gstate_out, d.gstate_in, nseg, a.Dk * a.Dv, 1};
       rev.s_in = E;
     }
     if (count && (e = launch_scan(sc, count, rows, st)) != hipSuccess) return e;

@@ -11,23 +11,39 @@ namespace pnr {
 namespace linattn {
 namespace {
 
+constexpr int kAhead = 4;
+
 struct ScanPair {
   ScanArgs p[2];
 };
 
+// A thread an element of the state, over the row's segments in order: a read and a write of each one's
+// state, bound by those bytes: 32 segments of 16 states of 128 x 128, 67 MB in 17 to 19 us.  kAhead reads
+// are asked for before the first is overwritten (1, 4 or 8 of them differ by less than 2 % of a pass).
 __global__ void __launch_bounds__(256) scan_kernel(ScanPair pair) {
   const ScanArgs& p = pair.p[blockIdx.z];
   const int i = blockIdx.y * 256 + threadIdx.x;
   if (i >= p.size) return;
   const size_t row = blockIdx.x;
   float s = p.s_in ? p.s_in[row * p.size + i] : 0.0f;
+  const int nseg = segments_of(row_len(p.a.lens, (int)(row / p.a.Hkv), p.a.T), p.seg_chunks);
   float* seg = p.seg + row * p.nseg * p.size + i;
   const float* dec = p.decay + row * p.nseg;
-  for (int k = 0; k < p.nseg; ++k) {
-    const int at = p.reverse ? p.nseg - 1 - k : k;
-    const float own = seg[(size_t)at * p.size];
-    seg[(size_t)at * p.size] = s;
-    s = fmaf(dec[at], s, own);
+  for (int k0 = 0; k0 < nseg; k0 += kAhead) {
+    float own[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j;
+      if (k < nseg) own[j] = seg[(size_t)(p.reverse ? nseg - 1 - k : k) * p.size];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j;
+      if (k >= nseg) break;
+      const int at = p.reverse ? nseg - 1 - k : k;
+      seg[(size_t)at * p.size] = s;
+      s = fmaf(dec[at], s, own[j]);
+    }
   }
   if (p.s_out) p.s_out[row * p.size + i] = s;
 }
@@ -85,7 +101,7 @@ hipError_t launch_linattn_forward(const LinAttn& a, const float* state_in, void*
   s.s_out = seg, s.seg_decay = decay;
   hipError_t e = run_sum<false>(s, st);
   if (e != hipSuccess) return e;
-  const ScanArgs sc{seg, decay, state_in, state_out, l.plan.nseg, a.Dk * a.Dv, 0};
+  const ScanArgs sc{a, l.plan.seg_chunks, seg, decay, state_in, state_out, l.plan.nseg, a.Dk * a.Dv, 0};
   if ((e = launch_scan(&sc, 1, (int64_t)a.B * a.Hkv, st)) != hipSuccess) return e;
   p.s_in = seg;
   return run_role<false, kOut>(p, st);

@@ -32,6 +32,12 @@ enum Kind {
   kDotK,        // dk, and from it c of the decay's gradient
 };
 
+// Segments with tokens of a row of n.  Those behind them have no sum, decay, entry state or crossing sum.
+__device__ __forceinline__ int segments_of(int n, int seg_chunks) {
+  const int64_t tokens = (int64_t)seg_chunks * kChunk;
+  return (int)((n + tokens - 1) / tokens);
+}
+
 struct RoleArgs {
   LinAttn a;
   Rows x, y, z, e;       // queries, keys, values; the rows that the outputs' dot products are taken with
@@ -358,16 +364,24 @@ __device__ __forceinline__ void add_outer(f32x4 (&S)[DK / 16], const typename Mm
   }
 }
 
-// A block walks the chunks of one segment of one state head, with the state in accumulators: a
-// wave holds 16 columns of S, all DK rows.  (With 32 columns a wave, half the waves and half the
-// reads of X and Y from LDS, 256 registers leave two waves a SIMD: 161 us where this takes
-// KOUT_US us, 16 heads of 128 x 128 over 32768 tokens.)  A chunk:
-//   scores    each wave one or two 16 x 16 tiles a query row tile: P^T = Y X^T, weighted, to LDS           (P is rounded to the
-//             element type: one rounding of each score before a sum over up to 64 of them)
+// A block walks the chunks of one segment of one state head, with the state in accumulators: a wave
+// holds 16 columns of S, all DK rows.  A chunk, in two halves with a barrier between them:
+//   scores    P^T = Y X^T, one or two 16 x 16 tiles a wave, weighted, to LDS (in bf16: one rounding
+//             of each score before a sum over up to 64 of them)
 //   inter     O^T = S^T X^T, weighted; S enters as bf16 (one rounding), or as three bf16 parts
 //             where a dot product in fp32 is taken from it
 //   intra     O^T += Z^T P^T
 //   update    S = exp(G_C) S + Y^T (w Z), w Z as three bf16 parts
+// X and E are done with after the first half and are loaded straight into LDS during the second; Y
+// and Z wait in registers.
+//
+// Measured, 16 heads of 128 x 128 in bf16 over 32768 tokens (kOut, 512 blocks, two a CU): 134 us for
+// 575 MB, 4.3 TB/s, 90 % of a copy's rate.  A chunk costs a CU 4.2 us with two blocks and 4.8 with
+// one; left out one at a time, of those 4.2 the update is 1.1, the outputs 0.7, the loads 0.5, the
+// scores 0.45, S^T X^T 0.4, Z^T P^T 0.2.  Matrix and vector instructions of a SIMD hardly overlap
+// here (24 products and 96 fused multiply-adds, two waves each: 775 and 558 cycles alone, 1214
+// together), so both are kept few.  32 columns a wave in half the waves, with half the reads of
+// X and Y from LDS: 145 us where this took 137.
 template <bool kBf16, int DK, int DV, bool kReverse, Kind kind, bool kVec>
 __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(RoleArgs p) {
   using M = Mma<kBf16>;
@@ -404,6 +418,9 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   const int col0 = wave * 16;                                  // the wave's first column
   const int it0 = wave / (kWaves / 4), jt0 = wave % (kWaves / 4) * JT;   // its score tiles
 
+  const int count = live > c_lo ? (live - c_lo) * nsub : 0;
+  const bool has_state = p.s_in && (count > 0 || p.s_out);     // a segment without tokens has no entry state
+
   f32x4 S[KT];
   auto s_at = [&](int kt, int r) {     // element (row, column) of accumulator register r
     const int i = state_row(kt, g4) + r, j = col0 + l15;
@@ -414,7 +431,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        S[kt][r] = (p.s_in && s_in_range(kt, r)) ? p.s_in[s_at(kt, r)] : 0.0f;
+        S[kt][r] = (has_state && s_in_range(kt, r)) ? p.s_in[s_at(kt, r)] : 0.0f;
 
   // the loads of S end here: a wait for them inside the loop would wait for the tiles behind them
 #pragma unroll
@@ -422,9 +439,9 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     asm volatile("" : "+v"(S[kt]));
 
   if constexpr (kind == kDotK) {
-    if (p.x_end) {
+    if (p.x_end && count > 0) {
       const size_t size = (size_t)p.dk * p.dv;
-      const float* after = seg + 1 < p.nseg ? p.s_entry + size : p.s_last - sbase + blockIdx.x / p.nseg * size;
+      const float* after = seg + 1 < segments_of(n, p.seg_chunks) ? p.s_entry + size : p.s_last - sbase + blockIdx.x / p.nseg * size;
       float s = 0.0f;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
@@ -495,7 +512,6 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
       w.end_hi = end_hi, w.end_lo = (float)(end - (double)end_hi);
     }
   };
-  const int count = live > c_lo ? (live - c_lo) * nsub : 0;
   if (count > 0) {
     fetch_direct(kReverse ? live - 1 : c_lo, 0);
     fetch(kReverse ? live - 1 : c_lo, 0);
@@ -764,7 +780,8 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 }
 
 // The sum of a segment alone, from a zero state, and the segment's decay: chunk_kernel's update, 128
-// tokens a step (64 in fp32), because keys and values in flight are what bounds it.
+// tokens a step (64 in fp32), because keys and values in flight are what bounds it: 16 heads of 128 x 128
+// over 32768 tokens in 78 us, 3.8 TB/s; 64 x 64 heads 22 us where 64 tokens a step took 25.
 template <bool kBf16, int DK, int DV, bool kReverse, bool kVec>
 __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleArgs p) {
   using M = Mma<kBf16>;
@@ -786,7 +803,8 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleAr
   const int h = blockIdx.x / p.nseg % a.Hkv, b = blockIdx.x / p.nseg / a.Hkv;
   const int first = seg * p.seg_chunks * kChunk;        // the segment's tokens: first .. n - 1
   const int n = min(row_len(a.lens, b, a.T), first + p.seg_chunks * kChunk);
-  const int steps = n > first ? (n - first + kStep - 1) / kStep : 0, count = steps * p.nkv;
+  if (n <= first) return;
+  const int steps = (n - first + kStep - 1) / kStep, count = steps * p.nkv;
   const int col0 = wave * 16;
   f32x4 S[KT];
 #pragma unroll
@@ -828,10 +846,8 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleAr
     if (lane == 0) lds_total[step & 1] = __builtin_amdgcn_exp2f((float)end);
     seg_log += end;
   };
-  if (count > 0) {
-    fetch(0, 0);
-    if (wave == 0) weigh(0);
-  }
+  fetch(0, 0);
+  if (wave == 0) weigh(0);
   for (int it = 0; it < count; ++it) {
     const int step = it / p.nkv, sub = it % p.nkv;
     const bool last_sub = sub == p.nkv - 1;
@@ -939,8 +955,10 @@ inline Plan make_plan(const LinAttn& a, bool backward) {
 }
 
 // In place over the segments' own sums: entry states, and the last exit state.  `reverse` runs from
-// the last segment to the first.
+// the last segment to the first.  A row's segments without tokens are left alone.
 struct ScanArgs {
+  LinAttn a;
+  int seg_chunks;
   float* seg;              // [rows][nseg][size]
   const float* decay;      // [rows][nseg]
   const float* s_in;       // [rows][size] or nullptr

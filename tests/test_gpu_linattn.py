@@ -339,3 +339,25 @@ def test_refusals_of_the_binding():
         pnr.linear_attention_step(q, k, v, g, c["state"])                                 # a sequence, not tokens
     with pytest.raises(pnr.PnrError, match="n_slots"):
         pnr.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], g[:, 0].contiguous(), c["state"][:1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("decay", ["token", "head"])
+def test_segments_without_tokens_read_nothing_of_the_workspace(dtype, decay):
+    """Rows that end before, at and behind a segment's end, and an empty one: what an earlier call
+    left in the workspace shows nowhere."""
+    c, go, gs = _case(91, 4, 1000, 4, 2, 64, 96, dtype, decay=decay, lens=[1000, 64, 65, 0])
+    kw = dict(scale=c["scale"], state=c["state"], lens=c["lens"])
+    args = (c["q"], c["k"], c["v"], c["log_decay"])
+    one, back = pnr.linear_attention(*args, **kw), pnr.linear_attention_backward(*args, go, grad_state=gs, **kw)
+    for run, ref in ((lambda w: pnr.linear_attention(*args, workspace=w, **kw), one),
+                     (lambda w: pnr.linear_attention_backward(*args, go, grad_state=gs, workspace=w, **kw), back)):
+        ws = ref["workspace"]
+        for fill in (0xFF, 0x7F):       # NaN, and 3.4e38
+            again = run(torch.full_like(ws.view(torch.uint8), fill).view(ws.dtype))
+            for n in ref:
+                if n != "workspace":
+                    assert torch.isfinite(ref[n]).all(), n
+                    assert torch.equal(ref[n], again[n]), n
+    _check(c, go, gs)
