@@ -18,8 +18,10 @@ struct ScanPair {
 };
 
 // A thread an element of the state, over the row's segments in order: a read and a write of each one's
-// state, bound by those bytes: 32 segments of 16 states of 128 x 128, 67 MB in 17 to 19 us.  kAhead reads
-// are asked for before the first is overwritten (1, 4 or 8 of them differ by less than 2 % of a pass).
+// state, bound by those bytes: 32 segments of 16 states of 128 x 128, 67 MB in 13 us, 5.1 TB/s.  The
+// states and decays of the next kAhead segments are asked for before this kAhead's states are
+// overwritten: a load behind the stores would wait for them (one segment at a time: 19 us; 2 or 8
+// ahead: as 4).
 __global__ void __launch_bounds__(256) scan_kernel(ScanPair pair) {
   const ScanArgs& p = pair.p[blockIdx.z];
   const int i = blockIdx.y * 256 + threadIdx.x;
@@ -29,21 +31,27 @@ __global__ void __launch_bounds__(256) scan_kernel(ScanPair pair) {
   const int nseg = segments_of(row_len(p.a.lens, (int)(row / p.a.Hkv), p.a.T), p.seg_chunks);
   float* seg = p.seg + row * p.nseg * p.size + i;
   const float* dec = p.decay + row * p.nseg;
-  for (int k0 = 0; k0 < nseg; k0 += kAhead) {
-    float own[kAhead];
+  auto at = [&](int k) { return p.reverse ? nseg - 1 - k : k; };
+  float own[2][kAhead], d[2][kAhead];
+  auto fetch = [&](int half, int k0) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = k0 + j;
-      if (k < nseg) own[j] = seg[(size_t)(p.reverse ? nseg - 1 - k : k) * p.size];
-    }
+    for (int j = 0; j < kAhead; ++j)
+      if (k0 + j < nseg) own[half][j] = seg[(size_t)at(k0 + j) * p.size], d[half][j] = dec[at(k0 + j)];
+  };
+  auto walk = [&](int half, int k0) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int k = k0 + j;
-      if (k >= nseg) break;
-      const int at = p.reverse ? nseg - 1 - k : k;
-      seg[(size_t)at * p.size] = s;
-      s = fmaf(dec[at], s, own[j]);
-    }
+    for (int j = 0; j < kAhead; ++j)
+      if (k0 + j < nseg) {
+        seg[(size_t)at(k0 + j) * p.size] = s;
+        s = fmaf(d[half][j], s, own[half][j]);
+      }
+  };
+  fetch(0, 0);
+  for (int k0 = 0; k0 < nseg; k0 += 2 * kAhead) {
+    fetch(1, k0 + kAhead);
+    walk(0, k0);
+    fetch(0, k0 + 2 * kAhead);
+    walk(1, k0 + kAhead);
   }
   if (p.s_out) p.s_out[row * p.size + i] = s;
 }
