@@ -14,7 +14,7 @@
 // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t would carry every token's rounding to the first.
 // The last term follows from <S, E> at the segment's end X by X <- X + sum b - sum c per chunk.
 //
-// 4 x 16 heads of 128 x 128 over 4096 tokens in bf16: sums 2 x 45 us, scan 28, dq with u and b 118 to
+// 4 x 16 heads of 128 x 128 over 4096 tokens in bf16: sums 2 x 45 us, scan 25, dq with u and b 118 to
 // 137, dk with c 123 to 142, dv 72 to 83, dg 13 (the spread is from box to box).  The dot products
 // cost dq and dk their three-part S, a fourth tile of rows and, dq, a second set of scores.
 #include <type_traits>
