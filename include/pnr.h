@@ -435,9 +435,9 @@ int pnr_last_profile(pnr_profile* out);
  *              state_in on)
  * Supported: dtype PNR_F32 and PNR_BF16, 1 <= D_k, D_v <= 128 (others PNR_E_UNSUPPORTED),
  * H <= 32768 and B H <= 8 million.  Products are accumulated, and states, decays and sums held,
- * in fp32.  With bf16 inputs, states and the decay's gradient are as exact as in fp32; o and the
- * gradients of q, k and v carry one rounding of each score and of the state to bf16 besides
- * their own.  A NaN or an infinity in a token reaches that token's and later outputs of its
+ * in fp32.  With bf16 inputs, states and the decay's gradient are as exact as in fp32, and o and the
+ * gradients of q, k and v are rounded once, at the end (inside, scores and the state are held
+ * to 2^-17 of each value).  A NaN or an infinity in a token reaches that token's and later outputs of its
  * row and head only (for a gradient, those of earlier tokens).  Outputs do not overlap inputs,
  * but for the states where it is said.
  *

@@ -74,7 +74,7 @@ struct Mma<true> {
   using Elt = uint16_t;
   using Frag = bf16x8;
   static constexpr int kPiece = 8;     // elements of a 16-byte piece
-  static constexpr int kPadY = 24, kPadZ = 8;   // elements of padding a row: rows start 12 and 4 banks apart
+  static constexpr int kPadZ = 8;      // elements of padding a row: rows start 4 banks apart
   static __device__ __forceinline__ f32x4 mul(Frag a, Frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -85,9 +85,12 @@ struct Mma<true> {
   template <int kStride>
   static __device__ __forceinline__ Frag cols(const Elt* tile, int pitch, int row0, int col0, int lane) {
     const Elt* p = tile + (row0 + (lane >> 4) * 8 + ((lane >> 2) & 3)) * pitch + col0 + (lane & 3) * kStride;
+    return cols_at(p, p + 4 * pitch);
+  }
+  static __device__ __forceinline__ Frag cols_at(const Elt* p, const Elt* four_rows_on) {
     using L = __attribute__((address_space(3))) s16x4;
     struct { s16x4 a, b; } w{__builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)p),
-                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + 4 * pitch))};
+                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)four_rows_on)};
     return __builtin_bit_cast(Frag, w);
   }
   static __device__ __forceinline__ Frag none() { return Frag{}; }
@@ -98,7 +101,7 @@ struct Mma<false> {
   using Elt = float;
   struct Frag { float v[8]; };
   static constexpr int kPiece = 4;
-  static constexpr int kPadY = 4, kPadZ = 4;
+  static constexpr int kPadZ = 4;
   static __device__ __forceinline__ f32x4 mul(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
@@ -124,9 +127,10 @@ struct Mma<false> {
 };
 
 // Eight fp32 values as an operand: in fp32 as they are; in bf16 as the sum of kParts bf16 values,
-// each the rounding of what the ones before it leave.  One part is good to 2^-9 of each value, and
-// goes where the result is rounded to bf16 anyway; three are good to 2^-27, and go where a
-// result in fp32 depends on them (two, 2^-18, showed in such results: 2e-6 of a state).
+// each the rounding of what the ones before it leave.  Two parts are good to 2^-17 of each value, and
+// go where the result is rounded to bf16 afterwards (one part, 2^-9, made outputs off by 2.3e-3 of their norm
+// where their own rounding is 1.7e-3); three are good to 2^-26, and go where a result in fp32 depends on
+// them (two showed in such results: 2e-6 of a state).
 template <bool kBf16, int kParts>
 struct Split;
 template <int kParts>
@@ -177,6 +181,46 @@ __device__ __forceinline__ int fresh(int v) {
 template <bool kBf16, int kCols, int kThreads>
 struct Direct;
 
+// 64 rows of keys in LDS, which are read by rows (scores) and by columns (the state's update).
+template <bool kBf16, int kCols>
+struct Keys;
+
+// bf16: no padding; the 16-byte pieces of a row are permuted by the row so that neither 16 rows of one
+// piece nor the four rows x four pieces of a transposing read meet in a bank.
+template <int kCols>
+struct Keys<true, kCols> {
+  using M = Mma<true>;
+  using Elt = M::Elt;
+  static constexpr int kPerRow = kCols / M::kPiece, kSize = kChunk * kCols;
+  static __device__ __forceinline__ int permute(int row) {
+    return (kCols == 128 ? (row & 3) << 2 : (row & 2) << 1) | (row >> 2 & 3);
+  }
+  // first element of a row's piece; rows 16 apart are permuted alike
+  static __device__ __forceinline__ int at(int row, int piece) { return (row * kPerRow + (piece ^ permute(row))) * M::kPiece; }
+  static __device__ __forceinline__ M::Frag rows(const Elt* t, int row, int k, int g) {
+    return M::rows(t + (at(row, g) ^ k * 32));
+  }
+  // rows 32 k + 8 g + 0 .. 7 of the columns that tile kt of the state stands for (see state_row)
+  static __device__ __forceinline__ M::Frag cols(const Elt* t, int k, int kt, int lane) {
+    const int row = (lane >> 4) * 8 + ((lane >> 2) & 3), first = at(row, lane & 3) ^ kt / 2 * 32;
+    const Elt* p = t + k * 32 * kCols + kt % 2 * 4;
+    return M::cols_at(p + first, p + (first ^ 8) + 4 * kCols);       // four rows on, the permutation differs by a piece
+  }
+};
+template <int kCols>
+struct Keys<false, kCols> {
+  using M = Mma<false>;
+  using Elt = M::Elt;
+  static constexpr int kPitch = kCols + 4, kSize = kChunk * kPitch;
+  static __device__ __forceinline__ int at(int row, int piece) { return row * kPitch + piece * M::kPiece; }
+  static __device__ __forceinline__ M::Frag rows(const Elt* t, int row, int k, int g) {
+    return M::rows(t + row * kPitch + k * 32 + g * 8);
+  }
+  static __device__ __forceinline__ M::Frag cols(const Elt* t, int k, int kt, int lane) {
+    return M::cols<8>(t, kPitch, k * 32, state_row(kt, 0), lane);
+  }
+};
+
 // A buffer from p on, of any length: offsets from kNowhere on lie behind its end, where loads give
 // zeros and stores are dropped.
 constexpr uint32_t kNowhere = 0x80000000u;
@@ -197,7 +241,7 @@ struct Source {
 };
 
 // 64 rows x kCols of one operand on its way from memory to LDS: 16-byte pieces in registers.
-template <bool kBf16, int kCols, int kThreads, int kPitch>
+template <bool kBf16, int kCols, int kThreads>
 struct Stage {
   using M = Mma<kBf16>;
   using Elt = typename M::Elt;
@@ -242,9 +286,19 @@ struct Stage {
     const int tid = threadIdx.x, c = (tid % kPerRow) * M::kPiece;
     return c < cols ? tid / kPerRow * pitch + c * (uint32_t)sizeof(Elt) : kNowhere;
   }
+  // rows `pitch` apart
+  template <int kPitch>
   __device__ __forceinline__ void store(Elt* tile) const {
     const int tid = fresh(threadIdx.x);
-    Elt* at = tile + (tid / kPerRow) * kPitch + (tid % kPerRow) * M::kPiece;
+    put<kPitch>(tile + (tid / kPerRow) * kPitch + (tid % kPerRow) * M::kPiece);
+  }
+  __device__ __forceinline__ void store_keys(Elt* tile) const {
+    static_assert(!kBf16 || kThreads / kPerRow % 16 == 0, "one permutation for all of a thread's rows");
+    const int tid = fresh(threadIdx.x);
+    put<Keys<kBf16, kCols>::kSize / kChunk>(tile + Keys<kBf16, kCols>::at(tid / kPerRow, tid % kPerRow));
+  }
+  template <int kPitch>
+  __device__ __forceinline__ void put(Elt* at) const {
 #pragma unroll
     for (int i = 0; i < kN; ++i) *(uint4*)(at + i * (kThreads / kPerRow) * kPitch) = v[i];
   }
@@ -318,18 +372,59 @@ __device__ __forceinline__ float group_sum(float v) {      // over the four grou
   return v + __shfl_xor(v, 32);
 }
 
-// Where the scores of row i from column j on stand, j a multiple of 4: rows of 64 without padding,
-// their 16-byte pieces permuted by the row so that 16 rows of one column spread over the banks.
-template <bool kBf16>
-__device__ __forceinline__ int score_at(int i, int j) {
-  constexpr int kPiece = Mma<kBf16>::kPiece;
-  return i * kChunk + (((j / kPiece) ^ (i & (64 / kPiece - 1))) * kPiece) + j % kPiece;
-}
-template <bool kBf16>
-__device__ __forceinline__ typename Mma<kBf16>::Frag score_rows(const typename Mma<kBf16>::Elt* p, int i, int j) {
-  if constexpr (kBf16) return Mma<true>::rows(p + score_at<true>(i, j));
-  else return Mma<false>::two(p + score_at<false>(i, j), p + score_at<false>(i, j + 4));
-}
+// A chunk's weighted scores in LDS, row i of which may see column j <= i (j >= i against time).
+template <bool kBf16, bool kReverse>
+struct Scores;
+
+// bf16: two parts, and of the 16 x 16 tiles only the ten on and before the diagonal.  16 rows of half a tile's
+// columns, 16 bytes each, lie side by side in the banks.
+template <bool kReverse>
+struct Scores<true, kReverse> {
+  using M = Mma<true>;
+  using Elt = M::Elt;
+  static constexpr int kParts = 2, kPart = 10 * 256, kSize = kParts * kPart;
+  static __device__ __forceinline__ int tile(int it, int jt) {
+    if (kReverse) it = 3 - it, jt = 3 - jt;
+    return (it * (it + 1) / 2 + jt) * 256;
+  }
+  // columns j .. j + 3 of row i, within tile (it, jt)
+  static __device__ __forceinline__ void put(Elt* p, int it, int jt, int i, int j, const float (&s)[4]) {
+    if (kReverse ? jt < it : jt > it) return;
+    Elt* at = p + tile(it, jt) + i * 16 + j;
+    const uint2 hi = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
+    *(uint2*)at = hi;
+    *(uint2*)(at + kPart) = make_uint2(pack_bf16(s[0] - __uint_as_float(hi.x << 16), s[1] - __uint_as_float(hi.x & 0xffff0000u)),
+                                       pack_bf16(s[2] - __uint_as_float(hi.y << 16), s[3] - __uint_as_float(hi.y & 0xffff0000u)));
+  }
+  // rows of tile row m, columns 32 k + 8 g + 0 .. 7: two tiles, one of which may be the one behind the diagonal
+  static __device__ __forceinline__ M::Frag rows(const Elt* p, int part, int m, int k, int lane) {
+    const int g = lane >> 4, half = g >> 1;
+    const M::Frag f = M::rows(p + part * kPart + tile(m, 2 * k) + (kReverse ? -half : half) * 256 + (lane & 15) * 16 + (g & 1) * 8);
+    if (m / 2 != k || m % 2 != (kReverse ? 1 : 0)) return f;
+    return half == (kReverse ? 0 : 1) ? M::none() : f;
+  }
+  static __device__ __forceinline__ float value(const Elt* p, int i, int j) {
+    const Elt* at = p + tile(i >> 4, j >> 4) + (i & 15) * 16 + (j & 15);
+    return bf16_to_f32(at[0]) + bf16_to_f32(at[kPart]);
+  }
+};
+// fp32: rows of 64 without padding, their 16-byte pieces permuted by the row so that 16 rows of one
+// column spread over the banks.
+template <bool kReverse>
+struct Scores<false, kReverse> {
+  using M = Mma<false>;
+  using Elt = M::Elt;
+  static constexpr int kParts = 1, kSize = kChunk * kChunk;
+  static __device__ __forceinline__ int at(int i, int j) { return i * kChunk + (((j / 4) ^ (i & 15)) * 4) + j % 4; }
+  static __device__ __forceinline__ void put(Elt* p, int it, int jt, int i, int j, const float (&s)[4]) {
+    *(float4*)(p + at(it * 16 + i, jt * 16 + j)) = make_float4(s[0], s[1], s[2], s[3]);
+  }
+  static __device__ __forceinline__ M::Frag rows(const Elt* p, int, int m, int k, int lane) {
+    const int i = m * 16 + (lane & 15), j = k * 32 + (lane >> 4) * 8;
+    return M::two(p + at(i, j), p + at(i, j + 4));
+  }
+  static __device__ __forceinline__ float value(const Elt* p, int i, int j) { return p[at(i, j)]; }
+};
 
 // A chunk's weights.
 struct alignas(16) Weights {
@@ -340,10 +435,11 @@ struct alignas(16) Weights {
   float end_hi, end_lo;              // G_C
 };
 
-// S += Y^T (w Z) over 32 tokens, for 16 columns of Z held as an operand; kGroup row tiles at a time.
+// S += Y^T (w Z) over the 32 tokens 32 k + 0 .. 31 of y, for 16 columns of Z held as an operand; kGroup row
+// tiles at a time.
 template <bool kBf16, int DK, int kGroup>
 __device__ __forceinline__ void add_outer(f32x4 (&S)[DK / 16], const typename Mma<kBf16>::Frag& zf, const float* w,
-                                          const typename Mma<kBf16>::Elt* y, int pitch, int lane) {
+                                          const typename Mma<kBf16>::Elt* y, int k, int lane) {
   using M = Mma<kBf16>;
   const float* wp = w + (lane >> 4) * 8;
   float v[8];
@@ -356,7 +452,7 @@ __device__ __forceinline__ void add_outer(f32x4 (&S)[DK / 16], const typename Mm
   for (int kt = 0; kt < DK / 16; kt += kGroup) {
     typename M::Frag yf[kGroup];
 #pragma unroll
-    for (int q = 0; q < kGroup; ++q) yf[q] = M::template cols<8>(y, pitch, 0, state_row(kt + q, 0), lane);
+    for (int q = 0; q < kGroup; ++q) yf[q] = Keys<kBf16, DK>::cols(y, k, kt + q, lane);
 #pragma unroll
     for (int part = (kBf16 ? 3 : 1); part--;)
 #pragma unroll
@@ -366,10 +462,9 @@ __device__ __forceinline__ void add_outer(f32x4 (&S)[DK / 16], const typename Mm
 
 // A block walks the chunks of one segment of one state head, with the state in accumulators: a wave
 // holds 16 columns of S, all DK rows.  A chunk, in two halves with a barrier between them:
-//   scores    P^T = Y X^T, one or two 16 x 16 tiles a wave, weighted, to LDS (in bf16: one rounding
-//             of each score before a sum over up to 64 of them)
-//   inter     O^T = S^T X^T, weighted; S enters as bf16 (one rounding), or as three bf16 parts
-//             where a dot product in fp32 is taken from it
+//   scores    P^T = Y X^T, two or four 16 x 16 tiles a wave, weighted, to LDS (in bf16: as two parts)
+//   inter     O^T = S^T X^T, weighted; S enters as two bf16 parts, or as three where a dot product in
+//             fp32 is taken from it
 //   intra     O^T += Z^T P^T
 //   update    S = exp(G_C) S + Y^T (w Z), w Z as three bf16 parts
 // X and E are done with after the first half and are loaded straight into LDS during the second; Y
@@ -390,16 +485,18 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   constexpr int kWaves = DV / 16, kThreads = kWaves * 64;
   constexpr int KT = DK / 16;               // row tiles of S
   constexpr int JT = 16 / kWaves;           // score tiles a wave takes of its query row tile
-  constexpr int PK = DK + M::kPadY, PV = DV + M::kPadZ;     // rows of Y and Z in LDS
+  constexpr int PV = DV + M::kPadZ;         // rows of Z in LDS
+  using KY = Keys<kBf16, DK>;
+  using SC = Scores<kBf16, kReverse>;
   constexpr bool kDots = kind == kDotQ || kind == kDotK;
-  constexpr int kParts = kDots ? 3 : 1;
+  constexpr int kParts = kDots ? 3 : 2;     // of S
   // LDS (bf16, 128 x 128: two blocks a CU, also with the dot products' arrays).  Arrays of their own,
   // so that a read of one need not wait for loads on their way to another.
   __shared__ alignas(16) Elt lds_x[kChunk * DK];           // Direct
-  __shared__ alignas(16) Elt lds_y[kChunk * PK];
+  __shared__ alignas(16) Elt lds_y[KY::kSize];
   __shared__ alignas(16) Elt lds_z[kChunk * PV];
   __shared__ alignas(16) Elt lds_e[kDots ? kChunk * DV : 1];          // Direct
-  __shared__ alignas(16) Elt lds_p[kChunk * kChunk];       // scores [i][j], see score_at
+  __shared__ alignas(16) Elt lds_p[SC::kSize];
   __shared__ Weights lds_w[2];                                        // this chunk's and the next one's
   __shared__ float lds_dot[kDots ? kWaves : 1][kChunk];               // the waves' parts of dot products and row sums
   __shared__ float lds_bsum[kDots ? kWaves : 1];
@@ -462,8 +559,8 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 
   using TX = Direct<kBf16, DK, kThreads>;
   using TE = Direct<kBf16, DV, kThreads>;
-  Stage<kBf16, DK, kThreads, PK> sx, sy;
-  Stage<kBf16, DV, kThreads, PV> sz, se;
+  Stage<kBf16, DK, kThreads> sx, sy;
+  Stage<kBf16, DV, kThreads> sz, se;
   const uint32_t es = sizeof(Elt);
   const uint32_t off_x = kVec ? TX::offset((uint32_t)p.x.st * es, p.dk) : 0, off_e = kVec && kDots ? TE::offset((uint32_t)p.e.st * es, p.dv) : 0;
   const uint32_t off_y = kVec ? decltype(sy)::offset((uint32_t)p.y.st * es, p.dk) : 0, off_z = kVec ? decltype(sz)::offset((uint32_t)p.z.st * es, p.dv) : 0;
@@ -533,8 +630,8 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         if constexpr (kDots) se.store_permuted(lds_e);
       }
     if (new_yz) {
-      sy.store(lds_y);
-      sz.store(lds_z);
+      sy.store_keys(lds_y);
+      sz.template store<PV>(lds_z);
     }
     const int next_sub = last_sub ? 0 : sub + 1, next_c = last_sub ? (kReverse ? c - 1 : c + 1) : c;
     if constexpr (kVec) {
@@ -556,7 +653,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         for (int k = 0; k < DK / 32; ++k) {
           const Frag xf = TX::rows(lds_x, i, k, g4 / 4);
 #pragma unroll
-          for (int q = 0; q < JT; ++q) P[q] = M::mul(M::rows(lds_y + ((jt0 + q) * 16 + l15) * PK + k * 32 + g4 * 2), xf, k ? P[q] : zero);
+          for (int q = 0; q < JT; ++q) P[q] = M::mul(KY::rows(lds_y, (jt0 + q) * 16 + l15, k, g4 / 4), xf, k ? P[q] : zero);
         }
         if constexpr (kind == kDotQ) {
 #pragma unroll
@@ -595,10 +692,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
               }
             }
           }
-          if constexpr (kBf16)
-            *(uint2*)(lds_p + score_at<true>(i, j0)) = make_uint2(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]));
-          else
-            *(float4*)(lds_p + score_at<false>(i, j0)) = make_float4(s[0], s[1], s[2], s[3]);
+          SC::put(lds_p, it0, jt, l15, g4, s);
         }
         if constexpr (kind == kDotQ) row = group_sum(row);
       }
@@ -610,7 +704,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] = S[2 * k][r], v[4 + r] = S[2 * k + 1][r];
           const Split<kBf16, kParts> sf(v);
-          constexpr int MG = kDots ? 2 : 4;     // row tiles at a time: three parts leave room for two
+          constexpr int MG = kDots ? 2 : 4;     // row tiles at a time: with dot products there is room for two
 #pragma unroll
           for (int m0 = 0; m0 < 4; m0 += MG) {
             Frag xf[MG];
@@ -667,9 +761,11 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            if (kReverse ? (k == 1 || m < 2) : (k == 0 || m >= 2))
-              O[m] = M::mul(zf[k], score_rows<kBf16>(lds_p, m * 16 + l15, k * 32 + g4 * 2), O[m]);
+          for (int part = SC::kParts; part--;)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              if (kReverse ? (k == 1 || m < 2) : (k == 0 || m >= 2))
+                O[m] = M::mul(zf[k], SC::rows(lds_p, part, m, k, lane2), O[m]);
       } else {
         // an infinity or a NaN among the values reaches only the outputs that may see its token:
         // a zero score times it would not be zero, so masked products are left out one by one
@@ -682,7 +778,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
           for (int m = 0; m < 4; ++m) {
             const int i = m * 16 + l15;
             if (kReverse ? j >= i : j <= i) {
-              const float s = Elem<kBf16>::load(lds_p + score_at<kBf16>(i, j & ~3) + (j & 3));
+              const float s = SC::value(lds_p, i, j);
 #pragma unroll
               for (int r = 0; r < 4; ++r) O[m][r] = fmaf(s, z[r], O[m][r]);
             }
@@ -751,7 +847,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         for (int kt = 0; kt < KT; ++kt) S[kt] *= total;
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) add_outer<kBf16, DK, kDots ? 2 : 4>(S, zf[k], wt.upd + k * 32, lds_y + k * 32 * PK, PK, lane2);
+      for (int k = 0; k < 2; ++k) add_outer<kBf16, DK, kDots ? 2 : 4>(S, zf[k], wt.upd + k * 32, lds_y, k, lane2);
     }
     // the next chunk's weights, where no other wave waits for them
     if (last_sub && it + 1 < count && wave == 0) weigh(next_c, ~step & 1);
@@ -789,10 +885,11 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleAr
   using Frag = typename M::Frag;
   constexpr int kWaves = DV / 16, kThreads = kWaves * 64, KT = DK / 16;
   constexpr int kHalves = kBf16 ? 2 : 1, kStep = kHalves * kChunk;
-  constexpr int PK = DK + M::kPadY, PV = DV + M::kPadZ;
-  using SY = Stage<kBf16, DK, kThreads, PK>;
-  using SZ = Stage<kBf16, DV, kThreads, PV>;
-  __shared__ alignas(16) Elt lds_y[kStep * PK];
+  constexpr int PV = DV + M::kPadZ;
+  using KY = Keys<kBf16, DK>;
+  using SY = Stage<kBf16, DK, kThreads>;
+  using SZ = Stage<kBf16, DV, kThreads>;
+  __shared__ alignas(16) Elt lds_y[kHalves * KY::kSize];
   __shared__ alignas(16) Elt lds_z[kStep * PV];
   __shared__ alignas(16) float lds_upd[2][kStep];       // the weights of y z^T, of this step and the next
   __shared__ float lds_total[2];
@@ -854,8 +951,8 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleAr
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kHalves; ++u) {
-      sy[u].store(lds_y + u * kChunk * PK);
-      sz[u].store(lds_z + u * kChunk * PV);
+      sy[u].store_keys(lds_y + u * KY::kSize);
+      sz[u].template store<PV>(lds_z + u * kChunk * PV);
     }
     if (it + 1 < count) fetch(last_sub ? step + 1 : step, last_sub ? 0 : sub + 1);
     __syncthreads();
@@ -868,7 +965,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleAr
 #pragma unroll
     for (int k = 0; k < kStep / 32; ++k) {
       const Frag zf = M::template cols<4>(lds_z, PV, k * 32, col0, ln);
-      add_outer<kBf16, DK, 4>(S, zf, lds_upd[step & 1] + k * 32, lds_y + k * 32 * PK, PK, ln);
+      add_outer<kBf16, DK, 4>(S, zf, lds_upd[step & 1] + k * 32, lds_y + k / 2 * KY::kSize, k % 2, ln);
     }
     // the next step's weights, where no other wave waits for them
     if (last_sub && it + 1 < count && wave == 0) weigh(step + 1);
