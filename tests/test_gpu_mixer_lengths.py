@@ -1,0 +1,37 @@
+"""The mixed layer on rows of unusual lengths: what a row hands on is what its own tokens leave, whatever
+the batch it lies in."""
+import torch
+import pytest
+
+from nonlinear_rnn_evaluation_amd import mixer
+
+
+def _layer():
+    return mixer.Mixer(48, 4, 2, 16, 24, seed=3)
+
+
+def _x(B, T, seed=4):
+    return torch.randn(B, T, 48, generator=torch.Generator().manual_seed(seed)).cuda()
+
+
+def _lens(*n):
+    return torch.tensor(n, dtype=torch.int32).cuda()
+
+
+def _near(a, b):
+    """The same fp32 computation in another batch: 1e-4, as the layer's other tests."""
+    assert torch.isfinite(a).all() and (a - b).abs().max() <= 1e-4 * b.abs().max().clamp(min=1e-3)
+
+
+@pytest.mark.gpu
+def test_an_empty_row_hands_on_the_initial_states():
+    m, x = _layer(), _x(3, 70)
+    r = m.prompt(x, _lens(70, 0, 1))
+    assert (r["h"][1] == 0).all() and (r["S"][1] == 0).all()
+    # its first token is the first token of a sequence
+    pool, slots, tok = r["S"].clone(), _lens(0, 1, 2), _x(3, 1, seed=5)
+    out, h = m.token(tok[:, 0].contiguous(), r["h"].contiguous(), pool, slots)
+    first = m.prompt(tok[1:2])
+    _near(out[1], first["out"][0, 0])
+    _near(h[1], first["h"][0])
+    _near(pool[1], first["S"][0])
