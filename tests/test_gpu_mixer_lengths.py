@@ -35,3 +35,13 @@ def test_an_empty_row_hands_on_the_initial_states():
     _near(out[1], first["out"][0, 0])
     _near(h[1], first["h"][0])
     _near(pool[1], first["S"][0])
+
+
+@pytest.mark.gpu
+def test_lengths_outside_the_sequence_are_clamped():
+    """As the attention takes them: min(max(n, 0), T) tokens."""
+    m, x = _layer(), _x(3, 70)
+    a, b = m.prompt(x, _lens(-3, 1000, 2 ** 31 - 1)), m.prompt(x, _lens(0, 70, 70))
+    for n in ("h", "S"):
+        assert torch.equal(a[n], b[n]), n
+    assert torch.equal(a["out"][1:], b["out"][1:])
