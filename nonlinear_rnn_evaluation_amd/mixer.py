@@ -59,12 +59,14 @@ class Mixer:
     def prompt(self, x, lens=None):
         """x [B, T, D], lens int32 [B] (row b has min(max(lens[b], 0), T) tokens): dict(out [B, T, D],
         h [B, D] and S, the states after each row's last token; a row without one hands the initial states
-        on, zeros).  What lies behind a row's end is not meaningful."""
+        on, zeros).  What lies behind a row's end in x is not read, and in out not meaningful."""
+        n = torch.full((x.shape[0],), x.shape[1], device=x.device) if lens is None else lens.long().clamp(0, x.shape[1])
+        if lens is not None:        # the recurrence runs over whole rows: zeros converge and stay finite
+            x = torch.where(torch.arange(x.shape[1], device=x.device)[None, :, None] < n[:, None, None], x, x.new_zeros(()))
         h = self._states(x, None)
         q, k, v, gate, g = self._project(h)
         r = pnr.linear_attention(q, k, v, g, lens=lens)
         y = self._normed(r["o"], gate)["y"].view(*x.shape[:2], -1)
-        n = torch.full((x.shape[0],), x.shape[1], device=x.device) if lens is None else lens.long().clamp(0, x.shape[1])
         last = h[torch.arange(len(h), device=h.device), (n - 1).clamp(min=0)]
         return dict(out=y @ self.W_out, S=r["state"], h=torch.where(n[:, None] > 0, last, torch.zeros_like(last)))
 

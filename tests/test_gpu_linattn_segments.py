@@ -1,0 +1,84 @@
+"""Linear attention where a block walks several chunks: segments of more than one chunk (many rows), and
+many rows without segments, against the fp64 token-by-token oracle.
+
+Tolerances, as the 2-norm of an output's error over the output's:
+  fp32 outputs and states  2^-20: an operand kept as three bf16 parts is off by at most 2^-26, a weight by
+                 the exponential's 2^-23 and the rounding of its argument, and the sums, over a memory of
+                 some tens of tokens, add about 2^-24 times the root of its length: 2^-21, and room
+                 for a factor of two
+  fp32 gradients 2^-19: as above, with products of two such operands
+  bf16 outputs   2^-8: the output's own rounding (2^-9 of each element at most) and room for ties
+  the decay's gradient 4 * 2^-19 of its terms' root sum of squares
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from nonlinear_rnn_evaluation_amd import pnr
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _near(name, got, ref, tol, norm=None):
+    got = got.double().cpu().numpy()
+    assert got.shape == ref.shape and np.isfinite(got).all(), name
+    norm = np.linalg.norm(ref) if norm is None else norm
+    err = np.linalg.norm(got - ref)
+    print(f"#   {name}: {err / max(norm, 1e-300):.2e} (tol {tol:.1e})", flush=True)
+    assert err <= tol * norm, (name, err, norm)
+
+
+def _check(seed, B, T, H, Hkv, Dk, Dv, dtype, decay, lens):
+    gen = torch.Generator().manual_seed(seed)
+    draw = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    q, k, v, go = (draw(B, T, h, d).to(dtype).cuda() for h, d in ((H, Dk), (Hkv, Dk), (Hkv, Dv), (H, Dv)))
+    g = -torch.empty(B, T, Hkv).exponential_(20.0, generator=gen) if decay == "token" else -0.1 / torch.arange(1, Hkv + 1)
+    g, state, gs = g.cuda(), draw(B, Hkv, Dk, Dv).cuda(), draw(B, Hkv, Dk, Dv).cuda()
+    ln = None if lens is None else torch.tensor([lens[b % len(lens)] for b in range(B)], dtype=torch.int32).cuda()
+    kw = dict(scale=Dk ** -0.5, state=state, lens=ln)
+    got = pnr.linear_attention(q, k, v, g, **kw)
+    d = pnr.linear_attention_backward(q, k, v, g, go, grad_state=gs, **kw)
+    q, k, v, g, go, state, gs = (t.double().cpu().numpy() for t in (q, k, v, g, go, state, gs))
+    n = None if ln is None else ln.cpu().numpy()
+    o, S = O.linear_attention(q, k, v, g, Dk ** -0.5, state, n)
+    ref = O.linear_attention_grad(q, k, v, g, Dk ** -0.5, go, state, n, gs)
+    out, grad = (2.0 ** -8, 2.0 ** -8) if dtype == BF16 else (2.0 ** -20, 2.0 ** -19)
+    _near("o", got["o"], o, out)
+    _near("state", got["state"], S, 2.0 ** -20)
+    for name in ("q", "k", "v"):
+        _near("grad_" + name, d[name], ref[name], grad)
+    _near("grad_state", d["state"], ref["state"], 2.0 ** -19)
+    each = np.linalg.norm(ref["log_decay"])
+    _near("grad_log_decay", d["log_decay"], ref["log_decay" if decay == "token" else "log_decay_head"], 4 * 2.0 ** -19, each)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("decay,lens", [("token", None), ("head", [1190, 700, 193, 64, 0, 1189])], ids=["even", "ragged"])
+def test_segments_of_several_chunks(decay, lens, dtype):
+    """64 state heads, 19 chunks: segments of 3 chunks in bf16 and 5 in fp32, the last one shorter, the last
+    chunk partly filled; ragged rows end inside, at and before segments' ends."""
+    _check(1, 8, 1190, 16, 8, 16, 24, dtype, decay, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_an_even_number_of_chunks_a_segment(dtype):
+    """40 state heads of 33 x 70 in rows that are not aligned, 32 chunks: segments of 3 and 6 chunks."""
+    _check(2, 10, 2048, 4, 4, 33, 70, dtype, "token", None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("decay,lens", [("head", None), ("token", [400, 128, 65, 0])], ids=["even", "ragged"])
+def test_many_rows_without_segments(decay, lens, dtype):
+    """300 state heads: a block walks all seven chunks of its row."""
+    _check(3, 30, 400, 20, 10, 16, 24, dtype, decay, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_wide_tiles_over_several_chunks(dtype):
+    """64 state heads of 128 x 128 shared by two query heads each, segments of several chunks."""
+    _check(4, 16, 640, 8, 4, 128, 128, dtype, "token", [640, 511, 129])

@@ -45,3 +45,20 @@ def test_lengths_outside_the_sequence_are_clamped():
     for n in ("h", "S"):
         assert torch.equal(a[n], b[n]), n
     assert torch.equal(a["out"][1:], b["out"][1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("junk", [float("nan"), float("inf"), -1e30])
+def test_padding_may_hold_anything(junk):
+    m, x = _layer(), _x(3, 70)
+    lens = _lens(70, 33, 0)
+    clean = x.clone()
+    clean[1, 33:], clean[2] = 0.0, 0.0
+    x[1, 33:], x[2] = junk, junk
+    kept = x.clone()
+    a, b = m.prompt(x, lens), m.prompt(clean, lens)
+    for n in ("h", "S"):
+        assert torch.equal(a[n], b[n]), n
+    for i, n in enumerate(lens.tolist()):
+        assert torch.equal(a["out"][i, :n], b["out"][i, :n])
+    assert torch.equal(x.nan_to_num(7.0), kept.nan_to_num(7.0))          # the caller's tensor stays as it is
