@@ -565,8 +565,16 @@ def _workspace(need: int, workspace: Optional[torch.Tensor], device: int, desc) 
     return workspace
 
 
-def _raise(what: str, rc: int) -> None:
-    raise PnrError(f"{what} returned {rc}: {pnr_last_error()}")
+def _call(fn, device: int, *args) -> None:
+    """One of the calls above on its tensors' device: a launch goes to the current one, and the default
+    stream's handle is the same on all."""
+    if torch.cuda.current_device() == device:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc < 0:
+        raise PnrError(f"{fn.__name__} returned {rc}: {pnr_last_error()}")
 
 
 def _linattn(q, k, v, log_decay, scale, lens, step: bool) -> tuple:
@@ -614,9 +622,7 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     args = (_on(dev, state, "state", torch.float32, shape), _on(dev, o, "o", q.dtype, (B, T, H, Dv)),
             _on(dev, state_out, "state_out", torch.float32, shape))
     workspace = _workspace(pnr_linattn_workspace_bytes(desc), workspace, dev, desc)
-    rc = pnr_linattn_forward(desc, *ptrs, *args)
-    if rc < 0:
-        _raise("pnr_linattn_forward", rc)
+    _call(pnr_linattn_forward, dev, desc, *ptrs, *args)
     return {"o": o, "state": state_out, "workspace": workspace}
 
 
@@ -635,11 +641,9 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
         o = torch.empty(B, H, Dv, dtype=q.dtype, device=q.device)
     n_slots = state.shape[0] if state.dim() else 0
     shape = (n_slots, Hkv, Dk, Dv)
-    rc = pnr_linattn_step(desc, *ptrs, _on(dev, state, "state", torch.float32, shape),
-                          _on(dev, slots, "slots", torch.int32, (B,)), n_slots, _on(dev, o, "o", q.dtype, (B, H, Dv)),
-                          _on(dev, state_out, "state_out", torch.float32, shape))
-    if rc < 0:
-        _raise("pnr_linattn_step", rc)
+    _call(pnr_linattn_step, dev, desc, *ptrs, _on(dev, state, "state", torch.float32, shape),
+          _on(dev, slots, "slots", torch.int32, (B,)), n_slots, _on(dev, o, "o", q.dtype, (B, H, Dv)),
+          _on(dev, state_out, "state_out", torch.float32, shape))
     return {"o": o, "state": state_out}
 
 
@@ -665,9 +669,7 @@ def linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     out = {n: torch.empty(like[n][0], dtype=like[n][1], device=q.device) for n in want
            if n != "state" or state is not None}
     workspace = _workspace(pnr_linattn_workspace_bytes_backward(desc), workspace, dev, desc)
-    rc = pnr_linattn_backward(desc, *ptrs, *args, *[_ptr(out.get(n)) for n in ("q", "k", "v", "log_decay", "state")])
-    if rc < 0:
-        _raise("pnr_linattn_backward", rc)
+    _call(pnr_linattn_backward, dev, desc, *ptrs, *args, *[_ptr(out.get(n)) for n in ("q", "k", "v", "log_decay", "state")])
     out["workspace"] = workspace
     return out
 
@@ -704,9 +706,7 @@ def group_norm(x: torch.Tensor, groups: int, *, weight: Optional[torch.Tensor] =
     out = _on(dev, y, "y", x.dtype, x.shape)
     mean, rstd = torch.empty(2, x.shape[0], max(groups, 1), dtype=torch.float32, device=x.device).unbind(0)
     workspace = _workspace(pnr_groupnorm_workspace_bytes(desc), workspace, dev, desc)
-    rc = pnr_groupnorm(desc, *ptrs, out, mean.data_ptr(), rstd.data_ptr())
-    if rc < 0:
-        _raise("pnr_groupnorm", rc)
+    _call(pnr_groupnorm, dev, desc, *ptrs, out, mean.data_ptr(), rstd.data_ptr())
     return {"y": y, "mean": mean, "rstd": rstd, "workspace": workspace}
 
 
@@ -728,8 +728,6 @@ def group_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean
            _on(dev, rstd, "rstd", torch.float32, stats))
     out = {n: torch.empty_like(args[n]) for n in want if args[n] is not None}
     workspace = _workspace(pnr_groupnorm_workspace_bytes_backward(desc), workspace, dev, desc)
-    rc = pnr_groupnorm_backward(desc, *ptrs, *ins, *[_ptr(out.get(n)) for n in ("x", "weight", "bias", "gate")])
-    if rc < 0:
-        _raise("pnr_groupnorm_backward", rc)
+    _call(pnr_groupnorm_backward, dev, desc, *ptrs, *ins, *[_ptr(out.get(n)) for n in ("x", "weight", "bias", "gate")])
     out["workspace"] = workspace
     return out
