@@ -560,6 +560,8 @@ def _workspace(need: int, workspace: Optional[torch.Tensor], device: int, desc) 
             workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", device))
         elif workspace.get_device() != device:
             raise ValueError(f"workspace is on {workspace.device}, not on cuda:{device}")
+        elif not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         desc.workspace = _ptr(workspace)
         desc.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace

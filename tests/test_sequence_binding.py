@@ -1,0 +1,17 @@
+"""Checks of the sequence-mixing binding that need no GPU."""
+import pytest
+import torch
+
+from nonlinear_rnn_evaluation_amd import pnr
+
+
+@pytest.mark.parametrize("ws", [torch.empty(1, dtype=torch.uint8).expand(4096), torch.empty(8192, dtype=torch.uint8)[::2]],
+                         ids=["expanded", "strided"])
+def test_a_workspace_covers_its_bytes(ws):
+    """The library is told the tensor's number of bytes: they have to be there, one after the other."""
+    desc = pnr.PnrNorm()
+    with pytest.raises(ValueError, match="contiguous"):
+        pnr._workspace(4096, ws, ws.get_device(), desc)
+    whole = torch.empty(1024, dtype=torch.float32)
+    assert pnr._workspace(4096, whole, whole.get_device(), desc) is whole
+    assert desc.workspace == whole.data_ptr() and desc.workspace_bytes == 4096
