@@ -12,6 +12,3 @@ def test_a_workspace_covers_its_bytes(ws):
     desc = pnr.PnrNorm()
     with pytest.raises(ValueError, match="contiguous"):
         pnr._workspace(4096, ws, ws.get_device(), desc)
-    whole = torch.empty(1024, dtype=torch.float32)
-    assert pnr._workspace(4096, whole, whole.get_device(), desc) is whole
-    assert desc.workspace == whole.data_ptr() and desc.workspace_bytes == 4096
