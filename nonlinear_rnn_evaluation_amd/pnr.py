@@ -527,6 +527,14 @@ _LINATTN = struct.Struct("8i d 9q 3P N")      # the layouts of pnr_linattn and p
 _NORM = struct.Struct("6i d 3P N")
 
 
+def _pack(struct_type, layout: struct.Struct, *fields):
+    """A descriptor from its fields in order."""
+    try:
+        return struct_type.from_buffer_copy(layout.pack(*fields))
+    except struct.error:
+        raise PnrError(f"a size of the request does not fit in 32 bits, or a stride in 64 (fields {fields})") from None
+
+
 def _raw_stream(device: int) -> int:
     """torch's current stream of a device, as a hipStream_t."""
     return torch._C._cuda_getCurrentRawStream(device)
@@ -598,10 +606,10 @@ def _linattn(q, k, v, log_decay, scale, lens, step: bool) -> tuple:
     token = log_decay.dim() != 1
     g = _on(dev, log_decay, "log_decay", torch.float32, (*lead, Hkv) if token else (Hkv,))
     T, qt, kt, vt = (1, 0, 0, 0) if step else (lead[1], a[1], b[1], c[1])
-    desc = PnrLinattn.from_buffer_copy(_LINATTN.pack(
-        lead[0], T, H, Hkv, Dk, Dv, code, DECAY_TOKEN if token else DECAY_HEAD, Dk ** -0.5 if scale is None else scale,
+    desc = _pack(
+        PnrLinattn, _LINATTN, lead[0], T, H, Hkv, Dk, Dv, code, DECAY_TOKEN if token else DECAY_HEAD, Dk ** -0.5 if scale is None else scale,
         a[0], qt, a[-2], b[0], kt, b[-2], c[0], vt, c[-2], _on(dev, lens, "lens", torch.int32, lead[:1]) or 0,
-        _raw_stream(dev), 0, 0))
+        _raw_stream(dev), 0, 0)
     return desc, (q.data_ptr(), k.data_ptr(), v.data_ptr(), g), (lead[0], T, H, Hkv, Dk, Dv), dev
 
 
@@ -689,8 +697,8 @@ def _norm(x, groups, weight, bias, gate, act, eps, lens) -> tuple:
         raise ValueError("libpnr takes device tensors")
     ptrs = (_on(dev, x, "x", x.dtype, shape), _on(dev, weight, "weight", torch.float32, params),
             _on(dev, bias, "bias", torch.float32, params), _on(dev, gate, "gate", x.dtype, shape))
-    desc = PnrNorm.from_buffer_copy(_NORM.pack(*shape, groups, code, act, eps,
-                                               _on(dev, lens, "lens", torch.int32, shape[:1]) or 0, _raw_stream(dev), 0, 0))
+    desc = _pack(PnrNorm, _NORM, *shape, groups, code, act, eps, _on(dev, lens, "lens", torch.int32, shape[:1]) or 0,
+                 _raw_stream(dev), 0, 0)
     return desc, ptrs, dev
 
 

@@ -12,3 +12,11 @@ def test_a_workspace_covers_its_bytes(ws):
     desc = pnr.PnrNorm()
     with pytest.raises(ValueError, match="contiguous"):
         pnr._workspace(4096, ws, ws.get_device(), desc)
+
+
+def test_sizes_beyond_the_descriptor_are_named():
+    x = torch.empty(2, 3, 8)
+    with pytest.raises(pnr.PnrError, match="32 bits"):
+        pnr._pack(pnr.PnrNorm, pnr._NORM, *x.shape, 2 ** 31, pnr.F32, pnr.ACT_NONE, 1e-5, 0, 0, 0, 0)
+    d = pnr._pack(pnr.PnrNorm, pnr._NORM, *x.shape, 4, pnr.F32, pnr.ACT_SILU, 1e-5, 0, 0, 0, 0)
+    assert (d.N, d.L, d.C, d.groups, d.dtype, d.act, d.eps) == (2, 3, 8, 4, pnr.F32, pnr.ACT_SILU, 1e-5)
