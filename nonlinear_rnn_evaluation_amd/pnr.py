@@ -714,7 +714,7 @@ def group_norm(x: torch.Tensor, groups: int, *, weight: Optional[torch.Tensor] =
     if y is None:
         y = torch.empty_like(x)
     out = _on(dev, y, "y", x.dtype, x.shape)
-    mean, rstd = torch.empty(2, x.shape[0], max(groups, 1), dtype=torch.float32, device=x.device).unbind(0)
+    mean, rstd = torch.empty(2, x.shape[0], min(max(groups, 1), x.shape[2]), dtype=torch.float32, device=x.device).unbind(0)
     workspace = _workspace(pnr_groupnorm_workspace_bytes(desc), workspace, dev, desc)
     _call(pnr_groupnorm, dev, desc, *ptrs, out, mean.data_ptr(), rstd.data_ptr())
     return {"y": y, "mean": mean, "rstd": rstd, "workspace": workspace}

@@ -36,3 +36,13 @@ def test_calls_select_their_tensors_device(monkeypatch):
     for p, q_ in zip(ref, calls()):
         assert torch.equal(p, q_)
     assert seen == [dev] * 5
+
+
+@pytest.mark.gpu
+def test_a_refused_number_of_groups_allocates_nothing_for_them():
+    x = torch.zeros(2, 3, 12, device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(pnr.PnrError, match="divide"):
+        pnr.group_norm(x, 10 ** 7)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
