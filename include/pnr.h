@@ -514,9 +514,9 @@ int pnr_linattn_backward(const pnr_linattn* desc, const void* q, const void* k, 
  * a whole map or sequence.  weight, bias fp32 [C], or both NULL; gate as x or NULL; lens int32
  * [N] or NULL: only the first min(max(lens[n], 0), L) positions of row n belong to it: the
  * others are not read, and y and the gradients are zeros there (a row with none has mean 0
- * and rstd 1 / sqrt(eps)).  N * groups <= 2e9, or 16 million where L > 1 or a group has more than
- * 512 channels.  mean, rstd: fp32 [N, groups] outputs, kept for the backward pass
- * (NULL: not wanted).  dtype PNR_F32 or PNR_BF16 (x, gate, y and their gradients).  The calls
+ * and rstd 1 / sqrt(eps)).  L <= 2^30, C <= 2^26, N * groups <= 2e9, or 16 million where L > 1 or a
+ * group has more than 512 channels.  mean, rstd: fp32 [N, groups] outputs, kept for the backward
+ * pass (NULL: not wanted).  dtype PNR_F32 or PNR_BF16 (x, gate, y and their gradients).  The calls
  * wait for nothing and allocate nothing.  Workspace sizes: 0 means none needed, or an
  * invalid request, which the call then names.
  */

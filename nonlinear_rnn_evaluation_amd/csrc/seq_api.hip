@@ -86,6 +86,9 @@ int validate(const pnr_norm* d) {
   if (int rc = check_dtype(d->dtype)) return rc;
   if (d->act < PNR_ACT_NONE || d->act > PNR_ACT_GELU) return record_error(PNR_E_INVALID, "unknown activation %d", d->act);
   if (!(d->eps > 0) || !isfinite(d->eps)) return record_error(PNR_E_INVALID, "eps must be finite and > 0");
+  // kernels and plans count a map's rows, two slabs of them ahead, and eight groups' channels in 32 bits; a launch
+  // holds 2^32 threads, 64 a channel in the sums of the parameters' gradients
+  if (d->L > (1 << 30) || d->C > (1 << 26)) return record_error(PNR_E_INVALID, "problem too large for this library's index range");
   // maps and wide groups take a block each at least
   const bool blocks = d->L != 1 || d->C / d->groups > 512;
   if ((double)d->N * d->L * d->C > 4.0e18 || (double)d->N * d->groups > (blocks ? 1.6e7 : 2.0e9))

@@ -1,0 +1,36 @@
+"""Requests of the sequence-mixing entry points beyond their index ranges: refused before any HIP call."""
+import os
+
+import pytest
+
+from nonlinear_rnn_evaluation_amd import pnr
+
+pytestmark = pytest.mark.skipif(not os.path.exists(pnr.LIB_PATH), reason="libpnr.so not built")
+
+POSITIONS, CHANNELS = 1 << 30, 1 << 26
+
+
+def _norm(N, L, C, groups, dtype=pnr.BF16, eps=1e-5):
+    return pnr.PnrNorm(N, L, C, groups, dtype, pnr.ACT_NONE, eps)
+
+
+@pytest.mark.parametrize("N,L,C,groups", [
+    # rows of a slab and steps behind the last one are counted in 32 bits
+    (1, 2 ** 31 - 1, 1, 1), (1, POSITIONS + 1, 1, 1), (1, 2 ** 31 - 64, 8, 8),
+    # so are eight times a group's channels; a launch holds 64 threads a channel
+    (1, 1, 2 ** 31 - 1, 1), (1, 1, CHANNELS + 1, 1), (1, 4, 2 ** 31 - 8, 1),
+])
+def test_norm_sizes_beyond_the_index_range(N, L, C, groups):
+    d = _norm(N, L, C, groups)
+    assert pnr.pnr_groupnorm_workspace_bytes(d) == 0 and "too large" in pnr.pnr_last_error()
+    assert pnr.pnr_groupnorm_workspace_bytes_backward(d) == 0
+    assert pnr.pnr_groupnorm(d, 4096, None, None, None, 4096, None, None) == pnr.E_INVALID
+    assert pnr.pnr_groupnorm_backward(d, 4096, None, None, None, 4096, 4096, 4096, *[None] * 4) == pnr.E_INVALID
+
+
+@pytest.mark.parametrize("N,L,C,groups", [(1, POSITIONS, 1, 1), (1, 1, CHANNELS, 1), (1, 9, CHANNELS - 1, 1),
+                                        (1, POSITIONS, 8, 8), (3, POSITIONS - 1, 7, 1)])
+def test_norm_sizes_at_the_limit_are_sized(N, L, C, groups):
+    d = _norm(N, L, C, groups)
+    assert pnr.pnr_groupnorm_workspace_bytes_backward(d) > 0
+    assert 0 < pnr.pnr_groupnorm_workspace_bytes(d) < 1 << 40
