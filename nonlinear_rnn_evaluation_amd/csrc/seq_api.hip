@@ -40,7 +40,7 @@ int validate(const pnr_linattn* d, bool step) {
   if (int rc = check_dtype(d->dtype)) return rc;
   if (d->decay != PNR_DECAY_HEAD && d->decay != PNR_DECAY_TOKEN)
     return record_error(PNR_E_INVALID, "unknown decay kind %d", d->decay);
-  if (!isfinite(d->scale)) return record_error(PNR_E_INVALID, "scale must be finite");
+  if (!isfinite((float)d->scale)) return record_error(PNR_E_INVALID, "scale must be finite, in fp32");
   for (int i = 0; i < 3; ++i)
     if ((!step || i != 1) && (d->q_stride[i] < 0 || d->k_stride[i] < 0 || d->v_stride[i] < 0))
       return record_error(PNR_E_INVALID, "strides must be >= 0");
@@ -85,7 +85,7 @@ int validate(const pnr_norm* d) {
   if (d->C % d->groups) return record_error(PNR_E_INVALID, "groups=%d must divide C=%d", d->groups, d->C);
   if (int rc = check_dtype(d->dtype)) return rc;
   if (d->act < PNR_ACT_NONE || d->act > PNR_ACT_GELU) return record_error(PNR_E_INVALID, "unknown activation %d", d->act);
-  if (!(d->eps > 0) || !isfinite(d->eps)) return record_error(PNR_E_INVALID, "eps must be finite and > 0");
+  if (!((float)d->eps > 0) || !isfinite((float)d->eps)) return record_error(PNR_E_INVALID, "eps must be finite and > 0, in fp32");
   // kernels and plans count a map's rows, two slabs of them ahead, and eight groups' channels in 32 bits; a launch
   // holds 2^32 threads, 64 a channel in the sums of the parameters' gradients
   if (d->L > (1 << 30) || d->C > (1 << 26)) return record_error(PNR_E_INVALID, "problem too large for this library's index range");

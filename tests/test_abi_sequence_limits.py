@@ -1,4 +1,5 @@
 """Requests of the sequence-mixing entry points beyond their index ranges: refused before any HIP call."""
+import ctypes
 import os
 
 import pytest
@@ -34,3 +35,20 @@ def test_norm_sizes_at_the_limit_are_sized(N, L, C, groups):
     d = _norm(N, L, C, groups)
     assert pnr.pnr_groupnorm_workspace_bytes_backward(d) > 0
     assert 0 < pnr.pnr_groupnorm_workspace_bytes(d) < 1 << 40
+
+
+@pytest.mark.parametrize("eps", [1e-60, 1e-46, 1e39])
+def test_an_eps_that_fp32_does_not_hold(eps):
+    """eps enters as fp32: 0 there makes a constant group NaN, infinity makes every output 0."""
+    d = _norm(2, 10, 8, 2, eps=eps)
+    assert pnr.pnr_groupnorm_workspace_bytes(d) == 0 and "eps" in pnr.pnr_last_error()
+    assert pnr.pnr_groupnorm(d, 4096, None, None, None, 4096, None, None) == pnr.E_INVALID
+    assert pnr.pnr_groupnorm_workspace_bytes(_norm(2, 10, 8, 2, eps=1e-30)) > 0
+
+
+@pytest.mark.parametrize("scale", [1e300, -1e39])
+def test_a_scale_that_fp32_does_not_hold(scale):
+    strides = [(ctypes.c_int64 * 3)(25600, 256, 64) for _ in range(3)]
+    d = pnr.PnrLinattn(2, 100, 4, 2, 64, 64, pnr.BF16, pnr.DECAY_HEAD, scale, *strides)
+    assert pnr.pnr_linattn_workspace_bytes_backward(d) == 0 and "scale" in pnr.pnr_last_error()
+    assert pnr.pnr_linattn_step(d, 4096, 4096, 4096, 4096, 4096, None, 2, 4096, 4096) == pnr.E_INVALID
