@@ -52,9 +52,11 @@ __device__ __forceinline__ void act_grads(int act, float (&u)[V], float (&d)[V])
   } else if (act == PNR_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float s = sigmoid(gelu_arg(u[i])), da = 1.5957691216057308f * fmaf(0.134145f * u[i], u[i], 1.0f);
+      // from |u| = 16 on s is 0 or 1: cut there, the slope's cube stays finite under a factor of zero
+      const float s = sigmoid(gelu_arg(u[i])), v = __builtin_amdgcn_fmed3f(u[i], -16.0f, 16.0f);
+      const float da = 1.5957691216057308f * fmaf(0.134145f * v, v, 1.0f);
       u[i] *= s;
-      d[i] = fmaf(u[i] * da, 1.0f - s, s);
+      d[i] = fmaf(v * s * da, 1.0f - s, s);
     }
   } else {
 #pragma unroll
