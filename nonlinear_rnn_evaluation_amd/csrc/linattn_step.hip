@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(256) step_kernel(StepArgs p) {
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    s[r] = s[r] * dec + v * ks[i0 + r];
+    // rows behind the keys' end stay zero: zero times an infinite value would not be
+    s[r] = i0 + r < a.Dk ? s[r] * dec + v * ks[i0 + r] : f32x4{0, 0, 0, 0};
     float* dst = p.s_out + at + r * a.Dv;
     if constexpr (kVec) {
       if (i0 + r < a.Dk && j0 < a.Dv) *(f32x4*)dst = s[r];
