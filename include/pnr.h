@@ -437,9 +437,16 @@ int pnr_last_profile(pnr_profile* out);
  * H <= 32768 and B H <= 8 million.  Products are accumulated, and states, decays and sums held,
  * in fp32.  With bf16 inputs, states and the decay's gradient are as exact as in fp32, and o and the
  * gradients of q, k and v are rounded once, at the end (inside, scores and the state are held
- * to 2^-17 of each value).  A NaN or an infinity in a token reaches that token's and later outputs of its
- * row and head only (for a gradient, those of earlier tokens).  Outputs do not overlap inputs,
- * but for the states where it is said.
+ * to 2^-17 of each value).
+ *
+ * A NaN or an infinity in a token reaches what the formulas compute from it, within its row and
+ * head: q_t reaches o_t; k_t, v_t and log_decay_t reach o from t on and the state after; k_t, v_t,
+ * log_decay_t reach dL/dq from t on, grad_o_t dL/dq_t; q_t and grad_o_t reach dL/dk and dL/dv up to
+ * t, log_decay_t those before t, v_t dL/dk_t, k_t dL/dv_t; q_t, grad_o_t and log_decay_t reach the
+ * entry state's gradient.  The decay's gradient is summed along the row, and any of them may reach
+ * all of it in its row and head.  An infinity may come out as a NaN.
+ *
+ * Outputs do not overlap inputs, but for the states where it is said.
  *
  * None of these calls waits for the device or allocates: the work is enqueued on
  * desc->stream, so they may be recorded into a HIP graph.  Return PNR_OK or a negative

@@ -5,9 +5,10 @@
 // 1..C, G_i = g_1 + ... + g_i and S the state at the chunk's start,
 //   out_i = exp(G_i) S^T x_i + sum_{j <= i} exp(G_i - G_j) (x_i . y_j) z_j
 //   S    <- exp(G_C) S + sum_j exp(G_C - G_j) y_j z_j^T
-// and against time, S being what later chunks send back,
-//   out_i = exp(G_C - G_i) S^T x_i + sum_{j >= i} exp(G_j - G_i) (x_i . y_j) z_j
-//   S    <- exp(G_C) S + sum_j exp(G_j) y_j z_j^T.
+// and against time, S being what later chunks send back and H_i = g_{i+1} + ... + g_C,
+//   out_i = exp(H_i) S^T x_i + sum_{j >= i} exp(H_i - H_j) (x_i . y_j) z_j
+//   S    <- exp(G_C) S + sum_j exp(G_C - H_j) y_j z_j^T.
+// Sums from the chunk's end, because a decay that is not finite then stays where it has a part.
 //         x    y    z    direction   state
 //   o     q    k    v    forward     S
 //   dq    do   v    k    forward     S transposed
@@ -428,11 +429,10 @@ struct Scores<false, kReverse> {
 
 // A chunk's weights.
 struct alignas(16) Weights {
-  float ghi[kChunk];                 // G in units of log2, as the sum of a float
+  float ghi[kChunk];                 // G, or H, in units of log2, as the sum of a float
   uint16_t glo[kChunk];              // ... and a bf16
   float upd[kChunk];                 // the weights of y z^T
   float total;                       // exp(G_C)
-  float end_hi, end_lo;              // G_C
 };
 
 // S += Y^T (w Z) over the 32 tokens 32 k + 0 .. 31 of y, for 16 columns of Z held as an operand; kGroup row
@@ -564,11 +564,14 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   const uint32_t es = sizeof(Elt);
   const uint32_t off_x = kVec ? TX::offset((uint32_t)p.x.st * es, p.dk) : 0, off_e = kVec && kDots ? TE::offset((uint32_t)p.e.st * es, p.dv) : 0;
   const uint32_t off_y = kVec ? decltype(sy)::offset((uint32_t)p.y.st * es, p.dk) : 0, off_z = kVec ? decltype(sz)::offset((uint32_t)p.z.st * es, p.dv) : 0;
+  // Lane l scans what G_l, or H_{63 - l}, has more than the lane before: the log decay of token l, or of token
+  // 64 - l; against time, lane 0 holds token 0, which only the chunk's whole decay has.
+  const int g_token = kReverse ? (lane ? kChunk - lane : 0) : lane, g_row = kReverse ? kChunk - 1 - lane : lane;
   float g_next = 0.0f;
   auto fetch = [&](int c, int sub) {
     const int t0 = c * kChunk;
     if (sub == 0 && wave == 0) {
-      const int t = min(t0 + lane, n - 1);
+      const int t = min(t0 + g_token, n - 1);
       g_next = a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h];
     }
     if constexpr (!kVec)
@@ -593,21 +596,19 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
         if constexpr (kDots) TE::load(Source<kBf16>(p.e, b, hh), off_e, t0, n, lds_e, wave);
       }
   };
-  // Wave 0 turns the log decays that it fetched into a chunk's weights.  G is an inclusive scan in
-  // 64 bits, because differences of sums of log decays (each down to -104) are what counts.
+  // Wave 0 turns the log decays that it fetched into a chunk's weights.  The scan is in 64 bits, because
+  // differences of sums of log decays (each down to -104) are what counts.
   auto weigh = [&](int c, int slot) {
-    const float g = c * kChunk + lane < n ? clamp_log_decay(g_next) : 0.0f;
-    const double x = wave_scan((double)g * 1.4426950408889634);
-    const double end = wave_last(x);
-    const float hi = (float)x, end_hi = (float)end;
+    const float g = c * kChunk + g_token < n ? clamp_log_decay(g_next) : 0.0f;
+    const double x = wave_scan(kReverse && lane == 0 ? 0.0 : (double)g * 1.4426950408889634);
+    double end = wave_last(x);
+    if (kReverse) end += (double)__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(g))) * 1.4426950408889634;
+    const float hi = (float)x;
     auto& w = lds_w[slot];
-    w.ghi[lane] = hi;
-    w.glo[lane] = f32_to_bf16((float)(x - (double)hi));
-    w.upd[lane] = __builtin_amdgcn_exp2f(kReverse ? hi : (float)(end - x)) * p.upd_scale;
-    if (lane == 0) {
-      w.total = __builtin_amdgcn_exp2f(end_hi);
-      w.end_hi = end_hi, w.end_lo = (float)(end - (double)end_hi);
-    }
+    w.ghi[g_row] = hi;
+    w.glo[g_row] = f32_to_bf16((float)(x - (double)hi));
+    w.upd[g_row] = __builtin_amdgcn_exp2f((float)(end - x)) * p.upd_scale;
+    if (lane == 0) w.total = __builtin_amdgcn_exp2f((float)end);
   };
   if (count > 0) {
     fetch_direct(kReverse ? live - 1 : c_lo, 0);
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
                                   __uint_as_float(gl.y << 16), __uint_as_float(gl.y & 0xffff0000u)};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float d = kReverse ? (ghv[r] - gi) + (glv[r] - gi_lo) : (gi - ghv[r]) + (gi_lo - glv[r]);
+              const float d = (gi - ghv[r]) + (gi_lo - glv[r]);
               s[r] = P[q][r] * (__builtin_amdgcn_exp2f(d) * p.p_scale);
             }
             if (jt == it0)
@@ -721,8 +722,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const int t = m * 16 + l15;
-          const float g = kReverse ? (wt.end_hi - wt.ghi[t]) + (wt.end_lo - bf16_to_f32(wt.glo[t])) : wt.ghi[t];
-          O[m] *= __builtin_amdgcn_exp2f(g) * p.inter_scale;
+          O[m] *= __builtin_amdgcn_exp2f(wt.ghi[t]) * p.inter_scale;
           if constexpr (kDots) {
             float d = 0.0f;
             const Elt* er = lds_e + TE::at(t, (col0 + g4) / M::kPiece) + (col0 + g4) % M::kPiece;
