@@ -10,13 +10,17 @@
 //   sum_{i >= t > j} W_ij + sum_{i >= t} b_i + sum_{j < t} c_j + exp(G_C) <S, E>,
 //   W_ij = scale exp(G_i - G_j) (do_i . v_j)(q_i . k_j),  b_i = the part of q_i . dq_i that comes
 //   from S,  c_j = the part of k_j . dk_j that comes from E.
-// No term is subtracted from a larger one except within a chunk, in fp32: the global form
-// dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t would carry every token's rounding to the first.
-// The last term follows from <S, E> at the segment's end X by X <- X + sum b - sum c per chunk.
+// The last term follows from X = <S, E> behind the chunk: X - sum c, and X - sum c + sum b is <S, E> before
+// it.  The rounding of these sums adds up along such a walk (as every token's does in the global form
+// dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t), so X is taken from the states themselves every kWalk
+// chunks, and what a walk misses of the value at its other end is spread over its chunks.  300 heads of 32 x 32
+// over 4096 tokens in fp32, one walk a row: dg off by 1.7e-6 of its norm, more the earlier the token, and
+// its sum over the tokens by 1.9e-5; walks of four chunks 3.5e-7 and 7.7e-7, for 1 % of a training pass.
 //
 // 4 x 16 heads of 128 x 128 over 4096 tokens in bf16: sums 2 x 45 us, scan 25, dq with u and b 118 to
 // 137, dk with c 123 to 142, dv 72 to 83, dg 13 (the spread is from box to box).  The dot products
 // cost dq and dk their three-part S, a fourth tile of rows and, dq, a second set of scores.
+#include <algorithm>
 #include <type_traits>
 
 #include "linattn_tile.h"
@@ -29,10 +33,11 @@ struct DecayArgs {
   LinAttn a;
   const float *u, *c;        // [B][Hkv][T]; u_t = b_t + sum_j W_tj - sum_i W_it
   const float* b;            // [B][Hkv][chunks]: sum b
-  const float* x_end;        // [B][Hkv][nseg], or nullptr: zeros
-  int seg_chunks, nseg;
+  const float* x_end;        // [B][Hkv][nseg][marks]
+  const float* x_first;      // [B][Hkv], or nullptr: zeros
+  int seg_chunks, nseg, marks;
   float* gg;                 // [B][T][Hkv] (per token), or
-  double* seg_sum;           // [B][Hkv][nseg]
+  double* walk_sum;          // [B][Hkv][nseg][marks]
 };
 
 __device__ __forceinline__ float wave_suffix_sum(float v, int lane) {
@@ -44,43 +49,62 @@ __device__ __forceinline__ float wave_suffix_sum(float v, int lane) {
   return v;
 }
 
-// A wave a segment, its chunks from the last to the first.
+// A wave a walk: up to kWalk chunks, from the last to the first.
 __global__ void __launch_bounds__(256) decay_grad_kernel(DecayArgs p) {
   const LinAttn& a = p.a;
   const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (w >= (int64_t)a.B * a.Hkv * p.nseg) return;
-  const int seg = w % p.nseg, h = w / p.nseg % a.Hkv, b = w / p.nseg / a.Hkv;
-  const int n = row_len(a.lens, b, a.T);
-  const size_t base = ((size_t)b * a.Hkv + h) * a.T;
-  const int chunks = (a.T + kChunk - 1) / kChunk, c_lo = seg * p.seg_chunks, c_hi = min(c_lo + p.seg_chunks, chunks);
-  float x = p.x_end && c_lo * kChunk < n ? p.x_end[w] : 0.0f;
-  double sum = 0.0;
-  for (int ch = c_hi - 1; ch >= c_lo; --ch) {
-    const int t = ch * kChunk + lane;
-    const bool in = t < a.T;
-    const float u = in ? p.u[base + t] : 0.0f, cc = in ? p.c[base + t] : 0.0f;
-    const float b_all = p.b[((size_t)b * a.Hkv + h) * chunks + ch];
-    const float us = wave_suffix_sum(u, lane), cs = wave_suffix_sum(cc, lane), c_all = __shfl(cs, 0);
-    const float g = a.g[a.decay_token ? ((size_t)b * a.T + (in ? t : 0)) * a.Hkv + h : (size_t)h];
-    x -= c_all;                                   // exp(G_C) <S, E>
-    // a decay that forgets everything passes no gradient
-    const float d = t < n && !(g <= kLogDecayMin) ? us + (c_all - cs) + x : 0.0f;
-    if (p.gg && in) p.gg[((size_t)b * a.T + t) * a.Hkv + h] = d;
-    sum += d;
-    x += b_all;
-  }
-  if (p.seg_sum) {
+  const int64_t per_row = (int64_t)p.nseg * p.marks, walks = (int64_t)a.B * a.Hkv * per_row;
+  for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < walks; w += (int64_t)gridDim.x * 4) {
+    const int mark = w % p.marks, seg = w / p.marks % p.nseg, h = w / per_row % a.Hkv, b = w / per_row / a.Hkv;
+    const int n = row_len(a.lens, b, a.T);
+    const size_t row = (size_t)b * a.Hkv + h;
+    const int chunks = (a.T + kChunk - 1) / kChunk, c_lo = seg * p.seg_chunks + mark * kWalk;
+    const int c_hi = min(min(c_lo + kWalk, (seg + 1) * p.seg_chunks), chunks);
+    const int live = min(c_hi, (n + kChunk - 1) / kChunk) - c_lo;       // chunks with tokens
+    float us[kWalk], cs[kWalk], b_all[kWalk], before[kWalk];
 #pragma unroll
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-    if (lane == 0) p.seg_sum[w] = sum;
+    for (int j = 0; j < kWalk; ++j) {
+      const int t = (c_lo + j) * kChunk + lane;
+      const bool in = j < live && t < a.T;
+      us[j] = in ? p.u[row * a.T + t] : 0.0f;
+      cs[j] = in ? p.c[row * a.T + t] : 0.0f;
+      b_all[j] = j < live ? p.b[row * chunks + c_lo + j] : 0.0f;
+    }
+    float x = live > 0 ? p.x_end[w] : 0.0f;
+    const float x_start = live <= 0 ? 0.0f : c_lo > 0 ? p.x_end[w - 1] : p.x_first ? p.x_first[row] : 0.0f;
+#pragma unroll
+    for (int j = kWalk; j--;) {
+      us[j] = wave_suffix_sum(us[j], lane);
+      const float after = wave_suffix_sum(cs[j], lane), all = __shfl(after, 0);
+      cs[j] = all - after;
+      x -= all;
+      before[j] = x;                                // exp(G_C) <S, E>
+      x += b_all[j];
+    }
+    const float missed = live > 0 ? (x - x_start) / live : 0.0f;
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < kWalk; ++j) {
+      const int t = (c_lo + j) * kChunk + lane;
+      if (c_lo + j >= c_hi || t >= a.T) continue;
+      const float g = a.g[a.decay_token ? ((size_t)b * a.T + t) * a.Hkv + h : (size_t)h];
+      // a decay that forgets everything passes no gradient
+      const float d = t < n && !(g <= kLogDecayMin) ? us[j] + cs[j] + (before[j] - missed * (live - j - 0.5f)) : 0.0f;
+      if (p.gg) p.gg[((size_t)b * a.T + t) * a.Hkv + h] = d;
+      sum += d;
+    }
+    if (p.walk_sum) {
+#pragma unroll
+      for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+      if (lane == 0) p.walk_sum[w] = sum;
+    }
   }
 }
 
-__global__ void __launch_bounds__(64) decay_head_kernel(const double* seg_sum, int B, int Hkv, int nseg, float* gg) {
+__global__ void __launch_bounds__(64) decay_head_kernel(const double* walk_sum, int B, int Hkv, int64_t walks, float* gg) {
   const int h = blockIdx.x;
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < (int64_t)B * nseg; i += 64) s += seg_sum[((i / nseg) * Hkv + h) * nseg + i % nseg];
+  for (int64_t i = threadIdx.x; i < B * walks; i += 64) s += walk_sum[((i / walks) * Hkv + h) * walks + i % walks];
 #pragma unroll
   for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
   if (threadIdx.x == 0) gg[h] = (float)s;
@@ -88,11 +112,13 @@ __global__ void __launch_bounds__(64) decay_head_kernel(const double* seg_sum, i
 
 struct BackwardLayout {
   Plan plan;
-  size_t s = 0, e = 0, last = 0, decay = 0, u = 0, b = 0, c = 0, x_end = 0, seg_sum = 0, total = 0;
+  int marks;
+  size_t s = 0, e = 0, last = 0, decay = 0, u = 0, b = 0, c = 0, mid = 0, x_end = 0, x_first = 0, walk_sum = 0, total = 0;
 };
 BackwardLayout backward_layout(const LinAttn& a) {
   BackwardLayout l;
   l.plan = make_plan(a, true);
+  l.marks = (l.plan.seg_chunks + kWalk - 1) / kWalk;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -104,8 +130,11 @@ BackwardLayout backward_layout(const LinAttn& a) {
   l.last = take(rows * a.Dk * a.Dv * 4);
   l.u = take(tokens), l.c = take(tokens);
   l.b = take(rows * ((a.T + kChunk - 1) / kChunk) * 4);
-  l.x_end = take(segs * 4);
-  l.seg_sum = take(segs * 8);
+  const auto tile = [](int d) { return (size_t)(d > 64 ? 128 : 64); };
+  l.mid = take(segs * (l.marks - 1) * tile(a.Dk) * tile(a.Dv) * 4);
+  l.x_end = take(segs * l.marks * 4);
+  l.x_first = take(rows * 4);
+  l.walk_sum = take(segs * l.marks * 8);
   l.total = off;
   return l;
 }
@@ -130,7 +159,9 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
   base.a = a;
   base.vec = rows_vec(a.q, a.Dk, a.bf16) && rows_vec(a.k, a.Dk, a.bf16) && rows_vec(a.v, a.Dv, a.bf16) &&
              rows_vec(d.go, a.Dv, a.bf16) && ((uintptr_t)d.gq | (uintptr_t)d.gk | (uintptr_t)d.gv) % 16 == 0;
-  base.seg_chunks = l.plan.seg_chunks, base.nseg = nseg;
+  base.seg_chunks = l.plan.seg_chunks, base.nseg = nseg, base.marks = l.marks;
+  float *x_end = (float*)(ws + l.x_end), *x_first = (float*)(ws + l.x_first);
+  float* mid = d.gg && l.marks > 1 ? (float*)(ws + l.mid) : nullptr;
   base.p_scale = a.scale;
   // forward in time: keys k, values v; backward: keys q, values do, times the scale
   RoleArgs fwd = base, rev = base;
@@ -167,7 +198,7 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     p.x = d.go, p.y = a.v, p.z = a.k, p.e = a.q;
     p.dk = a.Dv, p.dv = a.Dk, p.transposed = 1;
     p.o = d.gq;
-    p.u = u, p.b = b;
+    p.u = u, p.b = b, p.s_mid = mid;
     if (nseg == 1) p.s_out = last;
     if ((e = run_role<false, kDotQ>(p, st)) != hipSuccess) return e;
   }
@@ -178,7 +209,9 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     p.dk = a.Dv, p.dv = a.Dk, p.transposed = 1;
     p.o = d.gk;
     p.u = c;
-    if (d.gg && (d.gstate_out || nseg > 1)) p.x_end = (float*)(ws + l.x_end), p.s_entry = S, p.s_last = last;
+    p.s_mid = mid;
+    if (d.gg) p.x_end = x_end, p.s_entry = S, p.s_last = last;
+    if (d.gg && state_in) p.x_first = x_first, p.s_first = state_in;
     if (nseg == 1) p.s_out = d.gstate_in;
     if ((e = run_role<true, kDotK>(p, st)) != hipSuccess) return e;
   }
@@ -190,12 +223,11 @@ hipError_t launch_linattn_backward(const LinAttn& a, const float* state_in, cons
     if ((e = run_role<true, kOut>(p, st)) != hipSuccess) return e;
   }
   if (d.gg) {
-    DecayArgs p{a, u, c, b, nullptr, l.plan.seg_chunks, nseg, nullptr, nullptr};
-    if (a.decay_token) p.gg = d.gg; else p.seg_sum = (double*)(ws + l.seg_sum);
-    if (d.gstate_out || nseg > 1) p.x_end = (float*)(ws + l.x_end);
-    const int64_t waves = rows * nseg;
-    decay_grad_kernel<<<(unsigned)((waves + 3) / 4), 256, 0, st>>>(p);
-    if (!a.decay_token) decay_head_kernel<<<a.Hkv, 64, 0, st>>>(p.seg_sum, a.B, a.Hkv, nseg, d.gg);
+    DecayArgs p{a, u, c, b, x_end, state_in ? x_first : nullptr, l.plan.seg_chunks, nseg, l.marks, nullptr, nullptr};
+    if (a.decay_token) p.gg = d.gg; else p.walk_sum = (double*)(ws + l.walk_sum);
+    const int64_t walks = (int64_t)nseg * l.marks, waves = rows * walks;
+    decay_grad_kernel<<<(unsigned)std::min<int64_t>((waves + 3) / 4, 1 << 22), 256, 0, st>>>(p);
+    if (!a.decay_token) decay_head_kernel<<<a.Hkv, 64, 0, st>>>(p.walk_sum, a.B, a.Hkv, walks, d.gg);
     e = hipGetLastError();
   }
   return e;

@@ -22,6 +22,7 @@ namespace pnr {
 namespace linattn {
 
 constexpr int kChunk = 64;
+constexpr int kWalk = 4;        // chunks between two exact values of <S, E>, from a segment's start on (see linattn_bwd.hip)
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -53,9 +54,14 @@ struct RoleArgs {
   void* o;
   float* u;              // [B][Hkv][T]: u + b (kDotQ), c (kDotK) of the decay's gradient
   float* b;              // [B][Hkv][chunks]: sums of b (kDotQ)
-  float* x_end;          // kDotK: [B][Hkv][nseg] <state after the segment's last token, s_in>, or nullptr
-  const float* s_entry;  // ... that state, for all but the last segment: the next one's entry, [B][Hkv][nseg]
+  int marks;             // kWalk chunks each that a segment has
+  float* s_mid;          // kDotQ: [B][Hkv][nseg][marks - 1] states before all but the first of them, whole tiles in
+                         // the order of their registers, written; kDotK: read; or nullptr
+  float* x_end;          // kDotK: [B][Hkv][nseg][marks] <state after the last of these tokens, its gradient>, or nullptr
+  const float* s_entry;  // ... that state at a segment's end, for all but the last: the next one's entry, [B][Hkv][nseg]
   const float* s_last;   // ... and after the last, [B][Hkv]
+  float* x_first;        // kDotK: [B][Hkv] <state before the first token, its gradient>, or nullptr
+  const float* s_first;  // ... that state
   int seg_chunks, nseg;
 };
 
@@ -535,25 +541,33 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
   for (int kt = 0; kt < KT; ++kt)
     asm volatile("" : "+v"(S[kt]));
 
+  // the waves' parts of a sum go to lds_bsum, from where, after a barrier, thread 0 adds them
+  auto share = [&](float s) {
+    s = row16_sum(group_sum(s));
+    if (lane == 0) lds_bsum[wave] = s;
+  };
+  auto shared = [&]() {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) s += lds_bsum[w];
+    return s;
+  };
+  auto dot_state = [&](const float* other) {       // <S, other>, other a state at s_at
+    float s = 0.0f;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (s_in_range(kt, r)) s += S[kt][r] * other[s_at(kt, r)];
+    share(s);
+  };
+  const size_t s_size = (size_t)p.dk * p.dv;
+  const int row = blockIdx.x / p.nseg;
   if constexpr (kind == kDotK) {
     if (p.x_end && count > 0) {
-      const size_t size = (size_t)p.dk * p.dv;
-      const float* after = seg + 1 < segments_of(n, p.seg_chunks) ? p.s_entry + size : p.s_last - sbase + blockIdx.x / p.nseg * size;
-      float s = 0.0f;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (s_in_range(kt, r)) s += S[kt][r] * after[s_at(kt, r)];
-      s = row16_sum(group_sum(s));
-      if (lane == 0) lds_bsum[wave] = s;
+      dot_state(seg + 1 < segments_of(n, p.seg_chunks) ? p.s_entry + s_size : p.s_last - sbase + row * s_size);
       __syncthreads();
-      if (tid == 0) {
-        s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) s += lds_bsum[w];
-        p.x_end[blockIdx.x] = s;
-      }
+      if (tid == 0) p.x_end[(size_t)blockIdx.x * p.marks + (live - 1 - c_lo) / kWalk] = shared();
     }
   }
 
@@ -624,7 +638,26 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
     const auto& wt = lds_w[step & 1];
     const bool last_sub = sub == nsub - 1;
     const bool new_x = p.nq > 1 || sub == 0, new_yz = p.nkv > 1 || sub == 0;
+    // between two walks of kWalk chunks: S goes to s_mid, or meets the one that is there
+    const int ahead = c + (kReverse ? 1 : 0) - c_lo;          // the segment's chunks before the state in S
+    const bool mark = kDots && p.s_mid && it > 0 && sub == 0 && ahead % kWalk == 0;
+    if constexpr (kDots)
+      if (mark) {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        const __amdgpu_buffer_rsrc_t mid = buffer_at(p.s_mid + ((size_t)blockIdx.x * (p.marks - 1) + ahead / kWalk - 1) * (DK * DV));
+        const uint32_t off = (uint32_t)fresh(tid) * 16;
+        f32x4 dot = {0, 0, 0, 0};
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+          if constexpr (kind == kDotQ)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, S[kt]), mid, off, kt * kThreads * 16, 0);
+          else
+            dot += S[kt] * __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(mid, off, kt * kThreads * 16, 0));
+        if constexpr (kind == kDotK) share((dot[0] + dot[1]) + (dot[2] + dot[3]));
+      }
     __syncthreads();
+    if constexpr (kind == kDotK)
+      if (mark && tid == 0) p.x_end[(size_t)blockIdx.x * p.marks + ahead / kWalk - 1] = shared();
     if constexpr (!kVec)
       if (new_x) {
         sx.store_permuted(lds_x);
@@ -873,6 +906,14 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (s_in_range(kt, r)) p.s_out[s_at(kt, r)] = S[kt][r];
+  if constexpr (kind == kDotK) {
+    if (p.x_first && seg == 0) {
+      __syncthreads();
+      dot_state(p.s_first - sbase + row * s_size);
+      __syncthreads();
+      if (tid == 0) p.x_first[row] = shared();
+    }
+  }
 }
 
 // The sum of a segment alone, from a zero state, and the segment's decay: chunk_kernel's update, 128
