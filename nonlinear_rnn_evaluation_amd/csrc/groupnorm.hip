@@ -14,6 +14,7 @@
 // Variances come from deviations (two passes over registers, or running means that are joined by
 // their counts), never from a difference of sums of squares.  All of it is fp32 up to
 // the one rounding of each output.
+#include <algorithm>
 #include <initializer_list>
 #include <type_traits>
 
@@ -330,9 +331,10 @@ __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenArgs p) {
     }
 }
 
-// dw, db: sums of [rows][2][C] over the rows; 32 channels a block, 32 runs of rows joined in order.
+// dw, db: sums of [rows][2][C] over the rows, added to what is there (more) or in its place; 32 channels a
+// block, 32 runs of rows joined in order.
 // 256 rows of 2048 channels: 4.8 us.
-__global__ void __launch_bounds__(1024) param_sum_kernel(const float* part, int64_t rows, int C, float* gw, float* gb) {
+__global__ void __launch_bounds__(1024) param_sum_kernel(const float* part, int64_t rows, int C, bool more, float* gw, float* gb) {
   __shared__ float red[32][32];
   const int i = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
   float s = 0.0f;
@@ -344,8 +346,8 @@ __global__ void __launch_bounds__(1024) param_sum_kernel(const float* part, int6
   if (run == 0 && i < 2 * C) {
 #pragma unroll
     for (int k = 1; k < 32; ++k) s += red[k][threadIdx.x];
-    float* out = i < C ? gw : gb;
-    if (out) out[i < C ? i : i - C] = s;
+    float* out = i < C ? gw + i : gb + (i - C);
+    if (i < C ? gw : gb) *out = more ? *out + s : s;
   }
 }
 
@@ -399,7 +401,7 @@ struct MapArgs {
   const void* gy;
   const float *mean_in, *rstd_in;
   float* part;                // [N][nsplit][2][C]: sums of dz n and of dz over a slab
-  float* chan;                // [N][2][C]: over a row
+  float* chan;                // [N][2][C]: over a row; may be part where there is one slab
   float2* means;              // [N][groups]: mean(u n), mean(u)
   void *gx, *ggate;
 };
@@ -818,6 +820,31 @@ int most_splits(const Norm& a) {
   return s1 > sv ? s1 : sv;
 }
 
+// Maps whose slabs' results, `bytes` a map, a workspace holds at a time.  It stays bounded in the number of maps:
+// short maps and wide groups would leave more than their own size (2 or 4 bytes a value, 8 a channel).
+// 64 MB, or what eight blocks a CU take where that is more: gradients of 32768 tokens in one group of 8192 channels
+// (bf16, a block a token) 1024, 2048 and all tokens at a time: 8.4, 5.4 and 6.8 ms.  32768 maps of 2 x 2048 in
+// batches of 64 MB 1.73 ms, all at a time 1.97.
+int64_t batch_maps(const Norm& a, size_t bytes) {
+  const int V = vec_of(a);
+  const int c1 = map_plan(a, 1).ctiles, cv = map_vec(a, V) ? map_plan(a, V).ctiles : c1;
+  const int64_t n = (int64_t)(((size_t)64 << 20) / bytes), fill = 2048 / (c1 < cv ? c1 : cv);
+  const int64_t most = n > fill ? n : fill;
+  return most < 1 ? 1 : most < a.N ? most : a.N;
+}
+const void* at_map(const Norm& a, const void* p, int64_t n) {
+  return p ? (const char*)p + n * a.L * a.C * (a.bf16 ? 2 : 4) : nullptr;
+}
+void* at_map(const Norm& a, void* p, int64_t n) { return (void*)at_map(a, (const void*)p, n); }
+// the problem from map n on
+Norm from_map(const Norm& a, int64_t n, int64_t count) {
+  Norm b = a;
+  b.N = (int)count;
+  b.x = at_map(a, a.x, n), b.gate = at_map(a, a.gate, n);
+  if (a.lens) b.lens = a.lens + n;
+  return b;
+}
+
 struct TokenChoice {
   TokenPlan t;
   bool vec;
@@ -839,11 +866,13 @@ TokenChoice choose_tokens(const Norm& a, bool ok, bool grad) {
 int grad_blocks_per_cu(int ppl) { return ppl <= 2 ? 1 : 3; }
 constexpr int kMostGradBlocksPerCu = 3;
 
+size_t stats_bytes(const Norm& a) { return (size_t)most_splits(a) * a.groups * sizeof(float2); }
+
 }  // namespace
 
 size_t groupnorm_workspace(const Norm& a) {
   if (choose_tokens(a, true, false).t.ppl && choose_tokens(a, false, false).t.ppl) return 0;
-  return align256((size_t)a.N * most_splits(a) * a.groups * sizeof(float2));
+  return align256(batch_maps(a, stats_bytes(a)) * stats_bytes(a));
 }
 
 hipError_t launch_groupnorm(const Norm& a, void* y, float* mean, float* rstd, char* ws, hipStream_t st) {
@@ -856,31 +885,36 @@ hipError_t launch_groupnorm(const Norm& a, void* y, float* mean, float* rstd, ch
   }
   const bool vec = ok && map_vec(a, vec_of(a));
   MapArgs p{};
-  p.a = a, p.m = map_plan(a, vec ? vec_of(a) : 1), p.stats = (float2*)ws, p.y = y, p.mean = mean, p.rstd = rstd;
-  const unsigned grid = (unsigned)a.N * p.m.ctiles * p.m.nsplit;
-  with_types(a.bf16, vec, [&](auto b, auto v) {
-    map_stats_kernel<decltype(b)::value, decltype(v)::value><<<grid, 256, 0, st>>>(p);
-    map_norm_kernel<decltype(b)::value, decltype(v)::value><<<grid, 256, 0, st>>>(p);
-  });
-  return hipGetLastError();
+  p.m = map_plan(a, vec ? vec_of(a) : 1), p.stats = (float2*)ws;
+  const int64_t batch = batch_maps(a, stats_bytes(a));
+  for (int64_t n = 0; n < a.N; n += batch) {
+    p.a = from_map(a, n, batch < a.N - n ? batch : a.N - n);
+    p.y = at_map(a, y, n), p.mean = mean ? mean + n * a.groups : nullptr, p.rstd = rstd ? rstd + n * a.groups : nullptr;
+    const unsigned grid = (unsigned)p.a.N * p.m.ctiles * p.m.nsplit;
+    with_types(a.bf16, vec, [&](auto b, auto v) {
+      map_stats_kernel<decltype(b)::value, decltype(v)::value><<<grid, 256, 0, st>>>(p);
+      map_norm_kernel<decltype(b)::value, decltype(v)::value><<<grid, 256, 0, st>>>(p);
+    });
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 namespace {
 struct GradLayout {
-  size_t part = 0, chan = 0, means = 0, total = 0;
+  size_t chan = 0, means = 0, total = 0;       // maps: part lies at 0
+  int64_t batch = 0;
 };
 GradLayout grad_layout(const Norm& a) {
   GradLayout l;
-  if (a.L == 1) l.chan = align256((size_t)256 * kMostGradBlocksPerCu * 2 * a.C * 4);   // token form: partial sums
-  const size_t maps = align256((size_t)a.N * most_splits(a) * 2 * a.C * 4);
-  const bool tokens = choose_tokens(a, true, true).t.ppl && choose_tokens(a, false, true).t.ppl;
-  if (!tokens) {
-    l.chan = l.chan > maps ? l.chan : maps;
-    l.means = l.chan + align256((size_t)a.N * 2 * a.C * 4);
-    l.total = l.means + align256((size_t)a.N * a.groups * sizeof(float2));
-  } else {
-    l.total = l.chan;
-  }
+  if (a.L == 1) l.total = align256((size_t)256 * kMostGradBlocksPerCu * 2 * a.C * 4);   // token form: partial sums
+  if (choose_tokens(a, true, true).t.ppl && choose_tokens(a, false, true).t.ppl) return l;
+  // where a map is one slab, the slab's sums are the map's
+  const size_t row = (size_t)2 * a.C * 4, slabs = most_splits(a) > 1 ? most_splits(a) * row : 0, groups = a.groups * sizeof(float2);
+  l.batch = batch_maps(a, slabs + row + groups);
+  l.chan = align256(l.batch * slabs);
+  l.means = l.chan + align256(l.batch * row);
+  l.total = std::max(l.total, l.means + align256(l.batch * groups));
   return l;
 }
 }  // namespace
@@ -900,23 +934,28 @@ hipError_t launch_groupnorm_backward(const Norm& a, const void* gy, const float*
     const int bx = token_blocks(a, tc.t, grad_blocks_per_cu(tc.t.ppl));
     hipError_t e = run_tokens(p, tc.vec, true, bx, st);
     if (e != hipSuccess || !params) return e;
-    param_sum_kernel<<<sum_blocks, 1024, 0, st>>>(p.part, bx, a.C, gw, gb);
+    param_sum_kernel<<<sum_blocks, 1024, 0, st>>>(p.part, bx, a.C, false, gw, gb);
     return hipGetLastError();
   }
   const bool vec = ok && map_vec(a, vec_of(a));
   MapArgs p{};
-  p.a = a, p.m = map_plan(a, vec ? vec_of(a) : 1), p.gy = gy, p.mean_in = mean, p.rstd_in = rstd;
+  p.m = map_plan(a, vec ? vec_of(a) : 1);
   p.part = (float*)ws, p.chan = (float*)(ws + l.chan), p.means = (float2*)(ws + l.means);
-  p.gx = gx, p.ggate = ggate;
-  const unsigned grid = (unsigned)a.N * p.m.ctiles * p.m.nsplit;
-  with_types(a.bf16, vec, [&](auto b, auto v) {
-    constexpr bool kB = decltype(b)::value, kV = decltype(v)::value;
-    map_grad_kernel<kB, kV, true><<<grid, 256, 0, st>>>(p);
-    map_means_kernel<<<(unsigned)a.N * a.groups, 256, 0, st>>>(p);
-    if (gx || ggate) map_grad_kernel<kB, kV, false><<<grid, 256, 0, st>>>(p);
-  });
-  if (params) param_sum_kernel<<<sum_blocks, 1024, 0, st>>>(p.chan, a.N, a.C, gw, gb);
-  return hipGetLastError();
+  for (int64_t n = 0; n < a.N; n += l.batch) {
+    p.a = from_map(a, n, l.batch < a.N - n ? l.batch : a.N - n);
+    p.gy = at_map(a, gy, n), p.mean_in = mean + n * a.groups, p.rstd_in = rstd + n * a.groups;
+    p.gx = at_map(a, gx, n), p.ggate = at_map(a, ggate, n);
+    const unsigned grid = (unsigned)p.a.N * p.m.ctiles * p.m.nsplit;
+    with_types(a.bf16, vec, [&](auto b, auto v) {
+      constexpr bool kB = decltype(b)::value, kV = decltype(v)::value;
+      map_grad_kernel<kB, kV, true><<<grid, 256, 0, st>>>(p);
+      map_means_kernel<<<(unsigned)p.a.N * a.groups, 256, 0, st>>>(p);
+      if (gx || ggate) map_grad_kernel<kB, kV, false><<<grid, 256, 0, st>>>(p);
+    });
+    if (params) param_sum_kernel<<<sum_blocks, 1024, 0, st>>>(p.chan, p.a.N, a.C, n > 0, gw, gb);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace pnr
