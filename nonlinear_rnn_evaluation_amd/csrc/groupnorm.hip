@@ -380,7 +380,7 @@ MapPlan map_plan(const Norm& a, int V) {
   if (split > 64) split = 64;
   if (split < 1) split = 1;
   m.rows = (int)((a.L + split - 1) / split);
-  m.nsplit = m.rows > 0 ? (a.L + m.rows - 1) / m.rows : 1;
+  m.nsplit = m.rows > 0 ? (a.L - 1) / m.rows + 1 : 1;
   return m;
 }
 // a map's pieces must not straddle groups where a block holds a single wide one
