@@ -303,7 +303,11 @@ __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenArgs p) {
       const int c = (sub + k * lanes) * V;
       if (!there || c >= W) continue;
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[k][i] = rstd * (gy[k][i] - s1 - h[k][i] * s2);
+      for (int i = 0; i < V; ++i) {
+        // a row without positions: zeros, also under a weight or a bias that is not finite
+        h[k][i] = live ? rstd * (gy[k][i] - s1 - h[k][i] * s2) : 0.0f;
+        gate[k][i] = live ? gate[k][i] : 0.0f;
+      }
       if (p.gx) P::store(p.gx, base + c, h[k]);
       if (p.ggate) P::store(p.ggate, base + c, gate[k]);
     }

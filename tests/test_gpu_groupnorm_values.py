@@ -36,3 +36,21 @@ def test_gates_of_any_finite_size(L, act, dtype):
     assert (np.abs(got - want) <= tol * np.abs(want) + 2.0 ** -17 * np.abs(Y) + 1e-30).all()
     y, ref = f["y"].double().cpu().numpy(), O.group_norm(X, 3, gate=G, activation=act)[0]
     assert (np.abs(y - ref) <= tol * np.abs(ref) + 2.0 ** -17 * np.abs(np.where(G > 0, G, 1.0)) + 1e-30).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [1, 5])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_rows_without_positions_have_zero_gradients_whatever_the_weights(bad, gated, L):
+    gen = torch.Generator().manual_seed(4)
+    x, gy, gate = (torch.randn(6, L, 16, generator=gen).cuda() for _ in range(3))
+    w, b = torch.ones(16, device="cuda"), torch.zeros(16, device="cuda")
+    w[3], b[9] = bad, bad
+    lens = torch.tensor([L, 0, 0, L, 0, L], dtype=torch.int32).cuda()
+    for act in (pnr.ACT_NONE, pnr.ACT_SILU):
+        kw = dict(weight=w, bias=b, gate=gate if gated else None, act=act, lens=lens)
+        f = pnr.group_norm(x, 2, **kw)
+        d = pnr.group_norm_backward(gy, x, 2, f["mean"], f["rstd"], **kw)
+        for t in [f["y"], d["x"]] + ([d["gate"]] if gated else []):
+            assert (t[lens == 0] == 0).all()
