@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(256) token_kernel(TokenArgs p) {
   }
 }
 
-// The same tokens: 127 us for 671 MB, 5.3 TB/s.
+// The same tokens: 130 us for 671 MB, 5.2 TB/s.
 template <bool kBf16, bool kVec, int PPL, int kThreads>
 __global__ void __launch_bounds__(kThreads) token_grad_kernel(TokenArgs p) {
   using P = Piece<kBf16, kVec>;
@@ -439,7 +439,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return red[0] + red[1] + red[2] + red[3];
 }
 
-// 8 maps of 4096 x 320 in bf16, 32 groups: 11 us for 21 MB; too short to fill memory: two trips to it a
+// 8 maps of 4096 x 320 in bf16, 32 groups: 10 us for 21 MB; too short to fill memory: two trips to it a
 // thread, then the joins.
 template <bool kBf16, bool kVec>
 __global__ void __launch_bounds__(256) map_stats_kernel(MapArgs p) {
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(256) map_norm_kernel(MapArgs p) {
 }
 
 // Per channel, over a slab: sums of dz n and of dz (kSums); or the gradients of x and the gate.
-// 3 maps of 1001 x 330 in fp32: 7.3 us and 8.1 us for 8 MB read and 8 read, 4 written, by single elements
+// 3 maps of 1001 x 330 in fp32: 7.4 us and 7.9 us for 8 MB read and 8 read, 4 written, by single elements
 // (rows of 330 are not aligned); launches as short as these are bound by their trips to memory.
 template <bool kBf16, bool kVec, bool kSums>
 __global__ void __launch_bounds__(256) map_grad_kernel(MapArgs p) {

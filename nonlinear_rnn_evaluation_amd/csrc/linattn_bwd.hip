@@ -17,9 +17,9 @@
 // over 4096 tokens in fp32, one walk a row: dg off by 1.7e-6 of its norm, more the earlier the token, and
 // its sum over the tokens by 1.9e-5; walks of four chunks 3.5e-7 and 7.7e-7, for 1 % of a training pass.
 //
-// 4 x 16 heads of 128 x 128 over 4096 tokens in bf16: sums 2 x 45 us, scan 25, dq with u and b 118 to
-// 137, dk with c 123 to 142, dv 72 to 83, dg 13 (the spread is from box to box).  The dot products
-// cost dq and dk their three-part S, a fourth tile of rows and, dq, a second set of scores.
+// 4 x 16 heads of 128 x 128 over 4096 tokens in bf16: sums 42 and 45 us, scan 24, dq with u and b 144, dk
+// with c 152, dv 94, dg 9 (10 % more on some boxes).  The dot products cost dq and dk their three-part S
+// (two in dv), a fourth tile of rows and, dq, a second set of scores.
 #include <algorithm>
 #include <type_traits>
 

@@ -122,8 +122,9 @@ void launch_columns(const StepArgs& p, hipStream_t st) {
 }
 
 // 128 columns a block keep sixteen loads of a thread in flight; where that leaves CUs without a
-// block, 32 columns a block.  bf16, 32 query heads on 8 states of 128 x 128, 192 requests: 45.0 us
-// (4.47 TB/s) and 51.5; one request, 16 states of 64 x 64: 4.6 us and 4.2.
+// block, 32 columns a block.  bf16, 32 query heads on 8 states of 128 x 128, 192 requests, in 128 and in 32
+// columns: 48.8 us (4.2 TB/s) and 55.0, or 35.1 and 40.3 where the last-level cache still holds the pool
+// from the call before; one request, 16 states of 64 x 64: 5.6 us and 4.6.
 template <bool kBf16, bool kVec>
 void launch(const StepArgs& p, hipStream_t st) {
   if ((int64_t)p.a.B * p.a.Hkv < 256)

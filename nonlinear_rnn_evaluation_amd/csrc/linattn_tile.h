@@ -476,10 +476,10 @@ __device__ __forceinline__ void add_outer(f32x4 (&S)[DK / 16], const typename Mm
 // X and E are done with after the first half and are loaded straight into LDS during the second; Y
 // and Z wait in registers.
 //
-// Measured, 16 heads of 128 x 128 in bf16 over 32768 tokens (kOut, 512 blocks, two a CU): 134 us for
-// 575 MB, 4.3 TB/s, 90 % of a copy's rate.  A chunk costs a CU 4.2 us with two blocks and 4.8 with
-// one; left out one at a time, of those 4.2 the update is 1.1, the outputs 0.7, the loads 0.5, the
-// scores 0.45, S^T X^T 0.4, Z^T P^T 0.2.  Matrix and vector instructions of a SIMD hardly overlap
+// Measured, 16 heads of 128 x 128 in bf16 over 32768 tokens (kOut, 512 blocks, two a CU): 148 us for
+// 575 MB, 3.9 TB/s; with one part each of scores and state, 134.  A chunk then cost a CU 4.2 us with two
+// blocks (4.6 now) and 4.8 with one; left out one at a time, of those 4.2 the update was 1.1, the outputs
+// 0.7, the loads 0.5, the scores 0.45, S^T X^T 0.4, Z^T P^T 0.2.  Matrix and vector instructions of a SIMD hardly overlap
 // here (24 products and 96 fused multiply-adds, two waves each: 775 and 558 cycles alone, 1214
 // together), so both are kept few.  32 columns a wave in half the waves, with half the reads of
 // X and Y from LDS: 145 us where this took 137.
@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) chunk_kernel(Role
 
 // The sum of a segment alone, from a zero state, and the segment's decay: chunk_kernel's update, 128
 // tokens a step (64 in fp32), because keys and values in flight are what bounds it: 16 heads of 128 x 128
-// over 32768 tokens in 78 us, 3.8 TB/s; 64 x 64 heads 22 us where 64 tokens a step took 25.
+// over 32768 tokens in 76 us, 3.9 TB/s; 64 x 64 heads 22 us where 64 tokens a step took 25.
 template <bool kBf16, int DK, int DV, bool kReverse, bool kVec>
 __global__ void __launch_bounds__(DV * 4, kBf16 ? 4 : DV / 64) sum_kernel(RoleArgs p) {
   using M = Mma<kBf16>;
@@ -1074,11 +1074,21 @@ struct Plan {
 // Few rows and a long axis: the axis is cut into segments that run side by side, at the price of
 // one more pass over the keys and values for the segments' own sums, and of the recurrence
 // over the segments.  As many segments as fill the device (256 CUs, two blocks each of the widest
-// bf16 tiles, one of fp32's), from the length on where that pays; one head's pass in us, whole | cut:
-//            forward   128 x 128 bf16          backward  128 x 128 bf16   fp32
-//   192 tokens         17 | 19                           73 | 66          159 | 103
-//   320                25 | 19                           111 | 68         253 | 105
-//   4096              252 | 35                          1141 | 89        2984 | 125
+// bf16 tiles, one of fp32's), from the length on where that pays; one head's pass of 128 x 128 in us,
+// whole | cut:
+//            forward    bf16        fp32         backward   bf16         fp32
+//   128 tokens       15 | 19     33 | 30                   65 | 71    120 | 103
+//   192              19 | 19     46 | 30                   84 | 71    166 | 103
+//   320              28 | 19     73 | 30                  122 | 72    259 | 104
+//   4096            288 | 27    862 | 39                 1235 | 86   2988 | 118
+// The other end, rows of 2048 tokens:
+//            forward    bf16 128   bf16 64    fp32 128     backward   bf16 128   bf16 64    fp32 128
+//   64 rows         152 | 79   115 | 41   442 | 179              653 | 271   508 | 136  1561 | 574
+//   128             152 | 126  116 | 64   446 | 339              667 | 453   509 | 221  1573 | 1052
+//   160             155 | 160  116 | 80                          672 | 552   513 | 286
+//   192             159 | 206  116 | 104                         681 | 706   516 | 383
+//   256             168 | 248  117 | 111                         706 | 818   518 | 416
+// so from about 160 rows of wide bf16 heads on the rule cuts where the whole axis would be the faster.
 inline Plan make_plan(const LinAttn& a, bool backward) {
   const int chunks = (a.T + kChunk - 1) / kChunk;
   const int64_t rows = (int64_t)a.B * a.Hkv;
