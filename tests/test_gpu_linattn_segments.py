@@ -82,3 +82,22 @@ def test_many_rows_without_segments(decay, lens, dtype):
 def test_wide_tiles_over_several_chunks(dtype):
     """64 state heads of 128 x 128 shared by two query heads each, segments of several chunks."""
     _check(4, 16, 640, 8, 4, 128, 128, dtype, "token", [640, 511, 129])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,lens", [(30, 900, [900, 512, 257, 64, 0]), (2, 9000, [9000, 4097])], ids=["rows", "segments"])
+def test_walks_without_tokens_read_nothing_of_the_workspace(B, T, lens):
+    """Rows that end inside, at and behind the four chunks between two exact <state, gradient>: what an earlier
+    call left in the workspace shows nowhere."""
+    gen = torch.Generator().manual_seed(6)
+    q, k, v, go = (torch.randn(B, T, 10, 16, generator=gen).cuda() for _ in range(4))
+    g = -torch.empty(B, T, 10).exponential_(20.0, generator=gen).cuda()
+    state, gs = (torch.randn(B, 10, 16, 16, generator=gen).cuda() for _ in range(2))
+    ln = torch.tensor([lens[b % len(lens)] for b in range(B)], dtype=torch.int32).cuda()
+    kw = dict(state=state, grad_state=gs, lens=ln)
+    one = pnr.linear_attention_backward(q, k, v, g, go, **kw)
+    for fill in (0xFF, 0x7F):       # NaN, and 3.4e38
+        ws = torch.full_like(one["workspace"], fill)
+        again = pnr.linear_attention_backward(q, k, v, g, go, workspace=ws, **kw)
+        for n in ("q", "k", "v", "log_decay", "state"):
+            assert torch.isfinite(one[n]).all() and torch.equal(one[n], again[n]), n
