@@ -554,6 +554,166 @@ int pnr_groupnorm_backward(const pnr_norm* desc, const void* x, const float* wei
                            const void* gate, const void* grad_y, const float* mean, const float* rstd,
                            void* grad_x, float* grad_weight, float* grad_bias, void* grad_gate);
 
+/*
+ * Selective scan: the recurrence of a state space layer whose step width, input and read-out
+ * depend on the token.  For each batch row, channel e of E and state n of N, with g = e / (E / G)
+ * the channel's group:
+ *   delta = softplus(dt + dt_bias), or dt + dt_bias
+ *   h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t      h_0 = state_in or zeros
+ *   y_t = (sum over n of C_t h_t) + D u_t               and  y_t silu(z_t)  with a gate z
+ *
+ * Layout (device pointers, owned by the caller; elements of `dtype` unless stated):
+ *   u, dt, z    [B, T, E] with element strides {batch, token}; z may be NULL (no gate)
+ *   B, C        [B, T, G, N] with element strides {batch, token, group}
+ *               (strides >= 0, the last axis contiguous: slices of projections need no copy)
+ *   A           fp32 [E, N], finite; a decay is meant (A <= 0, delta >= 0), others are taken as they are
+ *   D, dt_bias  fp32 [E] or NULL (zeros)
+ *   state_in, state_out   fp32 [B, E, N]
+ *   y           [B, T, E] contiguous
+ *   lens        int32 [B] or NULL: row b has min(max(lens[b], 0), T) tokens.  What lies behind a
+ *               row's end is not read, its outputs and gradients are zeros, and the state is the one
+ *               after the row's last token (an empty row hands state_in on)
+ * Supported: dtype PNR_F32 and PNR_BF16, 1 <= N <= 64 (others PNR_E_UNSUPPORTED), G divides E,
+ * E <= 2^20, T <= 2^30, B G ceil(E / G / 64) <= 4 million.  Everything inside is fp32; outputs of
+ * `dtype` are rounded once, at the end.
+ *
+ * A NaN or an infinity in a token reaches what the formulas compute from it, within its row: u, dt,
+ * z and grad_y their channel, B and C the channels of their group; forwards in time for y and the
+ * states, backwards too for the gradients; grad_B and grad_C at a token are sums over the group's
+ * channels.  An infinity may come out as a NaN.
+ *
+ * Outputs do not overlap inputs, but for the states where it is said.  None of these calls waits
+ * for the device or allocates: the work is enqueued on desc->stream, so they may be recorded into a
+ * HIP graph.  Return PNR_OK or a negative pnr_status.
+ */
+typedef struct pnr_selscan {
+  int32_t B, T;          /* batch >= 1, tokens >= 0                                    */
+  int32_t E, N, G;       /* channels, states of a channel, groups of B and C            */
+  int32_t dtype;         /* pnr_dtype of u, dt, z, B, C, y and their gradients         */
+  int32_t softplus;      /* 1: delta = softplus(dt + dt_bias); 0: dt + dt_bias          */
+  int64_t u_stride[2], dt_stride[2], z_stride[2];  /* elements: batch, token            */
+  int64_t B_stride[3], C_stride[3];                /* elements: batch, token, group     */
+  const int32_t* lens;   /* [B] or NULL                                                */
+  void* stream;          /* hipStream_t, NULL = default stream                         */
+  void* workspace;       /* device scratch, 256-byte aligned                           */
+  size_t workspace_bytes;
+} pnr_selscan;
+
+/*
+ * All tokens of a sequence at once.  state_in may be NULL (zeros), state_out NULL (not wanted);
+ * they may be the same buffer.  Workspace: pnr_selscan_workspace_bytes() bytes (0: none needed, or
+ * an invalid request, which pnr_selscan_forward then names; pure host arithmetic).  With T = 0
+ * only state_out is written.
+ */
+size_t pnr_selscan_workspace_bytes(const pnr_selscan* desc);
+int pnr_selscan_forward(const pnr_selscan* desc, const void* u, const void* dt, const float* A,
+                        const void* Bt, const void* Ct, const float* D, const void* z,
+                        const float* dt_bias, const float* state_in, void* y, float* state_out);
+
+/*
+ * One token for each of B running requests (T, the token strides and lens are not read): u, dt, z
+ * [B, E], B and C [B, G, N], y [B, E] contiguous.  state_in and state_out are pools
+ * [n_slots, E, N]; request b's state is read from and written to slot slots[b] (int32 [B]), or slot
+ * b when slots is NULL (n_slots >= B then).  A slot outside [0, n_slots) marks an idle row: its y is
+ * zeros and no state is touched.  No two rows may name the same slot.  state_in and state_out may
+ * be the same buffer (updated in place); otherwise slots that no row names keep what they held in
+ * state_out.  No workspace.
+ */
+int pnr_selscan_step(const pnr_selscan* desc, const void* u, const void* dt, const float* A,
+                     const void* Bt, const void* Ct, const float* D, const void* z,
+                     const float* dt_bias, const float* state_in, const int32_t* slots, int n_slots,
+                     void* y, float* state_out);
+
+/*
+ * Gradients of a loss through pnr_selscan_forward, given grad_y (contiguous, as y) and
+ * grad_state_out = dL/dstate_out (NULL: zeros):
+ *   grad_u, grad_dt, grad_z   dtype, [B, T, E] contiguous
+ *   grad_B, grad_C            dtype, [B, T, G, N] contiguous, summed over the group's channels
+ *   grad_A                    fp32 [E, N]; grad_D, grad_dt_bias fp32 [E]; summed over rows and tokens
+ *   grad_state_in             fp32 [B, E, N]
+ * Every gradient output may be NULL (not wanted; grad_z needs a z); all are overwritten.  Sums
+ * are taken in an order that does not change from call to call.  The states are recomputed.
+ * Workspace: pnr_selscan_workspace_bytes_backward() bytes (0: invalid request).
+ */
+size_t pnr_selscan_workspace_bytes_backward(const pnr_selscan* desc);
+int pnr_selscan_backward(const pnr_selscan* desc, const void* u, const void* dt, const float* A,
+                         const void* Bt, const void* Ct, const float* D, const void* z,
+                         const float* dt_bias, const float* state_in, const void* grad_y,
+                         const float* grad_state_out, void* grad_u, void* grad_dt, float* grad_A,
+                         void* grad_B, void* grad_C, float* grad_D, void* grad_z,
+                         float* grad_dt_bias, float* grad_state_in);
+
+/*
+ * Activations kept in 8 bits until the backward pass reads them.  x [B, T, E] in `dtype` with
+ * element strides {batch, token} >= 0; 32 consecutive channels (the last block of a token may be
+ * shorter) share the least power of two 2^e, e >= -126, with |x| <= 127 * 2^e, and
+ *   codes      int8 [B, T, E]                   x / 2^e rounded to nearest, ties to even (at e = 122
+ *                                               at most 63: 2^128 is infinite)
+ *   exponents  uint8 [B, T, ceil(E / 32)]       e + 127, or 255 where the block holds a NaN or
+ *                                               an infinity: all of it reads back as NaN
+ * pnr_checkpoint_unpack writes code * 2^e to x [B, T, E] contiguous (exact in bf16 and in fp32;
+ * x_stride is not read).  E <= 2^20, T <= 2^30, B T ceil(E / 32) <= 2^40.  No workspace; the calls
+ * wait for nothing and allocate nothing.
+ */
+typedef struct pnr_checkpoint {
+  int32_t B, T, E;       /* B, E >= 1, T >= 0                                          */
+  int32_t dtype;         /* PNR_F32 or PNR_BF16                                        */
+  int64_t x_stride[2];   /* elements: batch, token                                     */
+  void* stream;
+} pnr_checkpoint;
+
+int pnr_checkpoint_pack(const pnr_checkpoint* desc, const void* x, int8_t* codes, uint8_t* exponents);
+int pnr_checkpoint_unpack(const pnr_checkpoint* desc, const int8_t* codes, const uint8_t* exponents, void* x);
+
+/*
+ * Causal convolution along time, each channel by itself, W taps:
+ *   p_t = bias + sum over j < W of weight[e, j] x_{t - W + 1 + j},   y = act(p)
+ * x [B, T, E] with element strides {batch, token} (>= 0, channels contiguous), or, with
+ * `exponents`, the codes [B, T, E] that pnr_checkpoint_pack wrote (x_stride is not read then).
+ * weight fp32 [E, W], bias fp32 [E] or NULL (zeros).  state_in [B, W - 1, E] are the inputs before
+ * the first (NULL: zeros), state_out [B, W - 1, E] the last W - 1 inputs of each row, state_in's
+ * among them where the row is shorter (NULL: not wanted).  y, the states and the gradients that
+ * are not fp32 are of `dtype` and contiguous.  lens int32 [B] or NULL: row b has
+ * min(max(lens[b], 0), T) tokens; what lies behind is not read, y and gradients are zeros there.
+ * dtype PNR_F32 or PNR_BF16, act PNR_ACT_NONE or PNR_ACT_SILU, 1 <= W <= 8 (others
+ * PNR_E_UNSUPPORTED), E <= 2^20, T <= 2^30, B (E / 64 + 1) <= 4 million.  Sums are fp32, outputs
+ * rounded once.  A NaN or an infinity reaches what the formulas compute from it, within its channel
+ * and row.  Outputs do not overlap inputs.  The calls wait for nothing and allocate nothing.
+ */
+typedef struct pnr_conv {
+  int32_t B, T, E, W;    /* B, E, W >= 1, T >= 0                                       */
+  int32_t dtype, act;    /* pnr_dtype, pnr_act                                         */
+  int64_t x_stride[2];   /* elements: batch, token                                     */
+  const int32_t* lens;   /* [B] or NULL                                                */
+  void* stream;
+  void* workspace;       /* device scratch, 256-byte aligned                           */
+  size_t workspace_bytes;
+} pnr_conv;
+
+int pnr_conv_forward(const pnr_conv* desc, const void* x, const uint8_t* exponents, const float* weight,
+                     const float* bias, const void* state_in, void* y, void* state_out);
+
+/*
+ * One token for each of B requests (T, the token stride and lens are not read): x and y [B, E],
+ * state_in and state_out pools [n_slots, W - 1, E], slots and idle rows as in pnr_selscan_step;
+ * the pools may be the same buffer.
+ */
+int pnr_conv_step(const pnr_conv* desc, const void* x, const float* weight, const float* bias,
+                  const void* state_in, const int32_t* slots, int n_slots, void* y, void* state_out);
+
+/*
+ * Gradients through pnr_conv_forward of these arguments, given grad_y [B, T, E] and grad_state_out
+ * (NULL: zeros): grad_x [B, T, E] and grad_state_in in `dtype`; grad_weight fp32 [E, W] and
+ * grad_bias fp32 [E], summed over rows and tokens in an order that does not change from call to
+ * call.  Each may be NULL; all are overwritten.  Workspace:
+ * pnr_conv_workspace_bytes_backward() bytes (0: invalid request).
+ */
+size_t pnr_conv_workspace_bytes_backward(const pnr_conv* desc);
+int pnr_conv_backward(const pnr_conv* desc, const void* x, const uint8_t* exponents, const float* weight,
+                      const float* bias, const void* state_in, const void* grad_y,
+                      const void* grad_state_out, void* grad_x, float* grad_weight, float* grad_bias,
+                      void* grad_state_in);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,7 @@
 // Internal interface of the sequence-mixing operators: linear attention with per-head
-// decay (linattn*.hip) and group norm with an activation (groupnorm.hip); their C entry
-// points are in seq_api.hip.
+// decay (linattn*.hip), group norm with an activation (groupnorm.hip), the selective scan
+// (selscan*.hip), the causal convolution (conv.hip) and 8-bit copies of activations
+// (checkpoint.hip); their C entry points are in seq_api.hip.
 #pragma once
 
 #include "common.h"
@@ -61,6 +62,63 @@ size_t groupnorm_workspace_backward(const Norm& a);
 hipError_t launch_groupnorm_backward(const Norm& a, const void* gy, const float* mean, const float* rstd, void* gx,
                                      float* gw, float* gb, void* ggate, char* ws, hipStream_t st);
 
+constexpr int kMaxStates = 64;    // of a channel of the selective scan
+constexpr int kMaxTaps = 8;       // of the convolution
+constexpr int kPackBlock = 32;    // values on one exponent in an 8-bit copy
+
+// A [B, T, E] operand: element strides between batch rows and tokens.
+struct Tokens {
+  const void* p;
+  int64_t sb, st;
+};
+
+// Device-side problem of the selective scan (pnr_selscan without host fields).
+struct SelScan {
+  int B, T, E, N, G;
+  int bf16, softplus;
+  Tokens u, dt, z;           // z.p may be nullptr
+  Rows Bt, Ct;               // [B, T, G, N]
+  const float *A, *D, *bias; // D, bias may be nullptr
+  const int32_t* lens;
+};
+
+struct SelScanGrads {
+  const void* gy;
+  const float* gstate_out;   // or nullptr
+  void *gu, *gdt, *gB, *gC, *gz;             // or nullptr
+  float *gA, *gD, *gbias, *gstate_in;        // or nullptr
+};
+
+size_t selscan_workspace(const SelScan& a);
+hipError_t launch_selscan_forward(const SelScan& a, const float* state_in, void* y, float* state_out, char* ws,
+                                  hipStream_t st);
+hipError_t launch_selscan_step(const SelScan& a, const float* state_in, const int32_t* slots, int n_slots, void* y,
+                               float* state_out, hipStream_t st);
+size_t selscan_workspace_backward(const SelScan& a);
+hipError_t launch_selscan_backward(const SelScan& a, const float* state_in, const SelScanGrads& d, char* ws,
+                                   hipStream_t st);
+
+struct Conv {
+  int B, T, E, W;
+  int bf16, silu;
+  Tokens x;
+  const uint8_t* exps;       // x holds int8 codes on these exponents, or nullptr
+  const float *weight, *bias;
+  const int32_t* lens;
+};
+
+hipError_t launch_conv_forward(const Conv& a, const void* state_in, void* y, void* state_out, hipStream_t st);
+hipError_t launch_conv_step(const Conv& a, const void* state_in, const int32_t* slots, int n_slots, void* y,
+                            void* state_out, hipStream_t st);
+size_t conv_workspace_backward(const Conv& a);
+hipError_t launch_conv_backward(const Conv& a, const void* state_in, const void* gy, const void* gstate_out, void* gx,
+                                float* gw, float* gb, void* gstate_in, char* ws, hipStream_t st);
+
+hipError_t launch_checkpoint_pack(const Tokens& x, int B, int T, int E, int bf16, int8_t* codes, uint8_t* exps,
+                                  hipStream_t st);
+hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t rows, int E, int bf16, void* x,
+                                    hipStream_t st);
+
 // ---- device helpers --------------------------------------------------------------------
 __device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
@@ -91,6 +149,21 @@ struct Elem<false> {
   static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 };
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// log(1 + e^x) without overflow and, where e^x is far below 1, without loss: log(w) of the rounded
+// w = 1 + e is scaled by e / (w - 1), what the rounding took.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = fast_exp(-fabsf(x)), w = 1.0f + e, d = w - 1.0f;
+  const float l = __builtin_amdgcn_logf(w) * kLn2 * (e * fast_rcp(d));
+  return fmaxf(x, 0.0f) + (d == 0.0f ? e : l);
+}
+
+// The value of an 8-bit copy's code on exponent byte s (255: not finite).
+__device__ __forceinline__ float unpack_code(int code, int s) {
+  return s == 255 ? __uint_as_float(0x7fc00000u) : ldexpf((float)code, s - 127);
+}
 
 __device__ __forceinline__ int row_len(const int32_t* lens, int b, int T) {
   if (!lens) return T;

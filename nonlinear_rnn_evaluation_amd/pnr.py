@@ -11,7 +11,7 @@ import ctypes
 import os
 import re
 import struct
-from typing import Optional
+from typing import NamedTuple, Optional, Union
 
 import torch
 
@@ -60,6 +60,26 @@ class PnrLinattn(ctypes.Structure):
 class PnrNorm(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int32), ("L", ctypes.c_int32), ("C", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("lens", ctypes.c_void_p), ("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PnrSelscan(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("G", ctypes.c_int32), ("dtype", ctypes.c_int32), ("softplus", ctypes.c_int32),
+                ("u_stride", ctypes.c_int64 * 2), ("dt_stride", ctypes.c_int64 * 2), ("z_stride", ctypes.c_int64 * 2),
+                ("B_stride", ctypes.c_int64 * 3), ("C_stride", ctypes.c_int64 * 3), ("lens", ctypes.c_void_p),
+                ("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PnrCheckpoint(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("E", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 2), ("stream", ctypes.c_void_p)]
+
+
+class PnrConv(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("E", ctypes.c_int32), ("W", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("x_stride", ctypes.c_int64 * 2),
                 ("lens", ctypes.c_void_p), ("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t)]
 
@@ -143,7 +163,18 @@ def load() -> ctypes.CDLL:
             ("pnr_groupnorm_workspace_bytes", [P(PnrNorm)], ctypes.c_size_t),
             ("pnr_groupnorm", [P(PnrNorm)] + [vp] * 7, ctypes.c_int),
             ("pnr_groupnorm_workspace_bytes_backward", [P(PnrNorm)], ctypes.c_size_t),
-            ("pnr_groupnorm_backward", [P(PnrNorm)] + [vp] * 11, ctypes.c_int)):
+            ("pnr_groupnorm_backward", [P(PnrNorm)] + [vp] * 11, ctypes.c_int),
+            ("pnr_selscan_workspace_bytes", [P(PnrSelscan)], ctypes.c_size_t),
+            ("pnr_selscan_forward", [P(PnrSelscan)] + [vp] * 11, ctypes.c_int),
+            ("pnr_selscan_step", [P(PnrSelscan)] + [vp] * 10 + [ctypes.c_int, vp, vp], ctypes.c_int),
+            ("pnr_selscan_workspace_bytes_backward", [P(PnrSelscan)], ctypes.c_size_t),
+            ("pnr_selscan_backward", [P(PnrSelscan)] + [vp] * 20, ctypes.c_int),
+            ("pnr_checkpoint_pack", [P(PnrCheckpoint)] + [vp] * 3, ctypes.c_int),
+            ("pnr_checkpoint_unpack", [P(PnrCheckpoint)] + [vp] * 3, ctypes.c_int),
+            ("pnr_conv_forward", [P(PnrConv)] + [vp] * 7, ctypes.c_int),
+            ("pnr_conv_step", [P(PnrConv)] + [vp] * 5 + [ctypes.c_int, vp, vp], ctypes.c_int),
+            ("pnr_conv_workspace_bytes_backward", [P(PnrConv)], ctypes.c_size_t),
+            ("pnr_conv_backward", [P(PnrConv)] + [vp] * 11, ctypes.c_int)):
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
     _lib = lib
@@ -366,6 +397,63 @@ def pnr_groupnorm_backward(desc: PnrNorm, x: int, weight: Optional[int], bias: O
 
 
 # ---- torch-level conveniences (allocation + marshalling) ---------------------------------
+def pnr_selscan_workspace_bytes(desc: PnrSelscan) -> int:
+    return load().pnr_selscan_workspace_bytes(ctypes.byref(desc))
+
+
+def pnr_selscan_forward(desc: PnrSelscan, u: int, dt: int, A: int, B: int, C: int, D: Optional[int], z: Optional[int],
+                        dt_bias: Optional[int], state_in: Optional[int], y: int, state_out: Optional[int]) -> int:
+    return load().pnr_selscan_forward(ctypes.byref(desc), u, dt, A, B, C, D, z, dt_bias, state_in, y, state_out)
+
+
+def pnr_selscan_step(desc: PnrSelscan, u: int, dt: int, A: int, B: int, C: int, D: Optional[int], z: Optional[int],
+                     dt_bias: Optional[int], state_in: int, slots: Optional[int], n_slots: int, y: int,
+                     state_out: int) -> int:
+    return load().pnr_selscan_step(ctypes.byref(desc), u, dt, A, B, C, D, z, dt_bias, state_in, slots, n_slots, y,
+                                   state_out)
+
+
+def pnr_selscan_workspace_bytes_backward(desc: PnrSelscan) -> int:
+    return load().pnr_selscan_workspace_bytes_backward(ctypes.byref(desc))
+
+
+def pnr_selscan_backward(desc: PnrSelscan, u: int, dt: int, A: int, B: int, C: int, D: Optional[int],
+                         z: Optional[int], dt_bias: Optional[int], state_in: Optional[int], grad_y: int,
+                         grad_state_out: Optional[int], *grads: Optional[int]) -> int:
+    """grads: u, dt, A, B, C, D, z, dt_bias, state_in."""
+    return load().pnr_selscan_backward(ctypes.byref(desc), u, dt, A, B, C, D, z, dt_bias, state_in, grad_y,
+                                       grad_state_out, *grads)
+
+
+def pnr_checkpoint_pack(desc: PnrCheckpoint, x: int, codes: int, exponents: int) -> int:
+    return load().pnr_checkpoint_pack(ctypes.byref(desc), x, codes, exponents)
+
+
+def pnr_checkpoint_unpack(desc: PnrCheckpoint, codes: int, exponents: int, x: int) -> int:
+    return load().pnr_checkpoint_unpack(ctypes.byref(desc), codes, exponents, x)
+
+
+def pnr_conv_forward(desc: PnrConv, x: int, exponents: Optional[int], weight: int, bias: Optional[int],
+                     state_in: Optional[int], y: int, state_out: Optional[int]) -> int:
+    return load().pnr_conv_forward(ctypes.byref(desc), x, exponents, weight, bias, state_in, y, state_out)
+
+
+def pnr_conv_step(desc: PnrConv, x: int, weight: int, bias: Optional[int], state_in: Optional[int],
+                  slots: Optional[int], n_slots: int, y: int, state_out: Optional[int]) -> int:
+    return load().pnr_conv_step(ctypes.byref(desc), x, weight, bias, state_in, slots, n_slots, y, state_out)
+
+
+def pnr_conv_workspace_bytes_backward(desc: PnrConv) -> int:
+    return load().pnr_conv_workspace_bytes_backward(ctypes.byref(desc))
+
+
+def pnr_conv_backward(desc: PnrConv, x: int, exponents: Optional[int], weight: int, bias: Optional[int],
+                      state_in: Optional[int], grad_y: int, grad_state_out: Optional[int], grad_x: Optional[int],
+                      grad_weight: Optional[int], grad_bias: Optional[int], grad_state_in: Optional[int]) -> int:
+    return load().pnr_conv_backward(ctypes.byref(desc), x, exponents, weight, bias, state_in, grad_y, grad_state_out,
+                                    grad_x, grad_weight, grad_bias, grad_state_in)
+
+
 class PnrError(RuntimeError):
     pass
 
@@ -525,6 +613,9 @@ def scan(kind: int, A: torch.Tensor, b: torch.Tensor, tile_len: int = 0) -> torc
 _SEQ_DT = {torch.float32: F32, torch.bfloat16: BF16}
 _LINATTN = struct.Struct("8i d 9q 3P N")      # the layouts of pnr_linattn and pnr_norm
 _NORM = struct.Struct("6i d 3P N")
+_SELSCAN = struct.Struct("7i 12q 3P N")        # ... of pnr_selscan, pnr_checkpoint and pnr_conv
+_CHECKPOINT = struct.Struct("4i 2q P")
+_CONV = struct.Struct("6i 2q 3P N")
 
 
 def _pack(struct_type, layout: struct.Struct, *fields):
@@ -739,5 +830,251 @@ def group_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, groups: int, mean
     out = {n: torch.empty_like(args[n]) for n in want if args[n] is not None}
     workspace = _workspace(pnr_groupnorm_workspace_bytes_backward(desc), workspace, dev, desc)
     _call(pnr_groupnorm_backward, dev, desc, *ptrs, *ins, *[_ptr(out.get(n)) for n in ("x", "weight", "bias", "gate")])
+    out["workspace"] = workspace
+    return out
+
+
+# ---- selective scan, the causal convolution before it, 8-bit copies of activations ----------------
+def _selscan(u, dt, A, B, C, D, z, dt_bias, softplus, lens, step: bool) -> tuple:
+    """The descriptor of a selective-scan call, the eight inputs' pointers, the sizes, the device."""
+    ty = u.dtype
+    code = _SEQ_DT.get(ty)
+    if code is None:
+        raise TypeError(f"the selective scan takes float32 or bfloat16 (got {ty})")
+    us, bs, dims = u.shape, B.shape, 2 if step else 3
+    if len(us) != dims or len(bs) != dims + 1:
+        raise ValueError("u, dt, z must be [B, E] and B, C [B, G, N]" if step else "u, dt, z must be [B, T, E] and B, C [B, T, G, N]")
+    lead, E, (G, N), dev = us[:-1], us[-1], bs[-2:], u.get_device()
+    a, b, c, d = u.stride(), dt.stride(), B.stride(), C.stride()
+    zs = (0,) * dims if z is None else z.stride()
+    if not (dt.dtype == B.dtype == C.dtype == ty and dev >= 0 and dt.get_device() == dev == B.get_device() == C.get_device()
+            and dt.shape == us and bs[:-2] == lead and C.shape == bs and (a[-1] == b[-1] == 1 or E == 1)
+            and (c[-1] == d[-1] == 1 or N == 1)
+            and (z is None or z.dtype == ty and z.get_device() == dev and z.shape == us and (zs[-1] == 1 or E == 1))):
+        for t, name, shape in ((u, "u", us), (dt, "dt", us), (z, "z", us), (B, "B", (*lead, G, N)), (C, "C", (*lead, G, N))):
+            if t is not None:
+                _rows(t, name, ty, shape, dev)
+    f32 = torch.float32
+    ptrs = (u.data_ptr(), dt.data_ptr(), _on(dev, A, "A", f32, (E, N)), B.data_ptr(), C.data_ptr(),
+            _on(dev, D, "D", f32, (E,)), None if z is None else z.data_ptr(), _on(dev, dt_bias, "dt_bias", f32, (E,)))
+    if step:
+        T, strides = 1, (a[0], 0, b[0], 0, zs[0], 0, c[0], 0, c[1], d[0], 0, d[1])
+    else:
+        T, strides = us[1], (a[0], a[1], b[0], b[1], zs[0], zs[1], *c[:3], *d[:3])
+    desc = _pack(PnrSelscan, _SELSCAN, us[0], T, E, N, G, code, bool(softplus), *strides,
+                 _on(dev, lens, "lens", torch.int32, lead[:1]) or 0, _raw_stream(dev), 0, 0)
+    return desc, ptrs, (us[0], E, N), dev
+
+
+def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *,
+                   D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                   dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                   state: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                   y: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_selscan_forward: h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t, y_t = (C_t . h_t + D u_t)
+    silu(z_t) over whole sequences, delta = softplus(dt + dt_bias), or dt + dt_bias.  u, dt, z [B,T,E] and
+    B, C [B,T,G,N] (float32 or bfloat16, strided as they come, last axis contiguous; a group is E / G
+    consecutive channels), A float32 [E,N], D and dt_bias float32 [E], state (before the first token,
+    zeros if None) float32 [B,E,N], lens int32 [B] (tokens of each row, T if None).  Returns
+    dict(y=[B,T,E], state=the state after each row's last token, workspace)."""
+    desc, ptrs, (nb, E, N), dev = _selscan(u, dt, A, B, C, D, z, dt_bias, softplus, lens, False)
+    if y is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    shape = (nb, E, N)
+    if state_out is None:
+        state_out = torch.empty(shape, dtype=torch.float32, device=u.device)
+    args = (_on(dev, state, "state", torch.float32, shape), _on(dev, y, "y", u.dtype, u.shape),
+            _on(dev, state_out, "state_out", torch.float32, shape))
+    workspace = _workspace(pnr_selscan_workspace_bytes(desc), workspace, dev, desc)
+    _call(pnr_selscan_forward, dev, desc, *ptrs, *args)
+    return {"y": y, "state": state_out, "workspace": workspace}
+
+
+def selective_scan_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                        state: torch.Tensor, *, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                        dt_bias: Optional[torch.Tensor] = None, softplus: bool = True,
+                        slots: Optional[torch.Tensor] = None, state_out: Optional[torch.Tensor] = None,
+                        y: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_selscan_step: one token for each of B requests.  u, dt, z [B,E], B, C [B,G,N]; state float32
+    [n_slots,E,N], the pool of running requests' states, of which request b has slot slots[b] (int32
+    [B]; slot b if None; a slot outside the pool marks an idle row).  The pool is updated in place
+    unless state_out gives another one of its shape.  Returns dict(y=[B,E], state=the updated pool)."""
+    desc, ptrs, (nb, E, N), dev = _selscan(u, dt, A, B, C, D, z, dt_bias, softplus, None, True)
+    if state_out is None:
+        state_out = state
+    if y is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    n_slots = state.shape[0] if state.dim() else 0
+    shape = (n_slots, E, N)
+    _call(pnr_selscan_step, dev, desc, *ptrs, _on(dev, state, "state", torch.float32, shape),
+          _on(dev, slots, "slots", torch.int32, (nb,)), n_slots, _on(dev, y, "y", u.dtype, u.shape),
+          _on(dev, state_out, "state_out", torch.float32, shape))
+    return {"y": y, "state": state_out}
+
+
+def selective_scan_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                            grad_y: torch.Tensor, *, D: Optional[torch.Tensor] = None,
+                            z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                            softplus: bool = True, state: Optional[torch.Tensor] = None,
+                            lens: Optional[torch.Tensor] = None, grad_state: Optional[torch.Tensor] = None,
+                            want=("u", "dt", "A", "B", "C", "D", "z", "dt_bias", "state"),
+                            workspace: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_selscan_backward: gradients through selective_scan of these arguments, given grad_y = dL/dy
+    [B,T,E] and grad_state = dL/d(returned state) (zeros if None).  Returns {name: gradient} for the
+    names in `want` whose argument is given (u, dt, B, C, z in their dtype, the others float32) and
+    "workspace"."""
+    desc, ptrs, (nb, E, N), dev = _selscan(u, dt, A, B, C, D, z, dt_bias, softplus, lens, False)
+    shape = (nb, E, N)
+    args = (_on(dev, state, "state", torch.float32, shape), _on(dev, grad_y, "grad_y", u.dtype, u.shape),
+            _on(dev, grad_state, "grad_state", torch.float32, shape))
+    given = dict(u=u, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, state=state)
+    unknown = set(want) - set(given)
+    if unknown:
+        raise ValueError(f"no gradient named {sorted(unknown)}")
+    out = {n: torch.empty(given[n].shape, dtype=given[n].dtype, device=u.device) for n in want if given[n] is not None}
+    workspace = _workspace(pnr_selscan_workspace_bytes_backward(desc), workspace, dev, desc)
+    _call(pnr_selscan_backward, dev, desc, *ptrs, *args, *[_ptr(out.get(n)) for n in given])
+    out["workspace"] = workspace
+    return out
+
+
+class Packed(NamedTuple):
+    """An activation in 8 bits: value = codes * 2^(exponents - 127), 32 channels an exponent."""
+    codes: torch.Tensor          # int8 [..., E]
+    exponents: torch.Tensor      # uint8 [..., ceil(E / 32)]
+
+
+def _packed(p: Packed) -> tuple:
+    """Shape, device and pointers of a packed activation."""
+    shape, dev = p.codes.shape, p.codes.get_device()
+    if len(shape) not in (2, 3):
+        raise ValueError(f"codes must be [rows, E] or [B, T, E] (got {tuple(shape)})")
+    if dev < 0:
+        raise ValueError("libpnr takes device tensors")
+    return shape, dev, _on(dev, p.codes, "codes", torch.int8, shape), \
+        _on(dev, p.exponents, "exponents", torch.uint8, (*shape[:-1], (shape[-1] + 31) // 32))
+
+
+def checkpoint_pack(x: torch.Tensor) -> Packed:
+    """Run pnr_checkpoint_pack: x [rows, E] or [B, T, E] (float32 or bfloat16, strided as it comes, last axis
+    contiguous) in 8 bits and an exponent for every 32 channels.  causal_conv and
+    causal_conv_backward read the result in place of x; checkpoint_unpack gives the values."""
+    code, dims, dev = _SEQ_DT.get(x.dtype), x.dim(), x.get_device()
+    if code is None:
+        raise TypeError(f"checkpoints are made of float32 or bfloat16 (got {x.dtype})")
+    if dims not in (2, 3):
+        raise ValueError(f"x must be [rows, E] or [B, T, E] (got {tuple(x.shape)})")
+    _rows(x, "x", x.dtype, x.shape, dev)
+    E, s = x.shape[-1], x.stride()
+    codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    exps = torch.empty(*x.shape[:-1], (E + 31) // 32, dtype=torch.uint8, device=x.device)
+    desc = _pack(PnrCheckpoint, _CHECKPOINT, *(x.shape if dims == 3 else (1, *x.shape)), code, s[0] if dims == 3 else 0, s[-2],
+                 _raw_stream(dev))
+    _call(pnr_checkpoint_pack, dev, desc, x.data_ptr(), codes.data_ptr(), exps.data_ptr())
+    return Packed(codes, exps)
+
+
+def checkpoint_unpack(packed: Packed, dtype: torch.dtype) -> torch.Tensor:
+    """Run pnr_checkpoint_unpack: the values of a packed activation (exact in both types)."""
+    code = _SEQ_DT.get(dtype)
+    if code is None:
+        raise TypeError(f"checkpoints are read as float32 or bfloat16 (got {dtype})")
+    shape, dev, codes, exps = _packed(packed)
+    x = torch.empty(shape, dtype=dtype, device=packed.codes.device)
+    desc = _pack(PnrCheckpoint, _CHECKPOINT, *(shape if len(shape) == 3 else (1, *shape)), code, 0, 0, _raw_stream(dev))
+    _call(pnr_checkpoint_unpack, dev, desc, codes, exps, x.data_ptr())
+    return x
+
+
+def _conv(x, weight, bias, act, lens, dtype, step: bool) -> tuple:
+    """The descriptor of a convolution, the pointers of x, its exponents, weight and bias, the shape of x,
+    the taps, the device.  dtype: of y and the states."""
+    code = _SEQ_DT.get(dtype)
+    if code is None:
+        raise TypeError(f"the convolution takes float32 or bfloat16 (got {dtype})")
+    if isinstance(x, Packed):
+        shape, dev, ptr, exps = _packed(x)
+        stride = (0, 0, 1)
+    else:
+        shape, dev, exps, stride = x.shape, x.get_device(), None, x.stride()
+        if not (x.dtype == dtype and dev >= 0 and (stride[-1] == 1 or shape[-1] == 1)):
+            _rows(x, "x", dtype, shape, dev)
+        ptr = x.data_ptr()
+    if len(shape) != (2 if step else 3):
+        raise ValueError("x must be " + ("[B, E]" if step else "[B, T, E]"))
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [E, W] (got {tuple(weight.shape)})")
+    E, W = shape[-1], weight.shape[1]
+    ptrs = (ptr, exps, _on(dev, weight, "weight", torch.float32, (E, W)), _on(dev, bias, "bias", torch.float32, (E,)))
+    desc = _pack(PnrConv, _CONV, shape[0], 1 if step else shape[1], E, W, code, act, stride[0], 0 if step else stride[1],
+                 _on(dev, lens, "lens", torch.int32, shape[:1]) or 0, _raw_stream(dev), 0, 0)
+    return desc, ptrs, shape, W, dev
+
+
+def causal_conv(x: Union[torch.Tensor, Packed], weight: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+                act: int = ACT_SILU, state: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                dtype: Optional[torch.dtype] = None, y: Optional[torch.Tensor] = None,
+                state_out: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_conv_forward: y_t = act(bias + sum_j weight[:, j] x_{t-W+1+j}), each channel by itself.
+    x [B,T,E] (float32 or bfloat16, strided as it comes, last axis contiguous) or a Packed copy of
+    it, weight float32 [E,W], bias float32 [E], state [B,W-1,E] in y's dtype (the inputs before the
+    first, zeros if None), lens int32 [B]; dtype is y's, which only a packed x needs.  Returns
+    dict(y=[B,T,E], state=the last W - 1 inputs of each row)."""
+    if dtype is None:
+        dtype = torch.bfloat16 if isinstance(x, Packed) else x.dtype
+    desc, ptrs, shape, W, dev = _conv(x, weight, bias, act, lens, dtype, False)
+    where, last = weight.device, (shape[0], W - 1, shape[2])
+    if y is None:
+        y = torch.empty(shape, dtype=dtype, device=where)
+    if state_out is None:
+        state_out = torch.empty(last, dtype=dtype, device=where)
+    _call(pnr_conv_forward, dev, desc, *ptrs, _on(dev, state, "state", dtype, last),
+          _on(dev, y, "y", dtype, shape), _on(dev, state_out, "state_out", dtype, last))
+    return {"y": y, "state": state_out}
+
+
+def causal_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+                     act: int = ACT_SILU, slots: Optional[torch.Tensor] = None,
+                     state_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_conv_step: one token for each of B requests.  x [B,E]; state [n_slots,W-1,E] in its dtype, the
+    pool of running requests' last inputs, with slots and state_out as in selective_scan_step.
+    Returns dict(y=[B,E], state=the updated pool)."""
+    if isinstance(x, Packed):
+        raise TypeError("a single token's x is a tensor")
+    desc, (px, _, pw, pb), shape, W, dev = _conv(x, weight, bias, act, None, x.dtype, True)
+    if state_out is None:
+        state_out = state
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    n_slots = state.shape[0] if state.dim() else 0
+    pool = (n_slots, W - 1, shape[1])
+    _call(pnr_conv_step, dev, desc, px, pw, pb, _on(dev, state, "state", x.dtype, pool),
+          _on(dev, slots, "slots", torch.int32, shape[:1]), n_slots, _on(dev, y, "y", x.dtype, shape),
+          _on(dev, state_out, "state_out", x.dtype, pool))
+    return {"y": y, "state": state_out}
+
+
+def causal_conv_backward(x: Union[torch.Tensor, Packed], weight: torch.Tensor, grad_y: torch.Tensor, *,
+                         bias: Optional[torch.Tensor] = None, act: int = ACT_SILU,
+                         state: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                         grad_state: Optional[torch.Tensor] = None, want=("x", "weight", "bias", "state"),
+                         workspace: Optional[torch.Tensor] = None) -> dict:
+    """Run pnr_conv_backward: gradients through causal_conv of these arguments, given grad_y = dL/dy [B,T,E]
+    (whose dtype the states have) and grad_state = dL/d(returned state) (zeros if None).  Returns
+    {name: gradient} for the names in `want` whose argument is given (x and state in grad_y's
+    dtype, weight and bias float32) and "workspace"."""
+    desc, ptrs, shape, W, dev = _conv(x, weight, bias, act, lens, grad_y.dtype, False)
+    dt, last = grad_y.dtype, (shape[0], W - 1, shape[2])
+    args = (_on(dev, state, "state", dt, last), _on(dev, grad_y, "grad_y", dt, shape),
+            _on(dev, grad_state, "grad_state", dt, last))
+    like = dict(x=(shape, dt), weight=(weight.shape, torch.float32),
+                bias=None if bias is None else (bias.shape, torch.float32), state=None if state is None else (last, dt))
+    unknown = set(want) - set(like)
+    if unknown:
+        raise ValueError(f"no gradient named {sorted(unknown)}")
+    out = {n: torch.empty(like[n][0], dtype=like[n][1], device=grad_y.device) for n in want if like[n]}
+    workspace = _workspace(pnr_conv_workspace_bytes_backward(desc), workspace, dev, desc)
+    _call(pnr_conv_backward, dev, desc, *ptrs, *args, *[_ptr(out.get(n)) for n in like])
     out["workspace"] = workspace
     return out

@@ -41,6 +41,8 @@ What it computes (sources are the five pages on this method):
 * ``linear_attention`` / ``linear_attention_grad`` -- the linear recurrence with a matrix state
   and a decay for each head, token by token, and its gradients from the adjoint's recurrence.
 * ``group_norm`` / ``group_norm_grad`` -- group norm with an activation, channels last.
+* ``selective_scan``, ``causal_conv``, their ``_grad`` forms and ``packed`` -- the state space layer's
+  recurrence, its short convolution and 8-bit copies of activations, from their definitions.
 * ``newton_chunked`` -- the sequence evaluated chunk by chunk, each chunk from the
   previous chunk's last state (ParaRNN overview, "Experimental Results": chunking to
   bound the memory of long sequences).
@@ -62,6 +64,7 @@ from .lowrank import lowrank_matrix, truncated
 from .backward import bptt, cell_vjp
 from .linattn import linear_attention, linear_attention_grad
 from .groupnorm import group_norm, group_norm_grad
+from .selscan import selective_scan, selective_scan_grad, causal_conv, causal_conv_grad, packed
 
 __all__ = [
     "CELL_GRU", "CELL_GRU_DIAG", "CELL_LSTM_DIAG", "JAC_FULL", "JAC_DIAG", "JAC_ZERO",
@@ -73,4 +76,5 @@ __all__ = [
     "lm_step_dense", "lm_step_kalman", "damped_step",
     "newton_chunked", "bptt", "cell_vjp", "lowrank_matrix", "truncated",
     "linear_attention", "linear_attention_grad", "group_norm", "group_norm_grad",
+    "selective_scan", "selective_scan_grad", "causal_conv", "causal_conv_grad", "packed",
 ]

@@ -1,0 +1,164 @@
+"""Refusals of the selective scan, the causal convolution and the 8-bit copies that need no GPU: bad requests
+are named before any HIP call (no compute call is made here)."""
+import ctypes
+import os
+
+import pytest
+
+from nonlinear_rnn_evaluation_amd import pnr
+
+pytestmark = pytest.mark.skipif(not os.path.exists(pnr.LIB_PATH), reason="libpnr.so not built")
+
+P = 4096
+
+
+def _scan(**kw):
+    d = dict(B=2, T=100, E=64, N=16, G=2, dtype=pnr.BF16, softplus=1)
+    s = {n: kw.pop(n, v) for n, v in dict(u_stride=(6400, 64), dt_stride=(6400, 64), z_stride=(6400, 64),
+                                          B_stride=(3200, 32, 16), C_stride=(3200, 32, 16)).items()}
+    d.update(kw)
+    return pnr.PnrSelscan(*d.values(), *[(ctypes.c_int64 * len(v))(*v) for v in s.values()])
+
+
+def _forward(d, u=P, dt=P, A=P, B=P, C=P, D=None, z=None, bias=None, state=None, y=P, out=None):
+    return pnr.pnr_selscan_forward(d, u, dt, A, B, C, D, z, bias, state, y, out)
+
+
+def _backward(d, z=None, gy=P, grads=(None,) * 9, **kw):
+    a = dict(u=P, dt=P, A=P, B=P, C=P)
+    a.update(kw)
+    return pnr.pnr_selscan_backward(d, *a.values(), None, z, None, None, gy, None, *grads)
+
+
+def _step(d, s_in=P, slots=None, n_slots=2, y=P, s_out=P):
+    return pnr.pnr_selscan_step(d, P, P, P, P, P, None, None, None, s_in, slots, n_slots, y, s_out)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(B=0), pnr.E_INVALID), (dict(E=0), pnr.E_INVALID), (dict(N=0), pnr.E_INVALID), (dict(G=0), pnr.E_INVALID),
+    (dict(G=3), pnr.E_INVALID), (dict(dtype=7), pnr.E_INVALID), (dict(dtype=pnr.F64), pnr.E_UNSUPPORTED),
+    (dict(softplus=2), pnr.E_INVALID), (dict(N=65), pnr.E_UNSUPPORTED), (dict(u_stride=(-1, 64)), pnr.E_INVALID),
+    (dict(B_stride=(0, 0, -16)), pnr.E_INVALID), (dict(E=(1 << 20) + 2), pnr.E_INVALID),
+    (dict(B=2 ** 31 - 1), pnr.E_INVALID), (dict(B=4, E=1 << 20, G=1 << 20), pnr.E_INVALID),
+])
+def test_invalid_scans(bad, code):
+    d = _scan(**bad)
+    assert pnr.pnr_selscan_workspace_bytes_backward(d) == 0 and pnr.pnr_last_error() != ""
+    assert pnr.pnr_selscan_workspace_bytes(d) == 0
+    assert _forward(d) == code and _backward(d) == code and _step(d) == code
+
+
+@pytest.mark.parametrize("bad", [dict(T=-1), dict(T=(1 << 30) + 1), dict(dt_stride=(0, -1)), dict(C_stride=(0, -1, 0))])
+def test_what_a_single_token_does_not_read(bad):
+    d = _scan(**bad)
+    assert _forward(d) == pnr.E_INVALID and _backward(d) == pnr.E_INVALID
+    assert _step(d, y=None) == pnr.E_INVALID and "y is NULL" in pnr.pnr_last_error()      # past the sizes
+
+
+def test_arguments_of_the_scan():
+    d = _scan()
+    for name in ("u", "dt", "A", "B", "C", "y"):
+        assert _forward(d, **{name: None}) == pnr.E_INVALID and "NULL" in pnr.pnr_last_error()
+        assert _forward(d, **{name: P + 1}) == pnr.E_INVALID and "aligned" in pnr.pnr_last_error()
+    for name in ("D", "z", "bias", "state", "out"):
+        assert _forward(d, **{name: P + 1}) == pnr.E_INVALID and "aligned" in pnr.pnr_last_error()
+    need = pnr.pnr_selscan_workspace_bytes_backward(d)
+    assert need > 0 and _backward(d) == pnr.E_WORKSPACE
+    d.workspace, d.workspace_bytes = P + 8, need
+    assert _backward(d) == pnr.E_WORKSPACE and "aligned" in pnr.pnr_last_error()
+    d.workspace, d.workspace_bytes = P, need - 1
+    assert _backward(d) == pnr.E_WORKSPACE and "required" in pnr.pnr_last_error()
+    assert _backward(d, gy=None) == pnr.E_INVALID
+    assert _backward(d, grads=(None,) * 6 + (P,) + (None,) * 2) == pnr.E_INVALID and "grad_z" in pnr.pnr_last_error()
+    for i in range(9):
+        g = [None] * 9
+        g[i] = P + 1
+        assert _backward(d, z=P, grads=g) == pnr.E_INVALID and "aligned" in pnr.pnr_last_error()
+    for kw in (dict(s_in=None), dict(s_out=None), dict(n_slots=1), dict(slots=P, n_slots=0), dict(slots=P + 2), dict(s_in=P + 2)):
+        assert _step(d, **kw) == pnr.E_INVALID, kw
+    lib = pnr.load()
+    assert lib.pnr_selscan_forward(None, *[P] * 11) == pnr.E_INVALID and lib.pnr_selscan_workspace_bytes(None) == 0
+    assert lib.pnr_selscan_backward(None, *[P] * 20) == pnr.E_INVALID and lib.pnr_selscan_workspace_bytes_backward(None) == 0
+
+
+def _conv(**kw):
+    d = dict(B=2, T=100, E=64, W=4, dtype=pnr.BF16, act=pnr.ACT_SILU)
+    s = kw.pop("x_stride", (6400, 64))
+    d.update(kw)
+    return pnr.PnrConv(*d.values(), (ctypes.c_int64 * 2)(*s))
+
+
+def _conv_calls(d):
+    return [pnr.pnr_conv_forward(d, P, None, P, None, None, P, None),
+            pnr.pnr_conv_backward(d, P, None, P, None, None, P, None, *[None] * 4),
+            pnr.pnr_conv_step(d, P, P, None, P, None, 2, P, P)]
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(B=0), pnr.E_INVALID), (dict(E=0), pnr.E_INVALID), (dict(W=0), pnr.E_INVALID), (dict(W=9), pnr.E_UNSUPPORTED),
+    (dict(dtype=5), pnr.E_INVALID), (dict(dtype=pnr.F64), pnr.E_UNSUPPORTED), (dict(act=3), pnr.E_INVALID), (dict(act=-1), pnr.E_INVALID),
+    (dict(act=pnr.ACT_GELU), pnr.E_UNSUPPORTED), (dict(x_stride=(-1, 64)), pnr.E_INVALID), (dict(E=(1 << 20) + 1), pnr.E_INVALID),
+    (dict(B=2 ** 31 - 1), pnr.E_INVALID),
+])
+def test_invalid_convolutions(bad, code):
+    d = _conv(**bad)
+    assert _conv_calls(d) == [code] * 3 and pnr.pnr_last_error() != ""
+    assert pnr.pnr_conv_workspace_bytes_backward(d) == 0
+
+
+def test_arguments_of_the_convolution():
+    d = _conv()
+    f = lambda x=P, e=None, w=P, b=None, s=None, y=P, o=None: pnr.pnr_conv_forward(d, x, e, w, b, s, y, o)  # noqa: E731
+    for kw in (dict(x=None), dict(w=None), dict(y=None), dict(x=P + 1), dict(w=P + 2), dict(b=P + 2), dict(s=P + 1), dict(y=P + 1),
+               dict(o=P + 1), dict(s=P, o=P)):
+        assert f(**kw) == pnr.E_INVALID, kw
+    assert _conv_calls(_conv(T=-1))[:2] == [pnr.E_INVALID] * 2
+    need = pnr.pnr_conv_workspace_bytes_backward(d)
+    b = lambda: pnr.pnr_conv_backward(d, P, None, P, None, None, P, None, *[None] * 4)  # noqa: E731
+    assert need > 0 and b() == pnr.E_WORKSPACE
+    d.workspace, d.workspace_bytes = P, need - 1
+    assert b() == pnr.E_WORKSPACE
+    for a in ((None, 2, P, P), (P, 0, P, P), (P, 1, None, P), (P, 1, P, None)):
+        s_in, n, y, s_out = (P, a[1], a[2], a[3]) if a[0] else (None, *a[1:])
+        assert pnr.pnr_conv_step(d, P, P, None, s_in, P, n, y, s_out) == pnr.E_INVALID, a
+    assert pnr.pnr_conv_step(d, P, P, None, P, None, 1, P, P) == pnr.E_INVALID      # without slots the pool holds every row
+    lib = pnr.load()
+    assert lib.pnr_conv_forward(None, *[P] * 7) == pnr.E_INVALID and lib.pnr_conv_workspace_bytes_backward(None) == 0
+    assert lib.pnr_conv_backward(None, *[P] * 11) == pnr.E_INVALID
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(B=0), pnr.E_INVALID), (dict(E=0), pnr.E_INVALID), (dict(T=-1), pnr.E_INVALID), (dict(dtype=4), pnr.E_INVALID),
+    (dict(dtype=pnr.F64), pnr.E_UNSUPPORTED), (dict(E=(1 << 20) + 1), pnr.E_INVALID), (dict(T=(1 << 30) + 1), pnr.E_INVALID),
+    (dict(B=2 ** 31 - 1, T=1 << 30, E=1 << 20), pnr.E_INVALID),
+])
+def test_invalid_checkpoints(bad, code):
+    kw = dict(B=2, T=100, E=64, dtype=pnr.BF16)
+    kw.update(bad)
+    d = pnr.PnrCheckpoint(*kw.values(), (ctypes.c_int64 * 2)(6400, 64))
+    assert pnr.pnr_checkpoint_pack(d, P, P, P) == code and pnr.pnr_checkpoint_unpack(d, P, P, P) == code
+    d = pnr.PnrCheckpoint(2, 100, 64, pnr.BF16, (ctypes.c_int64 * 2)(6400, -64))
+    assert pnr.pnr_checkpoint_pack(d, P, P, P) == pnr.E_INVALID
+    d.x_stride[1] = 64
+    for i in range(3):
+        for v in (None, P + 1):
+            a = [P] * 3
+            a[i] = v
+            if v is None or i == 0:
+                assert pnr.pnr_checkpoint_pack(d, *a) == pnr.E_INVALID
+            if v is None or i == 2:
+                assert pnr.pnr_checkpoint_unpack(d, *a) == pnr.E_INVALID
+    assert pnr.load().pnr_checkpoint_pack(None, P, P, P) == pnr.E_INVALID
+
+
+def test_descriptors_have_the_libraries_layout():
+    """Packed descriptors read back field by field."""
+    d = pnr._pack(pnr.PnrSelscan, pnr._SELSCAN, 1, 2, 3, 4, 5, 1, 1, *range(10, 22), 0, 77, 88, 99)
+    assert (d.B, d.T, d.E, d.N, d.G, d.dtype, d.softplus) == (1, 2, 3, 4, 5, 1, 1) and list(d.C_stride) == [19, 20, 21]
+    assert (list(d.u_stride), d.stream, d.workspace, d.workspace_bytes) == ([10, 11], 77, 88, 99)
+    d = pnr._pack(pnr.PnrConv, pnr._CONV, 1, 2, 3, 4, 1, 1, 10, 11, 0, 77, 88, 99)
+    assert (d.W, d.act, list(d.x_stride), d.stream, d.workspace_bytes) == (4, 1, [10, 11], 77, 99)
+    d = pnr._pack(pnr.PnrCheckpoint, pnr._CHECKPOINT, 1, 2, 3, 2, 10, 11, 77)
+    assert (d.E, d.dtype, list(d.x_stride), d.stream) == (3, 2, [10, 11], 77)
+    with pytest.raises(pnr.PnrError, match="32 bits"):
+        pnr._pack(pnr.PnrConv, pnr._CONV, 2 ** 31, 2, 3, 4, 1, 1, 10, 11, 0, 77, 88, 99)

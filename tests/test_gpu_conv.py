@@ -1,0 +1,289 @@
+"""The causal convolution on the GPU (pnr_conv_forward, _step, _backward) and 8-bit copies of activations
+(pnr_checkpoint_pack, _unpack), against the fp64 oracles on the same (rounded) inputs.
+
+Tolerances, as the 2-norm of an output's error over the 2-norm of the output:
+  fp32 outputs   2^-20: nine roundings of 2^-24 in a sum of eight taps, SiLU's few; sums over up to 1000
+                 tokens (gradients of weight and bias) add like sqrt(1000) = 2^5, and get 2^-18
+  bf16 outputs   2^-8 for their own rounding, and 2^-20
+Packing is exact but for its rounding, which is defined: codes, exponents and values are equal.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from nonlinear_rnn_evaluation_amd import pnr
+
+BF16, F32 = torch.bfloat16, torch.float32
+TOL = {BF16: 2.0 ** -8 + 2.0 ** -20, F32: 2.0 ** -20}
+SUMS = 2.0 ** -18
+NAMES = {pnr.ACT_NONE: "none", pnr.ACT_SILU: "silu"}
+
+
+def _case(seed, B, T, E, W, dtype, act=pnr.ACT_SILU, bias=True, state=True, lens=None, fused=False):
+    r = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=r)  # noqa: E731
+    x = n(B, T, 2 * E + 3).to(dtype).cuda()[..., 3:3 + E] if fused else n(B, T, E).to(dtype).cuda()
+    kw = dict(bias=n(E).cuda() if bias else None, act=act, state=n(B, W - 1, E).to(dtype).cuda() if state else None,
+              lens=None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda())
+    gy, gs = n(B, T, E).to(dtype).cuda(), n(B, W - 1, E).to(dtype).cuda() if state else None
+    for b, m in enumerate(lens or []):
+        x[b, max(0, min(m, T)):], gy[b, max(0, min(m, T)):] = float("nan"), float("inf")
+    return x, n(E, W).cuda(), gy, gs, kw
+
+
+def _f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def _clean(t):
+    return np.nan_to_num(_f64(t), nan=0, posinf=0, neginf=0)
+
+
+def _ref(kw):
+    return dict(bias=_f64(kw["bias"]), act=NAMES[kw["act"]], state=_f64(kw["state"]),
+                lens=None if kw["lens"] is None else kw["lens"].cpu().numpy())
+
+
+def _near(name, got, ref, tol):
+    got = _f64(got)
+    assert got.shape == ref.shape, name
+    assert np.isfinite(got).all(), f"{name}: not finite"
+    norm, err = np.linalg.norm(ref), np.linalg.norm(got - ref)
+    print(f"#   {name}: {err / max(norm, 1e-300):.2e} (tol {tol:.1e})", flush=True)
+    assert err <= tol * norm + 1e-30, (name, err, norm)
+
+
+def _check(x, w, gy, gs, kw):
+    dt, ref = gy.dtype, _ref(kw)
+    kept = pnr.checkpoint_pack(x)
+    for operand, values in ((x, _clean(x)), (kept, _clean(pnr.checkpoint_unpack(kept, dt)))):
+        got = pnr.causal_conv(operand, w, dtype=dt, **kw)
+        y, S = O.causal_conv(values, _f64(w), **ref)
+        _near("y", got["y"], y, TOL[dt])
+        assert np.array_equal(_f64(got["state"]), S)
+        d = pnr.causal_conv_backward(operand, w, gy, grad_state=gs, **kw)
+        want = O.causal_conv_grad(values, _f64(w), _clean(gy), gstate=_f64(gs), **ref)
+        for n in ("x", "weight", "bias", "state"):
+            if n in kw and kw[n] is None:
+                assert n not in d
+            else:
+                _near("grad_" + n, d[n], want[n], SUMS if n in ("weight", "bias") else TOL[dt])
+
+
+SHAPES = [
+    # B, T, E, W
+    (1, 1, 1, 1), (2, 1, 64, 4), (1, 2, 8, 4), (1, 3, 40, 5), (2, 5, 33, 8), (3, 31, 32, 2), (1, 32, 128, 3), (2, 33, 264, 4),
+    (1, 64, 2056, 4), (4, 65, 100, 6), (1, 200, 96, 7), (2, 1000, 24, 4), (1, 130, 4100, 4),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_forward_and_gradients(shape, dtype):
+    i = SHAPES.index(shape)
+    _check(*_case(i, *shape, dtype, act=i % 2, bias=i % 3 != 2, state=i % 4 != 3, fused=i % 5 == 1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[70, 0, 1, 69], [0, 0, 0, 0], [2, 3, 4, 33], [-3, 999, 31, 32]], ids=str)
+def test_rows_that_end_early(lens, dtype):
+    x, w, gy, gs, kw = _case(20, 4, 70, 72, 4, dtype, lens=lens)
+    ref = _ref(kw)
+    got, d = pnr.causal_conv(x, w, **kw), pnr.causal_conv_backward(x, w, gy, grad_state=gs, **kw)
+    y, S = O.causal_conv(_clean(x), _f64(w), **ref)
+    _near("y", got["y"], y, TOL[dtype])
+    assert np.array_equal(_f64(got["state"]), S)
+    want = O.causal_conv_grad(_clean(x), _f64(w), _clean(gy), gstate=_f64(gs), **ref)
+    for n in ("x", "weight", "bias", "state"):
+        _near("grad_" + n, d[n], want[n], SUMS if n in ("weight", "bias") else TOL[dtype])
+    for b, m in enumerate(lens):
+        m = max(0, min(m, 70))
+        assert not got["y"][b, m:].any() and not d["x"][b, m:].any()
+
+
+@pytest.mark.gpu
+def test_no_tokens():
+    x, w, gy, gs, kw = _case(21, 2, 0, 16, 4, F32)
+    assert torch.equal(pnr.causal_conv(x, w, **kw)["state"], kw["state"])
+    d = pnr.causal_conv_backward(x, w, gy, grad_state=gs, **kw)
+    assert torch.equal(d["state"], gs) and not d["weight"].any() and not d["bias"].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 2048, 4), (5, 100, 3), (3, 64, 8), (2, 33, 1), (4, 40, 2)], ids=str)
+def test_tokens_continue_a_sequence(shape, dtype):
+    B, E, W = shape
+    x, w, _, _, kw = _case(22, B, 10, E, W, dtype)
+    y, S = O.causal_conv(_f64(x), _f64(w), **_ref(kw))
+    pool = torch.randn(B + 2, W - 1, E, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
+    keep = pool.clone()
+    slots = torch.randperm(B + 2, generator=torch.Generator().manual_seed(3))[:B].to(torch.int32).cuda()
+    pool[slots.long()] = kw["state"]
+    for t in range(10):
+        r = pnr.causal_conv_step(x[:, t], w, pool, bias=kw["bias"], act=kw["act"], slots=slots)
+        _near(f"y[{t}]", r["y"], y[:, t], TOL[dtype])
+    assert np.array_equal(_f64(pool[slots.long()]), S)
+    others = [i for i in range(B + 2) if i not in slots.tolist()]
+    assert torch.equal(pool[others], keep[others])
+
+
+@pytest.mark.gpu
+def test_idle_rows_and_another_pool():
+    x, w, _, _, kw = _case(23, 4, 1, 64, 4, F32)
+    pool, out = torch.randn(6, 3, 64).cuda(), torch.full((6, 3, 64), 7.0).cuda()
+    keep = pool.clone()
+    slots = torch.tensor([5, -1, 2, 6], dtype=torch.int32).cuda()
+    r = pnr.causal_conv_step(x[:, 0], w, pool, bias=kw["bias"], slots=slots, state_out=out)
+    assert torch.equal(pool, keep) and not r["y"][[1, 3]].any() and r["y"][[0, 2]].any()
+    assert (out[[0, 1, 3, 4]] == 7.0).all()
+    assert torch.equal(out[[5, 2], :2], pool[[5, 2], 1:]) and torch.equal(out[[5, 2], 2], x[[0, 2], 0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_what_is_not_finite_stays_in_its_channel_and_time(dtype):
+    x, w, gy, gs, kw = _case(24, 2, 100, 40, 4, dtype)
+    ref, dref = pnr.causal_conv(x, w, **kw), pnr.causal_conv_backward(x, w, gy, grad_state=gs, **kw)
+    x[1, 50, 7] = float("nan")
+    got, d = pnr.causal_conv(x, w, **kw), pnr.causal_conv_backward(x, w, gy, grad_state=gs, **kw)
+    assert torch.isnan(got["y"][1, 50:54, 7]).all()
+    got["y"][1, 50:54, 7] = ref["y"][1, 50:54, 7]
+    assert torch.equal(got["y"], ref["y"]) and torch.isnan(d["weight"][7]).all()
+    assert torch.isnan(d["x"][1, 47:54, 7]).all()
+    d["x"][1, 47:54, 7] = dref["x"][1, 47:54, 7]
+    assert torch.equal(d["x"], dref["x"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("want", [("x",), ("weight",), ("bias", "state")], ids=str)
+def test_gradients_one_by_one(want):
+    x, w, gy, gs, kw = _case(25, 2, 77, 72, 4, BF16)
+    every, some = (pnr.causal_conv_backward(x, w, gy, grad_state=gs, want=n, **kw) for n in (("x", "weight", "bias", "state"), want))
+    assert set(some) == {*want, "workspace"}
+    for n in want:
+        assert torch.equal(every[n], some[n]), n
+
+
+@pytest.mark.gpu
+def test_streams_graphs_and_repeats():
+    x, w, gy, gs, kw = _case(26, 3, 500, 264, 4, BF16)
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        pnr.causal_conv_backward(pnr.checkpoint_pack(x), w, gy, grad_state=gs, **kw)
+    s.synchronize()
+    with torch.cuda.graph(g):
+        f, kept = pnr.causal_conv(x, w, **kw), pnr.checkpoint_pack(x)
+        b = pnr.causal_conv_backward(kept, w, gy, grad_state=gs, **kw)
+    for _ in range(4):
+        x.mul_(-1.25)
+        g.replay()
+        torch.cuda.synchronize()
+        ef, ek = pnr.causal_conv(x, w, **kw), pnr.checkpoint_pack(x)
+        eb = pnr.causal_conv_backward(ek, w, gy, grad_state=gs, **kw)
+        assert torch.equal(ef["y"], f["y"]) and torch.equal(ek.codes, kept.codes) and torch.equal(ek.exponents, kept.exponents)
+        for n in ("x", "weight", "bias", "state"):
+            assert torch.equal(eb[n], b[n]), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1), (3, 8), (5, 31), (2, 32), (7, 33), (4, 64), (9, 100), (3, 264), (2, 3, 40), (2, 0, 32), (1, 5, 2056)], ids=str)
+def test_packing_is_its_definition(shape, dtype):
+    r = torch.Generator().manual_seed(30 + len(shape))
+    E = shape[-1]
+    wide = torch.randn(*shape[:-1], E + 7, generator=r) * torch.exp(4 * torch.randn(*shape[:-1], 1, generator=r))
+    wide = wide.to(dtype)
+    for view in (lambda w: w[..., :E], lambda w: w[..., 7:], lambda w: w[..., :E].contiguous()):
+        x, dev = view(wide), view(wide.cuda())
+        p = pnr.checkpoint_pack(dev)
+        codes, exps, values = O.packed(_f64(x))
+        assert np.array_equal(p.codes.cpu().numpy(), codes) and np.array_equal(p.exponents.cpu().numpy(), exps)
+        for out in (BF16, F32):
+            assert np.array_equal(_f64(pnr.checkpoint_unpack(p, out)), values)
+
+
+@pytest.mark.gpu
+def test_packing_at_the_ends_of_the_range():
+    """Ties, the largest code, the smallest steps, values that are not finite, both signs of zero."""
+    x = torch.zeros(12, 64)
+    x[0, :4] = torch.tensor([127.0, 0.5, 1.5, -2.5])
+    x[1, :3] = torch.tensor([127.00001, 1.0, -127.00001])
+    x[2, :3] = torch.tensor([2.0 ** -149, -2.0 ** -130, 2.0 ** -126])
+    x[3, :3] = torch.tensor([2.0 ** -120, 2.0 ** -126, 1.5 * 2.0 ** -126])
+    x[4, :3] = torch.tensor([3.4028235e38, -3.4028235e38, 2.0 ** 121])
+    x[5, 3], x[6, 40], x[7, 0] = float("inf"), float("nan"), float("-inf")
+    x[8, 0] = -0.0
+    x[9, :2] = torch.tensor([127 * 2.0 ** -126, 0.5 * 2.0 ** -126])
+    x[10, 33:35] = torch.tensor([126.5, -126.49999])
+    x[11] = torch.linspace(-1, 1, 64)
+    for dtype in (F32, BF16):
+        for dev in (x.to(dtype).cuda(), x.to(dtype).repeat(1, 2).cuda()[:, :64], torch.cat([x.new_zeros(12, 1), x], 1).to(dtype).cuda()[:, 1:]):
+            p = pnr.checkpoint_pack(dev)
+            codes, exps, values = O.packed(_f64(x.to(dtype)))
+            assert np.array_equal(p.codes.cpu().numpy(), codes) and np.array_equal(p.exponents.cpu().numpy(), exps)
+            for out in (F32, BF16):
+                assert np.array_equal(_f64(pnr.checkpoint_unpack(p, out)), values, equal_nan=True)
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """2^31 elements and more, every token the same: packed, read back and convolved."""
+    E, T = 8192, (1 << 18) + 5
+    row = torch.randn(1, 1, E, generator=torch.Generator().manual_seed(31)).to(BF16).cuda()
+    x = row.expand(1, T, E)
+    p = pnr.checkpoint_pack(x)
+    want = pnr.checkpoint_unpack(pnr.checkpoint_pack(row[0]), BF16)[0]
+    got = pnr.checkpoint_unpack(p, BF16)
+    assert got.numel() > 1 << 31 and all(torch.equal(got[0, t], want) for t in (0, T // 2, T - 1))
+    del got
+    w = torch.randn(E, 2, generator=torch.Generator().manual_seed(32)).cuda()
+    a, b = pnr.causal_conv(x, w)["y"], pnr.causal_conv(want.view(1, 1, E).expand(1, 3, E), w)["y"]
+    c = pnr.causal_conv(row.expand(1, 3, E), w)["y"]
+    assert all(torch.equal(a[0, t], c[0, 2]) for t in (1, T // 2, T - 1))
+    a = pnr.causal_conv(p, w)["y"]
+    assert all(torch.equal(a[0, t], b[0, 2]) for t in (1, T // 2, T - 1))
+    gx = pnr.causal_conv_backward(p, w, a, want=("x",))["x"]
+    assert torch.equal(gx[0, 5], gx[0, T - 9]) and gx[0, T - 1].any()
+
+
+@pytest.mark.gpu
+def test_refusals():
+    x, w, gy, _, kw = _case(33, 2, 10, 32, 4, F32)
+    kw.pop("lens")
+    with pytest.raises(TypeError):
+        pnr.causal_conv(x.half(), w, **kw)
+    with pytest.raises(TypeError):
+        pnr.causal_conv(x, w.to(BF16), **kw)
+    with pytest.raises(TypeError):
+        pnr.causal_conv(x, w, **{**kw, "state": kw["state"].to(BF16)})
+    with pytest.raises(ValueError):
+        pnr.causal_conv(x, w[:31], **kw)
+    with pytest.raises(ValueError):
+        pnr.causal_conv(x[0], w, **kw)
+    with pytest.raises(ValueError):
+        pnr.causal_conv(x.cpu(), w, **kw)
+    with pytest.raises(pnr.PnrError, match="SiLU"):
+        pnr.causal_conv(x, w, **{**kw, "act": pnr.ACT_GELU})
+    with pytest.raises(pnr.PnrError, match="taps"):
+        pnr.causal_conv(x, torch.zeros(32, 9).cuda())
+    with pytest.raises(pnr.PnrError, match="state_out"):
+        pnr.causal_conv(x, w, state_out=kw["state"], **kw)
+    p = pnr.checkpoint_pack(x)
+    with pytest.raises(ValueError):
+        pnr.causal_conv(pnr.Packed(p.codes, p.exponents[:, :9]), w, dtype=F32, **kw)
+    with pytest.raises(TypeError):
+        pnr.causal_conv(pnr.Packed(p.codes.to(torch.uint8), p.exponents), w, dtype=F32, **kw)
+    with pytest.raises(TypeError):
+        pnr.checkpoint_pack(x.half())
+    with pytest.raises(TypeError):
+        pnr.checkpoint_unpack(p, torch.float16)
+    with pytest.raises(ValueError):
+        pnr.checkpoint_pack(x.transpose(1, 2))
+    with pytest.raises(TypeError):
+        pnr.causal_conv_step(pnr.Packed(p.codes[:, 0], p.exponents[:, 0]), w, kw["state"])
