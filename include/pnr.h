@@ -574,8 +574,9 @@ int pnr_groupnorm_backward(const pnr_norm* desc, const void* x, const float* wei
  *               row's end is not read, its outputs and gradients are zeros, and the state is the one
  *               after the row's last token (an empty row hands state_in on)
  * Supported: dtype PNR_F32 and PNR_BF16, 1 <= N <= 64 (others PNR_E_UNSUPPORTED), G divides E,
- * E <= 2^20, T <= 2^30, B G ceil(E / G / 64) <= 4 million.  Everything inside is fp32; outputs of
- * `dtype` are rounded once, at the end.
+ * E <= 2^20, T <= 2^30, B G ceil(E / G / 64) <= 4 million; token strides of u, dt and z up to 2^23
+ * (others PNR_E_UNSUPPORTED).  Everything inside is fp32; outputs of `dtype` are rounded once, at the
+ * end.
  *
  * A NaN or an infinity in a token reaches what the formulas compute from it, within its row: u, dt,
  * z and grad_y their channel, B and C the channels of their group; forwards in time for y and the

@@ -25,38 +25,68 @@ struct FwdArgs {
   float *sums, *width;       // [B, S, E, 4 R] states and [B, S, E] summed step widths of the segments
 };
 
-// One segment of one block's channels.  kSum: from zeros, only the state at its end and the sum of
-// its step widths; otherwise from the segment's first state to outputs.
+template <int kCtrl>
+__device__ __forceinline__ float quad_perm(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xf, 0xf, true));
+}
+
+// B and C of four tokens, this lane's states.
+template <bool kOut, int R>
+struct Four {
+  float B[4][R], C[4][kOut ? R : 1];
+  __device__ __forceinline__ void read(const float* s) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      read_states<R>(s + k * 8 * R, B[k]);
+      if constexpr (kOut) read_states<R>(s + k * 8 * R + 4 * R, C[k]);
+    }
+  }
+};
+
+// Token k of a quad's four: the states of this lane, and (kOut) the channel's output in lane k.
+template <int k, bool kOut, int R>
+__device__ __forceinline__ void token(float delta, float x, float (&h)[R], const float (&A)[R], const Four<kOut, R>& f, float& o, int nq) {
+  const float d = quad_perm<0x55 * k>(delta), xk = quad_perm<0x55 * k>(x);
+  float acc = 0.0f;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    h[i] = fmaf(h[i], __builtin_amdgcn_exp2f(d * A[i]), xk * f.B[k][i]);
+    if constexpr (kOut) acc = fmaf(h[i], f.C[k][i], acc);
+  }
+  if constexpr (kOut) {
+    acc += quad_perm<0xb1>(acc);
+    acc += quad_perm<0x4e>(acc);
+    o = nq == k ? acc : o;
+  }
+}
+
+// One segment of one block's channels.  kSum: from zeros, only the state at its end and the sum of its
+// step widths; otherwise from the segment's first state to outputs.  A quad holds a channel, R
+// states a lane.  Four tokens go at once: each lane of a quad prepares one of them (its step width,
+// softplus, gate) and hands it to the others.
 template <bool kBf16, int R, int kW, bool kSum>
-__global__ void __launch_bounds__(kW * 64) scan_kernel(FwdArgs p) {
+__global__ void __launch_bounds__(kW * 64, 1) scan_kernel(FwdArgs p) {
   using El = Elem<kBf16>;
   using T = typename El::type;
-  constexpr int NP = 4 * R, kTok = kStage<R>, kAhead = 8;
+  constexpr int NP = 4 * R, kTok = kStage<R>;
   __shared__ alignas(16) float bc[2][kTok * 2 * NP];
   const SelScan& a = p.a;
   const int seg = (int)(blockIdx.x / p.tiles);
-  const Tile w = tile_of<kW>(a, blockIdx.x % p.tiles, p.per_group);
+  const Tile w = tile_of<kW, kNarrow>(a, blockIdx.x % p.tiles, p.per_group);
   const int n = row_len(a.lens, w.b, a.T), t0 = seg * p.seg.len, tend = min(t0 + p.seg.len, a.T), t1 = min(tend, n);
-  const bool last = seg == p.seg.S - 1;
-  if (kSum && t0 >= t1) return;                      // the join skips it
-  const int lane = threadIdx.x & 63, nq = lane >> 2 & 3, e = w.e0 + min(lane, w.live - 1);
-  const bool busy = w.live > 0, live = lane < w.live;
-  float A[4][R], h[4][R];
-  int ch[4] = {e, away<1>(e), away<2>(e), away<3>(e)};
-  const bool whole = p.seg.S == 1;
+  if (kSum && t0 >= t1) return;
+  const int lane = threadIdx.x & 63, nq = lane & 3, c = lane >> 2, e = w.e0 + min(c, w.live - 1);
+  const bool busy = w.live > 0, live = c < w.live, whole = p.seg.S == 1;
+  const size_t mid = (((size_t)w.b * p.seg.S + seg) * a.E + e) * NP + nq * R, at = ((size_t)w.b * a.E + e) * a.N + nq * R;
+  float A[R], h[R];
   if (busy) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int s = nq * R + i;
-        A[r][i] = s < a.N ? exponent(a.A[(size_t)ch[r] * a.N + s]) : 0.0f;
-        h[r][i] = 0.0f;
-        if (!kSum && whole && s < a.N && p.s_in) h[r][i] = p.s_in[((size_t)w.b * a.E + ch[r]) * a.N + s];
-      }
-    if (!kSum && !whole)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) read_states<R>(p.sums + (((size_t)w.b * p.seg.S + seg) * a.E + ch[r]) * NP + nq * R, h[r]);
+    for (int i = 0; i < R; ++i) {
+      const bool real = nq * R + i < a.N;
+      A[i] = real ? exponent(a.A[(size_t)e * a.N + nq * R + i]) : 0.0f;
+      h[i] = !kSum && whole && real && p.s_in ? p.s_in[at + i] : 0.0f;
+    }
+    if (!kSum && !whole) read_states<R>(p.sums + mid, h);
   }
   const float bias = busy && a.bias ? a.bias[e] : 0.0f, D = !kSum && busy && a.D ? a.D[e] : 0.0f;
   const T* u = (const T*)a.u.p + w.b * a.u.sb;
@@ -66,88 +96,108 @@ __global__ void __launch_bounds__(kW * 64) scan_kernel(FwdArgs p) {
   T* y = (T*)p.y + (size_t)w.b * a.T * a.E;
   float total = 0.0f;
   if (t0 < t1) {
-    T ur[kAhead], dr[kAhead], zr[kAhead];
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int64_t at = min(t + k, t1 - 1);
-        ur[k] = (u + at * a.u.st)[e];
-        dr[k] = (dt + at * a.dt.st)[e];
-        if (gated) zr[k] = (z + at * a.z.st)[e];
-      }
+    constexpr int kDepth = 4;                 // fours of tokens on their way from memory
+    T ur[kDepth], dr[kDepth], zr[kDepth];
+    // Operands as buffers from the tile's first token on, tokens as 32-bit offsets: a wave that runs alone
+    // pays for every scalar instruction too (the plan keeps wide strides away).
+    const int su = (int)a.u.st * (int)sizeof(T), sd = (int)a.dt.st * (int)sizeof(T), sz = (int)a.z.st * (int)sizeof(T),
+              sy = a.E * (int)sizeof(T);
+    const int ou = nq * su + e * (int)sizeof(T), od = nq * sd + e * (int)sizeof(T), oz = nq * sz + e * (int)sizeof(T),
+              oy = nq * sy + e * (int)sizeof(T);
+    __amdgpu_buffer_rsrc_t bu, bd, bz, by;
+    int left = 0;                             // of the tile's tokens, this lane's from `left` on are not there
+    auto rebase = [&](int tile) {
+      bu = buffer_of(u + tile * a.u.st, true), bd = buffer_of(dt + tile * a.dt.st, true);
+      bz = buffer_of(z + (kSum ? 0 : tile * a.z.st), gated), by = buffer_of(y + (int64_t)tile * a.E, true);
+      left = t1 - tile - nq;
+    };
+    auto fetch = [&](int k, int i) {          // tokens k.. of the tile; zeros beyond the last token
+      const bool there = k < left;
+      ur[i] = load_buffer<T>(bu, there ? ou : kNowhere, k * su);
+      dr[i] = load_buffer<T>(bd, there ? od : kNowhere, k * sd);
+      if (!kSum) zr[i] = load_buffer<T>(bz, there ? oz : kNowhere, k * sz);
     };
     Stage<kBf16, R, kW, kTok> stage;
     stage.start(a, w);
     stage.fetch(t0, t1);
-    if (busy) fetch(t0);
+    // One wave a SIMD has nobody to fill its waits, so the steps of neighbouring fours overlap: while one
+    // runs through the states, the next one's widths are made and the last one's outputs gated.
+    float uv[2] = {}, zv[2] = {}, delta[2], x[2], done = 0.0f;
+    auto widths = [&](int k, int i, int j) {
+      uv[j] = El::load(&ur[i]), zv[j] = kSum ? 0.0f : El::load(&zr[i]);
+      delta[j] = step_width(El::load(&dr[i]) + bias, a.softplus, k < left);
+      x[j] = delta[j] * uv[j];
+    };
+    auto finish = [&](int k, int j, bool first) {           // the outputs of tokens k..k + 3
+      const float o = fmaf(D, uv[j], done);
+      store_buffer<kBf16>(o * gate_of(zv[j], gated), by, live && k < left && !first ? oy : kNowhere, first ? 0 : k * sy);
+    };
+    if (busy) {
+      rebase(t0);
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) fetch(4 * i, i);
+      widths(0, 0, 0);
+      fetch(4 * kDepth, 0);
+    }
     int buf = 0;
     for (int tile = t0; tile < t1; tile += kTok, buf ^= 1) {
       stage.put(bc[buf]);
-      __syncthreads();           // the other buffer's readers are past it: they met here after reading
+      __syncthreads();
       if (tile + kTok < t1) stage.fetch(tile + kTok, t1);
       if (!busy) continue;
-      const int stop = min(tile + kTok, t1);
-      for (int t = tile; t < stop; t += kAhead) {
-        float uv[kAhead], dv[kAhead], zv[kAhead];
+      if (tile > t0) {
+        if (!kSum) finish(kTok - 4, 1, false);              // of the tile before
+        rebase(tile);
+      }
+      Four<!kSum, R> f[2];
+      const float* s = bc[buf] + nq * R;
+      f[0].read(s);
+      const int here = min(kTok, t1 - tile);
+      for (int k0 = 0; k0 < here; k0 += 4 * kDepth) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) uv[k] = El::load(&ur[k]), dv[k] = El::load(&dr[k]), zv[k] = gated ? El::load(&zr[k]) : 0.0f;
-        if (t + kAhead < t1) fetch(t + kAhead);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (t + k >= stop) break;
-          const float raw = dv[k] + bias, delta = a.softplus ? softplus(raw) : raw;
-          float d[4], x[4], acc[4], Bv[R], Cv[R];
-          to_slots(delta, d);
-          to_slots(delta * uv[k], x);
-          const float* s = bc[buf] + (t + k - tile) * 2 * NP + nq * R;
-          read_states<R>(s, Bv);
-          if (!kSum) read_states<R>(s + NP, Cv);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            acc[r] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-              h[r][i] = fmaf(h[r][i], __builtin_amdgcn_exp2f(d[r] * A[r][i]), x[r] * Bv[i]);
-              if (!kSum) acc[r] = fmaf(h[r][i], Cv[i], acc[r]);
-            }
-          }
-          if (kSum) {
-            total += delta;
-          } else {
-            float o = fmaf(D, uv[k], from_slots(acc));
-            if (gated) o *= zv[k] * sigm(zv[k]);
-            if (live) El::store(y + (size_t)(t + k) * a.E + e, o);
-          }
+        for (int i = 0; i < kDepth; ++i) {
+          const int k = k0 + 4 * i;
+          if (k >= here) break;
+          f[(i + 1) % 2].read(s + (k + 4 < kTok ? (k + 4) * 2 * NP : 0));
+          float o = 0.0f;
+          token<0, !kSum, R>(delta[i % 2], x[i % 2], h, A, f[i % 2], o, nq);
+          if (!kSum) finish(k - 4, (i + 1) % 2, k == 0);
+          token<1, !kSum, R>(delta[i % 2], x[i % 2], h, A, f[i % 2], o, nq);
+          widths(k + 4, (i + 1) % kDepth, (i + 1) % 2);
+          fetch(k + 4 + 4 * kDepth, (i + 1) % kDepth);
+          token<2, !kSum, R>(delta[i % 2], x[i % 2], h, A, f[i % 2], o, nq);
+          token<3, !kSum, R>(delta[i % 2], x[i % 2], h, A, f[i % 2], o, nq);
+          if (kSum) total += delta[i % 2];
+          done = o;
         }
       }
+    }
+    if (!kSum && busy) {
+      const int k = ((t1 - 1 - t0) % kTok) / 4 * 4;
+      k / 4 % 2 ? finish(k, 1, false) : finish(k, 0, false);
     }
   }
   if (!busy) return;
   if (kSum) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      // a lane beyond the last channel repeats that channel's work and writes the same
-      float* out = p.sums + (((size_t)w.b * p.seg.S + seg) * a.E + ch[r]) * NP + nq * R;
-#pragma unroll
-      for (int i = 0; i < R; ++i) out[i] = h[r][i];
-    }
-    if (live) p.width[((size_t)w.b * p.seg.S + seg) * a.E + e] = total;
+    for (int i = 0; i < R; ++i) p.sums[mid + i] = h[i];
+    total += quad_perm<0xb1>(total);
+    total += quad_perm<0x4e>(total);
+    if (live && nq == 0) p.width[((size_t)w.b * p.seg.S + seg) * a.E + e] = total;
     return;
   }
   if (live)
-    for (int t = max(t0, t1); t < tend; ++t) El::store(y + (size_t)t * a.E + e, 0.0f);
-  // cut time: the join wrote the last state
-  if (whole && p.s_out)
+    for (int t = max(t0, t1) + nq; t < tend; t += 4) El::store(y + (size_t)t * a.E + e, 0.0f);
+  if (whole && p.s_out && live)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (nq * R + i < a.N) p.s_out[((size_t)w.b * a.E + ch[r]) * a.N + nq * R + i] = h[r][i];
+    for (int i = 0; i < R; ++i)
+      if (nq * R + i < a.N) p.s_out[at + i] = h[i];
 }
 
 // The recurrence over a row's segments: each segment's first state in place of its sum, and the last
-// state.  A thread a state.
+// state.  A thread a state; eight segments' sums are asked for before the first is used.
 __global__ void __launch_bounds__(256) join_kernel(FwdArgs p, int NP) {
+  constexpr int kBatch = 8;
   const SelScan& a = p.a;
   const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
   if (i >= (int64_t)a.B * a.E * NP) return;
@@ -158,11 +208,19 @@ __global__ void __launch_bounds__(256) join_kernel(FwdArgs p, int NP) {
   const size_t at = ((size_t)b * a.E + e) * a.N + s;
   float h = real && p.s_in ? p.s_in[at] : 0.0f;
   const size_t row = (size_t)b * p.seg.S * a.E + e;
-  for (int k = 0; k < segs; ++k) {
-    float* sum = p.sums + (row + (size_t)k * a.E) * NP + s;
-    const float own = *sum, d = p.width[row + (size_t)k * a.E];
-    *sum = h;
-    h = fmaf(h, __builtin_amdgcn_exp2f(d * A), own);
+  for (int k0 = 0; k0 < segs; k0 += kBatch) {
+    float own[kBatch], d[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const size_t r = row + (size_t)min(k0 + k, segs - 1) * a.E;
+      own[k] = p.sums[r * NP + s], d[k] = p.width[r];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k0 + k < segs) {
+        p.sums[(row + (size_t)(k0 + k) * a.E) * NP + s] = h;
+        h = fmaf(h, __builtin_amdgcn_exp2f(d[k] * A), own[k]);
+      }
   }
   if (p.s_out && real) p.s_out[at] = h;
 }
@@ -173,22 +231,31 @@ int states_of(const SelScan& a) {
   return R;
 }
 
-int waves_of(const SelScan& a) { return a.E / a.G <= kChannels ? 1 : 4; }
+// How a call is cut: waves of a block, blocks of a group, segments.
+struct Plan {
+  int waves, per_group;
+  Segments seg;
+};
 
-int blocks_per_group(const SelScan& a) {
-  const int ch = waves_of(a) * kChannels;
-  return (a.E / a.G + ch - 1) / ch;
-}
-
-// One segment where the channels fill the device; otherwise enough of them to.
-Segments segments_of(const SelScan& a) {
-  const int64_t waves = (int64_t)a.B * a.G * ((a.E / a.G + kChannels - 1) / kChannels);
-  const int most = (a.T + 63) / 64;                  // segments of 64 tokens at least
-  int S = 1;
-  if (waves < 768) S = (int)std::min<int64_t>(most, (4096 + waves - 1) / waves);
-  S = std::max(S, 1);
-  const int len = std::max(32, ((a.T + S - 1) / S + 31) / 32 * 32);
-  return {std::max(1, (a.T + len - 1) / len), len};
+Plan plan_of(const SelScan& a) {
+  Plan p{};
+  const int W = a.E / a.G;
+  p.waves = W <= kNarrow ? 1 : 4;
+  p.per_group = (W + p.waves * kNarrow - 1) / (p.waves * kNarrow);
+  const int64_t waves = (int64_t)a.B * a.G * ((W + kNarrow - 1) / kNarrow);
+  // One wave a SIMD goes through the tokens in one pass at 115 ns each; two passes over segments cost
+  // twice the instructions, but eight waves a SIMD fill each other's gaps.  bf16, 16 states, us in one
+  // pass and in the best number of segments: 1024 waves 520 and 485 (4 x 4096 tokens), 237 and 259
+  // (8 x 2000); 256 waves 473 and 150 (2 x 4096); 128 waves 4268 and 510 (32768).  A second pass and
+  // the join cost 8 us: 128 waves over 37 tokens 10.1 and 17.2.
+  // With row lengths some rows are expected to be short: what is cut behind their ends costs nothing, while in
+  // one pass the longest row sets the time.
+  const int64_t enough = a.lens ? 4096 : 1024, target = a.lens ? 16384 : 8192;
+  int64_t S = 1;
+  if (waves < enough && a.T > 128) S = std::min<int64_t>((a.T + 31) / 32, (target + waves - 1) / waves);
+  const int len = std::max(32, (int)((a.T + S - 1) / S + 31) / 32 * 32);
+  p.seg = {std::max(1, (a.T + len - 1) / len), len};
+  return p;
 }
 
 struct Layout {
@@ -214,32 +281,33 @@ void launch_pass(const FwdArgs& p, hipStream_t st) {
 }
 
 template <bool kBf16, int R>
-void launch_waves(const FwdArgs& p, hipStream_t st) {
-  waves_of(p.a) == 1 ? launch_pass<kBf16, R, 1>(p, st) : launch_pass<kBf16, R, 4>(p, st);
+void launch_shape(const FwdArgs& p, const Plan& plan, hipStream_t st) {
+  plan.waves == 1 ? launch_pass<kBf16, R, 1>(p, st) : launch_pass<kBf16, R, 4>(p, st);
 }
 
 template <bool kBf16>
-void launch(const FwdArgs& p, hipStream_t st) {
+void launch(const FwdArgs& p, const Plan& plan, hipStream_t st) {
   switch (states_of(p.a)) {
-    case 1: return launch_waves<kBf16, 1>(p, st);
-    case 2: return launch_waves<kBf16, 2>(p, st);
-    case 4: return launch_waves<kBf16, 4>(p, st);
-    case 8: return launch_waves<kBf16, 8>(p, st);
-    default: return launch_waves<kBf16, 16>(p, st);
+    case 1: return launch_shape<kBf16, 1>(p, plan, st);
+    case 2: return launch_shape<kBf16, 2>(p, plan, st);
+    case 4: return launch_shape<kBf16, 4>(p, plan, st);
+    case 8: return launch_shape<kBf16, 8>(p, plan, st);
+    default: return launch_shape<kBf16, 16>(p, plan, st);
   }
 }
 
 }  // namespace
 
-size_t selscan_workspace(const SelScan& a) { return layout(a, segments_of(a)).bytes; }
+size_t selscan_workspace(const SelScan& a) { return layout(a, plan_of(a).seg).bytes; }
 
 hipError_t launch_selscan_forward(const SelScan& a, const float* state_in, void* y, float* state_out, char* ws,
                                   hipStream_t st) {
-  FwdArgs p{a, state_in, y, state_out, segments_of(a), blocks_per_group(a)};
+  const Plan plan = plan_of(a);
+  FwdArgs p{a, state_in, y, state_out, plan.seg, plan.per_group};
   const Layout l = layout(a, p.seg);
   p.tiles = (int64_t)a.B * a.G * p.per_group;
   p.sums = (float*)(ws + l.sums), p.width = (float*)(ws + l.width);
-  a.bf16 ? launch<true>(p, st) : launch<false>(p, st);
+  a.bf16 ? launch<true>(p, plan, st) : launch<false>(p, plan, st);
   return hipGetLastError();
 }
 

@@ -18,6 +18,7 @@ namespace pnr {
 namespace selscan {
 
 constexpr int kChannels = 64;     // of a wave
+constexpr int kNarrow = 16;       // of a wave that holds one channel's states in a quad of lanes
 
 // The value of the lane 4 r places away in the row of 16 (away<4 - r> undoes away<r>).
 template <int r>
@@ -44,28 +45,64 @@ __device__ __forceinline__ float exponent(float A) {
   return x < -3e38f ? -3e38f : x;
 }
 
+// A buffer from p on, empty unless `there`: at kNowhere, or in an empty one, loads give zeros and writes
+// are dropped.
+constexpr int kNowhere = 0x7fffffff;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, bool there) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, there ? 0x7fffffff : 0, 0x00027000);
+}
+template <typename T>
+__device__ __forceinline__ T load_buffer(__amdgpu_buffer_rsrc_t from, int at, int base) {
+  if constexpr (sizeof(T) == 2)
+    return __builtin_amdgcn_raw_buffer_load_b16(from, at, base, 0);
+  else
+    return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(from, at, base, 0));
+}
+template <bool kBf16>
+__device__ __forceinline__ void store_buffer(float v, __amdgpu_buffer_rsrc_t to, int at, int base) {
+  if constexpr (kBf16)
+    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), to, at, base, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), to, at, base, 0);
+}
+
+// A token's step width, 0 for a token that is not there.  The softplus is taken in any case: a branch
+// would part the tokens' instructions, which fill each other's gaps.
+__device__ __forceinline__ float step_width(float raw, int soft, bool there) {
+  float s = softplus(raw);
+  asm volatile("" : "+v"(s));
+  return there ? (soft ? s : raw) : 0.0f;
+}
+
+// silu(z), or 1 without a gate; no branch, for the same reason.
+__device__ __forceinline__ float gate_of(float z, bool gated) {
+  float s = z * sigm(z);
+  asm volatile("" : "+v"(s));
+  return gated ? s : 1.0f;
+}
+
 // Where a wave works: row b, group g, its first channel e0 (of E) and how many of 64 it has.
 struct Tile {
   int b, g, e0, live;
 };
 
-// kW waves a block share a group's B and C; `per_group` blocks a group.
-template <int kW>
+// kW waves a block share a group's B and C, kCh channels each; `per_group` blocks a group.
+template <int kW, int kCh>
 __device__ __forceinline__ Tile tile_of(const SelScan& a, int64_t i, int per_group) {
   Tile t;
   const int W = a.E / a.G, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int first = (int)(i % per_group) * (kW * kChannels) + wave * kChannels;
+  const int first = (int)(i % per_group) * (kW * kCh) + wave * kCh;
   const int64_t rest = i / per_group;
   t.g = (int)(rest % a.G);
   t.b = (int)(rest / a.G);
   t.e0 = t.g * W + first;
-  t.live = min(W - first, kChannels);
+  t.live = min(W - first, kCh);
   return t;
 }
 
-// Tokens of B and C that a block stages at a time: 1024 values of both for up to 16 states a channel.
+// Tokens of B and C that a block stages at a time.
 template <int R>
-constexpr int kStage = R <= 4 ? 32 : 128 / R;
+constexpr int kStage = R <= 4 ? 32 : 16;
 
 // Stages B and C of tokens t.. as fp32 [token][B, C][4 R], zeros beyond `end` and the states.  The
 // values are fetched to registers first, so that they travel while the tile before is computed.
@@ -104,6 +141,40 @@ struct Stage {
 template <int R>
 __device__ __forceinline__ void read_states(const float* p, float (&v)[R]) {
   __builtin_memcpy(v, __builtin_assume_aligned(p, R >= 4 ? 16 : 4 * R), 4 * R);
+}
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// A token of the recurrence: h = exp2(d A) h + x B in each of four slots, B of this lane's states at
+// p (LDS).  x B is an outer product of the channels of four neighbouring lanes and four states, which
+// one matrix instruction adds to the decayed states: B's four values come from the four lanes, x
+// from each.  It is exact as a fused multiplication and addition is.
+template <int R>
+__device__ __forceinline__ void advance(float (&h)[4][R], const float (&A)[4][R], const float (&d)[4], const float (&x)[4],
+                                        const float* p, int lane) {
+  if constexpr (R >= 4) {
+    float b[R / 4];
+#pragma unroll
+    for (int m = 0; m < R / 4; ++m) b[m] = p[4 * m + (lane & 3)];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int m = 0; m < R / 4; ++m) {
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = h[r][4 * m + i] * __builtin_amdgcn_exp2f(d[r] * A[r][4 * m + i]);
+        v = __builtin_amdgcn_mfma_f32_4x4x1f32(b[m], x[r], v, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[r][4 * m + i] = v[i];
+      }
+  } else {
+    float b[R];
+    read_states<R>(p, b);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < R; ++i) h[r][i] = fmaf(h[r][i], __builtin_amdgcn_exp2f(d[r] * A[r][i]), x[r] * b[i]);
+  }
 }
 
 // How time is cut: S segments of `len` tokens, a multiple of 32.

@@ -122,7 +122,7 @@ bool negative(const int64_t* s, int n) {
   return false;
 }
 
-constexpr int kMaxTokens = 1 << 30, kMaxChannels = 1 << 20;
+constexpr int kMaxTokens = 1 << 30, kMaxChannels = 1 << 20, kMaxTokenStride = 1 << 23;
 constexpr double kMaxTiles = 4.0e6;      // of 64 channels: a launch holds 2^32 threads, 64 to 512 a tile
 
 // Sizes and enums; `step`: T, the token strides and lens are not part of the request.
@@ -139,6 +139,9 @@ int validate(const pnr_selscan* d, bool step) {
       d->C_stride[0] < 0 || d->B_stride[2] < 0 || d->C_stride[2] < 0 ||
       (!step && (d->B_stride[1] < 0 || d->C_stride[1] < 0)))
     return record_error(PNR_E_INVALID, "strides must be >= 0");
+  // tokens of a tile and those fetched ahead are 32-bit offsets
+  if (!step && d->T > 1 && (d->u_stride[1] > kMaxTokenStride || d->dt_stride[1] > kMaxTokenStride || d->z_stride[1] > kMaxTokenStride))
+    return record_error(PNR_E_UNSUPPORTED, "token strides up to %d elements are supported", kMaxTokenStride);
   if (d->N > kMaxStates) return record_error(PNR_E_UNSUPPORTED, "up to %d states a channel are supported (got N=%d)", kMaxStates, d->N);
   const double tiles = (double)d->B * d->G * ((d->E / d->G + 63) / 64);
   if (d->E > kMaxChannels || tiles > kMaxTiles || (!step && d->T > kMaxTokens))

@@ -152,12 +152,11 @@ struct Elem<false> {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// log(1 + e^x) without overflow and, where e^x is far below 1, without loss: log(w) of the rounded
-// w = 1 + e is scaled by e / (w - 1), what the rounding took.
+// log(1 + e^x) without overflow and, where e^x is far below 1, without loss: to log(w) of the rounded
+// w = 1 + e comes e - (w - 1), what the rounding took (over w, which is 1 where that counts).
 __device__ __forceinline__ float softplus(float x) {
-  const float e = fast_exp(-fabsf(x)), w = 1.0f + e, d = w - 1.0f;
-  const float l = __builtin_amdgcn_logf(w) * kLn2 * (e * fast_rcp(d));
-  return fmaxf(x, 0.0f) + (d == 0.0f ? e : l);
+  const float e = fast_exp(-fabsf(x)), w = 1.0f + e;
+  return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(w), kLn2, e - (w - 1.0f));
 }
 
 // The value of an 8-bit copy's code on exponent byte s (255: not finite).

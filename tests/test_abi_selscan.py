@@ -55,6 +55,14 @@ def test_what_a_single_token_does_not_read(bad):
     assert _step(d, y=None) == pnr.E_INVALID and "y is NULL" in pnr.pnr_last_error()      # past the sizes
 
 
+@pytest.mark.parametrize("name", ["u_stride", "dt_stride", "z_stride"])
+def test_token_strides(name):
+    far = {name: (0, (1 << 23) + 1)}
+    assert _forward(_scan(**far)) == pnr.E_UNSUPPORTED and "strides" in pnr.pnr_last_error()
+    assert _backward(_scan(**far)) == pnr.E_UNSUPPORTED
+    assert _forward(_scan(T=1, **far), y=None) == pnr.E_INVALID and "y is NULL" in pnr.pnr_last_error()
+
+
 def test_arguments_of_the_scan():
     d = _scan()
     for name in ("u", "dt", "A", "B", "C", "y"):
