@@ -3,179 +3,583 @@
 //   dC_t = sum_e gy h_t          dB_t = sum_e g delta u        q = sum_n g B_t
 //   du = D gy + delta q          ddelta = u q + sum_n g a h_{t-1} A
 //   dA = sum_t g a h_{t-1} delta      dD = sum_t gy u          dh_0 = a_1 g_1
-// One thread a channel: a walk forwards that keeps every state, and one back.
+//
+// Keeping every state would cost 4 N bytes a channel and token, many times what the call reads, so
+// they are made again, from coarse to fine:
+//   local_kernel   a segment forwards from zeros: its state every 16 tokens (a chunk), and where time is
+//                  cut the segment's sums for the recurrences of h and of g
+//   join_kernel    those recurrences over a row's segments
+//   walk_kernel    a segment's chunks, last to first: the chunk forwards once for the states
+//                  every four tokens (LDS), each four forwards again with all states and
+//                  decays in registers, and back through them
+// Instruction issue bounds it: some 25 slots a state and token in the walk and 8 before it.
 #include <algorithm>
 
-#include "seq_ops.h"
+#include "selscan_tile.h"
 
 namespace pnr {
 namespace {
+
+using namespace selscan;
+
+constexpr int R = 4;               // states of a channel in a lane: 16 in a wave
+constexpr int kChunk = 16, kFour = 4;
 
 struct BwdArgs {
   SelScan a;
   SelScanGrads d;
   const float* s_in;
-  float *hist, *part, *pA, *pD, *pb;      // states [B, T, N, E]; sums of a tile, and of a row
-  int tiles, per_group;                   // tiles of 64 channels: in all, a group
+  Segments seg;
+  int tiles, per_group;            // of 64 channels: in all, a group
+  int NB, chunks;                  // blocks of 16 states; chunks of a row
+  float *states, *reach;           // [B, chunks, E, 16 NB] and [B, chunks, E]: from the segment's start to the chunk's
+  float *hs, *gs, *width;          // [B, S, E, 16 NB] twice, [B, S, E]
+  float *part, *pA, *pD, *pb;      // [B, T, tiles, 2, 16 NB]; [B S, E, N], [B S, E], [B S, E]
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+// What a wave knows of its place: the tile, its states and its lanes' channels.
+struct Place {
+  Tile w;
+  int seg, lane, nq, e, n0;        // n0: this lane's first state
+  int ch[4];
+  bool live;
+};
+
+template <int NB>
+__device__ __forceinline__ Place place(const BwdArgs& p) {
+  Place x;
+  const int64_t per_seg = (int64_t)p.a.B * p.tiles;
+  x.seg = (int)(blockIdx.x / per_seg);
+  const int64_t i = blockIdx.x % per_seg;
+  const int W = p.a.E / p.a.G, first = (int)(i % p.per_group) * kChannels;
+  x.w.g = (int)(i / p.per_group % p.a.G), x.w.b = (int)(i / p.tiles);
+  x.w.e0 = x.w.g * W + first, x.w.live = min(W - first, kChannels);
+  x.lane = threadIdx.x & 63, x.nq = x.lane >> 2 & 3;
+  x.live = x.lane < x.w.live;
+  x.e = x.w.e0 + min(x.lane, x.w.live - 1);
+  x.n0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 16 + x.nq * R;
+  // a lane without a channel gets E - 1's numbers and is kept from storing; its slots hold zeros
+  x.ch[0] = x.live ? x.e : -1, x.ch[1] = away<1>(x.ch[0]), x.ch[2] = away<2>(x.ch[0]), x.ch[3] = away<3>(x.ch[0]);
+  return x;
 }
 
-template <bool kBf16, int NP>
-__global__ void __launch_bounds__(64) walk_kernel(BwdArgs p) {
-  using El = Elem<kBf16>;
-  using T = typename El::type;
-  const SelScan& a = p.a;
-  const int b = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles, g = tile / p.per_group;
-  const int W = a.E / a.G, w = tile % p.per_group * 64 + threadIdx.x;
-  const bool live = w < W;
-  const int e = g * W + (live ? w : 0), n = row_len(a.lens, b, a.T);
-  float A[NP], h[NP], G[NP], gA[NP];
-  const size_t at = ((size_t)b * a.E + e) * a.N;
+__device__ __forceinline__ void load_A(const SelScan& a, const Place& x, float (&A)[4][R]) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    A[i] = i < a.N ? a.A[(size_t)e * a.N + i] : 0.0f;
-    h[i] = i < a.N && p.s_in ? p.s_in[at + i] : 0.0f;
-    G[i] = i < a.N && p.d.gstate_out ? p.d.gstate_out[at + i] : 0.0f;
-    gA[i] = 0.0f;
-  }
-  const T* u = (const T*)a.u.p + b * a.u.sb + e;
-  const T* dt = (const T*)a.dt.p + b * a.dt.sb + e;
-  const T* z = a.z.p ? (const T*)a.z.p + b * a.z.sb + e : nullptr;
-  const T* Bt = (const T*)a.Bt.p + b * a.Bt.sb + g * a.Bt.sh;
-  const T* Ct = (const T*)a.Ct.p + b * a.Ct.sb + g * a.Ct.sh;
-  const float D = a.D ? a.D[e] : 0.0f, bias = a.bias ? a.bias[e] : 0.0f;
-  float* hist = p.hist + (size_t)b * a.T * a.N * a.E + e;
-  for (int t = 0; t < n; ++t) {
-    const float ut = El::load(u + t * a.u.st), raw = El::load(dt + t * a.dt.st) + bias;
-    const float delta = a.softplus ? softplus(raw) : raw, du = delta * ut;
+  for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const float Bv = i < a.N ? El::load(Bt + t * a.Bt.st + i) : 0.0f;
-      if (i < a.N && live) hist[((size_t)t * a.N + i) * a.E] = h[i];
-      h[i] = h[i] * __builtin_amdgcn_exp2f(delta * (A[i] * kLog2e)) + du * Bv;
-    }
-  }
-  float gD = 0.0f, gb = 0.0f;
-  for (int t = n - 1; t >= 0; --t) {
-    const size_t o = ((size_t)b * a.T + t) * a.E + e;
-    const float ut = El::load(u + t * a.u.st), raw = El::load(dt + t * a.dt.st) + bias;
-    const float delta = a.softplus ? softplus(raw) : raw, du = delta * ut;
-    float gy = live ? El::load((const T*)p.d.gy + o) : 0.0f;
-    const float gy0 = gy, zt = z ? El::load(z + t * a.z.st) : 0.0f, sg = sigm(zt);
-    if (z) gy *= zt * sg;
-    float y = D * ut, q = 0.0f, gd = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      if (i >= a.N) break;
-      const float Bv = El::load(Bt + t * a.Bt.st + i), Cv = El::load(Ct + t * a.Ct.st + i);
-      const float hp = live ? hist[((size_t)t * a.N + i) * a.E] : 0.0f;
-      const float dec = __builtin_amdgcn_exp2f(delta * (A[i] * kLog2e)), hn = hp * dec + du * Bv;
-      y += Cv * hn;
-      G[i] += gy * Cv;
-      q += G[i] * Bv;
-      const float dB = wave_sum(live ? G[i] * du : 0.0f), dC = wave_sum(live ? gy * hn : 0.0f);
-      if (threadIdx.x == 0) {
-        float* part = p.part + (((size_t)b * a.T + t) * p.tiles + tile) * 2 * a.N;
-        part[i] = dB, part[a.N + i] = dC;
-      }
-      G[i] *= dec;
-      gd += G[i] * hp * A[i];
-      gA[i] += G[i] * hp * delta;
-    }
-    gd += ut * q;
-    if (a.softplus) gd *= sigm(raw);
-    gD += gy * ut, gb += gd;
-    if (live) {
-      if (p.d.gu) El::store((T*)p.d.gu + o, D * gy + delta * q);
-      if (p.d.gdt) El::store((T*)p.d.gdt + o, gd);
-      if (p.d.gz) El::store((T*)p.d.gz + o, gy0 * y * sg * (1.0f + zt * (1.0f - sg)));
-    }
-  }
-  if (!live) return;
-  for (int t = n; t < a.T; ++t) {
-    const size_t o = ((size_t)b * a.T + t) * a.E + e;
-    if (p.d.gu) El::store((T*)p.d.gu + o, 0.0f);
-    if (p.d.gdt) El::store((T*)p.d.gdt + o, 0.0f);
-    if (p.d.gz) El::store((T*)p.d.gz + o, 0.0f);
-  }
-#pragma unroll
-  for (int i = 0; i < NP; ++i)
-    if (i < a.N) {
-      p.pA[at + i] = gA[i];
-      if (p.d.gstate_in) p.d.gstate_in[at + i] = G[i];
-    }
-  p.pD[(size_t)b * a.E + e] = gD, p.pb[(size_t)b * a.E + e] = gb;
+    for (int i = 0; i < R; ++i) A[r][i] = x.ch[r] >= 0 && x.n0 + i < a.N ? exponent(a.A[(size_t)x.ch[r] * a.N + x.n0 + i]) : 0.0f;
 }
 
-// The tiles' sums of dB and dC, in order.
+// Four states of each slot from, or to, [.., E, 16 NB] at row `row` of E channels.
+__device__ __forceinline__ void load_states(const float* p, size_t row, const BwdArgs& q, const Place& x, float (&h)[4][R]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f32x4 v{0, 0, 0, 0};
+    if (x.ch[r] >= 0) v = *(const f32x4*)(p + (row * q.a.E + x.ch[r]) * (16 * q.NB) + x.n0);
+#pragma unroll
+    for (int i = 0; i < R; ++i) h[r][i] = v[i];
+  }
+}
+__device__ __forceinline__ void store_states(float* p, size_t row, const BwdArgs& q, const Place& x, const float (&h)[4][R]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (x.ch[r] >= 0) *(f32x4*)(p + (row * q.a.E + x.ch[r]) * (16 * q.NB) + x.n0) = f32x4{h[r][0], h[r][1], h[r][2], h[r][3]};
+}
+
+// B and C of a chunk, this wave's 16 states: [token][B, C][16], zeros beyond `end` and the states.
 template <bool kBf16>
-__global__ void __launch_bounds__(64) token_kernel(BwdArgs p) {
+struct Chunk {
   using El = Elem<kBf16>;
   using T = typename El::type;
-  const SelScan& a = p.a;
-  for (int64_t row = blockIdx.x; row < (int64_t)a.B * a.T; row += gridDim.x) {
-    const bool live = row % a.T < row_len(a.lens, (int)(row / a.T), a.T);
-    for (int i = threadIdx.x; i < a.G * 2 * a.N; i += 64) {
-      const int g = i / (2 * a.N), k = i % (2 * a.N);
-      float s = 0.0f;
-      if (live)
-        for (int j = 0; j < p.per_group; ++j) s += p.part[((size_t)row * p.tiles + g * p.per_group + j) * 2 * a.N + k];
-      T* out = (T*)(k < a.N ? p.d.gB : p.d.gC);
-      if (out) El::store(out + ((size_t)row * a.G + g) * a.N + k % a.N, s);
+  T raw[kChunk * 32 / 64];
+  __device__ __forceinline__ void fetch(const BwdArgs& p, const Place& x, int t, int end) {
+    const SelScan& a = p.a;
+    const T* B = (const T*)a.Bt.p + x.w.b * a.Bt.sb + x.w.g * a.Bt.sh;
+    const T* C = (const T*)a.Ct.p + x.w.b * a.Ct.sb + x.w.g * a.Ct.sh;
+    const int n = (x.n0 & ~15) + (x.lane & 15), which = x.lane >> 4 & 1;
+#pragma unroll
+    for (int k = 0; k < kChunk * 32 / 64; ++k) {
+      const int64_t tok = t + 2 * k + (x.lane >> 5);
+      raw[k] = 0;
+      if (n < a.N && tok < end) raw[k] = which ? C[tok * a.Ct.st + n] : B[tok * a.Bt.st + n];
     }
+  }
+  __device__ __forceinline__ void put(float* lds, int lane) const {
+#pragma unroll
+    for (int k = 0; k < kChunk * 32 / 64; ++k) lds[k * 64 + lane] = El::load(&raw[k]);
+  }
+};
+
+// The channels' own values of tokens t.., by the lanes that own them; zeros where there is no token or channel.
+template <bool kBf16>
+struct Operand {
+  using T = typename Elem<kBf16>::type;
+  const T* p;
+  int64_t st;
+  int off;
+  __device__ __forceinline__ T get(int t, bool there) const { return load_buffer<T>(buffer_of(p + t * st, there), off, 0); }
+};
+template <bool kBf16>
+__device__ __forceinline__ Operand<kBf16> operand(const void* p, int64_t sb, int64_t st, const Place& x) {
+  using T = typename Elem<kBf16>::type;
+  return {p ? (const T*)p + x.w.b * sb : nullptr, st, x.live ? x.e * (int)sizeof(T) : kNowhere};
+}
+
+template <bool kBf16, int NB, bool kCut>
+__global__ void __launch_bounds__(NB * 64, 2) local_kernel(BwdArgs p) {
+  using El = Elem<kBf16>;
+  using T = typename El::type;
+  __shared__ alignas(16) float bc_all[NB][2][kChunk * 32];
+  const SelScan& a = p.a;
+  const Place x = place<NB>(p);
+  const int n = row_len(a.lens, x.w.b, a.T), t0 = x.seg * p.seg.len, t1 = min(t0 + p.seg.len, n);
+  if (t0 >= t1) return;
+  const int sb = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float(*bc)[kChunk * 32] = bc_all[sb];
+  float A[4][R], h[4][R] = {}, P[4][R], G[4][R] = {};
+  load_A(a, x, A);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int i = 0; i < R; ++i) P[r][i] = 1.0f;
+  const float bias = a.bias ? a.bias[x.e] : 0.0f;
+  const auto u = operand<kBf16>(a.u.p, a.u.sb, a.u.st, x), dt = operand<kBf16>(a.dt.p, a.dt.sb, a.dt.st, x),
+             z = operand<kBf16>(a.z.p, a.z.sb, a.z.st, x), gy = operand<kBf16>(p.d.gy, (int64_t)a.T * a.E, a.E, x);
+  T ur[kFour], dr[kFour], zr[kFour], gr[kFour];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < kFour; ++k) {
+      const bool there = t + k < t1;
+      ur[k] = u.get(t + k, there), dr[k] = dt.get(t + k, there);
+      if (kCut) zr[k] = z.get(t + k, there && a.z.p), gr[k] = gy.get(t + k, there);
+    }
+  };
+  float total = 0.0f;
+  Chunk<kBf16> stage;
+  stage.fetch(p, x, t0, t1);
+  fetch(t0);
+  int buf = 0;
+  for (int t = t0; t < t1; t += kChunk, buf ^= 1) {
+    stage.put(bc[buf], x.lane);
+    const size_t row = (size_t)x.w.b * p.chunks + t / kChunk;
+    if (t > t0) {
+      store_states(p.states, row, p, x, h);
+      if (sb == 0 && x.live) p.reach[row * a.E + x.e] = total;
+    }
+    if (!kCut && t + kChunk >= t1) break;        // the last chunk's end is nobody's start
+    stage.fetch(p, x, t + kChunk, t1);
+    __builtin_amdgcn_wave_barrier();             // a wave reads what it staged itself
+    for (int f = 0; f < kChunk && t + f < t1; f += kFour) {
+      float uv[kFour], dv[kFour], zv[kFour], gv[kFour];
+#pragma unroll
+      for (int k = 0; k < kFour; ++k) {
+        uv[k] = El::load(&ur[k]), dv[k] = El::load(&dr[k]);
+        if (kCut) zv[k] = El::load(&zr[k]), gv[k] = El::load(&gr[k]);
+      }
+      fetch(t + f + kFour);
+#pragma unroll
+      for (int k = 0; k < kFour; ++k) {
+        const float delta = step_width(dv[k] + bias, a.softplus, x.live && t + f + k < t1);
+        total += delta;
+        float d[4], s[4], g[4];
+        to_slots(delta, d);
+        to_slots(delta * uv[k], s);
+        if (kCut) to_slots(gv[k] * gate_of(zv[k], a.z.p), g);
+        const float* at = bc[buf] + (f + k) * 32 + x.nq * R + (x.lane & 3);
+        const float b = at[0], c = at[16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          f32x4 v, w{0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            const float dec = __builtin_amdgcn_exp2f(d[r] * A[r][i]);
+            v[i] = h[r][i] * dec;
+            P[r][i] *= dec;
+          }
+          v = __builtin_amdgcn_mfma_f32_4x4x1f32(b, s[r], v, 0, 0, 0);
+          if (kCut) w = __builtin_amdgcn_mfma_f32_4x4x1f32(c, g[r], w, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            h[r][i] = v[i];
+            if (kCut) G[r][i] = fmaf(P[r][i], w[i], G[r][i]);
+          }
+        }
+      }
+    }
+  }
+  if (!kCut) return;
+  const size_t row = (size_t)x.w.b * p.seg.S + x.seg;
+  store_states(p.hs, row, p, x, h);
+  store_states(p.gs, row, p, x, G);
+  if (sb == 0 && x.live) p.width[row * a.E + x.e] = total;
+}
+
+// The recurrences over a row's segments: in place of a segment's sums its first state, and the gradient
+// that reaches its last state from behind.  A thread a state; eight segments are asked for at once.
+__global__ void __launch_bounds__(256) join_kernel(BwdArgs p) {
+  constexpr int kBatch = 8;
+  const SelScan& a = p.a;
+  const int NP = 16 * p.NB;
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
+  if (i >= (int64_t)a.B * a.E * NP) return;
+  const int s = (int)(i % NP), e = (int)(i / NP % a.E), b = (int)(i / NP / a.E);
+  const int n = row_len(a.lens, b, a.T), segs = (n + p.seg.len - 1) / p.seg.len;
+  const bool real = s < a.N;
+  const float A = real ? exponent(a.A[(size_t)e * a.N + s]) : 0.0f;
+  const size_t at = ((size_t)b * a.E + e) * a.N + s, row = (size_t)b * p.seg.S * a.E + e;
+  float h = real && p.s_in ? p.s_in[at] : 0.0f, g = real && p.d.gstate_out ? p.d.gstate_out[at] : 0.0f;
+  if (p.seg.S > 1) {
+    auto walk = [&](float* sums, bool back, float& v) {
+      for (int k0 = 0; k0 < segs; k0 += kBatch) {
+        float own[kBatch], d[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int j = min(k0 + k, segs - 1);
+          const size_t r = row + (size_t)(back ? segs - 1 - j : j) * a.E;
+          own[k] = sums[r * NP + s], d[k] = p.width[r];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (k0 + k < segs) {
+            const int j = k0 + k;
+            sums[(row + (size_t)(back ? segs - 1 - j : j) * a.E) * NP + s] = v;
+            v = fmaf(v, __builtin_amdgcn_exp2f(d[k] * A), own[k]);
+          }
+      }
+    };
+    walk(p.hs, false, h);
+    walk(p.gs, true, g);
+    if (real && p.d.gstate_in) p.d.gstate_in[at] = g;
+  } else {                                        // one segment: its walk goes on to the first state
+    p.hs[row * NP + s] = h;
+    p.gs[row * NP + s] = g;
+    if (real && p.d.gstate_in && segs == 0) p.d.gstate_in[at] = g;
   }
 }
 
-__global__ void __launch_bounds__(256) row_kernel(const float* part, int rows, size_t n, float* out) {
+// Sums of dB and dC over the wave's channels (lane bits 0, 1, 4 and 5): the halves of the wave take one
+// each, then rows of 16 and neighbouring lanes two states each.  Lane l ends with state
+// 4 (l / 4 % 4) + (l / 16 % 2) + 2 (l % 2) of dB (l < 32) or dC.
+__device__ __forceinline__ float over_channels(const float (&b)[R], const float (&c)[R], int lane) {
+  float v[R], y[2];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(b[i]), __float_as_uint(c[i]), false, false);
+    v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), false, false);
+    y[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  const bool odd = lane & 1;
+  float o = (odd ? y[1] : y[0]) + quad_perm<0xb1>(odd ? y[0] : y[1]);
+  o += quad_perm<0x4e>(o);
+  return o;
+}
+
+template <bool kBf16, int NB>
+__global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
+  using El = Elem<kBf16>;
+  using T = typename El::type;
+  constexpr int kFours = kChunk / kFour;
+  __shared__ alignas(16) float bc_all[NB][kChunk * 32];
+  __shared__ f32x4 mid_all[NB][kFours][4][64];
+  __shared__ float sums[NB > 1 ? 2 : 1][NB > 1 ? NB : 1][3][NB > 1 ? kFour : 1][64];
+  const SelScan& a = p.a;
+  const SelScanGrads& d = p.d;
+  const Place x = place<NB>(p);
+  const int n = row_len(a.lens, x.w.b, a.T), t0 = x.seg * p.seg.len, tend = min(t0 + p.seg.len, a.T), t1 = min(tend, n);
+  const int sb = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* bc = bc_all[sb];
+  auto& mid = mid_all[sb];
+  const size_t seg_row = (size_t)x.w.b * p.seg.S + x.seg;
+  T* gu = d.gu ? (T*)d.gu + (size_t)x.w.b * a.T * a.E : nullptr;
+  T* gdt = d.gdt ? (T*)d.gdt + (size_t)x.w.b * a.T * a.E : nullptr;
+  T* gz = d.gz ? (T*)d.gz + (size_t)x.w.b * a.T * a.E : nullptr;
+  if (sb == 0 && x.live)
+    for (int t = max(t0, t1); t < tend; ++t) {
+      if (gu) El::store(gu + (size_t)t * a.E + x.e, 0.0f);
+      if (gdt) El::store(gdt + (size_t)t * a.E + x.e, 0.0f);
+      if (gz) El::store(gz + (size_t)t * a.E + x.e, 0.0f);
+    }
+  float A[4][R], g[4][R], dA[4][R] = {};
+  float dD = 0.0f, db = 0.0f;
+  if (t0 < t1) {
+    load_A(a, x, A);
+    load_states(p.gs, seg_row, p, x, g);
+    const float bias = a.bias ? a.bias[x.e] : 0.0f, D = a.D ? a.D[x.e] : 0.0f;
+    const auto u = operand<kBf16>(a.u.p, a.u.sb, a.u.st, x), dt = operand<kBf16>(a.dt.p, a.dt.sb, a.dt.st, x),
+               z = operand<kBf16>(a.z.p, a.z.sb, a.z.st, x), gy = operand<kBf16>(d.gy, (int64_t)a.T * a.E, a.E, x);
+    const bool gated = a.z.p;
+    const int at = x.live ? x.e * (int)sizeof(T) : kNowhere;
+    float* part = p.part + (((size_t)x.w.b * a.T) * p.tiles + x.w.g * p.per_group + (x.w.e0 - x.w.g * (a.E / a.G)) / kChannels) * 32 * NB;
+    const int part_at = (x.lane & 2) ? kNowhere
+                                     : ((x.lane >> 5) * 16 * NB + sb * 16 + x.nq * 4 + (x.lane >> 4 & 1) + 2 * (x.lane & 1)) * 4;
+    const float* reach = p.reach + x.e;
+    int turn = 0;
+    T ur[kFour], dr[kFour], zr[kFour], gr[kFour];
+    auto fetch = [&](int t, bool any) {
+#pragma unroll
+      for (int k = 0; k < kFour; ++k) {
+        const bool there = any && t + k < t1;
+        ur[k] = u.get(t + k, there), dr[k] = dt.get(t + k, there);
+        zr[k] = z.get(t + k, there && gated), gr[k] = gy.get(t + k, there);
+      }
+    };
+    Chunk<kBf16> stage;
+    const int last = (t1 - 1 - t0) / kChunk;
+    stage.fetch(p, x, t0 + last * kChunk, t1);
+    for (int c = last; c >= 0; --c) {
+      const int tc = t0 + c * kChunk, fours = (min(tc + kChunk, t1) - tc + kFour - 1) / kFour;
+      // the state at the chunk's start: the segment's, decayed, and what the segment added
+      float h[4][R];
+      load_states(p.hs, seg_row, p, x, h);
+      if (c > 0) {
+        const size_t row = (size_t)x.w.b * p.chunks + tc / kChunk;
+        float own[4][R], w[4];
+        load_states(p.states, row, p, x, own);
+        to_slots(x.live ? reach[row * a.E] : 0.0f, w);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < R; ++i) h[r][i] = fmaf(h[r][i], __builtin_amdgcn_exp2f(w[r] * A[r][i]), own[r][i]);
+      }
+      fetch(tc + (fours - 1) * kFour, true);
+      T us[kFour], ds[kFour];
+      auto fetch_ahead = [&](int f) {
+#pragma unroll
+        for (int k = 0; k < kFour; ++k) us[k] = u.get(tc + f * kFour + k, f < fours - 1), ds[k] = dt.get(tc + f * kFour + k, f < fours - 1);
+      };
+      fetch_ahead(0);
+      stage.put(bc, x.lane);
+      if (c > 0) stage.fetch(p, x, tc - kChunk, t1);
+      __builtin_amdgcn_wave_barrier();
+      const float* lane_bc = bc + x.nq * R;
+      auto keep = [&](int f) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mid[f][r][x.lane] = f32x4{h[r][0], h[r][1], h[r][2], h[r][3]};
+      };
+      keep(0);
+      // the states at each four's start
+#pragma unroll 1
+      for (int f = 0; f < fours - 1; ++f) {
+        float uv[kFour], dv[kFour];
+#pragma unroll
+        for (int k = 0; k < kFour; ++k) uv[k] = El::load(&us[k]), dv[k] = El::load(&ds[k]);
+        fetch_ahead(f + 1);
+#pragma unroll
+        for (int k = 0; k < kFour; ++k) {
+          const float delta = step_width(dv[k] + bias, a.softplus, x.live);
+          float dl[4], s[4];
+          to_slots(delta, dl);
+          to_slots(delta * uv[k], s);
+          advance<R>(h, A, dl, s, lane_bc + (f * kFour + k) * 32, x.lane);
+        }
+        keep(f + 1);
+      }
+#pragma unroll 1
+      for (int f = fours - 1; f >= 0; --f) {
+        const int t = tc + f * kFour;
+        float uv[kFour], raw[kFour], zv[kFour], gv[kFour], delta[kFour];
+#pragma unroll
+        for (int k = 0; k < kFour; ++k) {
+          uv[k] = El::load(&ur[k]), raw[k] = El::load(&dr[k]) + bias, zv[k] = El::load(&zr[k]), gv[k] = El::load(&gr[k]);
+          delta[k] = step_width(raw[k], a.softplus, x.live && t + k < t1);
+        }
+        // forwards: states before each token, and decays
+        float hist[kFour + 1][4][R], dec[kFour][4][R];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4 v = mid[f][r][x.lane];
+#pragma unroll
+          for (int i = 0; i < R; ++i) hist[0][r][i] = v[i];
+        }
+#pragma unroll
+        for (int k = 0; k < kFour; ++k) {
+          float dl[4], s[4];
+          to_slots(delta[k], dl);
+          to_slots(delta[k] * uv[k], s);
+          const float b = lane_bc[(f * kFour + k) * 32 + (x.lane & 3)];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              dec[k][r][i] = __builtin_amdgcn_exp2f(dl[r] * A[r][i]);
+              v[i] = hist[k][r][i] * dec[k][r][i];
+            }
+            v = __builtin_amdgcn_mfma_f32_4x4x1f32(b, s[r], v, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < R; ++i) hist[k + 1][r][i] = v[i];
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // and back
+        float ys[kFour], qs[kFour], ws[kFour];
+#pragma unroll
+        for (int k = kFour - 1; k >= 0; --k) {
+          const float* s = lane_bc + (f * kFour + k) * 32;
+          float Bv[R], Cv[R], dl[4], xs[4], gs[4], ya[4], qa[4], wa[4], dB[R] = {}, dC[R] = {};
+          read_states<R>(s, Bv);
+          read_states<R>(s + 16, Cv);
+          const float cl = s[16 + (x.lane & 3)];
+          to_slots(delta[k], dl);
+          to_slots(delta[k] * uv[k], xs);
+          to_slots(gv[k] * gate_of(zv[k], gated), gs);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            f32x4 v{g[r][0], g[r][1], g[r][2], g[r][3]};
+            v = __builtin_amdgcn_mfma_f32_4x4x1f32(cl, gs[r], v, 0, 0, 0);
+            ya[r] = qa[r] = wa[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const float hn = hist[k + 1][r][i];
+              ya[r] = fmaf(hn, Cv[i], ya[r]);
+              dC[i] = fmaf(gs[r], hn, dC[i]);
+              dB[i] = fmaf(xs[r], v[i], dB[i]);
+              qa[r] = fmaf(v[i], Bv[i], qa[r]);
+              g[r][i] = v[i] * dec[k][r][i];
+              const float through = g[r][i] * hist[k][r][i];
+              wa[r] = fmaf(through, A[r][i], wa[r]);
+              dA[r][i] = fmaf(through, dl[r], dA[r][i]);
+            }
+          }
+          ys[k] = from_slots(ya), qs[k] = from_slots(qa), ws[k] = from_slots(wa);
+          const float o = over_channels(dB, dC, x.lane);
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), buffer_of(part + (size_t)(t + k) * p.tiles * 32 * NB, t + k < t1), part_at, 0, 0);
+          if (k == 2) fetch(t - kFour, f > 0);  // two tokens' states and decays are done with
+          __builtin_amdgcn_sched_barrier(0);     // one token's values at a time in registers
+        }
+        // the tokens' gradients, from the sums over all states
+        if constexpr (NB > 1) {
+#pragma unroll
+          for (int k = 0; k < kFour; ++k) sums[turn][sb][0][k][x.lane] = ys[k], sums[turn][sb][1][k][x.lane] = qs[k], sums[turn][sb][2][k][x.lane] = ws[k];
+          __syncthreads();           // the turn before is read by all that met here
+          if (sb == 0)
+#pragma unroll
+            for (int k = 0; k < kFour; ++k)
+#pragma unroll
+              for (int j = 1; j < NB; ++j)
+                ys[k] += sums[turn][j][0][k][x.lane], qs[k] += sums[turn][j][1][k][x.lane], ws[k] += sums[turn][j][2][k][x.lane];
+          turn ^= 1;
+        }
+        if (sb == 0) {
+#pragma unroll
+          for (int k = 0; k < kFour; ++k) {
+            const bool there = t + k < t1;
+            const float sg = sigm(zv[k]), gated_gy = gated ? gv[k] * zv[k] * sg : gv[k];
+            const float y = fmaf(D, uv[k], ys[k]), gd = fmaf(uv[k], qs[k], kLn2 * ws[k]);
+            const float gt = a.softplus ? gd * sigm(raw[k]) : gd;
+            dD = fmaf(gated_gy, uv[k], dD);
+            db += there ? gt : 0.0f;
+            if (gu) store_buffer<kBf16>(fmaf(D, gated_gy, delta[k] * qs[k]), buffer_of(gu + (size_t)(t + k) * a.E, there), at, 0);
+            if (gdt) store_buffer<kBf16>(gt, buffer_of(gdt + (size_t)(t + k) * a.E, there), at, 0);
+            if (gz) store_buffer<kBf16>(gv[k] * y * sg * (1.0f + zv[k] * (1.0f - sg)), buffer_of(gz + (size_t)(t + k) * a.E, there), at, 0);
+          }
+        }
+      }
+    }
+    if (p.seg.S == 1 && d.gstate_in)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (x.ch[r] >= 0 && x.n0 + i < a.N) d.gstate_in[((size_t)x.w.b * a.E + x.ch[r]) * a.N + x.n0 + i] = g[r][i];
+  }
+  // sums over the segment's tokens (zeros where it has none)
+  if (p.pA)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (x.ch[r] >= 0 && x.n0 + i < a.N) p.pA[(seg_row * a.E + x.ch[r]) * a.N + x.n0 + i] = dA[r][i];
+  if (sb == 0 && x.live) {
+    if (p.pD) p.pD[seg_row * a.E + x.e] = dD;
+    if (p.pb) p.pb[seg_row * a.E + x.e] = db;
+  }
+}
+
+// The tiles' sums of dB and dC, in order.  A thread a value.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) token_kernel(BwdArgs p) {
+  using El = Elem<kBf16>;
+  using T = typename El::type;
+  const SelScan& a = p.a;
+  const int NP = 16 * p.NB;
+  const int64_t total = (int64_t)a.B * a.T * a.G * 2 * NP;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int k = (int)(i % (2 * NP)), n = k % NP;
+    const int64_t row = i / (2 * NP) / a.G;
+    const int g = (int)(i / (2 * NP) % a.G);
+    T* out = (T*)(k < NP ? p.d.gB : p.d.gC);
+    if (n >= a.N || !out) continue;
+    float s = 0.0f;
+    if (row % a.T < row_len(a.lens, (int)(row / a.T), a.T)) {
+      const float* part = p.part + ((size_t)row * p.tiles + g * p.per_group) * 2 * NP + k;
+#pragma unroll 8
+      for (int j = 0; j < p.per_group; ++j) s += part[(size_t)j * 2 * NP];
+    }
+    El::store(out + ((size_t)row * a.G + g) * a.N + n, s);
+  }
+}
+
+// Sums over rows and segments, in order.
+__global__ void __launch_bounds__(256) row_kernel(const float* part, int64_t rows, size_t n, float* out) {
   const size_t i = blockIdx.x * (size_t)256 + threadIdx.x;
   if (i >= n) return;
   float s = 0.0f;
-  for (int r = 0; r < rows; ++r) s += part[r * n + i];
+#pragma unroll 8
+  for (int64_t r = 0; r < rows; ++r) s += part[r * n + i];
   out[i] = s;
 }
 
 struct Layout {
-  size_t hist, part, pA, pD, pb, bytes;
-  int tiles, per_group;
+  size_t states, reach, hs, gs, width, part, pA, pD, pb, bytes;
+  int tiles, per_group, NB, chunks;
+  Segments seg;
 };
 
 Layout layout(const SelScan& a) {
   Layout l{};
-  auto up = [](size_t v) { return (v * 4 + 255) / 256 * 256; };
-  l.per_group = (a.E / a.G + 63) / 64;
+  l.per_group = (a.E / a.G + kChannels - 1) / kChannels;
   l.tiles = l.per_group * a.G;
-  const size_t be = (size_t)a.B * a.E, bt = (size_t)a.B * a.T;
-  l.part = l.hist + up(bt * a.E * a.N);
-  l.pA = l.part + up(bt * l.tiles * 2 * a.N);
-  l.pD = l.pA + up(be * a.N);
-  l.pb = l.pD + up(be);
-  l.bytes = l.pb + up(be);
+  l.NB = (a.N + 15) / 16;
+  const int64_t waves = (int64_t)a.B * l.tiles * l.NB;
+  int64_t S = 1;
+  if (waves < 2048) S = std::min<int64_t>((a.T + kChunk - 1) / kChunk, (4096 + waves - 1) / waves);
+  S = std::max<int64_t>(S, 1);
+  const int len = std::max(kChunk, (int)(((a.T + S - 1) / S + kChunk - 1) / kChunk * kChunk));
+  l.seg = {std::max(1, (a.T + len - 1) / len), len};
+  l.chunks = (a.T + kChunk - 1) / kChunk;
+  size_t at = 0;
+  auto take = [&](size_t floats) {
+    const size_t here = at;
+    at += (floats * 4 + 255) / 256 * 256;
+    return here;
+  };
+  const size_t be = (size_t)a.B * a.E, NP = 16 * l.NB;
+  l.states = take(be * l.chunks * NP);
+  l.reach = take(be * l.chunks);
+  l.hs = take(be * l.seg.S * NP), l.gs = take(be * l.seg.S * NP), l.width = take(be * l.seg.S);
+  l.part = take((size_t)a.B * a.T * l.tiles * 2 * NP);
+  l.pA = take(be * l.seg.S * a.N), l.pD = take(be * l.seg.S), l.pb = take(be * l.seg.S);
+  l.bytes = at;
   return l;
 }
 
-template <bool kBf16>
+template <bool kBf16, int NB>
 void launch(const BwdArgs& p, hipStream_t st) {
   const SelScan& a = p.a;
-  const int blocks = a.B * p.tiles;
-  if (a.N <= 4)
-    walk_kernel<kBf16, 4><<<blocks, 64, 0, st>>>(p);
-  else if (a.N <= 16)
-    walk_kernel<kBf16, 16><<<blocks, 64, 0, st>>>(p);
-  else
-    walk_kernel<kBf16, 64><<<blocks, 64, 0, st>>>(p);
+  const unsigned blocks = (unsigned)((int64_t)a.B * p.tiles * p.seg.S);
+  if (p.seg.S > 1)
+    local_kernel<kBf16, NB, true><<<blocks, NB * 64, 0, st>>>(p);
+  else if (a.T > kChunk)
+    local_kernel<kBf16, NB, false><<<blocks, NB * 64, 0, st>>>(p);
+  join_kernel<<<(unsigned)(((int64_t)a.B * a.E * 16 * NB + 255) / 256), 256, 0, st>>>(p);
+  walk_kernel<kBf16, NB><<<blocks, NB * 64, 0, st>>>(p);
   if ((p.d.gB || p.d.gC) && a.T > 0)
-    token_kernel<kBf16><<<(unsigned)std::min<int64_t>((int64_t)a.B * a.T, 1 << 20), 64, 0, st>>>(p);
-  auto rows = [&](const float* part, size_t n, float* out) {
-    if (out) row_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, a.B, n, out);
-  };
-  rows(p.pA, (size_t)a.E * a.N, p.d.gA);
-  rows(p.pD, a.E, p.d.gD);
-  rows(p.pb, a.E, p.d.gbias);
+    token_kernel<kBf16><<<(unsigned)std::min<int64_t>(((int64_t)a.B * a.T * a.G * 32 * NB + 255) / 256, 1 << 20), 256, 0, st>>>(p);
 }
 
 }  // namespace
@@ -185,9 +589,24 @@ size_t selscan_workspace_backward(const SelScan& a) { return layout(a).bytes; }
 hipError_t launch_selscan_backward(const SelScan& a, const float* state_in, const SelScanGrads& d, char* ws,
                                    hipStream_t st) {
   const Layout l = layout(a);
-  const BwdArgs p{a, d, state_in, (float*)(ws + l.hist), (float*)(ws + l.part), (float*)(ws + l.pA), (float*)(ws + l.pD),
-                  (float*)(ws + l.pb), l.tiles, l.per_group};
-  a.bf16 ? launch<true>(p, st) : launch<false>(p, st);
+  auto at = [&](size_t off) { return (float*)(ws + off); };
+  const BwdArgs p{a, d, state_in, l.seg, l.tiles, l.per_group, l.NB, l.chunks, at(l.states), at(l.reach), at(l.hs), at(l.gs),
+                  at(l.width), at(l.part), d.gA ? at(l.pA) : nullptr, d.gD ? at(l.pD) : nullptr, d.gbias ? at(l.pb) : nullptr};
+  auto by_states = [&](auto bf16) {
+    switch (l.NB) {
+      case 1: return launch<bf16, 1>(p, st);
+      case 2: return launch<bf16, 2>(p, st);
+      case 3: return launch<bf16, 3>(p, st);
+      default: return launch<bf16, 4>(p, st);
+    }
+  };
+  a.bf16 ? by_states(std::true_type{}) : by_states(std::false_type{});
+  auto rows = [&](const float* part, size_t n, float* out) {
+    if (out) row_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, (int64_t)a.B * l.seg.S, n, out);
+  };
+  rows(p.pA, (size_t)a.E * a.N, d.gA);
+  rows(p.pD, a.E, d.gD);
+  rows(p.pb, a.E, d.gbias);
   return hipGetLastError();
 }
 

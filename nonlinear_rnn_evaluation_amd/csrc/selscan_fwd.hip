@@ -25,11 +25,6 @@ struct FwdArgs {
   float *sums, *width;       // [B, S, E, 4 R] states and [B, S, E] summed step widths of the segments
 };
 
-template <int kCtrl>
-__device__ __forceinline__ float quad_perm(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xf, 0xf, true));
-}
-
 // B and C of four tokens, this lane's states.
 template <bool kOut, int R>
 struct Four {

@@ -39,6 +39,11 @@ __device__ __forceinline__ float from_slots(const float (&s)[4]) {
   return (s[0] + away<3>(s[1])) + (away<2>(s[2]) + away<1>(s[3]));
 }
 
+template <int kCtrl>
+__device__ __forceinline__ float quad_perm(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kCtrl, 0xf, 0xf, true));
+}
+
 // A for exponents of 2, finite where A is: a step width of 0 leaves the state.
 __device__ __forceinline__ float exponent(float A) {
   const float x = A * kLog2e;
