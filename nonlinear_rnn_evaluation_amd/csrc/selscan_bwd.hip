@@ -41,7 +41,7 @@ struct BwdArgs {
 struct Place {
   Tile w;
   int seg, lane, nq, e, n0;        // n0: this lane's first state
-  int ch[4];
+  int ch[4], off[4];               // the slots' channels (-1: none), and their states' offsets
   bool live;
 };
 
@@ -57,9 +57,10 @@ __device__ __forceinline__ Place place(const BwdArgs& p) {
   x.lane = threadIdx.x & 63, x.nq = x.lane >> 2 & 3;
   x.live = x.lane < x.w.live;
   x.e = x.w.e0 + min(x.lane, x.w.live - 1);
-  x.n0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 16 + x.nq * R;
-  // a lane without a channel gets E - 1's numbers and is kept from storing; its slots hold zeros
+  x.n0 = (NB > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 16 : 0) + x.nq * R;
   x.ch[0] = x.live ? x.e : -1, x.ch[1] = away<1>(x.ch[0]), x.ch[2] = away<2>(x.ch[0]), x.ch[3] = away<3>(x.ch[0]);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x.off[r] = x.ch[r] >= 0 ? (x.ch[r] * (16 * NB) + x.n0) * 4 : kNowhere;
   return x;
 }
 
@@ -70,60 +71,68 @@ __device__ __forceinline__ void load_A(const SelScan& a, const Place& x, float (
     for (int i = 0; i < R; ++i) A[r][i] = x.ch[r] >= 0 && x.n0 + i < a.N ? exponent(a.A[(size_t)x.ch[r] * a.N + x.n0 + i]) : 0.0f;
 }
 
-// Four states of each slot from, or to, [.., E, 16 NB] at row `row` of E channels.
-__device__ __forceinline__ void load_states(const float* p, size_t row, const BwdArgs& q, const Place& x, float (&h)[4][R]) {
+// Four states of each slot from, or to, [.., E, 16 NB] at row `row` of E channels.  A slot without a channel
+// reads zeros and writes nowhere.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void load_states(const float* p, size_t row, const BwdArgs& q, const Place& x, f32x4 (&h)[4]) {
+  const __amdgpu_buffer_rsrc_t from = buffer_of(p + row * q.a.E * (16 * q.NB), true);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    f32x4 v{0, 0, 0, 0};
-    if (x.ch[r] >= 0) v = *(const f32x4*)(p + (row * q.a.E + x.ch[r]) * (16 * q.NB) + x.n0);
-#pragma unroll
-    for (int i = 0; i < R; ++i) h[r][i] = v[i];
-  }
+  for (int r = 0; r < 4; ++r) h[r] = __builtin_bit_cast(f32x4, (u32x4)__builtin_amdgcn_raw_buffer_load_b128(from, x.off[r], 0, 0));
 }
 __device__ __forceinline__ void store_states(float* p, size_t row, const BwdArgs& q, const Place& x, const float (&h)[4][R]) {
+  const __amdgpu_buffer_rsrc_t to = buffer_of(p + row * q.a.E * (16 * q.NB), true);
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    if (x.ch[r] >= 0) *(f32x4*)(p + (row * q.a.E + x.ch[r]) * (16 * q.NB) + x.n0) = f32x4{h[r][0], h[r][1], h[r][2], h[r][3]};
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{h[r][0], h[r][1], h[r][2], h[r][3]}), to, x.off[r], 0, 0);
 }
 
-// B and C of a chunk, this wave's 16 states: [token][B, C][16], zeros beyond `end` and the states.
+// B and C of a chunk, this wave's 16 states: [token][B, C][16], zeros beyond `end` and the states.  A lane
+// takes every second token's B or C of one state; what is not there is read elsewhere and dropped.
 template <bool kBf16>
 struct Chunk {
   using El = Elem<kBf16>;
   using T = typename El::type;
-  T raw[kChunk * 32 / 64];
-  __device__ __forceinline__ void fetch(const BwdArgs& p, const Place& x, int t, int end) {
-    const SelScan& a = p.a;
-    const T* B = (const T*)a.Bt.p + x.w.b * a.Bt.sb + x.w.g * a.Bt.sh;
-    const T* C = (const T*)a.Ct.p + x.w.b * a.Ct.sb + x.w.g * a.Ct.sh;
-    const int n = (x.n0 & ~15) + (x.lane & 15), which = x.lane >> 4 & 1;
-#pragma unroll
-    for (int k = 0; k < kChunk * 32 / 64; ++k) {
-      const int64_t tok = t + 2 * k + (x.lane >> 5);
-      raw[k] = 0;
-      if (n < a.N && tok < end) raw[k] = which ? C[tok * a.Ct.st + n] : B[tok * a.Bt.st + n];
-    }
+  static constexpr int kEach = kChunk * 32 / 64;
+  T raw[kEach];
+  const T* from;
+  int64_t st;
+  int half;
+  bool state;
+  __device__ __forceinline__ void start(const SelScan& a, const Place& x) {
+    const int n = (x.n0 & ~15) + (x.lane & 15);
+    const Rows& r = x.lane >> 4 & 1 ? a.Ct : a.Bt;
+    state = n < a.N;
+    from = (const T*)r.p + x.w.b * r.sb + x.w.g * r.sh + (state ? n : 0);
+    st = r.st, half = x.lane >> 5;
   }
-  __device__ __forceinline__ void put(float* lds, int lane) const {
+  __device__ __forceinline__ void fetch(int t, int end) {       // end: of the row's segment, behind t
 #pragma unroll
-    for (int k = 0; k < kChunk * 32 / 64; ++k) lds[k * 64 + lane] = El::load(&raw[k]);
+    for (int k = 0; k < kEach; ++k) raw[k] = from[min(t + 2 * k + half, end - 1) * st];
+  }
+  __device__ __forceinline__ void put(float* lds, int lane, int t, int end) const {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) lds[k * 64 + lane] = state && t + 2 * k + half < end ? El::load(&raw[k]) : 0.0f;
   }
 };
 
-// The channels' own values of tokens t.., by the lanes that own them; zeros where there is no token or channel.
+// A [B, T, E] operand, by the lanes that own its channels: a buffer from a chunk's first token on, tokens as
+// 32-bit offsets (the entry points keep wide strides away).  Lanes without a channel read zeros.
 template <bool kBf16>
 struct Operand {
   using T = typename Elem<kBf16>::type;
-  const T* p;
+  const T* row;
   int64_t st;
   int off;
-  __device__ __forceinline__ T get(int t, bool there) const { return load_buffer<T>(buffer_of(p + t * st, there), off, 0); }
+  bool given;
+  __amdgpu_buffer_rsrc_t buf;
+  __device__ __forceinline__ Operand(const void* p, int64_t sb, int64_t stride, const Place& x)
+      : row((const T*)p + (p ? x.w.b * sb : 0)), st(stride), off(x.live ? x.e * (int)sizeof(T) : kNowhere), given(p) {}
+  __device__ __forceinline__ void rebase(int t) { buf = buffer_of(row + (given ? t * st : 0), given); }
+  __device__ __forceinline__ T get(int k) const { return load_buffer<T>(buf, off, k * (int)st * (int)sizeof(T)); }
+  __device__ __forceinline__ void set(int k, bool there, float v) const {
+    store_buffer<kBf16>(v, buf, there ? off : kNowhere, k * (int)st * (int)sizeof(T));
+  }
 };
-template <bool kBf16>
-__device__ __forceinline__ Operand<kBf16> operand(const void* p, int64_t sb, int64_t st, const Place& x) {
-  using T = typename Elem<kBf16>::type;
-  return {p ? (const T*)p + x.w.b * sb : nullptr, st, x.live ? x.e * (int)sizeof(T) : kNowhere};
-}
 
 template <bool kBf16, int NB, bool kCut>
 __global__ void __launch_bounds__(NB * 64, 2) local_kernel(BwdArgs p) {
@@ -134,7 +143,7 @@ __global__ void __launch_bounds__(NB * 64, 2) local_kernel(BwdArgs p) {
   const Place x = place<NB>(p);
   const int n = row_len(a.lens, x.w.b, a.T), t0 = x.seg * p.seg.len, t1 = min(t0 + p.seg.len, n);
   if (t0 >= t1) return;
-  const int sb = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sb = NB > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   float(*bc)[kChunk * 32] = bc_all[sb];
   float A[4][R], h[4][R] = {}, P[4][R], G[4][R] = {};
   load_A(a, x, A);
@@ -143,48 +152,62 @@ __global__ void __launch_bounds__(NB * 64, 2) local_kernel(BwdArgs p) {
 #pragma unroll
     for (int i = 0; i < R; ++i) P[r][i] = 1.0f;
   const float bias = a.bias ? a.bias[x.e] : 0.0f;
-  const auto u = operand<kBf16>(a.u.p, a.u.sb, a.u.st, x), dt = operand<kBf16>(a.dt.p, a.dt.sb, a.dt.st, x),
-             z = operand<kBf16>(a.z.p, a.z.sb, a.z.st, x), gy = operand<kBf16>(p.d.gy, (int64_t)a.T * a.E, a.E, x);
+  Operand<kBf16> u(a.u.p, a.u.sb, a.u.st, x), dt(a.dt.p, a.dt.sb, a.dt.st, x), z(kCut ? a.z.p : nullptr, a.z.sb, a.z.st, x),
+      gy(p.d.gy, (int64_t)a.T * a.E, a.E, x);
   T ur[kFour], dr[kFour], zr[kFour], gr[kFour];
-  auto fetch = [&](int t) {
+  int end = 0;                                   // of the row's segment, from the chunk's start
+  auto fetch = [&](int k0) {                     // a token behind the end is the last one again
 #pragma unroll
     for (int k = 0; k < kFour; ++k) {
-      const bool there = t + k < t1;
-      ur[k] = u.get(t + k, there), dr[k] = dt.get(t + k, there);
-      if (kCut) zr[k] = z.get(t + k, there && a.z.p), gr[k] = gy.get(t + k, there);
+      const int at = min(k0 + k, end - 1);
+      ur[k] = u.get(at), dr[k] = dt.get(at);
+      if (kCut) zr[k] = z.get(at), gr[k] = gy.get(at);
     }
+  };
+  auto rebase = [&](int t) {
+    u.rebase(t), dt.rebase(t), end = t1 - t;
+    if (kCut) z.rebase(t), gy.rebase(t);
   };
   float total = 0.0f;
   Chunk<kBf16> stage;
-  stage.fetch(p, x, t0, t1);
-  fetch(t0);
+  stage.start(a, x);
+  stage.fetch(t0, t1);
+  rebase(t0);
+  fetch(0);
   int buf = 0;
   for (int t = t0; t < t1; t += kChunk, buf ^= 1) {
-    stage.put(bc[buf], x.lane);
+    stage.put(bc[buf], x.lane, t, t1);
     const size_t row = (size_t)x.w.b * p.chunks + t / kChunk;
     if (t > t0) {
       store_states(p.states, row, p, x, h);
       if (sb == 0 && x.live) p.reach[row * a.E + x.e] = total;
     }
     if (!kCut && t + kChunk >= t1) break;        // the last chunk's end is nobody's start
-    stage.fetch(p, x, t + kChunk, t1);
+    stage.fetch(min(t + kChunk, t1 - 1), t1);
     __builtin_amdgcn_wave_barrier();             // a wave reads what it staged itself
     for (int f = 0; f < kChunk && t + f < t1; f += kFour) {
+      const int left = t1 - t - f;
       float uv[kFour], dv[kFour], zv[kFour], gv[kFour];
 #pragma unroll
       for (int k = 0; k < kFour; ++k) {
         uv[k] = El::load(&ur[k]), dv[k] = El::load(&dr[k]);
         if (kCut) zv[k] = El::load(&zr[k]), gv[k] = El::load(&gr[k]);
       }
-      fetch(t + f + kFour);
+      if (f + kFour == kChunk) {
+        rebase(min(t + kChunk, t1 - 1));
+        fetch(0);
+      } else {
+        fetch(f + kFour);
+      }
 #pragma unroll
       for (int k = 0; k < kFour; ++k) {
-        const float delta = step_width(dv[k] + bias, a.softplus, x.live && t + f + k < t1);
+        const bool there = k < left;
+        const float delta = step_width(dv[k] + bias, a.softplus, x.live && there);
         total += delta;
         float d[4], s[4], g[4];
         to_slots(delta, d);
-        to_slots(delta * uv[k], s);
-        if (kCut) to_slots(gv[k] * gate_of(zv[k], a.z.p), g);
+        to_slots(there ? delta * uv[k] : 0.0f, s);
+        if (kCut) to_slots(there ? gv[k] * gate_of(zv[k], a.z.p) : 0.0f, g);
         const float* at = bc[buf] + (f + k) * 32 + x.nq * R + (x.lane & 3);
         const float b = at[0], c = at[16];
 #pragma unroll
@@ -201,7 +224,10 @@ __global__ void __launch_bounds__(NB * 64, 2) local_kernel(BwdArgs p) {
 #pragma unroll
           for (int i = 0; i < R; ++i) {
             h[r][i] = v[i];
-            if (kCut) G[r][i] = fmaf(P[r][i], w[i], G[r][i]);
+            if (kCut) {
+              G[r][i] = fmaf(P[r][i], w[i], G[r][i]);
+              asm volatile("" : "+v"(G[r][i]));     // here, not behind the loop's branches with all its factors waiting
+            }
           }
         }
       }
@@ -290,7 +316,7 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
   const SelScanGrads& d = p.d;
   const Place x = place<NB>(p);
   const int n = row_len(a.lens, x.w.b, a.T), t0 = x.seg * p.seg.len, tend = min(t0 + p.seg.len, a.T), t1 = min(tend, n);
-  const int sb = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sb = NB > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   float* bc = bc_all[sb];
   auto& mid = mid_all[sb];
   const size_t seg_row = (size_t)x.w.b * p.seg.S + x.seg;
@@ -307,53 +333,67 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
   float dD = 0.0f, db = 0.0f;
   if (t0 < t1) {
     load_A(a, x, A);
-    load_states(p.gs, seg_row, p, x, g);
+    f32x4 back[4];
+    load_states(p.gs, seg_row, p, x, back);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < R; ++i) g[r][i] = back[r][i];
     const float bias = a.bias ? a.bias[x.e] : 0.0f, D = a.D ? a.D[x.e] : 0.0f;
-    const auto u = operand<kBf16>(a.u.p, a.u.sb, a.u.st, x), dt = operand<kBf16>(a.dt.p, a.dt.sb, a.dt.st, x),
-               z = operand<kBf16>(a.z.p, a.z.sb, a.z.st, x), gy = operand<kBf16>(d.gy, (int64_t)a.T * a.E, a.E, x);
+    Operand<kBf16> u(a.u.p, a.u.sb, a.u.st, x), dt(a.dt.p, a.dt.sb, a.dt.st, x), z(a.z.p, a.z.sb, a.z.st, x),
+        gy(d.gy, (int64_t)a.T * a.E, a.E, x), ou(d.gu, (int64_t)a.T * a.E, a.E, x), od(d.gdt, (int64_t)a.T * a.E, a.E, x),
+        oz(d.gz, (int64_t)a.T * a.E, a.E, x);
     const bool gated = a.z.p;
-    const int at = x.live ? x.e * (int)sizeof(T) : kNowhere;
     float* part = p.part + (((size_t)x.w.b * a.T) * p.tiles + x.w.g * p.per_group + (x.w.e0 - x.w.g * (a.E / a.G)) / kChannels) * 32 * NB;
     const int part_at = (x.lane & 2) ? kNowhere
                                      : ((x.lane >> 5) * 16 * NB + sb * 16 + x.nq * 4 + (x.lane >> 4 & 1) + 2 * (x.lane & 1)) * 4;
     const float* reach = p.reach + x.e;
     int turn = 0;
     T ur[kFour], dr[kFour], zr[kFour], gr[kFour];
-    auto fetch = [&](int t, bool any) {
+    auto fetch = [&](int k0, int end) {          // a token behind the end is the last one again
 #pragma unroll
       for (int k = 0; k < kFour; ++k) {
-        const bool there = any && t + k < t1;
-        ur[k] = u.get(t + k, there), dr[k] = dt.get(t + k, there);
-        zr[k] = z.get(t + k, there && gated), gr[k] = gy.get(t + k, there);
+        const int at = min(k0 + k, end - 1);
+        ur[k] = u.get(at), dr[k] = dt.get(at), zr[k] = z.get(at), gr[k] = gy.get(at);
       }
+    };
+    T us[kFour], ds[kFour];
+    auto fetch_ahead = [&](int k0, int end) {
+#pragma unroll
+      for (int k = 0; k < kFour; ++k) us[k] = u.get(min(k0 + k, end - 1)), ds[k] = dt.get(min(k0 + k, end - 1));
+    };
+    auto begin = [&](int c, f32x4 (&own)[4], f32x4 (&entry)[4], float& added) {     // what a chunk starts from
+      const int tc = t0 + c * kChunk, end = min(kChunk, t1 - tc);
+      u.rebase(tc), dt.rebase(tc), z.rebase(tc), gy.rebase(tc);
+      load_states(p.hs, seg_row, p, x, entry);
+      const size_t row = (size_t)x.w.b * p.chunks + tc / kChunk;
+      load_states(p.states, row, p, x, own);
+      added = reach[row * a.E];
+      fetch((end - 1) / kFour * kFour, end);
+      fetch_ahead(0, end);
     };
     Chunk<kBf16> stage;
     const int last = (t1 - 1 - t0) / kChunk;
-    stage.fetch(p, x, t0 + last * kChunk, t1);
+    stage.start(a, x);
+    stage.fetch(t0 + last * kChunk, t1);
     for (int c = last; c >= 0; --c) {
-      const int tc = t0 + c * kChunk, fours = (min(tc + kChunk, t1) - tc + kFour - 1) / kFour;
-      // the state at the chunk's start: the segment's, decayed, and what the segment added
-      float h[4][R];
-      load_states(p.hs, seg_row, p, x, h);
-      if (c > 0) {
-        const size_t row = (size_t)x.w.b * p.chunks + tc / kChunk;
-        float own[4][R], w[4];
-        load_states(p.states, row, p, x, own);
-        to_slots(x.live ? reach[row * a.E] : 0.0f, w);
+      const int tc = t0 + c * kChunk, end = min(kChunk, t1 - tc), fours = (end + kFour - 1) / kFour;
+      ou.rebase(tc), od.rebase(tc), oz.rebase(tc);
+      const __amdgpu_buffer_rsrc_t out_part = buffer_of(part + (size_t)tc * p.tiles * 32 * NB, true);
+      const int part_step = p.tiles * 32 * NB * 4;
+      // the state at the chunk's start: the segment's, decayed, and what the segment added (the first chunk's
+      // place in `states` and `reach` holds nothing)
+      f32x4 own[4], entry[4];
+      float h[4][R], w[4], added;
+      begin(c, own, entry, added);
+      to_slots(x.live && c > 0 ? added : 0.0f, w);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int i = 0; i < R; ++i) h[r][i] = fmaf(h[r][i], __builtin_amdgcn_exp2f(w[r] * A[r][i]), own[r][i]);
-      }
-      fetch(tc + (fours - 1) * kFour, true);
-      T us[kFour], ds[kFour];
-      auto fetch_ahead = [&](int f) {
-#pragma unroll
-        for (int k = 0; k < kFour; ++k) us[k] = u.get(tc + f * kFour + k, f < fours - 1), ds[k] = dt.get(tc + f * kFour + k, f < fours - 1);
-      };
-      fetch_ahead(0);
-      stage.put(bc, x.lane);
-      if (c > 0) stage.fetch(p, x, tc - kChunk, t1);
+        for (int i = 0; i < R; ++i)
+          h[r][i] = fmaf(entry[r][i], __builtin_amdgcn_exp2f(w[r] * A[r][i]), c > 0 ? own[r][i] : 0.0f);
+      stage.put(bc, x.lane, tc, t1);
+      if (c > 0) stage.fetch(tc - kChunk, t1);
       __builtin_amdgcn_wave_barrier();
       const float* lane_bc = bc + x.nq * R;
       auto keep = [&](int f) {
@@ -367,7 +407,7 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
         float uv[kFour], dv[kFour];
 #pragma unroll
         for (int k = 0; k < kFour; ++k) uv[k] = El::load(&us[k]), dv[k] = El::load(&ds[k]);
-        fetch_ahead(f + 1);
+        fetch_ahead((f + 1) * kFour, end);
 #pragma unroll
         for (int k = 0; k < kFour; ++k) {
           const float delta = step_width(dv[k] + bias, a.softplus, x.live);
@@ -380,12 +420,13 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
       }
 #pragma unroll 1
       for (int f = fours - 1; f >= 0; --f) {
-        const int t = tc + f * kFour;
+        const int k0 = f * kFour;
         float uv[kFour], raw[kFour], zv[kFour], gv[kFour], delta[kFour];
 #pragma unroll
         for (int k = 0; k < kFour; ++k) {
-          uv[k] = El::load(&ur[k]), raw[k] = El::load(&dr[k]) + bias, zv[k] = El::load(&zr[k]), gv[k] = El::load(&gr[k]);
-          delta[k] = step_width(raw[k], a.softplus, x.live && t + k < t1);
+          const bool there = k0 + k < end;
+          uv[k] = there ? El::load(&ur[k]) : 0.0f, raw[k] = El::load(&dr[k]) + bias, zv[k] = El::load(&zr[k]);
+          gv[k] = there ? El::load(&gr[k]) : 0.0f, delta[k] = step_width(raw[k], a.softplus, x.live && there);
         }
         // forwards: states before each token, and decays
         float hist[kFour + 1][4][R], dec[kFour][4][R];
@@ -400,7 +441,7 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
           float dl[4], s[4];
           to_slots(delta[k], dl);
           to_slots(delta[k] * uv[k], s);
-          const float b = lane_bc[(f * kFour + k) * 32 + (x.lane & 3)];
+          const float b = lane_bc[(k0 + k) * 32 + (x.lane & 3)];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             f32x4 v;
@@ -417,9 +458,22 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
         __builtin_amdgcn_sched_barrier(0);
         // and back
         float ys[kFour], qs[kFour], ws[kFour];
+        auto finish = [&](int k) {                // a token's gradients, from the sums over all states
+          const bool there = k0 + k < end;
+          const float sg = sigm(zv[k]), gated_gy = gated ? gv[k] * zv[k] * sg : gv[k];
+          const float y = fmaf(D, uv[k], ys[k]), gd = fmaf(uv[k], qs[k], kLn2 * ws[k]);
+          float slope = sigm(raw[k]);
+          asm volatile("" : "+v"(slope));         // no branch between tokens
+          const float gt = a.softplus ? gd * slope : gd;
+          dD = fmaf(gated_gy, uv[k], dD);
+          db += there ? gt : 0.0f;
+          ou.set(k0 + k, there, fmaf(D, gated_gy, delta[k] * qs[k]));
+          od.set(k0 + k, there, gt);
+          oz.set(k0 + k, there, gv[k] * y * sg * (1.0f + zv[k] * (1.0f - sg)));
+        };
 #pragma unroll
         for (int k = kFour - 1; k >= 0; --k) {
-          const float* s = lane_bc + (f * kFour + k) * 32;
+          const float* s = lane_bc + (k0 + k) * 32;
           float Bv[R], Cv[R], dl[4], xs[4], gs[4], ya[4], qa[4], wa[4], dB[R] = {}, dC[R] = {};
           read_states<R>(s, Bv);
           read_states<R>(s + 16, Cv);
@@ -433,25 +487,39 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
             v = __builtin_amdgcn_mfma_f32_4x4x1f32(cl, gs[r], v, 0, 0, 0);
             ya[r] = qa[r] = wa[r] = 0.0f;
 #pragma unroll
+            for (int i = 0; i < R; ++i) g[r][i] = v[i];
+          }
+          if (k == 0) {                            // the four's first states, read again
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const f32x4 v = mid[f][r][x.lane];
+#pragma unroll
+              for (int i = 0; i < R; ++i) hist[0][r][i] = v[i];
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+#pragma unroll
             for (int i = 0; i < R; ++i) {
-              const float hn = hist[k + 1][r][i];
+              const float hn = hist[k + 1][r][i], gn = g[r][i];
               ya[r] = fmaf(hn, Cv[i], ya[r]);
               dC[i] = fmaf(gs[r], hn, dC[i]);
-              dB[i] = fmaf(xs[r], v[i], dB[i]);
-              qa[r] = fmaf(v[i], Bv[i], qa[r]);
-              g[r][i] = v[i] * dec[k][r][i];
+              dB[i] = fmaf(xs[r], gn, dB[i]);
+              qa[r] = fmaf(gn, Bv[i], qa[r]);
+              g[r][i] = gn * dec[k][r][i];
               const float through = g[r][i] * hist[k][r][i];
               wa[r] = fmaf(through, A[r][i], wa[r]);
               dA[r][i] = fmaf(through, dl[r], dA[r][i]);
+              asm volatile("" : "+v"(dA[r][i]));    // here, not behind the loop's branches, where 64 products wait for it
             }
           }
           ys[k] = from_slots(ya), qs[k] = from_slots(qa), ws[k] = from_slots(wa);
           const float o = over_channels(dB, dC, x.lane);
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), buffer_of(part + (size_t)(t + k) * p.tiles * 32 * NB, t + k < t1), part_at, 0, 0);
-          if (k == 2) fetch(t - kFour, f > 0);  // two tokens' states and decays are done with
-          __builtin_amdgcn_sched_barrier(0);     // one token's values at a time in registers
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), out_part, k0 + k < end ? part_at : kNowhere, (k0 + k) * part_step, 0);
+          if constexpr (NB == 1) finish(k);
+          if (k == 1) fetch(f > 0 ? k0 - kFour : 0, end);     // three tokens' states and decays are done with  // two tokens' states and decays are done with
         }
-        // the tokens' gradients, from the sums over all states
         if constexpr (NB > 1) {
 #pragma unroll
           for (int k = 0; k < kFour; ++k) sums[turn][sb][0][k][x.lane] = ys[k], sums[turn][sb][1][k][x.lane] = qs[k], sums[turn][sb][2][k][x.lane] = ws[k];
@@ -464,20 +532,10 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
                 ys[k] += sums[turn][j][0][k][x.lane], qs[k] += sums[turn][j][1][k][x.lane], ws[k] += sums[turn][j][2][k][x.lane];
           turn ^= 1;
         }
-        if (sb == 0) {
+        if constexpr (NB > 1)
+          if (sb == 0)
 #pragma unroll
-          for (int k = 0; k < kFour; ++k) {
-            const bool there = t + k < t1;
-            const float sg = sigm(zv[k]), gated_gy = gated ? gv[k] * zv[k] * sg : gv[k];
-            const float y = fmaf(D, uv[k], ys[k]), gd = fmaf(uv[k], qs[k], kLn2 * ws[k]);
-            const float gt = a.softplus ? gd * sigm(raw[k]) : gd;
-            dD = fmaf(gated_gy, uv[k], dD);
-            db += there ? gt : 0.0f;
-            if (gu) store_buffer<kBf16>(fmaf(D, gated_gy, delta[k] * qs[k]), buffer_of(gu + (size_t)(t + k) * a.E, there), at, 0);
-            if (gdt) store_buffer<kBf16>(gt, buffer_of(gdt + (size_t)(t + k) * a.E, there), at, 0);
-            if (gz) store_buffer<kBf16>(gv[k] * y * sg * (1.0f + zv[k] * (1.0f - sg)), buffer_of(gz + (size_t)(t + k) * a.E, there), at, 0);
-          }
-        }
+            for (int k = 0; k < kFour; ++k) finish(k);
       }
     }
     if (p.seg.S == 1 && d.gstate_in)
