@@ -76,13 +76,13 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
         if (c % L == 0) p.exps[exp_at] = (uint8_t)s;
       }
     } else if (live) {
-      const int s = p.exps[exp_at];
+      const float step = unpack_step(p.exps[exp_at]);
       int8_t q[kV];
       __builtin_memcpy(q, __builtin_assume_aligned(p.codes + at, kV), kV);
       T* out = (T*)p.out + at;
       T raw[kV];
 #pragma unroll
-      for (int k = 0; k < kV; ++k) El::store(&raw[k], unpack_code(q[k], s));
+      for (int k = 0; k < kV; ++k) El::store(&raw[k], q[k] * step);
       __builtin_memcpy(__builtin_assume_aligned(out, sizeof(T) * kV > 16 ? 16 : sizeof(T) * kV), raw, sizeof(raw));
     }
   }

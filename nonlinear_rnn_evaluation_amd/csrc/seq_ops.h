@@ -159,10 +159,8 @@ __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(w), kLn2, e - (w - 1.0f));
 }
 
-// The value of an 8-bit copy's code on exponent byte s (255: not finite).
-__device__ __forceinline__ float unpack_code(int code, int s) {
-  return s == 255 ? __uint_as_float(0x7fc00000u) : ldexpf((float)code, s - 127);
-}
+// What a code of an 8-bit copy counts on exponent byte s: 2^(s - 127), s >= 1; NaN on 255 (not finite).
+__device__ __forceinline__ float unpack_step(int s) { return __uint_as_float(s == 255 ? 0x7fc00000u : (uint32_t)s << 23); }
 
 __device__ __forceinline__ int row_len(const int32_t* lens, int b, int T) {
   if (!lens) return T;
