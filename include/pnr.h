@@ -574,7 +574,7 @@ int pnr_groupnorm_backward(const pnr_norm* desc, const void* x, const float* wei
  *               row's end is not read, its outputs and gradients are zeros, and the state is the one
  *               after the row's last token (an empty row hands state_in on)
  * Supported: dtype PNR_F32 and PNR_BF16, 1 <= N <= 64 (others PNR_E_UNSUPPORTED), G divides E,
- * E <= 2^20, T <= 2^30, B G ceil(E / G / 64) <= 4 million; token strides of u, dt and z up to 2^23
+ * E <= 2^20, T <= 2^30, G ceil(E / G / 64) <= 65536, B times that <= 4 million; token strides of u, dt and z up to 2^23
  * (others PNR_E_UNSUPPORTED).  Everything inside is fp32; outputs of `dtype` are rounded once, at the
  * end.
  *

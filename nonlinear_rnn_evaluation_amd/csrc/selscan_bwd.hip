@@ -242,14 +242,10 @@ __global__ void __launch_bounds__(NB * 64, 2) local_kernel(BwdArgs p) {
 
 // The recurrences over a row's segments: in place of a segment's sums its first state, and the gradient
 // that reaches its last state from behind.  A thread a state; eight segments are asked for at once.
-__global__ void __launch_bounds__(256) join_kernel(BwdArgs p) {
+__device__ __forceinline__ void join_state(const BwdArgs& p, int s, int e, int b, int NP) {
   constexpr int kBatch = 8;
   const SelScan& a = p.a;
-  const int NP = 16 * p.NB;
-  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-  if (i >= (int64_t)a.B * a.E * NP) return;
-  const int s = (int)(i % NP), e = (int)(i / NP % a.E), b = (int)(i / NP / a.E);
-  const int n = row_len(a.lens, b, a.T), segs = (n + p.seg.len - 1) / p.seg.len;
+  const int n = row_len(a.lens, b, a.T), segs = (int)(((int64_t)n + p.seg.len - 1) / p.seg.len);
   const bool real = s < a.N;
   const float A = real ? exponent(a.A[(size_t)e * a.N + s]) : 0.0f;
   const size_t at = ((size_t)b * a.E + e) * a.N + s, row = (size_t)b * p.seg.S * a.E + e;
@@ -281,6 +277,12 @@ __global__ void __launch_bounds__(256) join_kernel(BwdArgs p) {
     p.gs[row * NP + s] = g;
     if (real && p.d.gstate_in && segs == 0) p.d.gstate_in[at] = g;
   }
+}
+
+__global__ void __launch_bounds__(256) join_kernel(BwdArgs p) {
+  const int NP = 16 * p.NB, E = p.a.E;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < (int64_t)p.a.B * E * NP; i += (int64_t)gridDim.x * 256)
+    join_state(p, (int)(i % NP), (int)(i / NP % E), (int)(i / NP / E), NP);
 }
 
 // Sums of dB and dC over the wave's channels (lane bits 0, 1, 4 and 5): the halves of the wave take one
@@ -607,8 +609,8 @@ Layout layout(const SelScan& a) {
   int64_t S = 1;
   if (waves < 2048) S = std::min<int64_t>((a.T + kChunk - 1) / kChunk, (4096 + waves - 1) / waves);
   S = std::max<int64_t>(S, 1);
-  const int len = std::max(kChunk, (int)(((a.T + S - 1) / S + kChunk - 1) / kChunk * kChunk));
-  l.seg = {std::max(1, (a.T + len - 1) / len), len};
+  const int64_t len = std::max<int64_t>(kChunk, ((a.T + S - 1) / S + kChunk - 1) / kChunk * kChunk);
+  l.seg = {(int)std::max<int64_t>(1, (a.T + len - 1) / len), (int)len};
   l.chunks = (a.T + kChunk - 1) / kChunk;
   size_t at = 0;
   auto take = [&](size_t floats) {
@@ -634,7 +636,7 @@ void launch(const BwdArgs& p, hipStream_t st) {
     local_kernel<kBf16, NB, true><<<blocks, NB * 64, 0, st>>>(p);
   else if (a.T > kChunk)
     local_kernel<kBf16, NB, false><<<blocks, NB * 64, 0, st>>>(p);
-  join_kernel<<<(unsigned)(((int64_t)a.B * a.E * 16 * NB + 255) / 256), 256, 0, st>>>(p);
+  join_kernel<<<(unsigned)std::min<int64_t>(((int64_t)a.B * a.E * 16 * NB + 255) / 256, 1 << 22), 256, 0, st>>>(p);
   walk_kernel<kBf16, NB><<<blocks, NB * 64, 0, st>>>(p);
   if ((p.d.gB || p.d.gC) && a.T > 0)
     token_kernel<kBf16><<<(unsigned)std::min<int64_t>(((int64_t)a.B * a.T * a.G * 32 * NB + 255) / 256, 1 << 20), 256, 0, st>>>(p);

@@ -191,13 +191,10 @@ __global__ void __launch_bounds__(kW * 64, 1) scan_kernel(FwdArgs p) {
 
 // The recurrence over a row's segments: each segment's first state in place of its sum, and the last
 // state.  A thread a state; eight segments' sums are asked for before the first is used.
-__global__ void __launch_bounds__(256) join_kernel(FwdArgs p, int NP) {
+__device__ __forceinline__ void join_state(const FwdArgs& p, int s, int e, int b, int NP) {
   constexpr int kBatch = 8;
   const SelScan& a = p.a;
-  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-  if (i >= (int64_t)a.B * a.E * NP) return;
-  const int s = (int)(i % NP), e = (int)(i / NP % a.E), b = (int)(i / NP / a.E);
-  const int n = row_len(a.lens, b, a.T), segs = (n + p.seg.len - 1) / p.seg.len;
+  const int n = row_len(a.lens, b, a.T), segs = (int)(((int64_t)n + p.seg.len - 1) / p.seg.len);
   const bool real = s < a.N;
   const float A = real ? exponent(a.A[(size_t)e * a.N + s]) : 0.0f;
   const size_t at = ((size_t)b * a.E + e) * a.N + s;
@@ -218,6 +215,12 @@ __global__ void __launch_bounds__(256) join_kernel(FwdArgs p, int NP) {
       }
   }
   if (p.s_out && real) p.s_out[at] = h;
+}
+
+__global__ void __launch_bounds__(256) join_kernel(FwdArgs p, int NP) {
+  const SelScan& a = p.a;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < (int64_t)a.B * a.E * NP; i += (int64_t)gridDim.x * 256)
+    join_state(p, (int)(i % NP), (int)(i / NP % a.E), (int)(i / NP / a.E), NP);
 }
 
 int states_of(const SelScan& a) {
@@ -248,8 +251,8 @@ Plan plan_of(const SelScan& a) {
   const int64_t enough = a.lens ? 4096 : 1024, target = a.lens ? 16384 : 8192;
   int64_t S = 1;
   if (waves < enough && a.T > 128) S = std::min<int64_t>((a.T + 31) / 32, (target + waves - 1) / waves);
-  const int len = std::max(32, (int)((a.T + S - 1) / S + 31) / 32 * 32);
-  p.seg = {std::max(1, (a.T + len - 1) / len), len};
+  const int64_t len = std::max<int64_t>(32, ((a.T + S - 1) / S + 31) / 32 * 32);
+  p.seg = {(int)std::max<int64_t>(1, (a.T + len - 1) / len), (int)len};
   return p;
 }
 
@@ -270,7 +273,7 @@ void launch_pass(const FwdArgs& p, hipStream_t st) {
   const unsigned blocks = (unsigned)(p.tiles * p.seg.S);
   if (p.seg.S > 1) {
     scan_kernel<kBf16, R, kW, true><<<blocks, kW * 64, 0, st>>>(p);
-    join_kernel<<<(unsigned)(((int64_t)p.a.B * p.a.E * 4 * R + 255) / 256), 256, 0, st>>>(p, 4 * R);
+    join_kernel<<<(unsigned)std::min<int64_t>(((int64_t)p.a.B * p.a.E * 4 * R + 255) / 256, 1 << 22), 256, 0, st>>>(p, 4 * R);
   }
   scan_kernel<kBf16, R, kW, false><<<blocks, kW * 64, 0, st>>>(p);
 }

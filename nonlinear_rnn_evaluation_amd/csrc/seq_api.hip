@@ -143,8 +143,9 @@ int validate(const pnr_selscan* d, bool step) {
   if (!step && d->T > 1 && (d->u_stride[1] > kMaxTokenStride || d->dt_stride[1] > kMaxTokenStride || d->z_stride[1] > kMaxTokenStride))
     return record_error(PNR_E_UNSUPPORTED, "token strides up to %d elements are supported", kMaxTokenStride);
   if (d->N > kMaxStates) return record_error(PNR_E_UNSUPPORTED, "up to %d states a channel are supported (got N=%d)", kMaxStates, d->N);
-  const double tiles = (double)d->B * d->G * ((d->E / d->G + 63) / 64);
-  if (d->E > kMaxChannels || tiles > kMaxTiles || (!step && d->T > kMaxTokens))
+  // the partial sums of 16 tokens over a row's tiles are 32-bit offsets
+  const double tiles = (double)d->G * ((d->E / d->G + 63) / 64);
+  if (d->E > kMaxChannels || tiles > 65536 || d->B * tiles > kMaxTiles || (!step && d->T > kMaxTokens))
     return record_error(PNR_E_INVALID, "problem too large for this library's index range");
   return PNR_OK;
 }

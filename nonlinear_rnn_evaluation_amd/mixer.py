@@ -1,8 +1,8 @@
-"""A sequence layer that mixes a nonlinear recurrence with linear attention, used three ways.
+"""Two sequence layers beside the nonlinear recurrence, each used three ways.
 
     python -m nonlinear_rnn_evaluation_amd.mixer
 
-One layer, on x [B, T, D]:
+``Mixer`` mixes the recurrence with linear attention, on x [B, T, D]:
 
     h = diagonal GRU states of x                         pnr.evaluate       (parallel Newton)
     q, k, v, gate, a = slices of h W_in                  one projection
@@ -14,6 +14,17 @@ One layer, on x [B, T, D]:
 ``token`` continues, one token for each request, with the attention states in a pool;
 ``gradients`` runs it forward and back.  The projections are torch products; the rest runs in
 the HIP library.
+
+``StateSpace`` is a selective state space layer, on x [B, T, D]:
+
+    x, z = halves of x W_in                              one projection
+    u = silu(causal convolution of x)                    pnr.causal_conv
+    dt, B, C = slices of u W_x, dt = dt W_dt
+    y = selective scan of u, gated by silu(z)            pnr.selective_scan
+    out = y W_out
+
+with the same three methods.  Its ``gradients`` keeps the convolution's input in 8 bits
+(pnr.checkpoint_pack) and u not at all: u is made again from the copy.
 """
 from __future__ import annotations
 
@@ -101,6 +112,78 @@ class Mixer:
                     W_in=h.flatten(0, 1).T @ grad_p.flatten(0, 1), W_out=y.flatten(0, 1).T @ grad_out.flatten(0, 1))
 
 
+class StateSpace:
+    """The layer's parameters: E channels of N states in G groups, W taps, step widths of rank R."""
+
+    def __init__(self, D: int, E: int, N: int = 16, *, G: int = 1, W: int = 4, R: int = 8, seed: int = 0, device="cuda"):
+        self.D, self.E, self.N, self.G, self.W, self.R = D, E, N, G, W, R
+        g = torch.Generator().manual_seed(seed)
+        self.sizes = [R, G * N, G * N]                                    # dt, B, C
+
+        def draw(*shape, scale):
+            return (torch.randn(*shape, generator=g) * scale).to(device)
+        self.W_in = draw(D, 2 * E, scale=D ** -0.5)
+        self.conv_w, self.conv_b = draw(E, W, scale=W ** -0.5), draw(E, scale=W ** -0.5)
+        self.W_x = draw(E, sum(self.sizes), scale=E ** -0.5)
+        self.W_dt = draw(R, E, scale=R ** -0.5)
+        width = torch.exp(torch.rand(E, generator=g) * 4.6 - 6.9)         # step widths of 0.001 to 0.1
+        self.dt_bias = (width + torch.log(-torch.expm1(-width))).to(device)
+        self.A_log = torch.log(torch.arange(1.0, N + 1)).expand(E, N).contiguous().to(device)
+        self.D_skip = torch.ones(E, device=device)
+        self.W_out = draw(E, D, scale=E ** -0.5)
+
+    def _inner(self, u):
+        """What the scan takes besides u: dt, A, B, C; B and C are strided slices."""
+        low, B, C = (u @ self.W_x).split(self.sizes, -1)
+        shape = (self.G, self.N)
+        return low, low @ self.W_dt, -torch.exp(self.A_log), B.unflatten(-1, shape), C.unflatten(-1, shape)
+
+    def prompt(self, x, lens=None):
+        """x [B, T, D], lens int32 [B]: dict(out [B, T, D], conv [B, W - 1, E] and S [B, E, N], the states after
+        each row's last token).  What lies behind a row's end in x is not used, and in out not meaningful."""
+        if lens is not None:
+            live = torch.arange(x.shape[1], device=x.device)[None, :, None] < lens[:, None, None]
+            x = torch.where(live, x, x.new_zeros(()))
+        xs, z = (x @ self.W_in).chunk(2, -1)
+        c = pnr.causal_conv(xs, self.conv_w, bias=self.conv_b, lens=lens)
+        _, dt, A, B, C = self._inner(c["y"])
+        r = pnr.selective_scan(c["y"], dt, A, B, C, D=self.D_skip, z=z, dt_bias=self.dt_bias, lens=lens)
+        return dict(out=r["y"] @ self.W_out, conv=c["state"], S=r["state"])
+
+    def token(self, x, conv, pool, slots):
+        """x [B, D], one token for each request, whose states lie in slot slots[b] of the pools conv
+        [n_slots, W - 1, E] and pool [n_slots, E, N], which are updated in place.  Returns out [B, D]."""
+        xs, z = (x @ self.W_in).chunk(2, -1)
+        u = pnr.causal_conv_step(xs, self.conv_w, conv, bias=self.conv_b, slots=slots)["y"]
+        _, dt, A, B, C = self._inner(u)
+        return pnr.selective_scan_step(u, dt, A, B, C, pool, D=self.D_skip, z=z, dt_bias=self.dt_bias, slots=slots)["y"] @ self.W_out
+
+    def gradients(self, x, grad_out, keep=True):
+        """out for x [B, T, D] and the gradients of <out, grad_out>: dict of x and of the parameters.  With keep,
+        what the backward pass needs of the convolution's input waits in 8 bits."""
+        xs, z = (x @ self.W_in).chunk(2, -1)
+        conv = dict(bias=self.conv_b)
+        u = pnr.causal_conv(xs, self.conv_w, **conv)["y"]
+        _, dt, A, B, C = self._inner(u)
+        y = pnr.selective_scan(u, dt, A, B, C, D=self.D_skip, z=z, dt_bias=self.dt_bias)["y"]
+        out = y @ self.W_out
+        kept = pnr.checkpoint_pack(xs) if keep else xs
+        del xs, u, dt, B, C
+        # back: u again, the output projection, the scan, its inputs' projections, the convolution
+        u = pnr.causal_conv(kept, self.conv_w, dtype=x.dtype, **conv)["y"]
+        low, dt, A, B, C = self._inner(u)
+        d = pnr.selective_scan_backward(u, dt, A, B, C, grad_out @ self.W_out.T, D=self.D_skip, z=z, dt_bias=self.dt_bias)
+        grad_low = torch.cat([d["dt"] @ self.W_dt.T, d["B"].flatten(2), d["C"].flatten(2)], -1)
+        dc = pnr.causal_conv_backward(kept, self.conv_w, d["u"] + grad_low @ self.W_x.T, **conv)
+        grad_in = torch.cat([dc["x"], d["z"]], -1)
+
+        def outer(a, b):
+            return a.flatten(0, 1).T @ b.flatten(0, 1)
+        return dict(out=out, x=grad_in @ self.W_in.T, W_in=outer(x, grad_in), conv_w=dc["weight"], conv_b=dc["bias"],
+                    W_x=outer(u, grad_low), W_dt=outer(low, d["dt"]), dt_bias=d["dt_bias"], A_log=d["A"] * A,
+                    D_skip=d["D"], W_out=outer(y, grad_out))
+
+
 def main():
     m = Mixer(D=256, H=8, H_kv=4, Dk=64, Dv=64)
     gen = torch.Generator(device="cuda").manual_seed(1)
@@ -119,6 +202,18 @@ def main():
         out, h = m.token(x[rows, at].contiguous(), h, pool, slots)
         worst = max(worst, (out - whole["out"][rows, at]).abs().max().item())
     print(f"prompt against token by token: largest difference {worst:.2e}")
+    layer = StateSpace(D=256, E=512)
+    full, start = layer.prompt(x, lens), layer.prompt(x, short)
+    conv, states, worst = torch.zeros(8, 3, 512, device="cuda"), torch.zeros(8, 512, 16, device="cuda"), 0.0
+    conv[slots.long()], states[slots.long()] = start["conv"], start["S"]
+    for i in range(10):
+        at = short.long() + i
+        out = layer.token(x[rows, at].contiguous(), conv, states, slots)
+        worst = max(worst, (out - full["out"][rows, at]).abs().max().item())
+    print(f"state space layer, prompt against token by token: largest difference {worst:.2e}")
+    one = torch.ones_like(x)
+    exact, kept = (layer.gradients(x, one, keep=k)["conv_w"] for k in (False, True))
+    print(f"its taps' gradient from an input kept in 8 bits: off by {((kept - exact).norm() / exact.norm()).item():.1e} of its norm")
     target = torch.randn(x.shape, generator=gen, device="cuda")
     loss = []
     for _ in range(5):
