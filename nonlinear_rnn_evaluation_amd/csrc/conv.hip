@@ -7,6 +7,7 @@
 // tokens, and keeps the last W - 1 inputs (and, backwards, gradients) in registers, so that
 // within a run everything is read once; W - 1 tokens are read again where runs meet.
 #include <algorithm>
+#include <type_traits>
 
 #include "seq_ops.h"
 
@@ -58,17 +59,35 @@ struct Inputs {
   const T* s;                      // state_in or nullptr
   int64_t st;
   int E, blocks, W;
+  // A token of the row as it lies in memory, and its values.
+  struct Raw {
+    std::conditional_t<kKept, int8_t, T> v[kV];
+    uint8_t e;
+  };
+  __device__ __forceinline__ Raw raw(int t) const {
+    Raw r;
+    if constexpr (kKept) {
+      __builtin_memcpy(r.v, __builtin_assume_aligned(codes + (int64_t)t * E, kV), kV);
+      r.e = exps[(int64_t)t * blocks];
+    } else {
+      __builtin_memcpy(r.v, __builtin_assume_aligned(x + t * st, sizeof(r.v)), sizeof(r.v));
+      r.e = 0;
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void values(const Raw& r, float (&v)[kV]) {
+    const float step = kKept ? unpack_step(r.e) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      if constexpr (kKept)
+        v[k] = r.v[k] * step;
+      else
+        v[k] = Elem<sizeof(T) == 2>::load(&r.v[k]);
+    }
+  }
   __device__ __forceinline__ void get(int t, float (&v)[kV]) const {
     if (t >= 0) {
-      if constexpr (kKept) {
-        int8_t q[kV];
-        __builtin_memcpy(q, __builtin_assume_aligned(codes + (int64_t)t * E, kV), kV);
-        const float step = unpack_step(exps[(int64_t)t * blocks]);
-#pragma unroll
-        for (int k = 0; k < kV; ++k) v[k] = q[k] * step;
-      } else {
-        load_values<T, kV>(x + t * st, v);
-      }
+      values(raw(t), v);
     } else if (s) {
       load_values<T, kV>(s + (int64_t)(t + W - 1) * E, v);
     } else {
@@ -118,7 +137,7 @@ __device__ __forceinline__ void load_taps(const Conv& a, int c, float (&wt)[W][k
   }
 }
 
-constexpr int kAhead = 4;          // tokens asked for before the first is used
+constexpr int kAhead = 2;          // tokens of a step; the next step's are asked for before it
 
 template <typename T, int kV, int W, bool kKept>
 __global__ void __launch_bounds__(256) forward_kernel(ConvArgs p) {
@@ -127,7 +146,7 @@ __global__ void __launch_bounds__(256) forward_kernel(ConvArgs p) {
     Place w;
     if (!place<kV>(p, block, w)) continue;
     const int n = row_len(a.lens, w.b, a.T), t0 = w.run * p.run, t1 = min(t0 + p.run, a.T);
-    const auto in = inputs<T, kV, kKept>(a, p.s_in, w.b, w.c);
+    auto in = inputs<T, kV, kKept>(a, p.s_in, w.b, w.c);
     float wt[W][kV], bias[kV], x[W - 1 + kAhead][kV];
     load_taps<kV, W>(a, w.c, wt, bias);
     T* y = (T*)p.y + (int64_t)w.b * a.T * a.E + w.c;
@@ -135,9 +154,16 @@ __global__ void __launch_bounds__(256) forward_kernel(ConvArgs p) {
     if (t0 < end)
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) in.get(t0 - (W - 1) + j, x[j]);
+    typename decltype(in)::Raw rx[kAhead];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) rx[i] = in.raw(min(t + i, end - 1));
+    };
+    if (t0 < end) fetch(t0);
     for (int t = t0; t < end; t += kAhead) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) in.get(min(t + i, end - 1), x[W - 1 + i]);
+      for (int i = 0; i < kAhead; ++i) in.values(rx[i], x[W - 1 + i]);
+      fetch(t + kAhead);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (t + i >= end) break;
@@ -183,7 +209,7 @@ __global__ void __launch_bounds__(256) backward_kernel(ConvArgs p) {
     Place w;
     if (!place<kV>(p, block, w)) continue;
     const int n = row_len(a.lens, w.b, a.T), t0 = w.run * p.run, t1 = min(t0 + p.run, a.T);
-    const auto in = inputs<T, kV, kKept>(a, p.s_in, w.b, w.c);
+    auto in = inputs<T, kV, kKept>(a, p.s_in, w.b, w.c);
     float wt[W][kV], bias[kV], x[W - 1 + kAhead][kV], g[W - 1 + kAhead][kV], gw[W][kV], gb[kV];
     load_taps<kV, W>(a, w.c, wt, bias);
 #pragma unroll
@@ -202,13 +228,28 @@ __global__ void __launch_bounds__(256) backward_kernel(ConvArgs p) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) in.get(t0 - (W - 1) + j, x[j]);
     // token t closes the gradient of input t - W + 1
-    for (int t = t0; t < stop; t += kAhead) {
+    struct Values {
+      T v[kV];
+    };
+    typename decltype(in)::Raw rx[kAhead];
+    Values rg[kAhead];
+    auto fetch = [&](int t) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int at = min(min(t + i, stop - 1), n - 1);
-        in.get(at, x[W - 1 + i]);
-        load_values<T, kV>(gy + (int64_t)at * a.E, g[W - 1 + i]);
+        rx[i] = in.raw(at);
+        __builtin_memcpy(rg[i].v, __builtin_assume_aligned(gy + (int64_t)at * a.E, sizeof(T) * kV), sizeof(T) * kV);
       }
+    };
+    if (t0 < stop) fetch(t0);
+    for (int t = t0; t < stop; t += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        in.values(rx[i], x[W - 1 + i]);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) g[W - 1 + i][k] = Elem<sizeof(T) == 2>::load(&rg[i].v[k]);
+      }
+      fetch(t + kAhead);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const bool live = t + i < min(stop, n), own = t + i < end;
@@ -346,8 +387,8 @@ __global__ void __launch_bounds__(256) step_kernel(ConvArgs p, const int32_t* sl
 }
 
 // Tokens of a thread: long runs read few tokens twice and leave few partial sums, short ones fill the device.
-// bf16, four taps, us with 16, 32 and 64 tokens: forward 8 x 2000 x 2048 22, 26 and 35, forward 4 x 4096 x
-// 4096 78, 71 and 68, backward 177 + 18, 156 + 8 and 174 + 5 (the gradients and the sums over runs).
+// bf16, four taps, us with 16, 32 and 64 tokens: forward 8 x 2000 x 2048 19.4, 22 and 23, forward 4 x 4096 x
+// 4096 60, 55 and 52, backward 129 + 18, 104 + 9 and 108 + 5 (the gradients and the sums over runs).
 int run_of(const Conv& a) {
   int run = 32;
   while (run > 8 && (int64_t)a.B * ((a.T + run - 1) / run) * (a.E / 4 + 1) < 400000) run /= 2;
@@ -389,7 +430,7 @@ hipError_t by_taps(int W, F&& f) {
 }
 
 // f with the element type, the channels of a thread (four where every operand is aligned to them; with eight
-// of them in bf16 the registers leave one wave a SIMD: 84 us forward where 71, 222 backward where 156) and
+// of them in bf16 the registers left one wave a SIMD: 84 us forward where 71, 222 backward where 156) and
 // whether x is an 8-bit copy, as types.
 template <typename F>
 hipError_t by_type(const Conv& a, bool vec, F&& f) {
