@@ -241,14 +241,14 @@ Plan plan_of(const SelScan& a) {
   p.waves = W <= kNarrow ? 1 : 4;
   p.per_group = (W + p.waves * kNarrow - 1) / (p.waves * kNarrow);
   const int64_t waves = (int64_t)a.B * a.G * ((W + kNarrow - 1) / kNarrow);
-  // One wave a SIMD goes through the tokens in one pass at 115 ns each; two passes over segments cost
-  // twice the instructions, but eight waves a SIMD fill each other's gaps.  bf16, 16 states, us in one
-  // pass and in the best number of segments: 1024 waves 520 and 485 (4 x 4096 tokens), 237 and 259
-  // (8 x 2000); 256 waves 473 and 150 (2 x 4096); 128 waves 4268 and 510 (32768).  A second pass and
-  // the join cost 8 us: 128 waves over 37 tokens 10.1 and 17.2.
+  // One wave a SIMD goes through the tokens in one pass at 120 ns each; two passes over segments cost
+  // twice the instructions, but many waves a SIMD fill each other's gaps.  bf16, 16 states, us in one
+  // pass and in two over 12288 to 16384 waves: 1792 waves 672 and 825, 1536 waves 341 and 365 (2048
+  // tokens), 1024 waves 520 and 483 (4096 tokens), 244 and 241 (2000), 256 waves 473 and 152, 128 waves
+  // 4268 and 510 (32768).  A second pass and the join cost 8 us: 128 waves over 37 tokens 10.1 and 17.2.
   // With row lengths some rows are expected to be short: what is cut behind their ends costs nothing, while in
   // one pass the longest row sets the time.
-  const int64_t enough = a.lens ? 4096 : 1024, target = a.lens ? 16384 : 8192;
+  const int64_t enough = a.lens ? 4096 : 1280, target = a.lens ? 16384 : 12288;
   int64_t S = 1;
   if (waves < enough && a.T > 128) S = std::min<int64_t>((a.T + 31) / 32, (target + waves - 1) / waves);
   const int64_t len = std::max<int64_t>(32, ((a.T + S - 1) / S + 31) / 32 * 32);
