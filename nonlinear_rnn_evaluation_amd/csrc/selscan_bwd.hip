@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(NB * 64, 2) local_kernel(BwdArgs p) {
 }
 
 // The recurrences over a row's segments: in place of a segment's sums its first state, and the gradient
-// that reaches its last state from behind.  A thread a state; eight segments are asked for at once.
+// that reaches its last state from behind.  A thread a state; eight segments of each are asked for at once.
 __device__ __forceinline__ void join_state(const BwdArgs& p, int s, int e, int b, int NP) {
   constexpr int kBatch = 8;
   const SelScan& a = p.a;
@@ -251,26 +251,25 @@ __device__ __forceinline__ void join_state(const BwdArgs& p, int s, int e, int b
   const size_t at = ((size_t)b * a.E + e) * a.N + s, row = (size_t)b * p.seg.S * a.E + e;
   float h = real && p.s_in ? p.s_in[at] : 0.0f, g = real && p.d.gstate_out ? p.d.gstate_out[at] : 0.0f;
   if (p.seg.S > 1) {
-    auto walk = [&](float* sums, bool back, float& v) {
-      for (int k0 = 0; k0 < segs; k0 += kBatch) {
-        float own[kBatch], d[kBatch];
+    for (int k0 = 0; k0 < segs; k0 += kBatch) {      // h from the first segment on, g from the last
+      float own[2][kBatch], d[2][kBatch];
+      size_t r[2][kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int j = min(k0 + k, segs - 1);
-          const size_t r = row + (size_t)(back ? segs - 1 - j : j) * a.E;
-          own[k] = sums[r * NP + s], d[k] = p.width[r];
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (k0 + k < segs) {
-            const int j = k0 + k;
-            sums[(row + (size_t)(back ? segs - 1 - j : j) * a.E) * NP + s] = v;
-            v = fmaf(v, __builtin_amdgcn_exp2f(d[k] * A), own[k]);
-          }
+      for (int k = 0; k < kBatch; ++k) {
+        const int j = min(k0 + k, segs - 1);
+        r[0][k] = row + (size_t)j * a.E, r[1][k] = row + (size_t)(segs - 1 - j) * a.E;
+        own[0][k] = p.hs[r[0][k] * NP + s], d[0][k] = p.width[r[0][k]];
+        own[1][k] = p.gs[r[1][k] * NP + s], d[1][k] = p.width[r[1][k]];
       }
-    };
-    walk(p.hs, false, h);
-    walk(p.gs, true, g);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k0 + k < segs) {
+          p.hs[r[0][k] * NP + s] = h;
+          h = fmaf(h, __builtin_amdgcn_exp2f(d[0][k] * A), own[0][k]);
+          p.gs[r[1][k] * NP + s] = g;
+          g = fmaf(g, __builtin_amdgcn_exp2f(d[1][k] * A), own[1][k]);
+        }
+    }
     if (real && p.d.gstate_in) p.d.gstate_in[at] = g;
   } else {                                        // one segment: its walk goes on to the first state
     p.hs[row * NP + s] = h;
@@ -560,15 +559,31 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
   }
 }
 
-// The tiles' sums of dB and dC, in order.  A thread a value.
+// What is summed over blocks of the walk, each value by one thread and in order: dB and dC of a token over the
+// tiles (the first `token_blocks` blocks), and dA, dD and the bias's gradient over rows and segments.
 template <bool kBf16>
-__global__ void __launch_bounds__(256) token_kernel(BwdArgs p) {
+__global__ void __launch_bounds__(256) sum_kernel(BwdArgs p, unsigned token_blocks) {
   using El = Elem<kBf16>;
   using T = typename El::type;
   const SelScan& a = p.a;
+  if (blockIdx.x >= token_blocks) {
+    const size_t i = (blockIdx.x - token_blocks) * (size_t)256 + threadIdx.x, nA = (size_t)a.E * a.N;
+    const bool inA = i < nA, inD = !inA && i < nA + a.E;
+    if (i >= nA + 2 * (size_t)a.E) return;
+    const float* part = inA ? p.pA : inD ? p.pD : p.pb;
+    float* out = inA ? p.d.gA : inD ? p.d.gD : p.d.gbias;
+    if (!out) return;
+    const size_t n = inA ? nA : a.E, j = inA ? i : inD ? i - nA : i - nA - a.E;
+    const int64_t rows = (int64_t)a.B * p.seg.S;
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t r = 0; r < rows; ++r) s += part[r * n + j];
+    out[j] = s;
+    return;
+  }
   const int NP = 16 * p.NB;
   const int64_t total = (int64_t)a.B * a.T * a.G * 2 * NP;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)token_blocks * 256) {
     const int k = (int)(i % (2 * NP)), n = k % NP;
     const int64_t row = i / (2 * NP) / a.G;
     const int g = (int)(i / (2 * NP) % a.G);
@@ -582,16 +597,6 @@ __global__ void __launch_bounds__(256) token_kernel(BwdArgs p) {
     }
     El::store(out + ((size_t)row * a.G + g) * a.N + n, s);
   }
-}
-
-// Sums over rows and segments, in order.
-__global__ void __launch_bounds__(256) row_kernel(const float* part, int64_t rows, size_t n, float* out) {
-  const size_t i = blockIdx.x * (size_t)256 + threadIdx.x;
-  if (i >= n) return;
-  float s = 0.0f;
-#pragma unroll 8
-  for (int64_t r = 0; r < rows; ++r) s += part[r * n + i];
-  out[i] = s;
 }
 
 struct Layout {
@@ -638,8 +643,10 @@ void launch(const BwdArgs& p, hipStream_t st) {
     local_kernel<kBf16, NB, false><<<blocks, NB * 64, 0, st>>>(p);
   join_kernel<<<(unsigned)std::min<int64_t>(((int64_t)a.B * a.E * 16 * NB + 255) / 256, 1 << 22), 256, 0, st>>>(p);
   walk_kernel<kBf16, NB><<<blocks, NB * 64, 0, st>>>(p);
-  if ((p.d.gB || p.d.gC) && a.T > 0)
-    token_kernel<kBf16><<<(unsigned)std::min<int64_t>(((int64_t)a.B * a.T * a.G * 32 * NB + 255) / 256, 1 << 20), 256, 0, st>>>(p);
+  const int64_t tokens = p.d.gB || p.d.gC ? (int64_t)a.B * a.T * a.G * 32 * NB : 0;
+  const unsigned token_blocks = (unsigned)std::min<int64_t>((tokens + 255) / 256, 1 << 20);
+  const unsigned row_blocks = p.pA || p.pD || p.pb ? (unsigned)(((int64_t)a.E * (a.N + 2) + 255) / 256) : 0;
+  if (token_blocks + row_blocks) sum_kernel<kBf16><<<token_blocks + row_blocks, 256, 0, st>>>(p, token_blocks);
 }
 
 }  // namespace
@@ -661,12 +668,6 @@ hipError_t launch_selscan_backward(const SelScan& a, const float* state_in, cons
     }
   };
   a.bf16 ? by_states(std::true_type{}) : by_states(std::false_type{});
-  auto rows = [&](const float* part, size_t n, float* out) {
-    if (out) row_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(part, (int64_t)a.B * l.seg.S, n, out);
-  };
-  rows(p.pA, (size_t)a.E * a.N, d.gA);
-  rows(p.pD, a.E, d.gD);
-  rows(p.pb, a.E, d.gbias);
   return hipGetLastError();
 }
 
