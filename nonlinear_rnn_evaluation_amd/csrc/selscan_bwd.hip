@@ -12,7 +12,10 @@
 //   walk_kernel    a segment's chunks, last to first: the chunk forwards once for the states
 //                  every four tokens (LDS), each four forwards again with all states and
 //                  decays in registers, and back through them
-// Instruction issue bounds it: some 25 slots a state and token in the walk and 8 before it.
+//   sum_kernel     what is summed over blocks
+// Instruction issue bounds it: 10 slots a state and token before the walk, 24 in it (4.5 and 4.5 of them
+// make states again).  bf16, 4 x 4096 tokens of 4096 channels x 16 states: 385, 15, 950 and 32 us.
+// States every 8 tokens instead of 16 cost the walk 1290 us where 1030: each chunk starts with waits.
 #include <algorithm>
 
 #include "selscan_tile.h"
@@ -23,7 +26,55 @@ namespace {
 using namespace selscan;
 
 constexpr int R = 4;               // states of a channel in a lane: 16 in a wave
+constexpr int kChannels = 64;      // of a wave
 constexpr int kChunk = 16, kFour = 4;
+
+// A wave owns 64 channels, one a lane, and 16 of their states: lane l holds, for four channels, the four
+// states that start at 4 (l / 4 % 4).  Its slot r belongs to the channel of the lane 4 r places away in
+// its row of 16, so that
+//   - what a channel needs once a token is computed by one lane, and a rotation of the row brings it to
+//     the three others that hold the rest of its states;
+//   - a sum over a channel's states is one rotation and one addition a slot, and ends in the lane
+//     that owns the channel;
+//   - a sum over channels (dB, dC) starts from four of them in a lane: 22 slots a token for 16 states
+//     of 64 channels.  With a channel a lane in a quad, as forwards, it would be four times that.
+
+// The value of the lane 4 r places away in the row of 16 (away<4 - r> undoes away<r>).
+template <int r>
+__device__ __forceinline__ float away(float x) {
+  if constexpr (r % 4 == 0) return x;
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + 4 * (r % 4), 0xf, 0xf, true));
+}
+template <int r>
+__device__ __forceinline__ int away(int x) {
+  if constexpr (r % 4 == 0) return x;
+  return __builtin_amdgcn_update_dpp(0, x, 0x120 + 4 * (r % 4), 0xf, 0xf, true);
+}
+__device__ __forceinline__ void to_slots(float x, float (&s)[4]) {
+  s[0] = x, s[1] = away<1>(x), s[2] = away<2>(x), s[3] = away<3>(x);
+}
+// The sum of a channel's four partial sums, in its lane.
+__device__ __forceinline__ float from_slots(const float (&s)[4]) {
+  return (s[0] + away<3>(s[1])) + (away<2>(s[2]) + away<1>(s[3]));
+}
+
+// A token of the recurrence: h = exp2(d A) h + x B in each of four slots, B of this lane's states at
+// p (LDS).  x B is an outer product of the channels of four neighbouring lanes and four states, which
+// one matrix instruction adds to the decayed states: B's four values come from the four lanes, x
+// from each.  It is exact as a fused multiplication and addition is.
+__device__ __forceinline__ void advance(float (&h)[4][R], const float (&A)[4][R], const float (&d)[4], const float (&x)[4],
+                                        const float* p, int lane) {
+  const float b = p[lane & 3];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = h[r][i] * __builtin_amdgcn_exp2f(d[r] * A[r][i]);
+    v = __builtin_amdgcn_mfma_f32_4x4x1f32(b, x[r], v, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < R; ++i) h[r][i] = v[i];
+  }
+}
 
 struct BwdArgs {
   SelScan a;
@@ -35,6 +86,11 @@ struct BwdArgs {
   float *states, *reach;           // [B, chunks, E, 16 NB] and [B, chunks, E]: from the segment's start to the chunk's
   float *hs, *gs, *width;          // [B, S, E, 16 NB] twice, [B, S, E]
   float *part, *pA, *pD, *pb;      // [B, T, tiles, 2, 16 NB]; [B S, E, N], [B S, E], [B S, E]
+};
+
+// Where a wave works: row b, group g, its first channel e0 (of E) and how many of 64 it has.
+struct Tile {
+  int b, g, e0, live;
 };
 
 // What a wave knows of its place: the tile, its states and its lanes' channels.
@@ -415,7 +471,7 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
           float dl[4], s[4];
           to_slots(delta, dl);
           to_slots(delta * uv[k], s);
-          advance<R>(h, A, dl, s, lane_bc + (f * kFour + k) * 32, x.lane);
+          advance(h, A, dl, s, lane_bc + (f * kFour + k) * 32, x.lane);
         }
         keep(f + 1);
       }

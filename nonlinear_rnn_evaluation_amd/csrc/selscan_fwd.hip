@@ -25,6 +25,63 @@ struct FwdArgs {
   float *sums, *width;       // [B, S, E, 4 R] states and [B, S, E] summed step widths of the segments
 };
 
+// Where a wave works: row b, group g, its first channel e0 (of E) and how many it has.
+struct Tile {
+  int b, g, e0, live;
+};
+
+// kW waves a block share a group's B and C, 16 channels each; `per_group` blocks a group.
+constexpr int kChannels = 16;
+template <int kW>
+__device__ __forceinline__ Tile tile_of(const SelScan& a, int64_t i, int per_group) {
+  Tile t;
+  const int W = a.E / a.G, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = (int)(i % per_group) * (kW * kChannels) + wave * kChannels;
+  const int64_t rest = i / per_group;
+  t.g = (int)(rest % a.G);
+  t.b = (int)(rest / a.G);
+  t.e0 = t.g * W + first;
+  t.live = min(W - first, kChannels);
+  return t;
+}
+
+// Tokens of B and C that a block stages at a time.
+template <int R>
+constexpr int kStage = R <= 4 ? 32 : 16;
+
+// Stages B and C of tokens t.. as fp32 [token][B, C][4 R], zeros beyond `end` and the states.  The
+// values are fetched to registers first, so that they travel while the tile before is computed.
+template <bool kBf16, int R, int kW, int kTok>
+struct Stage {
+  using El = Elem<kBf16>;
+  using T = typename El::type;
+  static constexpr int NP = 4 * R, kEach = (kTok * 2 * NP + kW * 64 - 1) / (kW * 64);
+  T raw[kEach];
+  const T *B, *C;
+  int64_t bt, ct;
+  int N;
+  __device__ __forceinline__ void start(const SelScan& a, const Tile& w) {
+    B = (const T*)a.Bt.p + w.b * a.Bt.sb + w.g * a.Bt.sh;
+    C = (const T*)a.Ct.p + w.b * a.Ct.sb + w.g * a.Ct.sh;
+    bt = a.Bt.st, ct = a.Ct.st, N = a.N;
+  }
+  __device__ __forceinline__ void fetch(int t, int end) {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = threadIdx.x + k * kW * 64, n = i % NP, tok = t + i / (2 * NP);
+      raw[k] = 0;
+      if (i < kTok * 2 * NP && n < N && tok < end) raw[k] = i / NP % 2 ? C[tok * ct + n] : B[tok * bt + n];
+    }
+  }
+  __device__ __forceinline__ void put(float* lds) const {
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int i = threadIdx.x + k * kW * 64;
+      if (i < kTok * 2 * NP) lds[i] = El::load(&raw[k]);
+    }
+  }
+};
+
 // B and C of four tokens, this lane's states.
 template <bool kOut, int R>
 struct Four {
@@ -67,7 +124,7 @@ __global__ void __launch_bounds__(kW * 64, 1) scan_kernel(FwdArgs p) {
   __shared__ alignas(16) float bc[2][kTok * 2 * NP];
   const SelScan& a = p.a;
   const int seg = (int)(blockIdx.x / p.tiles);
-  const Tile w = tile_of<kW, kNarrow>(a, blockIdx.x % p.tiles, p.per_group);
+  const Tile w = tile_of<kW>(a, blockIdx.x % p.tiles, p.per_group);
   const int n = row_len(a.lens, w.b, a.T), t0 = seg * p.seg.len, tend = min(t0 + p.seg.len, a.T), t1 = min(tend, n);
   if (kSum && t0 >= t1) return;
   const int lane = threadIdx.x & 63, nq = lane & 3, c = lane >> 2, e = w.e0 + min(c, w.live - 1);
@@ -238,9 +295,9 @@ struct Plan {
 Plan plan_of(const SelScan& a) {
   Plan p{};
   const int W = a.E / a.G;
-  p.waves = W <= kNarrow ? 1 : 4;
-  p.per_group = (W + p.waves * kNarrow - 1) / (p.waves * kNarrow);
-  const int64_t waves = (int64_t)a.B * a.G * ((W + kNarrow - 1) / kNarrow);
+  p.waves = W <= kChannels ? 1 : 4;
+  p.per_group = (W + p.waves * kChannels - 1) / (p.waves * kChannels);
+  const int64_t waves = (int64_t)a.B * a.G * ((W + kChannels - 1) / kChannels);
   // One wave a SIMD goes through the tokens in one pass at 120 ns each; two passes over segments cost
   // twice the instructions, but many waves a SIMD fill each other's gaps.  bf16, 16 states, us in one
   // pass and in two over 12288 to 16384 waves: 1792 waves 672 and 825, 1536 waves 341 and 365 (2048
