@@ -16,6 +16,10 @@ struct PackArgs {
   Tokens x;
   int64_t rows;
   int T, E, blocks;          // blocks: of 32 values in a row
+  bool even;                 // x's rows are x.st apart throughout
+  int lanes, per_row;        // threads of a row (a power of two, at most 256); of them with work
+  int col_blocks;
+  int64_t row_blocks;        // of 256 / lanes rows
   int8_t* codes;
   uint8_t* exps;
   void* out;                 // unpack
@@ -28,10 +32,17 @@ __device__ __forceinline__ int exponent_byte(uint32_t m) {
   return max((int)(m >> 23) - 6 + ((m & 0x7fffffu) > 0x7e0000u), 1);
 }
 
-// On the top exponent 2^122, 64 steps are beyond fp32's (and bf16's) largest value.
-__device__ __forceinline__ int code_of(float x, int s) {
-  const int q = s == 255 ? 0 : (int)rintf(ldexpf(x, 127 - s));
-  return s == 249 ? min(max(q, -63), 63) : q;
+// The codes of kV values on exponent byte s.  x 2^(127 - s) is exact, and adding 3 2^22 rounds it to a whole
+// number, ties to even, whose lowest byte is the code.
+template <int kV>
+__device__ __forceinline__ void codes_of(float (&v)[kV], int s, int8_t (&q)[kV]) {
+  const float scale = __uint_as_float((uint32_t)(254 - s) << 23);
+  if (s == 249) {            // on the top exponent 2^122, 64 steps are beyond fp32's (and bf16's) largest value
+#pragma unroll
+    for (int k = 0; k < kV; ++k) v[k] = fminf(fmaxf(v[k], -63.0f * 0x1p122f), 63.0f * 0x1p122f);
+  }
+#pragma unroll
+  for (int k = 0; k < kV; ++k) q[k] = s == 255 ? (int8_t)0 : (int8_t)__float_as_uint(fmaf(v[k], scale, 12582912.0f));
 }
 
 // kV values a lane: 8 (four lanes a block) or 1 (32 lanes a block).
@@ -40,19 +51,17 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
   using El = Elem<kBf16>;
   using T = typename El::type;
   constexpr int L = kPackBlock / kV;                       // lanes of a block
-  const int per_row = p.blocks * L;
-  const int64_t total = p.rows * per_row, padded = (total + 255) / 256 * 256;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < padded; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = min(i, total - 1) / per_row;       // a block's lanes stay together
-    const int c = (int)(min(i, total - 1) % per_row), e = c * kV;
-    const bool live = i < total && e < p.E;                // kV divides E or is 1
+  const int per = 256 / p.lanes, c = blockIdx.x % p.col_blocks * p.lanes + (threadIdx.x & (p.lanes - 1)), e = c * kV;
+  for (int64_t rb = blockIdx.x / p.col_blocks; rb < p.row_blocks; rb += gridDim.x / p.col_blocks) {
+    const int64_t row = rb * per + threadIdx.x / p.lanes;
+    const bool live = row < p.rows && e < p.E;             // kV divides E or is 1
     const int64_t at = row * p.E + e, exp_at = row * p.blocks + c / L;
     if constexpr (kPack) {
-      const T* x = (const T*)p.x.p + row / p.T * p.x.sb + row % p.T * p.x.st + e;
       float v[kV];
 #pragma unroll
       for (int k = 0; k < kV; ++k) v[k] = 0.0f;
       if (live) {
+        const T* x = (const T*)p.x.p + (p.even ? row * p.x.st : row / p.T * p.x.sb + row % p.T * p.x.st) + e;
         if constexpr (kV == 1) {
           v[0] = El::load(x);
         } else {
@@ -70,8 +79,7 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
       const int s = exponent_byte(m);
       if (live) {
         int8_t q[kV];
-#pragma unroll
-        for (int k = 0; k < kV; ++k) q[k] = (int8_t)code_of(v[k], s);
+        codes_of(v, s, q);
         __builtin_memcpy(__builtin_assume_aligned(p.codes + at, kV), q, kV);
         if (c % L == 0) p.exps[exp_at] = (uint8_t)s;
       }
@@ -89,9 +97,14 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
 }
 
 template <bool kBf16, int kV, bool kPack>
-void launch(const PackArgs& p, hipStream_t st) {
-  const int64_t total = p.rows * p.blocks * (kPackBlock / kV);
-  checkpoint_kernel<kBf16, kV, kPack><<<(unsigned)std::min<int64_t>((total + 255) / 256, 1 << 16), 256, 0, st>>>(p);
+void launch(PackArgs p, hipStream_t st) {
+  p.per_row = p.blocks * (kPackBlock / kV);                // whole blocks of 32: their lanes stay together
+  p.lanes = kPackBlock / kV;
+  while (p.lanes < 256 && p.lanes < p.per_row) p.lanes *= 2;
+  p.col_blocks = (p.per_row + p.lanes - 1) / p.lanes;
+  p.row_blocks = (p.rows + 256 / p.lanes - 1) / (256 / p.lanes);
+  const int64_t most = std::max<int64_t>(1, (1 << 20) / p.col_blocks);
+  checkpoint_kernel<kBf16, kV, kPack><<<(unsigned)(std::min(p.row_blocks, most) * p.col_blocks), 256, 0, st>>>(p);
 }
 
 template <bool kPack>
@@ -110,14 +123,19 @@ hipError_t launch(const PackArgs& p, bool bf16, bool vec, hipStream_t st) {
 hipError_t launch_checkpoint_pack(const Tokens& x, int B, int T, int E, int bf16, int8_t* codes, uint8_t* exps,
                                   hipStream_t st) {
   const int es = bf16 ? 2 : 4;
-  const PackArgs p{x, (int64_t)B * T, T, E, (E + kPackBlock - 1) / kPackBlock, codes, exps, nullptr};
+  PackArgs p{};
+  p.x = x, p.rows = (int64_t)B * T, p.T = T, p.E = E, p.blocks = (E + kPackBlock - 1) / kPackBlock;
+  p.even = B == 1 || x.sb == (int64_t)T * x.st;
+  p.codes = codes, p.exps = exps;
   const bool vec = E % 8 == 0 && (uintptr_t)x.p % 16 == 0 && x.sb * es % 16 == 0 && x.st * es % 16 == 0 && (uintptr_t)codes % 8 == 0;
   return launch<true>(p, bf16, vec, st);
 }
 
 hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t rows, int E, int bf16, void* x,
                                     hipStream_t st) {
-  const PackArgs p{{}, rows, 1, E, (E + kPackBlock - 1) / kPackBlock, const_cast<int8_t*>(codes), const_cast<uint8_t*>(exps), x};
+  PackArgs p{};
+  p.rows = rows, p.E = E, p.blocks = (E + kPackBlock - 1) / kPackBlock;
+  p.codes = const_cast<int8_t*>(codes), p.exps = const_cast<uint8_t*>(exps), p.out = x;
   const bool vec = E % 8 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)codes % 8 == 0;
   return launch<false>(p, bf16, vec, st);
 }
