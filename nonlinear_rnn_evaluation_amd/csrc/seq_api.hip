@@ -155,9 +155,11 @@ SelScan problem(const pnr_selscan* d, const void* u, const void* dt, const float
   SelScan a{};
   a.B = d->B, a.T = d->T, a.E = d->E, a.N = d->N, a.G = d->G;
   a.bf16 = d->dtype == PNR_BF16, a.softplus = d->softplus;
-  a.u = {u, d->u_stride[0], d->u_stride[1]};
-  a.dt = {dt, d->dt_stride[0], d->dt_stride[1]};
-  a.z = {z, d->z_stride[0], d->z_stride[1]};
+  // a single token's stride may be anything, and the kernels' 32-bit offsets of tokens that are not there count on it
+  auto stride = [&](const int64_t* s) { return d->T > 1 ? s[1] : 0; };
+  a.u = {u, d->u_stride[0], stride(d->u_stride)};
+  a.dt = {dt, d->dt_stride[0], stride(d->dt_stride)};
+  a.z = {z, d->z_stride[0], stride(d->z_stride)};
   a.Bt = {Bt, d->B_stride[0], d->B_stride[1], d->B_stride[2]};
   a.Ct = {Ct, d->C_stride[0], d->C_stride[1], d->C_stride[2]};
   a.A = A, a.D = D, a.bias = bias;

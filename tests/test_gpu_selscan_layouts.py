@@ -112,6 +112,23 @@ def test_a_single_token_has_no_stride():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("stride", [(1 << 24) + 1, (1 << 31) - 1, (1 << 31) + 5, (1 << 40) + (1 << 26) + 3])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_a_single_tokens_stride_is_in_no_offset(dtype, stride):
+    """Strides whose lower 32 bits are large too."""
+    c, gy, gs = _case(46, 2, 1, 40, 16, 1, dtype)
+    args, kw = _split(c)
+    ref, dref = pnr.selective_scan(*args, **kw), pnr.selective_scan_backward(*args, gy, grad_state=gs, **kw)
+    odd = lambda t: t.as_strided(t.shape, (t.stride(0), stride, *t.stride()[2:]))  # noqa: E731
+    kw["z"] = odd(kw["z"])
+    args = [a if a.dim() == 2 else odd(a) for a in args]
+    got, d = pnr.selective_scan(*args, **kw), pnr.selective_scan_backward(*args, gy, grad_state=gs, **kw)
+    assert torch.equal(ref["y"], got["y"]) and torch.equal(ref["state"], got["state"])
+    for n in GRADS:
+        assert torch.equal(dref[n], d[n]), n
+
+
+@pytest.mark.gpu
 def test_a_large_batch_of_convolutions_is_its_rows():
     """Long runs of tokens a thread against short ones: outputs and input gradients have one order of sums."""
     g = torch.Generator().manual_seed(45)
