@@ -679,7 +679,7 @@ int pnr_checkpoint_unpack(const pnr_checkpoint* desc, const int8_t* codes, const
  * dtype PNR_F32 or PNR_BF16, act PNR_ACT_NONE or PNR_ACT_SILU, 1 <= W <= 8 (others
  * PNR_E_UNSUPPORTED), E <= 2^20, T <= 2^30, B (E / 64 + 1) <= 4 million.  Sums are fp32, outputs
  * rounded once.  A NaN or an infinity reaches what the formulas compute from it, within its channel
- * and row.  Outputs do not overlap inputs.  The calls wait for nothing and allocate nothing.
+ * and row; an infinity may come out as a NaN.  Outputs do not overlap inputs.  The calls wait for nothing and allocate nothing.
  */
 typedef struct pnr_conv {
   int32_t B, T, E, W;    /* B, E, W >= 1, T >= 0                                       */
@@ -697,7 +697,7 @@ int pnr_conv_forward(const pnr_conv* desc, const void* x, const uint8_t* exponen
 /*
  * One token for each of B requests (T, the token stride and lens are not read): x and y [B, E],
  * state_in and state_out pools [n_slots, W - 1, E], slots and idle rows as in pnr_selscan_step;
- * the pools may be the same buffer.
+ * the pools may be the same buffer, and NULL with a single tap, which has no state.
  */
 int pnr_conv_step(const pnr_conv* desc, const void* x, const float* weight, const float* bias,
                   const void* state_in, const int32_t* slots, int n_slots, void* y, void* state_out);

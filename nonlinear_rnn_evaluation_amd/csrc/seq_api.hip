@@ -430,9 +430,9 @@ int pnr_conv_step(const pnr_conv* desc, const void* x, const float* weight, cons
   if (int rc = check_inputs(desc, a, false)) return rc;
   const size_t es = a.bf16 ? 2 : 4;
   if (!y || !aligned(y, es)) return record_error(PNR_E_INVALID, "y is NULL or misaligned");
-  if (desc->W > 1)
-    if (int rc = check_pool(state_in, state_out, slots, n_slots, desc->B, es)) return rc;
-  if (desc->W == 1 && (!aligned(slots, 4) || n_slots < 1)) return record_error(PNR_E_INVALID, "slots is misaligned, or n_slots < 1");
+  const void* none = &a;                 // a single tap has no state: any aligned address stands for the pools
+  const bool pools = desc->W > 1;
+  if (int rc = check_pool(pools ? state_in : none, pools ? state_out : none, slots, n_slots, desc->B, es)) return rc;
   return hip_status(launch_conv_step(a, state_in, slots, n_slots, y, state_out, (hipStream_t)desc->stream),
                     "causal convolution step");
 }

@@ -130,6 +130,9 @@ def test_arguments_of_the_convolution():
         s_in, n, y, s_out = (P, a[1], a[2], a[3]) if a[0] else (None, *a[1:])
         assert pnr.pnr_conv_step(d, P, P, None, s_in, P, n, y, s_out) == pnr.E_INVALID, a
     assert pnr.pnr_conv_step(d, P, P, None, P, None, 1, P, P) == pnr.E_INVALID      # without slots the pool holds every row
+    one = _conv(W=1)                                                                # also where it holds nothing
+    for slots, n in ((None, 1), (P, 0), (P + 2, 2)):
+        assert pnr.pnr_conv_step(one, P, P, None, None, slots, n, P, None) == pnr.E_INVALID, (slots, n)
     lib = pnr.load()
     assert lib.pnr_conv_forward(None, *[P] * 7) == pnr.E_INVALID and lib.pnr_conv_workspace_bytes_backward(None) == 0
     assert lib.pnr_conv_backward(None, *[P] * 11) == pnr.E_INVALID
