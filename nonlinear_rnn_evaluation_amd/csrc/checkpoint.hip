@@ -4,7 +4,9 @@
 //
 // Memory bounds both directions: 2 or 4 bytes and 33 / 32 of one an element.  Four lanes hold a
 // block, eight values each, so that loads are 16 bytes wide and the largest value meets in a
-// quad; operands off that alignment take a lane a value.
+// quad; operands off that alignment take a lane a value.  16384 x 4096 bf16 pack in 43 us (4.7 TB/s) and
+// unpack in 32 (6.3, partly from the last-level cache).  Rows and columns come from the launch: a division an
+// item made packing 50 us, bound by issue.
 #include <algorithm>
 
 #include "seq_ops.h"

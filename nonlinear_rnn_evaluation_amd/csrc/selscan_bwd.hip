@@ -14,7 +14,7 @@
 //                  decays in registers, and back through them
 //   sum_kernel     what is summed over blocks
 // Instruction issue bounds it: 10 slots a state and token before the walk, 24 in it (4.5 and 4.5 of them
-// make states again).  bf16, 4 x 4096 tokens of 4096 channels x 16 states: 385, 15, 950 and 32 us.
+// make states again).  bf16, 4 x 4096 tokens of 4096 channels x 16 states: 387, 15, 958 and 32 us.
 // States every 8 tokens instead of 16 cost the walk 1290 us where 1030: each chunk starts with waits.
 #include <algorithm>
 
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
           const float o = over_channels(dB, dC, x.lane);
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), out_part, k0 + k < end ? part_at : kNowhere, (k0 + k) * part_step, 0);
           if constexpr (NB == 1) finish(k);
-          if (k == 1) fetch(f > 0 ? k0 - kFour : 0, end);     // three tokens' states and decays are done with  // two tokens' states and decays are done with
+          if (k == 1) fetch(f > 0 ? k0 - kFour : 0, end);     // three tokens' states and decays are done with
         }
         if constexpr (NB > 1) {
 #pragma unroll
