@@ -3,8 +3,8 @@
 // step but that rounding exact.
 //
 // Memory bounds both directions: 2 or 4 bytes and 33 / 32 of one an element.  Four lanes hold a
-// block, eight values each, so that loads are 16 bytes wide and the largest value meets in a
-// quad; operands off that alignment take a lane a value.  16384 x 4096 bf16 pack in 43 us (4.7 TB/s) and
+// block, eight values each, so that loads are 16 bytes wide, on whatever address a row starts, and the
+// largest value meets in a quad.  16384 x 4096 bf16 pack in 43 us (4.7 TB/s) and
 // unpack in 32 (6.3, partly from the last-level cache).  Rows and columns come from the launch: a division an
 // item made packing 50 us, bound by issue.
 #include <algorithm>
@@ -14,12 +14,14 @@
 namespace pnr {
 namespace {
 
+constexpr int kV = 8;        // values of a lane
+
 struct PackArgs {
   Tokens x;
   int64_t rows;
   int T, E, blocks;          // blocks: of 32 values in a row
   bool even;                 // x's rows are x.st apart throughout
-  int lanes, per_row;        // threads of a row (a power of two, at most 256); of them with work
+  int lanes;                 // threads of a row in a block: a power of two, at most 256
   int col_blocks;
   int64_t row_blocks;        // of 256 / lanes rows
   int8_t* codes;
@@ -34,9 +36,8 @@ __device__ __forceinline__ int exponent_byte(uint32_t m) {
   return max((int)(m >> 23) - 6 + ((m & 0x7fffffu) > 0x7e0000u), 1);
 }
 
-// The codes of kV values on exponent byte s.  x 2^(127 - s) is exact, and adding 3 2^22 rounds it to a whole
+// The codes of a lane's values on exponent byte s.  x 2^(127 - s) is exact, and adding 3 2^22 rounds it to a whole
 // number, ties to even, whose lowest byte is the code.
-template <int kV>
 __device__ __forceinline__ void codes_of(float (&v)[kV], int s, int8_t (&q)[kV]) {
   const float scale = __uint_as_float((uint32_t)(254 - s) << 23);
   if (s == 249) {            // on the top exponent 2^122, 64 steps are beyond fp32's (and bf16's) largest value
@@ -47,8 +48,31 @@ __device__ __forceinline__ void codes_of(float (&v)[kV], int s, int8_t (&q)[kV])
   for (int k = 0; k < kV; ++k) q[k] = s == 255 ? (int8_t)0 : (int8_t)__float_as_uint(fmaf(v[k], scale, 12582912.0f));
 }
 
-// kV values a lane: 8 (four lanes a block) or 1 (32 lanes a block).
-template <bool kBf16, int kV, bool kPack>
+// Values between memory and a lane: eight at once, or the last few of a row.  kWhole: all rows are eights, aligned
+// to 16 bytes or their own size.
+template <bool kWhole, typename T>
+__device__ __forceinline__ void load_some(const T* p, int n, T (&v)[kV]) {
+  if (kWhole)
+    __builtin_memcpy(v, __builtin_assume_aligned(p, sizeof(v) < 16 ? sizeof(v) : 16), sizeof(v));
+  else if (n == kV)
+    __builtin_memcpy(v, p, sizeof(v));
+  else
+#pragma unroll
+    for (int k = 0; k < kV; ++k) v[k] = k < n ? p[k] : T(0);
+}
+template <bool kWhole, typename T>
+__device__ __forceinline__ void store_some(T* p, int n, const T (&v)[kV]) {
+  if (kWhole)
+    __builtin_memcpy(__builtin_assume_aligned(p, sizeof(v) < 16 ? sizeof(v) : 16), v, sizeof(v));
+  else if (n == kV)
+    __builtin_memcpy(p, v, sizeof(v));
+  else
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+      if (k < n) p[k] = v[k];
+}
+
+template <bool kBf16, bool kPack, bool kWhole>
 __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
   using El = Elem<kBf16>;
   using T = typename El::type;
@@ -56,7 +80,8 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
   const int per = 256 / p.lanes, c = blockIdx.x % p.col_blocks * p.lanes + (threadIdx.x & (p.lanes - 1)), e = c * kV;
   for (int64_t rb = blockIdx.x / p.col_blocks; rb < p.row_blocks; rb += gridDim.x / p.col_blocks) {
     const int64_t row = rb * per + threadIdx.x / p.lanes;
-    const bool live = row < p.rows && e < p.E;             // kV divides E or is 1
+    const int n = row < p.rows ? min(kV, p.E - e) : 0;
+    const bool live = n > 0;
     const int64_t at = row * p.E + e, exp_at = row * p.blocks + c / L;
     if constexpr (kPack) {
       float v[kV];
@@ -64,14 +89,10 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
       for (int k = 0; k < kV; ++k) v[k] = 0.0f;
       if (live) {
         const T* x = (const T*)p.x.p + (p.even ? row * p.x.st : row / p.T * p.x.sb + row % p.T * p.x.st) + e;
-        if constexpr (kV == 1) {
-          v[0] = El::load(x);
-        } else {
-          T raw[kV];
-          __builtin_memcpy(raw, __builtin_assume_aligned(x, 16), sizeof(raw));
+        T raw[kV];
+        load_some<kWhole>(x, n, raw);
 #pragma unroll
-          for (int k = 0; k < kV; ++k) v[k] = El::load(&raw[k]);
-        }
+        for (int k = 0; k < kV; ++k) v[k] = El::load(&raw[k]);
       }
       uint32_t m = 0;
 #pragma unroll
@@ -82,40 +103,41 @@ __global__ void __launch_bounds__(256) checkpoint_kernel(PackArgs p) {
       if (live) {
         int8_t q[kV];
         codes_of(v, s, q);
-        __builtin_memcpy(__builtin_assume_aligned(p.codes + at, kV), q, kV);
+        store_some<kWhole>(p.codes + at, n, q);
         if (c % L == 0) p.exps[exp_at] = (uint8_t)s;
       }
     } else if (live) {
       const float step = unpack_step(p.exps[exp_at]);
       int8_t q[kV];
-      __builtin_memcpy(q, __builtin_assume_aligned(p.codes + at, kV), kV);
-      T* out = (T*)p.out + at;
+      load_some<kWhole>(p.codes + at, n, q);
       T raw[kV];
 #pragma unroll
       for (int k = 0; k < kV; ++k) El::store(&raw[k], q[k] * step);
-      __builtin_memcpy(__builtin_assume_aligned(out, sizeof(T) * kV > 16 ? 16 : sizeof(T) * kV), raw, sizeof(raw));
+      store_some<kWhole>((T*)p.out + at, n, raw);
     }
   }
 }
 
-template <bool kBf16, int kV, bool kPack>
+template <bool kBf16, bool kPack, bool kWhole>
 void launch(PackArgs p, hipStream_t st) {
-  p.per_row = p.blocks * (kPackBlock / kV);                // whole blocks of 32: their lanes stay together
+  const int per_row = p.blocks * (kPackBlock / kV);        // whole blocks of 32: their lanes stay together
   p.lanes = kPackBlock / kV;
-  while (p.lanes < 256 && p.lanes < p.per_row) p.lanes *= 2;
-  p.col_blocks = (p.per_row + p.lanes - 1) / p.lanes;
+  while (p.lanes < 256 && p.lanes < per_row) p.lanes *= 2;
+  p.col_blocks = (per_row + p.lanes - 1) / p.lanes;
   p.row_blocks = (p.rows + 256 / p.lanes - 1) / (256 / p.lanes);
   const int64_t most = std::max<int64_t>(1, (1 << 20) / p.col_blocks);
-  checkpoint_kernel<kBf16, kV, kPack><<<(unsigned)(std::min(p.row_blocks, most) * p.col_blocks), 256, 0, st>>>(p);
+  checkpoint_kernel<kBf16, kPack, kWhole><<<(unsigned)(std::min(p.row_blocks, most) * p.col_blocks), 256, 0, st>>>(p);
 }
 
 template <bool kPack>
-hipError_t launch(const PackArgs& p, bool bf16, bool vec, hipStream_t st) {
+hipError_t launch(const PackArgs& p, bool bf16, bool whole, hipStream_t st) {
+  // 16384 x 4096 bf16, us as whole rows and as any others: packing 37 and 42, unpacking 33 and 41 (the few last values'
+  // loads and stores are in everybody's way); a lane a value took 215 and 160 for 4095
   if (p.rows > 0) {
     if (bf16)
-      vec ? launch<true, 8, kPack>(p, st) : launch<true, 1, kPack>(p, st);
+      whole ? launch<true, kPack, true>(p, st) : launch<true, kPack, false>(p, st);
     else
-      vec ? launch<false, 8, kPack>(p, st) : launch<false, 1, kPack>(p, st);
+      whole ? launch<false, kPack, true>(p, st) : launch<false, kPack, false>(p, st);
   }
   return hipGetLastError();
 }
@@ -129,8 +151,8 @@ hipError_t launch_checkpoint_pack(const Tokens& x, int B, int T, int E, int bf16
   p.x = x, p.rows = (int64_t)B * T, p.T = T, p.E = E, p.blocks = (E + kPackBlock - 1) / kPackBlock;
   p.even = B == 1 || x.sb == (int64_t)T * x.st;
   p.codes = codes, p.exps = exps;
-  const bool vec = E % 8 == 0 && (uintptr_t)x.p % 16 == 0 && x.sb * es % 16 == 0 && x.st * es % 16 == 0 && (uintptr_t)codes % 8 == 0;
-  return launch<true>(p, bf16, vec, st);
+  const bool whole = E % kV == 0 && (uintptr_t)x.p % 16 == 0 && x.sb * es % 16 == 0 && x.st * es % 16 == 0 && (uintptr_t)codes % kV == 0;
+  return launch<true>(p, bf16, whole, st);
 }
 
 hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, int64_t rows, int E, int bf16, void* x,
@@ -138,8 +160,8 @@ hipError_t launch_checkpoint_unpack(const int8_t* codes, const uint8_t* exps, in
   PackArgs p{};
   p.rows = rows, p.E = E, p.blocks = (E + kPackBlock - 1) / kPackBlock;
   p.codes = const_cast<int8_t*>(codes), p.exps = const_cast<uint8_t*>(exps), p.out = x;
-  const bool vec = E % 8 == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)codes % 8 == 0;
-  return launch<false>(p, bf16, vec, st);
+  const bool whole = E % kV == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)codes % kV == 0;
+  return launch<false>(p, bf16, whole, st);
 }
 
 }  // namespace pnr

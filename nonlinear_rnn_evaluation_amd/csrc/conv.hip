@@ -7,7 +7,8 @@
 // tokens, and keeps the last W - 1 inputs (and, backwards, gradients) in registers, so that
 // within a run everything is read once; W - 1 tokens are read again where runs meet.
 // 4 x 4096 x 4096 bf16, 4 taps, SiLU: forward 55 us (4.9 TB/s), gradients from an 8-bit copy 104 us
-// (3.3 TB/s, issue 71 % of the time) and 9 for the sums.  Eight channels a thread took half as long again.
+// (3.3 TB/s, issue 71 % of the time) and 9 for the sums.  Eight channels a
+// thread took up to 1.4 times that.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,7 +34,7 @@ struct ConvArgs {
 template <typename T, int kV>
 __device__ __forceinline__ void load_values(const T* p, float (&v)[kV]) {
   T raw[kV];
-  __builtin_memcpy(raw, __builtin_assume_aligned(p, sizeof(raw)), sizeof(raw));
+  __builtin_memcpy(raw, p, sizeof(raw));
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
     if constexpr (sizeof(T) == 2)
@@ -47,7 +48,7 @@ __device__ __forceinline__ void store_values(T* p, const float (&v)[kV]) {
   T raw[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) Elem<sizeof(T) == 2>::store(&raw[k], v[k]);
-  __builtin_memcpy(__builtin_assume_aligned(p, sizeof(raw)), raw, sizeof(raw));
+  __builtin_memcpy(p, raw, sizeof(raw));
 }
 
 // The inputs of a row, from position -(W - 1) on: the state's before token 0.
@@ -67,10 +68,10 @@ struct Inputs {
   __device__ __forceinline__ Raw raw(int t) const {
     Raw r;
     if constexpr (kKept) {
-      __builtin_memcpy(r.v, __builtin_assume_aligned(codes + (int64_t)t * E, kV), kV);
+      __builtin_memcpy(r.v, codes + (int64_t)t * E, kV);
       r.e = exps[(int64_t)t * blocks];
     } else {
-      __builtin_memcpy(r.v, __builtin_assume_aligned(x + t * st, sizeof(r.v)), sizeof(r.v));
+      __builtin_memcpy(r.v, x + t * st, sizeof(r.v));
       r.e = 0;
     }
     return r;
@@ -111,7 +112,8 @@ __device__ __forceinline__ Inputs<T, kV, kKept> inputs(const Conv& a, const void
   return in;
 }
 
-// The work of a thread: its first channel, row and run; false where it has none.
+// The work of a thread: its first channel, row and run; false where it has none.  A row's last thread goes back to
+// the last kV channels, some of which its neighbour has too: both write the same values.
 struct Place {
   int b, run, c;
 };
@@ -122,7 +124,7 @@ __device__ __forceinline__ bool place(const ConvArgs& p, int64_t block, Place& w
   const int per = 256 / p.lanes, col = cb * p.lanes + threadIdx.x % p.lanes;
   w.run = (int)(rest % p.run_blocks) * per + threadIdx.x / p.lanes;
   w.b = (int)(rest / p.run_blocks);
-  w.c = col * kV;
+  w.c = min(col * kV, p.a.E - kV);
   return col < p.cols && w.run < p.runs;
 }
 
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(256) backward_kernel(ConvArgs p) {
       for (int i = 0; i < kAhead; ++i) {
         const int at = min(min(t + i, stop - 1), n - 1);
         rx[i] = in.raw(at);
-        __builtin_memcpy(rg[i].v, __builtin_assume_aligned(gy + (int64_t)at * a.E, sizeof(T) * kV), sizeof(T) * kV);
+        __builtin_memcpy(rg[i].v, gy + (int64_t)at * a.E, sizeof(T) * kV);
       }
     };
     if (t0 < stop) fetch(t0);
@@ -398,7 +400,7 @@ int run_of(const Conv& a) {
 ConvArgs arguments(const Conv& a, int kV) {
   ConvArgs p{};
   p.a = a;
-  p.cols = a.E / kV;
+  p.cols = (a.E + kV - 1) / kV;
   p.lanes = 1;
   while (p.lanes < 256 && p.lanes < p.cols) p.lanes *= 2;
   p.run = run_of(a);
@@ -429,7 +431,7 @@ hipError_t by_taps(int W, F&& f) {
   return hipGetLastError();
 }
 
-// f with the element type, the channels of a thread (four where every operand is aligned to them; with eight
+// f with the element type, the channels of a thread (four, on whatever address they start; with eight
 // of them in bf16 the registers left one wave a SIMD: 84 us forward where 71, 222 backward where 156) and
 // whether x is an 8-bit copy, as types.
 template <typename F>
@@ -441,21 +443,15 @@ hipError_t by_type(const Conv& a, bool vec, F&& f) {
   return vec ? kept(float{}, Four{}) : kept(float{}, One{});
 }
 
-bool vectors(const Conv& a, std::initializer_list<const void*> ptrs) {
-  const int bytes = a.bf16 ? 8 : 16;
-  bool ok = a.E % 4 == 0;
-  if (a.exps)
-    ok = ok && (uintptr_t)a.x.p % 4 == 0;
-  else
-    ok = ok && (uintptr_t)a.x.p % bytes == 0 && a.x.sb % 4 == 0 && a.x.st % 4 == 0;
-  for (const void* p : ptrs) ok = ok && (uintptr_t)p % bytes == 0;
-  return ok;
-}
+// Whether a thread takes four channels: an 8-bit copy's last four have to share an exponent then.  4 x 4096 x 4095 bf16,
+// us with four and with one a thread: forward 58 and 65, from an 8-bit copy 41 and 62, gradients 133 and 175, from the
+// copy 122 and 169.
+bool fours(const Conv& a) { return a.E >= 4 && (!a.exps || (a.E - 1) % kPackBlock >= 3); }
 
 }  // namespace
 
 hipError_t launch_conv_forward(const Conv& a, const void* state_in, void* y, void* state_out, hipStream_t st) {
-  return by_type(a, vectors(a, {state_in, y, state_out}), [&](auto t, auto v, auto kept) {
+  return by_type(a, fours(a), [&](auto t, auto v, auto kept) {
     ConvArgs p = arguments(a, v);
     p.s_in = state_in, p.y = y, p.s_out = state_out;
     return by_taps(a.W, [&](auto w) { forward_kernel<decltype(t), v, w, kept><<<grid(p.blocks), 256, 0, st>>>(p); });
@@ -464,7 +460,8 @@ hipError_t launch_conv_forward(const Conv& a, const void* state_in, void* y, voi
 
 hipError_t launch_conv_step(const Conv& a, const void* state_in, const int32_t* slots, int n_slots, void* y,
                             void* state_out, hipStream_t st) {
-  return by_type(a, vectors(a, {state_in, y, state_out}), [&](auto t, auto v, auto kept) {
+  // pools may be updated in place, so no channel is two threads'
+  return by_type(a, a.E % 4 == 0, [&](auto t, auto v, auto kept) {
     ConvArgs p = arguments(a, v);
     p.s_in = state_in, p.y = y, p.s_out = state_out;
     const unsigned blocks = (unsigned)(((int64_t)a.B * p.cols + 255) / 256);
@@ -482,7 +479,7 @@ size_t conv_workspace_backward(const Conv& a) {
 
 hipError_t launch_conv_backward(const Conv& a, const void* state_in, const void* gy, const void* gstate_out, void* gx,
                                 float* gw, float* gb, void* gstate_in, char* ws, hipStream_t st) {
-  return by_type(a, vectors(a, {state_in, gy, gstate_out, gx}), [&](auto t, auto v, auto kept) {
+  return by_type(a, fours(a), [&](auto t, auto v, auto kept) {
     ConvArgs p = arguments(a, v);
     p.s_in = state_in, p.gy = gy, p.gs_out = gstate_out, p.gx = gx;
     p.part = gw || gb ? (float*)ws : nullptr;

@@ -287,3 +287,31 @@ def test_refusals():
         pnr.checkpoint_pack(x.transpose(1, 2))
     with pytest.raises(TypeError):
         pnr.causal_conv_step(pnr.Packed(p.codes[:, 0], p.exponents[:, 0]), w, kw["state"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("E", [1, 2, 3, 4, 5, 7, 9, 31, 33, 34, 35, 36, 63, 65, 67, 70, 101])
+def test_any_number_of_channels_is_part_of_a_wider_one(E, dtype):
+    """Channels by themselves, and blocks of 32 that end early: the same bits as with channels of zeros behind."""
+    wide = (E + 31) // 32 * 32
+    gen = torch.Generator().manual_seed(E)
+    draw = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    x, gy, s, gs = (draw(2, t, E).to(dtype) for t in (21, 21, 3, 3))
+    w, b = draw(E, 4), draw(E)
+    lens = torch.tensor([21, 6], dtype=torch.int32, device="cuda")
+    pad = lambda t, d=-1: torch.cat([t, t.new_zeros(*(wide - E if i == d % t.dim() else n for i, n in enumerate(t.shape)))], d)  # noqa: E731
+    kept, kept_wide = pnr.checkpoint_pack(x), pnr.checkpoint_pack(pad(x))
+    assert torch.equal(kept.codes, kept_wide.codes[..., :E]) and torch.equal(kept.exponents, kept_wide.exponents)
+    assert torch.equal(pnr.checkpoint_unpack(kept, dtype), pnr.checkpoint_unpack(kept_wide, dtype)[..., :E])
+    for one, two in ((x, pad(x)), (kept, kept_wide)):
+        a = pnr.causal_conv(one, w, bias=b, state=s, lens=lens, dtype=dtype)
+        r = pnr.causal_conv(two, pad(w, 0), bias=pad(b), state=pad(s), lens=lens, dtype=dtype)
+        assert torch.equal(a["y"], r["y"][..., :E]) and torch.equal(a["state"], r["state"][..., :E])
+        a = pnr.causal_conv_backward(one, w, gy, bias=b, state=s, lens=lens, grad_state=gs)
+        r = pnr.causal_conv_backward(two, pad(w, 0), pad(gy), bias=pad(b), state=pad(s), lens=lens, grad_state=pad(gs))
+        assert torch.equal(a["x"], r["x"][..., :E]) and torch.equal(a["state"], r["state"][..., :E])
+        assert torch.equal(a["weight"], r["weight"][:E]) and torch.equal(a["bias"], r["bias"][:E])
+    a = pnr.causal_conv_step(x[:, 0].contiguous(), w, s.clone(), bias=b)
+    r = pnr.causal_conv_step(pad(x[:, 0]), pad(w, 0), pad(s), bias=pad(b))
+    assert torch.equal(a["y"], r["y"][..., :E]) and torch.equal(a["state"], r["state"][..., :E])
