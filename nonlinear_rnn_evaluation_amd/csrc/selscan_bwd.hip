@@ -17,6 +17,7 @@
 // make states again).  bf16, 4 x 4096 tokens of 4096 channels x 16 states: 387, 15, 958 and 32 us.
 // States every 8 tokens instead of 16 cost the walk 1290 us where 1030: each chunk starts with waits.
 #include <algorithm>
+#include <cmath>
 
 #include "selscan_tile.h"
 
@@ -669,6 +670,9 @@ Layout layout(const SelScan& a) {
   const int64_t waves = (int64_t)a.B * l.tiles * l.NB;
   int64_t S = 1;
   if (waves < 2048) S = std::min<int64_t>((a.T + kChunk - 1) / kChunk, (4096 + waves - 1) / waves);
+  // Few channels: the join's segments follow each other, as do a segment's tokens.  us with 2048 segments, with 512 and
+  // with 128: 32768 tokens of 64 channels 422, 203 and 397; 8192 tokens with 512 and with 256: 133 and 107.
+  S = std::min<int64_t>(S, (int64_t)std::sqrt(8.0 * a.T));
   S = std::max<int64_t>(S, 1);
   const int64_t len = std::max<int64_t>(kChunk, ((a.T + S - 1) / S + kChunk - 1) / kChunk * kChunk);
   l.seg = {(int)std::max<int64_t>(1, (a.T + len - 1) / len), (int)len};
