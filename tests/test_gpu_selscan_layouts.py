@@ -97,6 +97,15 @@ def test_many_groups(E, G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [None, [4999, 2500]], ids=["whole", "ragged"])
+def test_few_channels_over_many_tokens(lens):
+    """Long enough that the number of segments follows from the tokens alone.  Roundings of 2^-24 over 5000 tokens
+    add like sqrt(5000) = 2^6.2, which is below the bound of 2^-17 too."""
+    c, gy, gs = _case(47, 2, 5000, 5, 4, 1, F32, lens=lens)
+    _check(c, gy, gs)
+
+
+@pytest.mark.gpu
 def test_a_single_token_has_no_stride():
     """Strides of a dimension of one element mean nothing, however large."""
     c, gy, gs = _case(44, 2, 1, 40, 16, 1, F32)
