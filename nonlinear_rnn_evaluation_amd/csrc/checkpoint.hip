@@ -131,7 +131,7 @@ void launch(PackArgs p, hipStream_t st) {
 
 template <bool kPack>
 hipError_t launch(const PackArgs& p, bool bf16, bool whole, hipStream_t st) {
-  // 16384 x 4096 bf16, us as whole rows and as any others: packing 37 and 42, unpacking 33 and 41 (the few last values'
+  // 16384 x 4096 bf16, us in a loop over one tensor, as whole rows and as any others: packing 37 and 42, unpacking 33 and 41 (the few last values'
   // loads and stores are in everybody's way); a lane a value took 215 and 160 for 4095
   if (p.rows > 0) {
     if (bf16)
