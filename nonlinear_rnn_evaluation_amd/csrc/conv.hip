@@ -260,11 +260,13 @@ __global__ void __launch_bounds__(256) backward_kernel(ConvArgs p) {
           float s = bias[k];
 #pragma unroll
           for (int j = 0; j < W; ++j) s = fmaf(wt[j][k], x[i + j][k], s);
-          const float gp = a.silu ? g[W - 1 + i][k] * silu_slope(s) : g[W - 1 + i][k], mine = own ? gp : 0.0f;
+          const float gp = a.silu ? g[W - 1 + i][k] * silu_slope(s) : g[W - 1 + i][k];
           g[W - 1 + i][k] = live ? gp : 0.0f;
-          gb[k] += mine;
+          if (own) {             // no product with zero: tokens behind the run may not be finite
+            gb[k] += gp;
 #pragma unroll
-          for (int j = 0; j < W; ++j) gw[j][k] = fmaf(mine, x[i + j][k], gw[j][k]);
+            for (int j = 0; j < W; ++j) gw[j][k] = fmaf(gp, x[i + j][k], gw[j][k]);
+          }
         }
         const int s = t + i - (W - 1);
         if (gx && s >= t0 && t + i < stop) {

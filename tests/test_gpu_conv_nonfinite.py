@@ -1,0 +1,53 @@
+"""What a NaN or an infinity reaches in the convolution's gradients: exactly the outputs whose formula contains it
+(pnr_conv_backward against the fp64 oracle, which walks the formula's terms and no others).
+
+An infinite result may come out as a NaN, so where the oracle is not finite the kernel is only asked not to be
+either; everywhere else the tolerances of test_gpu_conv.py hold.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from nonlinear_rnn_evaluation_amd import pnr
+from test_gpu_conv import BF16, F32, NAMES, SUMS, TOL, _case, _f64
+
+GRADS = ("x", "weight", "bias", "state")
+
+
+def _same_reach(name, got, ref, tol):
+    got = _f64(got)
+    bad = ~np.isfinite(ref)
+    assert np.array_equal(~np.isfinite(got), bad), (name, np.argwhere(~np.isfinite(got) != bad)[:8].tolist())
+    norm, err = np.linalg.norm(ref[~bad]), np.linalg.norm(got[~bad] - ref[~bad])
+    assert err <= tol * norm + 1e-30, (name, err, norm)
+
+
+def _check(x, values, w, gy, gs, kw):
+    dt = gy.dtype
+    d = pnr.causal_conv_backward(x, w, gy, grad_state=gs, **kw)
+    with np.errstate(all="ignore"):
+        want = O.causal_conv_grad(values, _f64(w), _f64(gy), gstate=_f64(gs), bias=_f64(kw["bias"]), act=NAMES[kw["act"]],
+                                  state=_f64(kw["state"]), lens=None if kw["lens"] is None else kw["lens"].cpu().numpy())
+    for n in GRADS:
+        _same_reach("grad_" + n, d[n], want[n], SUMS if n in ("weight", "bias") else TOL[dt])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", [pnr.ACT_NONE, pnr.ACT_SILU], ids=["none", "silu"])
+@pytest.mark.parametrize("value", ["inf", "nan"])
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 8, 9, 10, 11, 40])
+def test_a_token_near_a_rows_end(n, value, act, dtype):
+    """A token meets tap j where W - 1 - j tokens follow it: the last one only the last tap, and so on.  Rows
+    that end inside a run of tokens, at its end and just behind it; from x itself and from an 8-bit copy."""
+    for back in (1, 2, 3, 4):
+        if back > n:
+            continue
+        for lens in (None, [n, 40]):
+            x, w, gy, gs, kw = _case(50 + n, 2, n if lens is None else 40, 40, 4, dtype, act=act)
+            kw["lens"] = None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda()
+            x[0, n - back, 7] = float(value)
+            _check(x, _f64(x), w, gy, gs, kw)
+            kept = pnr.checkpoint_pack(x)
+            _check(kept, _f64(pnr.checkpoint_unpack(kept, dtype)), w, gy, gs, kw)
