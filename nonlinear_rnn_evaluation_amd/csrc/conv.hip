@@ -270,13 +270,12 @@ __global__ void __launch_bounds__(256) backward_kernel(ConvArgs p) {
         }
         const int s = t + i - (W - 1);
         if (gx && s >= t0 && t + i < stop) {
-          float o[kV];
+          float o[kV] = {};
 #pragma unroll
-          for (int k = 0; k < kV; ++k) {
-            o[k] = 0.0f;
+          for (int j = 0; j < W; ++j)
+            if (t + i - j < n)   // taps that met tokens
 #pragma unroll
-            for (int j = 0; j < W; ++j) o[k] = fmaf(wt[j][k], g[i + W - 1 - j][k], o[k]);
-          }
+              for (int k = 0; k < kV; ++k) o[k] = fmaf(wt[j][k], g[i + W - 1 - j][k], o[k]);
           if (gs && t + i >= n) {
             float v[kV];
             load_values<T, kV>(gs + (int64_t)(t + i - n) * a.E, v);

@@ -51,3 +51,16 @@ def test_a_token_near_a_rows_end(n, value, act, dtype):
             _check(x, _f64(x), w, gy, gs, kw)
             kept = pnr.checkpoint_pack(x)
             _check(kept, _f64(pnr.checkpoint_unpack(kept, dtype)), w, gy, gs, kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("value", ["inf", "nan"])
+@pytest.mark.parametrize("tap", [0, 1, 2, 3])
+def test_a_tap(tap, value, dtype):
+    """Without an activation a token's gradient contains the taps that the tokens behind it used."""
+    for n, lens in ((33, None), (40, [40, 9]), (40, [3, 0])):
+        x, w, gy, gs, kw = _case(60 + tap, 2, n, 36, 4, dtype, act=pnr.ACT_NONE)
+        kw["lens"] = None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda()
+        w[5, tap] = float(value)
+        _check(x, _f64(x), w, gy, gs, kw)
