@@ -572,6 +572,15 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
               asm volatile("" : "+v"(dA[r][i]));    // here, not behind the loop's branches, where 64 products wait for it
             }
           }
+          if (k > 0 && k0 + k >= end) {            // behind the row's end, where the walk begins: a width of 0 times a
+#pragma unroll                                     // state that need not be finite
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int i = 0; i < R; ++i) {
+                dA[r][i] = 0.0f;
+                asm volatile("" : "+v"(dA[r][i]));  // a branch: as selections the walk took 1.1 times as long
+              }
+          }
           ys[k] = from_slots(ya), qs[k] = from_slots(qa), ws[k] = from_slots(wa);
           const float o = over_channels(dB, dC, x.lane);
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), out_part, k0 + k < end ? part_at : kNowhere, (k0 + k) * part_step, 0);

@@ -1,0 +1,54 @@
+"""What a NaN, an infinity or a very large value reaches in the selective scan: exactly the outputs whose formula
+contains it (against the fp64 oracle, which walks the formula's terms and no others).
+
+An infinite result may come out as a NaN, so where the oracle is not finite the kernel is only asked not to be
+either; everywhere else the tolerances of test_gpu_selscan.py hold.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from nonlinear_rnn_evaluation_amd import pnr
+from test_gpu_selscan import BF16, F32, GRADS, TOKENS, TOL, _case, _f64, _split
+
+
+def _same_reach(name, got, ref, tol):
+    got = _f64(got)
+    bad = ~np.isfinite(ref)
+    assert np.array_equal(~np.isfinite(got), bad), (name, np.argwhere(~np.isfinite(got) != bad)[:8].tolist())
+    norm, err = np.linalg.norm(ref[~bad]), np.linalg.norm(got[~bad] - ref[~bad])
+    assert err <= tol * norm + 1e-30, (name, err, norm)
+
+
+def _ref(c):
+    names = dict(u="u", dt="dt", A="A", B="B", C="C", D="D", z="z", bias="dt_bias", state="state")
+    return dict({k: _f64(c[v]) for k, v in names.items()}, softplus=c["softplus"],
+                lens=None if c["lens"] is None else c["lens"].cpu().numpy())
+
+
+def _check_gradients(c, gy, gs):
+    dt = c["u"].dtype
+    args, kw = _split(c)
+    d = pnr.selective_scan_backward(*args, gy, grad_state=gs, **kw)
+    with np.errstate(all="ignore"):
+        want = O.selective_scan_grad(gy=_f64(gy), gstate=_f64(gs), **_ref(c))
+    for n in GRADS:
+        if n in d:
+            _same_reach("grad_" + n, d[n], want[n], TOL[dt] if n in TOKENS else TOL[F32])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("where,value", [("u", "nan"), ("u", "inf"), ("B", "nan"), ("B", "-inf")], ids=str)
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 7, 15, 17, 18, 70])
+def test_a_rows_last_token(n, where, value, dtype):
+    """The state behind the last token meets only grad_C there: no decay follows, and grad_A does not contain
+    it, however many tokens the row has."""
+    for N, lens in ((16, None), (24, None), (5, [n, 0])):
+        T = n if lens is None else n + 6
+        c, gy, gs = _case(50 + n, 2, T, 70, N, 1, dtype, gated=n % 2 == 0)
+        c["lens"] = None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda()
+        c[where] = c[where].clone()
+        c[where][(0, n - 1, 7) if where == "u" else (0, n - 1, 0, 2)] = float(value)
+        _check_gradients(c, gy, gs)
