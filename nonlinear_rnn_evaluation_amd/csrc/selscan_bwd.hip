@@ -121,11 +121,15 @@ __device__ __forceinline__ Place place(const BwdArgs& p) {
   return x;
 }
 
+// A of a state that only fills a block of 16: decays are 1, and 0 at an infinite width, where 0 would make them
+// NaN and the channel's sums with them.
+constexpr float kNoState = -1.17549435e-38f;
+
 __device__ __forceinline__ void load_A(const SelScan& a, const Place& x, float (&A)[4][R]) {
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int i = 0; i < R; ++i) A[r][i] = x.ch[r] >= 0 && x.n0 + i < a.N ? exponent(a.A[(size_t)x.ch[r] * a.N + x.n0 + i]) : 0.0f;
+    for (int i = 0; i < R; ++i) A[r][i] = x.ch[r] >= 0 && x.n0 + i < a.N ? exponent(a.A[(size_t)x.ch[r] * a.N + x.n0 + i]) : kNoState;
 }
 
 // Four states of each slot from, or to, [.., E, 16 NB] at row `row` of E channels.  A slot without a channel
@@ -304,7 +308,7 @@ __device__ __forceinline__ void join_state(const BwdArgs& p, int s, int e, int b
   const SelScan& a = p.a;
   const int n = row_len(a.lens, b, a.T), segs = (int)(((int64_t)n + p.seg.len - 1) / p.seg.len);
   const bool real = s < a.N;
-  const float A = real ? exponent(a.A[(size_t)e * a.N + s]) : 0.0f;
+  const float A = real ? exponent(a.A[(size_t)e * a.N + s]) : kNoState;
   const size_t at = ((size_t)b * a.E + e) * a.N + s, row = (size_t)b * p.seg.S * a.E + e;
   float h = real && p.s_in ? p.s_in[at] : 0.0f, g = real && p.d.gstate_out ? p.d.gstate_out[at] : 0.0f;
   if (p.seg.S > 1) {

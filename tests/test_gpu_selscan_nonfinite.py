@@ -27,6 +27,15 @@ def _ref(c):
                 lens=None if c["lens"] is None else c["lens"].cpu().numpy())
 
 
+def _check_forward(c):
+    args, kw = _split(c)
+    got = pnr.selective_scan(*args, **kw)
+    with np.errstate(all="ignore"):
+        y, S = O.selective_scan(**_ref(c))
+    _same_reach("y", got["y"], y, TOL[c["u"].dtype])
+    _same_reach("state", got["state"], S, TOL[F32])
+
+
 def _check_gradients(c, gy, gs):
     dt = c["u"].dtype
     args, kw = _split(c)
@@ -51,4 +60,18 @@ def test_a_rows_last_token(n, where, value, dtype):
         c["lens"] = None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda()
         c[where] = c[where].clone()
         c[where][(0, n - 1, 7) if where == "u" else (0, n - 1, 0, 2)] = float(value)
+        _check_gradients(c, gy, gs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("value", ["inf", "-inf", "nan"])
+@pytest.mark.parametrize("where", ["dt", "z", "u", "C"])
+def test_a_token_inside_a_row(where, value, dtype):
+    """An infinite step width forgets: nothing of the gradients behind it reaches the tokens before.  State counts
+    with and without a remainder of the 16 that a wave holds."""
+    for N in (16, 11, 24):
+        c, gy, gs = _case(70, 2, 70, 70, N, 1, dtype)
+        c[where] = c[where].clone()
+        c[where][(0, 41, 7) if where != "C" else (0, 41, 0, 2)] = float(value)
         _check_gradients(c, gy, gs)
