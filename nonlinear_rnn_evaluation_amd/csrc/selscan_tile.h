@@ -18,7 +18,7 @@ __device__ __forceinline__ float quad_perm(float x) {
 // A for exponents of 2, finite where A is: a step width of 0 leaves the state.
 __device__ __forceinline__ float exponent(float A) {
   const float x = A * kLog2e;
-  return x < -3e38f ? -3e38f : x;
+  return x < -3e38f ? -3e38f : x > 3e38f ? 3e38f : x;
 }
 
 // A buffer from p on, empty unless `there`: at kNowhere, or in an empty one, loads give zeros and writes

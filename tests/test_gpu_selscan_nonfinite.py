@@ -75,3 +75,22 @@ def test_a_token_inside_a_row(where, value, dtype):
         c[where] = c[where].clone()
         c[where][(0, 41, 7) if where != "C" else (0, 41, 0, 2)] = float(value)
         _check_gradients(c, gy, gs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_no_step_width_leaves_a_state_whatever_the_decay(sign):
+    c, gy, gs = _case(72, 2, 40, 64, 16, 1, F32, softplus=False, bias=False, gated=False)
+    c["A"].fill_(sign * 3.3e38)
+    c["dt"].zero_()
+    args, kw = _split(c)
+    got = pnr.selective_scan(*args, **kw)
+    assert torch.equal(got["state"], c["state"])
+    y, _ = O.selective_scan(**_ref(c))
+    _same_reach("y", got["y"], y, TOL[F32])
+    one = pnr.selective_scan_step(*[a if a.dim() == 2 else a[:, 3] for a in args], c["state"].clone(), D=c["D"], softplus=False)
+    assert torch.equal(one["state"], c["state"])
+    d = pnr.selective_scan_backward(*args, gy, grad_state=gs, want=("u", "state", "C"), **kw)
+    want = O.selective_scan_grad(gy=_f64(gy), gstate=_f64(gs), **_ref(c))
+    for n in ("u", "state", "C"):
+        _same_reach("grad_" + n, d[n], want[n], TOL[F32])
