@@ -567,6 +567,8 @@ int pnr_groupnorm_backward(const pnr_norm* desc, const void* x, const float* wei
  *   B, C        [B, T, G, N] with element strides {batch, token, group}
  *               (strides >= 0, the last axis contiguous: slices of projections need no copy)
  *   A           fp32 [E, N], finite; a decay is meant (A <= 0, delta >= 0), others are taken as they are
+ *               (the gradients of states that grow may be NaN, zero ones too, from a stretch of tokens
+ *               on whose sum of delta A is beyond fp32's exponent)
  *   D, dt_bias  fp32 [E] or NULL (zeros)
  *   state_in, state_out   fp32 [B, E, N]
  *   y           [B, T, E] contiguous

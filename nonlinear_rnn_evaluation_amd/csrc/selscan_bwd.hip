@@ -326,9 +326,9 @@ __device__ __forceinline__ void join_state(const BwdArgs& p, int s, int e, int b
       for (int k = 0; k < kBatch; ++k)
         if (k0 + k < segs) {
           p.hs[r[0][k] * NP + s] = h;
-          h = fmaf(h, __builtin_amdgcn_exp2f(d[0][k] * A), own[0][k]);
+          h = carried(h, d[0][k] * A, factor(d[0][k] * A), own[0][k]);
           p.gs[r[1][k] * NP + s] = g;
-          g = fmaf(g, __builtin_amdgcn_exp2f(d[1][k] * A), own[1][k]);
+          g = carried(g, d[1][k] * A, factor(d[1][k] * A), own[1][k]);
         }
     }
     if (real && p.d.gstate_in) p.d.gstate_in[at] = g;

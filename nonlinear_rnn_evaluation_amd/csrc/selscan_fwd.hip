@@ -276,7 +276,7 @@ __device__ __forceinline__ void join_state(const FwdArgs& p, int s, int e, int b
     for (int k = 0; k < kBatch; ++k)
       if (k0 + k < segs) {
         p.sums[(row + (size_t)(k0 + k) * a.E) * NP + s] = h;
-        h = fmaf(h, __builtin_amdgcn_exp2f(d[k] * A), own[k]);
+        h = carried(h, d[k] * A, factor(d[k] * A), own[k]);
       }
   }
   if (p.s_out && real) p.s_out[at] = h;

@@ -21,6 +21,11 @@ __device__ __forceinline__ float exponent(float A) {
   return x < -3e38f ? -3e38f : x > 3e38f ? 3e38f : x;
 }
 
+// A decay over a segment as a factor, and what it leaves of h with own added.  2^x alone may be beyond fp32 (states
+// that grow): three factors reach from the least number beyond the largest, and a zero state stays zero.
+__device__ __forceinline__ float factor(float x) { return __builtin_amdgcn_exp2f(x > 127.0f ? fminf(x, 381.0f) * (1.0f / 3.0f) : x); }
+__device__ __forceinline__ float carried(float h, float x, float f, float own) { return fmaf(x > 127.0f ? h * f * f : h, f, own); }
+
 // A buffer from p on, empty unless `there`: at kNowhere, or in an empty one, loads give zeros and writes
 // are dropped.
 constexpr int kNowhere = 0x7fffffff;

@@ -78,6 +78,24 @@ def test_a_token_inside_a_row(where, value, dtype):
 
 
 @pytest.mark.gpu
+def test_a_state_that_grows():
+    """delta < 0: a segment's growth beyond fp32's range leaves a zero state zero and scales a tiny one."""
+    E, N, T = 64, 16, 170
+    c, _, _ = _case(71, 1, T, E, N, 1, F32, softplus=False, bias=False, state=False)
+    c["A"].fill_(-2.8)
+    c["dt"].fill_(-1.0)
+    c["u"].zero_()
+    c["u"][:, 127] = 1e-36
+    args, kw = _split(c)
+    got = pnr.selective_scan(*args, **kw)
+    y, S = O.selective_scan(**_ref(c))
+    assert np.abs(S).max() < 3e38 and not y[:, :127].any()
+    # the exponents reach 28 + 90 = 2^6.9, each rounded twice: 2^-23 of them, beside the usual bound
+    _same_reach("y", got["y"], y, 2.0 ** -15)
+    _same_reach("state", got["state"], S, 2.0 ** -15)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_no_step_width_leaves_a_state_whatever_the_decay(sign):
     c, gy, gs = _case(72, 2, 40, 64, 16, 1, F32, softplus=False, bias=False, gated=False)
