@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
         float ys[kFour], qs[kFour], ws[kFour];
         auto finish = [&](int k) {                // a token's gradients, from the sums over all states
           const bool there = k0 + k < end;
-          const float sg = sigm(zv[k]), gated_gy = gated ? gv[k] * zv[k] * sg : gv[k];
+          const float sg = sigm(zv[k]), gated_gy = gated ? gv[k] * (zv[k] * sg) : gv[k];
           const float y = fmaf(D, uv[k], ys[k]), gd = fmaf(uv[k], qs[k], kLn2 * ws[k]);
           float slope = sigm(raw[k]);
           asm volatile("" : "+v"(slope));         // no branch between tokens
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(NB * 64, 2) walk_kernel(BwdArgs p) {
           db += there ? gt : 0.0f;
           ou.set(k0 + k, there, fmaf(D, gated_gy, delta[k] * qs[k]));
           od.set(k0 + k, there, gt);
-          oz.set(k0 + k, there, gv[k] * y * sg * (1.0f + zv[k] * (1.0f - sg)));
+          oz.set(k0 + k, there, gv[k] * (sg * (1.0f + zv[k] * (1.0f - sg))) * y);   // a closed gate before anything large
         };
 #pragma unroll
         for (int k = kFour - 1; k >= 0; --k) {

@@ -112,3 +112,11 @@ def test_no_step_width_leaves_a_state_whatever_the_decay(sign):
     want = O.selective_scan_grad(gy=_f64(gy), gstate=_f64(gs), **_ref(c))
     for n in ("u", "state", "C"):
         _same_reach("grad_" + n, d[n], want[n], TOL[F32])
+
+
+@pytest.mark.gpu
+def test_a_closed_gate():
+    """silu(z) is zero far below: no product of large values before it may overflow."""
+    c, gy, gs = _case(73, 1, 40, 64, 16, 1, F32)
+    c["z"][0, 9], gy[0, 9], c["u"][0, 9] = -1e20, 1e20, 1e19
+    _check_gradients(c, gy, gs)
