@@ -426,7 +426,8 @@ int pnr_conv_forward(const pnr_conv* desc, const void* x, const uint8_t* exponen
 int pnr_conv_step(const pnr_conv* desc, const void* x, const float* weight, const float* bias, const void* state_in,
                   const int32_t* slots, int n_slots, void* y, void* state_out) {
   if (int rc = validate(desc, true)) return rc;
-  const Conv a = problem(desc, x, nullptr, weight, bias);
+  Conv a = problem(desc, x, nullptr, weight, bias);
+  a.T = 1, a.x.st = 0, a.lens = nullptr;       // not read; the launch's geometry counts tokens
   if (int rc = check_inputs(desc, a, false)) return rc;
   const size_t es = a.bf16 ? 2 : 4;
   if (!y || !aligned(y, es)) return record_error(PNR_E_INVALID, "y is NULL or misaligned");
