@@ -167,12 +167,12 @@ SelScan problem(const pnr_selscan* d, const void* u, const void* dt, const float
   return a;
 }
 
-int check_inputs(const pnr_selscan* d, const SelScan& a, bool empty) {
+int check_inputs(const SelScan& a, bool empty) {
   const size_t es = a.bf16 ? 2 : 4;
   if (!empty && (!a.u.p || !a.dt.p || !a.A || !a.Bt.p || !a.Ct.p))
     return record_error(PNR_E_INVALID, "u, dt, A, B and C must be non-NULL");
   if (!aligned(a.u.p, es) || !aligned(a.dt.p, es) || !aligned(a.z.p, es) || !aligned(a.Bt.p, es) || !aligned(a.Ct.p, es) ||
-      !aligned(a.A, 4) || !aligned(a.D, 4) || !aligned(a.bias, 4) || !aligned(d->lens, 4))
+      !aligned(a.A, 4) || !aligned(a.D, 4) || !aligned(a.bias, 4) || !aligned(a.lens, 4))
     return record_error(PNR_E_INVALID, "a pointer is not aligned to its element size");
   return PNR_OK;
 }
@@ -214,9 +214,9 @@ Conv problem(const pnr_conv* d, const void* x, const uint8_t* exps, const float*
   return a;
 }
 
-int check_inputs(const pnr_conv* d, const Conv& a, bool empty) {
+int check_inputs(const Conv& a, bool empty) {
   if ((!empty && !a.x.p) || !a.weight) return record_error(PNR_E_INVALID, "x and weight must be non-NULL");
-  if (!aligned(a.x.p, a.exps ? 1 : a.bf16 ? 2 : 4) || !aligned(a.weight, 4) || !aligned(a.bias, 4) || !aligned(d->lens, 4))
+  if (!aligned(a.x.p, a.exps ? 1 : a.bf16 ? 2 : 4) || !aligned(a.weight, 4) || !aligned(a.bias, 4) || !aligned(a.lens, 4))
     return record_error(PNR_E_INVALID, "a pointer is not aligned to its element size");
   return PNR_OK;
 }
@@ -347,7 +347,7 @@ int pnr_selscan_forward(const pnr_selscan* desc, const void* u, const void* dt, 
                         void* y, float* state_out) {
   if (int rc = validate(desc, false)) return rc;
   const SelScan a = problem(desc, u, dt, A, Bt, Ct, D, z, dt_bias);
-  if (int rc = check_inputs(desc, a, desc->T == 0)) return rc;
+  if (int rc = check_inputs(a, desc->T == 0)) return rc;
   if ((desc->T > 0 && !y) || !aligned(y, a.bf16 ? 2 : 4)) return record_error(PNR_E_INVALID, "y is NULL or misaligned");
   if (!aligned(state_in, 4) || !aligned(state_out, 4)) return record_error(PNR_E_INVALID, "a state pointer is misaligned");
   if (int rc = check_workspace(desc->workspace, desc->workspace_bytes, selscan_workspace(a))) return rc;
@@ -359,8 +359,9 @@ int pnr_selscan_step(const pnr_selscan* desc, const void* u, const void* dt, con
                      const void* Ct, const float* D, const void* z, const float* dt_bias, const float* state_in,
                      const int32_t* slots, int n_slots, void* y, float* state_out) {
   if (int rc = validate(desc, true)) return rc;
-  const SelScan a = problem(desc, u, dt, A, Bt, Ct, D, z, dt_bias);
-  if (int rc = check_inputs(desc, a, false)) return rc;
+  SelScan a = problem(desc, u, dt, A, Bt, Ct, D, z, dt_bias);
+  a.T = 1, a.lens = nullptr;                   // not read
+  if (int rc = check_inputs(a, false)) return rc;
   if (!y || !aligned(y, a.bf16 ? 2 : 4)) return record_error(PNR_E_INVALID, "y is NULL or misaligned");
   if (int rc = check_pool(state_in, state_out, slots, n_slots, desc->B, 4)) return rc;
   return hip_status(launch_selscan_step(a, state_in, slots, n_slots, y, state_out, (hipStream_t)desc->stream),
@@ -379,7 +380,7 @@ int pnr_selscan_backward(const pnr_selscan* desc, const void* u, const void* dt,
                          float* grad_state_in) {
   if (int rc = validate(desc, false)) return rc;
   const SelScan a = problem(desc, u, dt, A, Bt, Ct, D, z, dt_bias);
-  if (int rc = check_inputs(desc, a, desc->T == 0)) return rc;
+  if (int rc = check_inputs(a, desc->T == 0)) return rc;
   const size_t es = a.bf16 ? 2 : 4;
   if (desc->T > 0 && !grad_y) return record_error(PNR_E_INVALID, "grad_y must be non-NULL");
   if (grad_z && !z) return record_error(PNR_E_INVALID, "grad_z without a z");
@@ -415,7 +416,7 @@ int pnr_conv_forward(const pnr_conv* desc, const void* x, const uint8_t* exponen
                      const void* state_in, void* y, void* state_out) {
   if (int rc = validate(desc, false)) return rc;
   const Conv a = problem(desc, x, exponents, weight, bias);
-  if (int rc = check_inputs(desc, a, desc->T == 0)) return rc;
+  if (int rc = check_inputs(a, desc->T == 0)) return rc;
   const size_t es = a.bf16 ? 2 : 4;
   if ((desc->T > 0 && !y) || !aligned(y, es)) return record_error(PNR_E_INVALID, "y is NULL or misaligned");
   if (!aligned(state_in, es) || !aligned(state_out, es)) return record_error(PNR_E_INVALID, "a state pointer is misaligned");
@@ -428,7 +429,7 @@ int pnr_conv_step(const pnr_conv* desc, const void* x, const float* weight, cons
   if (int rc = validate(desc, true)) return rc;
   Conv a = problem(desc, x, nullptr, weight, bias);
   a.T = 1, a.x.st = 0, a.lens = nullptr;       // not read; the launch's geometry counts tokens
-  if (int rc = check_inputs(desc, a, false)) return rc;
+  if (int rc = check_inputs(a, false)) return rc;
   const size_t es = a.bf16 ? 2 : 4;
   if (!y || !aligned(y, es)) return record_error(PNR_E_INVALID, "y is NULL or misaligned");
   const void* none = &a;                 // a single tap has no state: any aligned address stands for the pools
@@ -448,7 +449,7 @@ int pnr_conv_backward(const pnr_conv* desc, const void* x, const uint8_t* expone
                       float* grad_weight, float* grad_bias, void* grad_state_in) {
   if (int rc = validate(desc, false)) return rc;
   const Conv a = problem(desc, x, exponents, weight, bias);
-  if (int rc = check_inputs(desc, a, desc->T == 0)) return rc;
+  if (int rc = check_inputs(a, desc->T == 0)) return rc;
   const size_t es = a.bf16 ? 2 : 4;
   if (desc->T > 0 && !grad_y) return record_error(PNR_E_INVALID, "grad_y must be non-NULL");
   if (!aligned(grad_y, es) || !aligned(grad_x, es) || !aligned(state_in, es) || !aligned(grad_state_out, es) ||
