@@ -164,11 +164,14 @@ class StateSpace:
         xs, z = (x @ self.W_in).chunk(2, -1)
         conv = dict(bias=self.conv_b)
         u = pnr.causal_conv(xs, self.conv_w, **conv)["y"]
-        _, dt, A, B, C = self._inner(u)
+        low, dt, A, B, C = self._inner(u)
         y = pnr.selective_scan(u, dt, A, B, C, D=self.D_skip, z=z, dt_bias=self.dt_bias)["y"]
+        del u, low, dt, B, C
         out = y @ self.W_out
-        kept = pnr.checkpoint_pack(xs) if keep else xs
-        del xs, u, dt, B, C
+        kept = xs
+        if keep:                                                          # xs and z are halves of one tensor: both go
+            kept, z = pnr.checkpoint_pack(xs), z.contiguous()
+        del xs
         # back: u again, the output projection, the scan, its inputs' projections, the convolution
         u = pnr.causal_conv(kept, self.conv_w, dtype=x.dtype, **conv)["y"]
         low, dt, A, B, C = self._inner(u)
