@@ -939,10 +939,20 @@ def selective_scan_backward(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, 
     return out
 
 
-class Packed(NamedTuple):
-    """An activation in 8 bits: value = codes * 2^(exponents - 127), 32 channels an exponent."""
+class _Copy(NamedTuple):
     codes: torch.Tensor          # int8 [..., E]
     exponents: torch.Tensor      # uint8 [..., ceil(E / 32)]
+
+
+class Packed(_Copy):
+    """An activation in 8 bits, (codes, exponents): value = codes * 2^(exponents - 127), 32 channels an exponent.
+    dtype is the type it was made of, None where nobody said."""
+    dtype: Optional[torch.dtype] = None
+
+    def __new__(cls, codes: torch.Tensor, exponents: torch.Tensor, dtype: Optional[torch.dtype] = None):
+        self = super().__new__(cls, codes, exponents)
+        self.dtype = dtype
+        return self
 
 
 def _packed(p: Packed) -> tuple:
@@ -972,7 +982,7 @@ def checkpoint_pack(x: torch.Tensor) -> Packed:
     desc = _pack(PnrCheckpoint, _CHECKPOINT, *(x.shape if dims == 3 else (1, *x.shape)), code, s[0] if dims == 3 else 0, s[-2],
                  _raw_stream(dev))
     _call(pnr_checkpoint_pack, dev, desc, x.data_ptr(), codes.data_ptr(), exps.data_ptr())
-    return Packed(codes, exps)
+    return Packed(codes, exps, x.dtype)
 
 
 def checkpoint_unpack(packed: Packed, dtype: torch.dtype) -> torch.Tensor:
@@ -1019,10 +1029,12 @@ def causal_conv(x: Union[torch.Tensor, Packed], weight: torch.Tensor, *, bias: O
     """Run pnr_conv_forward: y_t = act(bias + sum_j weight[:, j] x_{t-W+1+j}), each channel by itself.
     x [B,T,E] (float32 or bfloat16, strided as it comes, last axis contiguous) or a Packed copy of
     it, weight float32 [E,W], bias float32 [E], state [B,W-1,E] in y's dtype (the inputs before the
-    first, zeros if None), lens int32 [B]; dtype is y's, which only a packed x needs.  Returns
+    first, zeros if None), lens int32 [B]; dtype is y's, for a packed x (None: what it was made of).  Returns
     dict(y=[B,T,E], state=the last W - 1 inputs of each row)."""
     if dtype is None:
-        dtype = torch.bfloat16 if isinstance(x, Packed) else x.dtype
+        dtype = x.dtype
+        if dtype is None:
+            raise ValueError("causal_conv of a packed x whose type is not known needs a dtype")
     desc, ptrs, shape, W, dev = _conv(x, weight, bias, act, lens, dtype, False)
     where, last = weight.device, (shape[0], W - 1, shape[2])
     if y is None:
