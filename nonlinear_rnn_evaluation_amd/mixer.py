@@ -23,8 +23,8 @@ the HIP library.
     y = selective scan of u, gated by silu(z)            pnr.selective_scan
     out = y W_out
 
-with the same three methods.  Its ``gradients`` keeps the convolution's input in 8 bits
-(pnr.checkpoint_pack) and u not at all: u is made again from the copy.
+with the same three methods.  Its ``gradients`` keeps the convolution's input, on request in 8 bits
+(pnr.checkpoint_pack), and u not at all: u is made again from what was kept.
 """
 from __future__ import annotations
 
@@ -158,9 +158,10 @@ class StateSpace:
         _, dt, A, B, C = self._inner(u)
         return pnr.selective_scan_step(u, dt, A, B, C, pool, D=self.D_skip, z=z, dt_bias=self.dt_bias, slots=slots)["y"] @ self.W_out
 
-    def gradients(self, x, grad_out, keep=True):
+    def gradients(self, x, grad_out, keep=False):
         """out for x [B, T, D] and the gradients of <out, grad_out>: dict of x and of the parameters.  With keep,
-        what the backward pass needs of the convolution's input waits in 8 bits."""
+        what the backward pass needs of the convolution's input waits in 8 bits: out is that of x, and the gradients
+        are those at the rounded input, in everything that follows from it (u, dt, B and C)."""
         xs, z = (x @ self.W_in).chunk(2, -1)
         conv = dict(bias=self.conv_b)
         u = pnr.causal_conv(xs, self.conv_w, **conv)["y"]
