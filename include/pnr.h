@@ -563,7 +563,8 @@ int pnr_groupnorm_backward(const pnr_norm* desc, const void* x, const float* wei
  *   y_t = (sum over n of C_t h_t) + D u_t               and  y_t silu(z_t)  with a gate z
  *
  * Layout (device pointers, owned by the caller; elements of `dtype` unless stated):
- *   u, dt, z    [B, T, E] with element strides {batch, token}; z may be NULL (no gate)
+ *   u, dt, z    [B, T, E] with element strides {batch, token}; z may be NULL (no gate; its strides are
+ *               checked all the same, zeros will do)
  *   B, C        [B, T, G, N] with element strides {batch, token, group}
  *               (strides >= 0, the last axis contiguous: slices of projections need no copy)
  *   A           fp32 [E, N], finite; a decay is meant (A <= 0, delta >= 0), others are taken as they are
@@ -672,7 +673,8 @@ int pnr_checkpoint_unpack(const pnr_checkpoint* desc, const int8_t* codes, const
  * Causal convolution along time, each channel by itself, W taps:
  *   p_t = bias + sum over j < W of weight[e, j] x_{t - W + 1 + j},   y = act(p)
  * x [B, T, E] with element strides {batch, token} (>= 0, channels contiguous), or, with
- * `exponents`, the codes [B, T, E] that pnr_checkpoint_pack wrote (x_stride is not read then).
+ * `exponents`, the codes [B, T, E] that pnr_checkpoint_pack wrote (x_stride is not used then, only
+ * checked to be >= 0).
  * weight fp32 [E, W], bias fp32 [E] or NULL (zeros).  state_in [B, W - 1, E] are the inputs before
  * the first (NULL: zeros), state_out [B, W - 1, E] the last W - 1 inputs of each row, state_in's
  * among them where the row is shorter (NULL: not wanted).  y, the states and the gradients that

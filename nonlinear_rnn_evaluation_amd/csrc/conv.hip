@@ -6,8 +6,9 @@
 // Memory bounds it: x in and y out.  A thread takes a few neighbouring channels and a run of
 // tokens, and keeps the last W - 1 inputs (and, backwards, gradients) in registers, so that
 // within a run everything is read once; W - 1 tokens are read again where runs meet.
-// 4 x 4096 x 4096 bf16, 4 taps, SiLU: forward 55 us (4.9 TB/s), gradients from an 8-bit copy 104 us
-// (3.3 TB/s, issue 71 % of the time) and 9 for the sums.  Eight channels a
+// 4 x 4096 x 4096 bf16, 4 taps, SiLU: forward 57 us (4.7 TB/s), gradients from an 8-bit copy 104 us
+// (3.3 TB/s, issue 80 % of the time; 128 registers, four waves a SIMD) and 9 for the sums, as a profiler times the
+// kernels; whole calls in a row take 52 and 105, and 112 for gradients from x itself.  Eight channels a
 // thread took up to 1.4 times that.
 #include <algorithm>
 #include <type_traits>
@@ -390,8 +391,8 @@ __global__ void __launch_bounds__(256) step_kernel(ConvArgs p, const int32_t* sl
 }
 
 // Tokens of a thread: long runs read few tokens twice and leave few partial sums, short ones fill the device.
-// bf16, four taps, us with 16, 32 and 64 tokens: forward 8 x 2000 x 2048 19.4, 22 and 23, forward 4 x 4096 x
-// 4096 60, 55 and 52, backward 129 + 18, 104 + 9 and 108 + 5 (the gradients and the sums over runs).
+// bf16, four taps, us with 16, 32 and 64 tokens: forward 8 x 2000 x 2048 19.4, 22 and 23; 4 x 4096 x 4096 forward 49, 52
+// and 51, gradients from x 139, 112 and 112, from an 8-bit copy 133, 105 and 106 (with the sums over runs).
 int run_of(const Conv& a) {
   int run = 32;
   while (run > 8 && (int64_t)a.B * ((a.T + run - 1) / run) * (a.E / 4 + 1) < 400000) run /= 2;
@@ -445,8 +446,8 @@ hipError_t by_type(const Conv& a, bool vec, F&& f) {
 }
 
 // Whether a thread takes four channels: an 8-bit copy's last four have to share an exponent then.  4 x 4096 x 4095 bf16,
-// us with four and with one a thread: forward 58 and 65, from an 8-bit copy 41 and 62, gradients 133 and 175, from the
-// copy 122 and 169.
+// us with four and with one a thread: forward 56 and 63, from an 8-bit copy 42 and 60, gradients 124 and 172, from the
+// copy 115 and 172.
 bool fours(const Conv& a) { return a.E >= 4 && (!a.exps || (a.E - 1) % kPackBlock >= 3); }
 
 }  // namespace

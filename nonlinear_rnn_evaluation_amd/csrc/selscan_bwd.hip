@@ -14,7 +14,7 @@
 //                  decays in registers, and back through them
 //   sum_kernel     what is summed over blocks
 // Instruction issue bounds it: 10 slots a state and token before the walk, 24 in it (4.5 and 4.5 of them
-// make states again).  bf16, 4 x 4096 tokens of 4096 channels x 16 states: 387, 15, 958 and 32 us.
+// make states again).  bf16, 4 x 4096 tokens of 4096 channels x 16 states: 388, 15, 924 and 33 us.
 // States every 8 tokens instead of 16 cost the walk 1290 us where 1030: each chunk starts with waits.
 #include <algorithm>
 #include <cmath>
@@ -683,6 +683,8 @@ Layout layout(const SelScan& a) {
   const int64_t waves = (int64_t)a.B * l.tiles * l.NB;
   int64_t S = 1;
   if (waves < 2048) S = std::min<int64_t>((a.T + kChunk - 1) / kChunk, (4096 + waves - 1) / waves);
+  // us in one piece and cut, 1024 tokens in bf16: 16 states, 1024 waves 2082 and 1259, 1536 waves 2171 and 2001, 1984 waves 2399 and
+  // 2388; 32 states (two waves a tile) 1024 waves 2210 and 1757; 64 states (one wave a SIMD has room) 1024 waves 1581 and 1704.
   // Few channels: the join's segments follow each other, as do a segment's tokens.  us with 2048 segments, with 512 and
   // with 128: 32768 tokens of 64 channels 422, 203 and 397; 8192 tokens with 512 and with 256: 133 and 107.
   S = std::min<int64_t>(S, (int64_t)std::sqrt(8.0 * a.T));

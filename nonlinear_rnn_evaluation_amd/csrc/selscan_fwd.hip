@@ -8,10 +8,10 @@
 //
 // A quad of lanes holds a channel, so that what the states share (step width, gate, conversions)
 // costs each lane a quarter, and four tokens go at once, so that their steps fill each other's
-// gaps when a wave has its SIMD to itself.  9.2 slots a state and token, and vector
-// instructions issue 93 to 98 % of the time: 4 x 4096 x 4096 x 16 in bf16 302 us, after 220
-// for the sums where time is cut.  64 channels a wave with matrix instructions for the outer products, as
-// backwards, came within 7 % of it and was slower for small calls.
+// gaps when a wave has its SIMD to itself.  9.2 slots a state and token; 4 x 4096 x 4096 x 16 in bf16 301 us, after
+// 224 for the sums where time is cut, vector instructions issuing 98 and 92 % of the time (32768 x 2048 x 16: 93 and 87 %;
+// rows that end early: 69 and 61 %, since every block cuts its row as a full one).  64 channels a wave with matrix
+// instructions for the outer products, as backwards, came within 7 % of it and was slower for small calls.
 #include <algorithm>
 #include <cmath>
 
@@ -311,8 +311,14 @@ Plan plan_of(const SelScan& a) {
   // pass and in two over 12288 to 16384 waves: 1792 waves 672 and 825, 1536 waves 341 and 365 (2048
   // tokens), 1024 waves 520 and 483 (4096 tokens), 244 and 241 (2000), 256 waves 473 and 152, 128 waves
   // 4268 and 510 (32768).  A second pass and the join cost 8 us: 128 waves over 37 tokens 10.1 and 17.2.
+  // Other counts of states, us in one pass and in two: 4 states, 2048 tokens, 1024 waves 179 and 134, 1536 waves 256
+  // and 231; 32 states 768 waves 364 and 355, 1024 waves 369 and 464; 64 states (one wave a SIMD has room) 512 waves
+  // 645 and 590, 768 waves 648 and 828, 1024 waves 654 and 1071, 1536 waves 1308 and 1579.  So from 32 states on two
+  // passes cost up to 1.6 times one between 768 and 1280 waves.  fp32, 16 states: 1024 waves 283 and 268, 1536 356 and 393.
   // With row lengths some rows are expected to be short: what is cut behind their ends costs nothing, while in
-  // one pass the longest row sets the time.
+  // one pass the longest row sets the time.  2000 tokens, rows half full, us in one pass and in two: 1024 waves 236 and
+  // 183, 1792 waves 261 and 248, 2560 waves 295 and 368, 3840 waves 339 and 504; lengths that are all 2000: 1280 waves 332
+  // and 301, 1792 waves 336 and 420, 3840 waves 576 and 863.  So the second pass is lost from some 2000 waves on.
   const int64_t enough = a.lens ? 4096 : 1280, target = a.lens ? 16384 : 12288;
   int64_t S = 1;
   if (waves < enough && a.T > 128) S = std::min<int64_t>((a.T + 31) / 32, (target + waves - 1) / waves);

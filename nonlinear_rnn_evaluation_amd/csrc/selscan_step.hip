@@ -2,8 +2,8 @@
 //   h' = exp(delta A) h + delta u B,   y = (C . h' + D u) silu(z)
 //
 // The state is read and written once (8 bytes an element; the rest is a few per cent of that), so
-// memory bounds a full batch and the launch a small one: 256 requests of 4096 x 16 take 36 us, 42
-// with a pool that no cache holds (3.2 TB/s); one of 2048 x 16 takes 3.7.  A channel's states lie in the registers
+// memory bounds a full batch and the launch a small one: 256 requests of 4096 x 16 take 35 us, 42
+// with a pool that no cache holds (3.2 TB/s); one of 2048 x 16 takes 3.9.  A channel's states lie in the registers
 // of LPC neighbouring lanes, four consecutive ones each, and C . h' meets by shuffles.
 #include "selscan_tile.h"
 

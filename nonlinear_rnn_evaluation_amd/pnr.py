@@ -396,7 +396,6 @@ def pnr_groupnorm_backward(desc: PnrNorm, x: int, weight: Optional[int], bias: O
                                          grad_weight, grad_bias, grad_gate)
 
 
-# ---- torch-level conveniences (allocation + marshalling) ---------------------------------
 def pnr_selscan_workspace_bytes(desc: PnrSelscan) -> int:
     return load().pnr_selscan_workspace_bytes(ctypes.byref(desc))
 
@@ -454,6 +453,7 @@ def pnr_conv_backward(desc: PnrConv, x: int, exponents: Optional[int], weight: i
                                     grad_x, grad_weight, grad_bias, grad_state_in)
 
 
+# ---- torch-level conveniences (allocation + marshalling) ---------------------------------
 class PnrError(RuntimeError):
     pass
 
