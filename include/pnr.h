@@ -605,7 +605,8 @@ typedef struct pnr_selscan {
 
 /*
  * All tokens of a sequence at once.  state_in may be NULL (zeros), state_out NULL (not wanted);
- * they may be the same buffer.  Workspace: pnr_selscan_workspace_bytes() bytes (0: none needed, or
+ * they may be the same buffer.  Workspace: pnr_selscan_workspace_bytes() bytes for the same desc (whether
+ * lens is given counts; 0: none needed, or
  * an invalid request, which pnr_selscan_forward then names; pure host arithmetic).  With T = 0
  * only state_out is written.
  */
